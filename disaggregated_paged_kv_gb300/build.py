@@ -1,6 +1,6 @@
 """Builds libkvx.so in-tree for sm_103a (GB300) with nvcc.
 
-The three translation units compile in parallel; the CUDA runtime is linked statically, so
+The translation units compile in parallel; the CUDA runtime is linked statically, so
 the library needs only the driver at run time.  Output: disaggregated_paged_kv_gb300/libkvx.so.
 """
 from __future__ import annotations
@@ -17,7 +17,8 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libkvx.so")
 SOURCES = ["kvx_api.cu", "kvx_plan.cu", "kvx_copy.cu", "kvx_fused.cu", "kvx_noalloc.cu",
-           "kvx_stream.cu", "kvx_narrow.cu", "kvx_reshard.cu", "kvx_small.cu"]
+           "kvx_stream.cu", "kvx_narrow.cu", "kvx_reshard.cu", "kvx_small.cu", "kvx_tables.cu",
+           "kvx_attn.cu", "kvx_attn_general.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

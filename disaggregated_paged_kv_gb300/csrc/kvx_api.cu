@@ -13,21 +13,8 @@
 #include <new>
 
 #include "kvx_internal.cuh"
+#include "kvx_layout.cuh"
 #include "kvx_reshard.cuh"
-
-struct kvx_layout {
-  int32_t num_layers, kv_heads, head_dim, elem, kind, page_size;
-  int32_t kv_planes;  // planes per layer: 2 (K, V) or 1 (MLA latent)
-  int32_t vec;        // widest access (16, 8, 4, 2, 1 bytes) every row and head vector allows
-  int32_t planes;
-  int64_t num_slots;
-  int64_t row_bytes, seg_bytes;
-  int64_t slot_stride;  // NHD
-  int64_t page_bytes;   // HND
-  int64_t extent;       // bytes one plane spans from its start
-  uintptr_t lo, hi;     // envelope of all planes
-  uintptr_t plane[KVX_MAX_PLANES];
-};
 
 namespace {
 
@@ -488,6 +475,7 @@ kvx_status kvx_layout_create(const kvx_layout_desc *d, kvx_layout_t *out) {
   l->kv_heads = d->kv_heads;
   l->head_dim = d->head_dim;
   l->elem = eb;
+  l->dtype = d->dtype;
   l->kind = d->kind;
   l->kv_planes = kvp;
   l->planes = kvp * d->num_layers;

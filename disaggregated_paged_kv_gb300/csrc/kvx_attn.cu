@@ -1,0 +1,416 @@
+// kvx_attn.cu -- kvx_shared_attention: checks, the plan, the join, and the choice of kernels.
+//
+// Lengths and query starts are device data, so the split of the work is made on the device: a
+// one-CTA plan kernel cuts the prefix (rows of all tokens) and every request's own keys into
+// items of about equal key counts, so that their number suits the GPU, and the item kernels walk
+// that list with a grid that does not depend on it.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "kvx_attn.cuh"
+#include "kvx_internal.cuh"
+#include "kvx_launch.cuh"
+#include "kvx_layout.cuh"
+
+namespace kvx {
+namespace {
+
+constexpr int kPlanCta = 1024;
+
+__device__ __forceinline__ int64_t block_sum(int64_t x, int64_t *sm) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+  __syncthreads();
+  if (lane == 0) sm[w] = x;
+  __syncthreads();
+  int64_t t = 0;
+  for (int i = 0; i < (int)(blockDim.x >> 5); ++i) t += sm[i];
+  return t;
+}
+
+// Exclusive block-wide sum; *total gets the whole.
+__device__ __forceinline__ int64_t block_excl(int64_t x, int64_t *total, int64_t *sm) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  int64_t y = x;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t u = __shfl_up_sync(~0u, y, d);
+    if (lane >= d) y += u;
+  }
+  __syncthreads();
+  if (lane == 31) sm[w] = y;
+  __syncthreads();
+  int64_t before = 0, t = 0;
+  for (int i = 0; i < nw; ++i) {
+    if (i < w) before += sm[i];
+    t += sm[i];
+  }
+  *total = t;
+  return before + y - x;
+}
+
+// A request's query tokens and length as the kernels use them: clamped into what can be
+// addressed, whatever the arrays hold.
+struct Req {
+  int32_t t0, n, len;
+};
+
+__device__ __forceinline__ Req request(const AttnParams &p, int b, int32_t *bad) {
+  Req r;
+  r.t0 = b;
+  r.n = 1;
+  if (p.q_start) {
+    const int32_t a = p.q_start[b], z = p.q_start[b + 1];
+    if (a < 0 || z < a || z > p.n_q || (b == 0 && a != 0)) {
+      *bad = max(*bad, (int32_t)KVX_ERR_INVALID_ARG);
+      r.t0 = 0, r.n = 0;
+    } else {
+      r.t0 = a, r.n = z - a;
+    }
+  }
+  r.len = p.seq_lens[b];
+  if (r.len < 0) {
+    *bad = max(*bad, (int32_t)KVX_ERR_INVALID_ARG);
+    r.len = 0;
+  } else if (r.len > (int64_t)p.max_pages * p.page_size) {
+    *bad = max(*bad, (int32_t)KVX_ERR_OUT_OF_RANGE);
+    r.len = 0;
+  }
+  return r;
+}
+
+__global__ void __launch_bounds__(kPlanCta) attn_plan_kernel(const AttnParams p) {
+  __shared__ int64_t sm[32];
+  const int tid = threadIdx.x, n = p.n_reqs;
+  int32_t bad = 0;
+  if (tid == 0) *p.status = KVX_OK;
+  for (int t = tid; t < p.n_q; t += kPlanCta) p.owner[t] = -1, p.limit[t] = 0;
+  __syncthreads();
+  // how many key tiles there are in all, over the row tiles that read them
+  int64_t work = 0;
+  int32_t most = 0;
+  for (int b = tid; b < n; b += kPlanCta) {
+    const Req r = request(p, b, &bad);
+    const int64_t rows = (int64_t)r.n * p.group, tiles = (rows + p.row_tile - 1) / p.row_tile;
+    work += tiles * max(0, r.len - p.prefix_len);
+    most = max(most, r.len);
+    for (int i = 0; i < r.n; ++i) {
+      p.owner[r.t0 + i] = b;
+      p.limit[r.t0 + i] = max(0, r.len - r.n + i + 1);
+    }
+  }
+  for (int o = 16; o; o >>= 1) most = max(most, __shfl_xor_sync(~0u, most, o));
+  work = block_sum(work, sm);
+  __syncthreads();
+  if ((tid & 31) == 0) sm[tid >> 5] = most;
+  __syncthreads();
+  for (int i = 0; i < 32; ++i) most = max(most, (int32_t)sm[i]);
+  const int32_t prefix = min(p.prefix_len, most);
+  const int64_t prows = (int64_t)p.n_q * p.group;
+  const int64_t ptiles = (prows + p.row_tile - 1) / p.row_tile;
+  work = (work + ptiles * prefix) * p.kv_heads;
+  int64_t chunk = (work + p.target - 1) / p.target;
+  chunk = max(chunk, (int64_t)kAttnMinSplit);
+  chunk = (chunk + kAttnSplitTile - 1) / kAttnSplitTile * kAttnSplitTile;
+  chunk = min(chunk, (int64_t)1 << 30);
+  // segs, their items and partial rows; seg 0 is the prefix
+  int64_t items = 0, parts = 0;
+  for (int s0 = 0; s0 <= n; s0 += kPlanCta) {
+    const int s = s0 + tid;
+    AttnSeg g = {};
+    int64_t ni = 0, np = 0;
+    if (s <= n) {
+      if (s == 0) {
+        g.rows = (int32_t)prows;
+        g.key1 = prefix;
+      } else {
+        const Req r = request(p, s - 1, &bad);
+        g.row0 = r.t0 * p.group;
+        g.rows = r.n * p.group;
+        g.key0 = p.prefix_len;
+        g.key1 = max(r.len, p.prefix_len);
+      }
+      g.chunk = (int32_t)chunk;
+      if (g.rows > 0) g.splits = (int32_t)((g.key1 - g.key0 + chunk - 1) / chunk);
+      ni = (int64_t)((g.rows + p.row_tile - 1) / p.row_tile) * g.splits * p.kv_heads;
+      np = (int64_t)g.rows * g.splits * p.kv_heads;
+    }
+    int64_t ti, tp;
+    const int64_t bi = block_excl(ni, &ti, sm), bp = block_excl(np, &tp, sm);
+    g.part = parts + bp;
+    if (s <= n) {
+      p.segs[s] = g;
+      p.item_base[s] = (int32_t)(items + bi);
+    }
+    items += ti;
+    parts += tp;
+  }
+  // overlapping query ranges could ask for more than the workspace holds
+  if (items > p.max_items || parts > p.max_parts) {
+    bad = max(bad, (int32_t)KVX_ERR_INVALID_ARG);
+    items = 0;
+  }
+  const int any_range = __syncthreads_or(bad == KVX_ERR_OUT_OF_RANGE);
+  const int any_arg = __syncthreads_or(bad == KVX_ERR_INVALID_ARG);
+  const int64_t made = (any_range || any_arg) ? 0 : items;
+  if (tid == 0) {
+    p.head->n_items = (int32_t)made;
+    p.head->prefix_splits = p.segs[0].splits;
+    if (any_range) atomicMax(p.status, (int32_t)KVX_ERR_OUT_OF_RANGE);
+    else if (any_arg) atomicMax(p.status, (int32_t)KVX_ERR_INVALID_ARG);
+  }
+  // the item list: kv heads of one split and row tile side by side, so that neighbouring CTAs
+  // read neighbouring heads of the same rows
+  for (int64_t i = tid; i < made; i += kPlanCta) {
+    int lo = 0, hi = n;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (p.item_base[mid] <= i) lo = mid;
+      else hi = mid - 1;
+    }
+    const AttnSeg g = p.segs[lo];
+    int32_t k = (int32_t)(i - p.item_base[lo]);
+    const int32_t h = k % p.kv_heads;
+    k /= p.kv_heads;
+    const int32_t sp = k % g.splits, tile = k / g.splits;
+    AttnItem it;
+    it.row0 = g.row0 + tile * p.row_tile;
+    it.rows = min(p.row_tile, g.rows - tile * p.row_tile);
+    it.key0 = g.key0 + sp * g.chunk;
+    it.key1 = (int32_t)min((int64_t)g.key1, (int64_t)it.key0 + g.chunk);
+    it.table = lo - 1;
+    it.head = h;
+    it.part = g.part + ((int64_t)h * g.splits + sp) * g.rows + tile * p.row_tile;
+    p.items[i] = it;
+  }
+}
+
+__device__ __forceinline__ void put(float *o, float x) { *o = x; }
+__device__ __forceinline__ void put(__half *o, float x) { *o = __float2half_rn(x); }
+__device__ __forceinline__ void put(__nv_bfloat16 *o, float x) { *o = __float2bfloat16_rn(x); }
+
+constexpr int kJoinWarps = 4;
+
+// One warp joins the parts of one (token, query head), prefix splits first, in order.
+template <typename IO>
+__global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const AttnParams p) {
+  attn_wait_prior();
+  const int lane = threadIdx.x & 31;
+  const int64_t w = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+  if (w >= (int64_t)p.n_q * p.q_heads) return;
+  const int t = (int)(w / p.q_heads), qh = (int)(w - (int64_t)t * p.q_heads);
+  const int h = qh / p.group, r = t * p.group + qh - h * p.group;
+  const int D = p.head_dim, b = p.owner[t];
+  IO *out = reinterpret_cast<IO *>(p.out + t * p.out_tok + qh * p.out_head);
+  const AttnSeg sp = p.segs[0];
+  AttnSeg so = {};
+  if (b >= 0) so = p.segs[1 + b];
+  const int n0 = b >= 0 ? sp.splits : 0, n = p.head->n_items > 0 ? n0 + so.splits : 0;
+  auto part = [&](int i) {
+    return i < n0 ? sp.part + ((int64_t)h * sp.splits + i) * sp.rows + (r - sp.row0)
+                  : so.part + ((int64_t)h * so.splits + (i - n0)) * so.rows + (r - so.row0);
+  };
+  float top = -INFINITY;
+  for (int i = lane; i < n; i += 32) top = fmaxf(top, p.part_m[part(i)]);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+  const float base = top == -INFINITY ? 0.f : top;
+  float l = 0.f;
+  for (int i = 0; i < n; ++i) {
+    const int64_t x = part(i);
+    l = fmaf(exp2f(p.part_m[x] - base), p.part_l[x], l);
+  }
+  const float inv = l == 0.f ? 0.f : p.v_scale / l;
+  for (int d0 = 0; d0 < D; d0 += 128) {
+    float acc[4] = {};
+    for (int i = 0; i < n; ++i) {
+      const int64_t x = part(i);
+      const float f = exp2f(p.part_m[x] - base);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int d = d0 + c * 32 + lane;
+        if (d < D) acc[c] = fmaf(f, p.part_o[x * D + d], acc[c]);
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int d = d0 + c * 32 + lane;
+      if (d < D) put(out + d, l == 0.f ? 0.f : acc[c] * inv);
+    }
+  }
+  if (p.lse && lane == 0)
+    p.lse[w] = l == 0.f ? -INFINITY : (base + log2f(l)) * 0.693147180559945309f;
+}
+
+struct Sizes {
+  int64_t segs_off, base_off, limit_off, owner_off, items_off, m_off, l_off, o_off, total;
+  int64_t max_items, max_parts;
+  int32_t target;
+};
+
+constexpr int kTargetItems = 152 * 8;
+
+// Bounds on what the plan makes: with c keys a split, sum over segs of tiles * ceil(keys / c) *
+// kv_heads <= target + tiles in all * kv_heads, and a tile has at most row_tile rows.
+Sizes sizes(int64_t n_q, int64_t n_reqs, int64_t q_heads, int64_t kv_heads, int64_t prefix,
+            int64_t D, int row_tile) {
+  Sizes z = {};
+  const int64_t group = q_heads / kv_heads;
+  const int64_t tiles = (n_q * group + row_tile - 1) / row_tile + n_reqs +
+                        (prefix > 0 ? (n_q * group + row_tile - 1) / row_tile : 0);
+  z.target = kTargetItems;
+  z.max_items = z.target + tiles * kv_heads;
+  z.max_parts = std::min(z.max_items * row_tile,
+                         z.target * (int64_t)row_tile + 2 * n_q * q_heads);
+  z.segs_off = sizeof(AttnHeader);
+  z.base_off = align_up(z.segs_off + (int64_t)sizeof(AttnSeg) * (n_reqs + 1), 256);
+  z.limit_off = align_up(z.base_off + 4 * (n_reqs + 2), 256);
+  z.owner_off = align_up(z.limit_off + 4 * n_q, 256);
+  z.items_off = align_up(z.owner_off + 4 * n_q, 256);
+  z.m_off = align_up(z.items_off + (int64_t)sizeof(AttnItem) * z.max_items, 256);
+  z.l_off = align_up(z.m_off + 4 * z.max_parts, 256);
+  z.o_off = align_up(z.l_off + 4 * z.max_parts, 256);
+  z.total = align_up(z.o_off + 4 * z.max_parts * D, 256);
+  return z;
+}
+
+bool shape_ok(const kvx_layout *l, int64_t n_q, int64_t n_reqs, int64_t q_heads, int64_t prefix) {
+  return l && l->kv_planes == 2 && l->head_dim <= KVX_ATTN_MAX_HEAD_DIM && n_q >= 0 &&
+         n_reqs >= 0 && n_reqs <= KVX_MAX_TABLE_REQUESTS && q_heads >= 1 &&
+         q_heads % l->kv_heads == 0 && prefix >= 0 && n_q * q_heads <= (int64_t)1 << 30;
+}
+
+bool mult(const void *p, uintptr_t a) { return (uintptr_t)p % a == 0; }
+
+static_assert(sizeof(kvx_attn_args) == 152, "the binding mirrors this structure");
+
+}  // namespace
+}  // namespace kvx
+
+extern "C" size_t kvx_attention_workspace_size(kvx_layout_t pool, int32_t n_q, int32_t n_reqs,
+                                               int32_t q_heads, int32_t prefix_len) {
+  if (!kvx::shape_ok(pool, n_q, n_reqs, q_heads, prefix_len)) return 0;
+  return (size_t)kvx::sizes(n_q, n_reqs, q_heads, pool->kv_heads, prefix_len, pool->head_dim,
+                            kvx::kAttnGeneralRows).total;
+}
+
+extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_args *args,
+                                           void *d_ws, size_t ws_bytes, int32_t *d_status,
+                                           kvx_stream_t stream) {
+  using namespace kvx;
+  if (!pool || !args || !d_status) return KVX_ERR_INVALID_ARG;
+  const kvx_attn_args &a = *args;
+  if (a.reserved != 0 || a.reserved2 != 0 || !shape_ok(pool, a.n_q, a.n_reqs, a.q_heads, a.prefix_len) ||
+      a.layer < 0 || a.layer >= pool->num_layers || a.page_size < 1 || a.max_pages < 1 ||
+      a.table_stride < a.max_pages || a.n_prefix_pages < 0 || a.page_size > pool->num_slots)
+    return KVX_ERR_INVALID_ARG;
+  if (pool->dtype == KVX_FP8 ? (a.q_dtype != KVX_F16 && a.q_dtype != KVX_BF16)
+                             : a.q_dtype != pool->dtype)
+    return KVX_ERR_INVALID_ARG;
+  if (pool->kind == KVX_HND_PAGED && pool->page_size != a.page_size) return KVX_ERR_INVALID_ARG;
+  if ((int64_t)a.n_prefix_pages * a.page_size < a.prefix_len ||
+      (a.prefix_len > 0 && !a.prefix_pages))
+    return KVX_ERR_INVALID_ARG;
+  if (!a.q_start && a.n_q != a.n_reqs) return KVX_ERR_INVALID_ARG;
+  if (a.n_reqs > 0 && (!a.tables || !a.seq_lens)) return KVX_ERR_INVALID_ARG;
+  if (a.n_q > 0 && (!a.q || !a.out)) return KVX_ERR_INVALID_ARG;
+  if (!std::isfinite(a.scale) || !std::isfinite(a.k_scale) || !std::isfinite(a.v_scale))
+    return KVX_ERR_INVALID_ARG;
+  const int64_t io = a.q_dtype == KVX_F32 ? 4 : 2, most = ((int64_t)1 << 40);
+  for (int64_t x : {a.q_token_stride, a.q_head_stride, a.out_token_stride, a.out_head_stride,
+                    a.table_stride})
+    if (x < 0 || x > most) return KVX_ERR_INVALID_ARG;
+  if (!mult(a.q, io) || !mult(a.out, io)) return KVX_ERR_ALIGNMENT;
+  for (const void *q : {(const void *)a.tables, (const void *)a.prefix_pages,
+                        (const void *)a.seq_lens, (const void *)a.q_start, (const void *)a.lse,
+                        (const void *)d_status})
+    if (!mult(q, 4)) return KVX_ERR_ALIGNMENT;
+  if (a.n_q > 0) {
+    const uintptr_t b0 = (uintptr_t)a.out;
+    const uintptr_t b1 = b0 + ((a.n_q - 1) * a.out_token_stride + (a.q_heads - 1) * a.out_head_stride +
+                               pool->head_dim) * io;
+    for (int i = 2 * a.layer; i < 2 * a.layer + 2; ++i)
+      if (b0 < pool->plane[i] + pool->extent && pool->plane[i] < b1) return KVX_ERR_OVERLAP;
+  }
+  const Sizes z = sizes(a.n_q, a.n_reqs, a.q_heads, pool->kv_heads, a.prefix_len, pool->head_dim,
+                        kAttnGeneralRows);
+  if (!d_ws || !mult(d_ws, 256) || (int64_t)ws_bytes < z.total) return KVX_ERR_NO_WORKSPACE;
+
+  AttnParams p;
+  std::memset(&p, 0, sizeof(p));
+  const int64_t seg = pool->seg_bytes;
+  p.pool.k = reinterpret_cast<const char *>(pool->plane[2 * a.layer]);
+  p.pool.v = reinterpret_cast<const char *>(pool->plane[2 * a.layer + 1]);
+  const bool hnd = pool->kind == KVX_HND_PAGED;
+  p.pool.page_stride = hnd ? pool->page_bytes : pool->slot_stride * a.page_size;
+  p.pool.tok_stride = hnd ? seg : pool->slot_stride;
+  p.pool.head_stride = hnd ? seg * a.page_size : seg;
+  p.pool.num_pages = pool->num_slots / a.page_size;
+  p.pool.page_size = a.page_size;
+  p.pool.page_shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (a.page_size == (1 << i)) p.pool.page_shift = i;
+  p.tables = a.tables;
+  p.table_stride = a.table_stride;
+  p.prefix_pages = a.prefix_pages;
+  p.seq_lens = a.seq_lens;
+  p.q_start = a.q_start;
+  p.q = static_cast<const char *>(a.q);
+  p.out = static_cast<char *>(a.out);
+  p.q_tok = a.q_token_stride * io;
+  p.q_head = a.q_head_stride * io;
+  p.out_tok = a.out_token_stride * io;
+  p.out_head = a.out_head_stride * io;
+  p.lse = a.lse;
+  p.scale_log2 = (float)((double)a.scale * a.k_scale * 1.4426950408889634);
+  p.v_scale = a.v_scale;
+  p.n_q = a.n_q;
+  p.n_reqs = a.n_reqs;
+  p.q_heads = a.q_heads;
+  p.kv_heads = pool->kv_heads;
+  p.group = a.q_heads / pool->kv_heads;
+  p.head_dim = pool->head_dim;
+  p.page_size = a.page_size;
+  p.max_pages = a.max_pages;
+  p.prefix_len = a.prefix_len;
+  p.row_tile = kAttnGeneralRows;
+  p.target = z.target;
+  p.max_items = (int32_t)z.max_items;
+  p.max_parts = z.max_parts;
+  char *ws = static_cast<char *>(d_ws);
+  p.head = reinterpret_cast<AttnHeader *>(ws);
+  p.segs = reinterpret_cast<AttnSeg *>(ws + z.segs_off);
+  p.item_base = reinterpret_cast<int32_t *>(ws + z.base_off);
+  p.limit = reinterpret_cast<int32_t *>(ws + z.limit_off);
+  p.owner = reinterpret_cast<int32_t *>(ws + z.owner_off);
+  p.items = reinterpret_cast<AttnItem *>(ws + z.items_off);
+  p.part_m = reinterpret_cast<float *>(ws + z.m_off);
+  p.part_l = reinterpret_cast<float *>(ws + z.l_off);
+  p.part_o = reinterpret_cast<float *>(ws + z.o_off);
+  p.status = d_status;
+
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  void *kargs[] = {&p};
+  cudaError_t e = cudaLaunchKernel((const void *)attn_plan_kernel, dim3(1), dim3(kPlanCta), kargs, 0, s);
+  if (e == cudaSuccess && a.n_q > 0) {
+    e = launch_attn_general(p, pool->dtype, a.q_dtype, 152 * 2, s);
+    if (e == cudaSuccess) {
+      const void *join = a.q_dtype == KVX_F32   ? (const void *)attn_join_kernel<float>
+                         : a.q_dtype == KVX_F16 ? (const void *)attn_join_kernel<__half>
+                                                : (const void *)attn_join_kernel<__nv_bfloat16>;
+      const int64_t rows = (int64_t)a.n_q * a.q_heads;
+      e = launch_pdl(join, dim3((unsigned)((rows + kJoinWarps - 1) / kJoinWarps)),
+                     dim3(kJoinWarps * 32), kargs, s);
+    }
+  }
+  if (e != cudaSuccess) {
+    record_cuda_error(e);
+    return KVX_ERR_CUDA;
+  }
+  return KVX_OK;
+}

@@ -123,6 +123,65 @@ class HeadPart(ctypes.Structure):
 
 assert ctypes.sizeof(HeadPart) == 24
 
+class TablesArgs(ctypes.Structure):
+    """kvx_tables_args (kvx.h): device addresses and sizes of one block_tables call."""
+    _fields_ = [
+        ("n_reqs", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("old_lens", ctypes.c_void_p),
+        ("new_lens", ctypes.c_void_p),
+        ("prefix_pages", ctypes.c_void_p),
+        ("n_prefix_pages", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("tables", ctypes.c_void_p),
+        ("table_stride", ctypes.c_int64),
+        ("free_pages", ctypes.c_void_p),
+        ("n_free", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("cursor", ctypes.c_void_p),
+        ("next_cursor", ctypes.c_void_p),
+        ("q_start", ctypes.c_void_p),
+        ("slots", ctypes.c_void_p),
+        ("positions", ctypes.c_void_p),
+        ("max_tokens", ctypes.c_int64),
+    ]
+
+
+class AttnArgs(ctypes.Structure):
+    """kvx_attn_args (kvx.h): device addresses, strides and sizes of one shared_attention call."""
+    _fields_ = [
+        ("layer", ctypes.c_int32),
+        ("q_dtype", ctypes.c_int32),
+        ("q_heads", ctypes.c_int32),
+        ("n_q", ctypes.c_int32),
+        ("n_reqs", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("prefix_len", ctypes.c_int32),
+        ("table_stride", ctypes.c_int64),
+        ("tables", ctypes.c_void_p),
+        ("prefix_pages", ctypes.c_void_p),
+        ("n_prefix_pages", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("seq_lens", ctypes.c_void_p),
+        ("q_start", ctypes.c_void_p),
+        ("q", ctypes.c_void_p),
+        ("q_token_stride", ctypes.c_int64),
+        ("q_head_stride", ctypes.c_int64),
+        ("out", ctypes.c_void_p),
+        ("out_token_stride", ctypes.c_int64),
+        ("out_head_stride", ctypes.c_int64),
+        ("lse", ctypes.c_void_p),
+        ("scale", ctypes.c_float),
+        ("k_scale", ctypes.c_float),
+        ("v_scale", ctypes.c_float),
+        ("reserved2", ctypes.c_int32),
+    ]
+
+
+MAX_TABLE_REQUESTS = 65536
+ATTN_MAX_HEAD_DIM = 256
+
 RESHARD_MAX_LAYOUTS = 64
 RESHARD_MAX_PARTS = 128
 RESHARD_MAX_PLANE_TABLE = 3072
@@ -170,6 +229,10 @@ _SIGS = {
                               _VP, _U32, _VP]),
     "kvx_execute": (_I32, [_I32, _VP, _VP, _VP, _I32, _I64, _VP, _SZ, _VP, _SZ, _VP, _U32, _VP]),
     "kvx_plan_export": (_I32, [_VP, _SZ, _I64, _VP, _I64, _VP, _VP]),
+    "kvx_tables_workspace_size": (_SZ, [_I32]),
+    "kvx_block_tables": (_I32, [_VP, ctypes.POINTER(TablesArgs), _VP, _SZ, _VP, _VP]),
+    "kvx_attention_workspace_size": (_SZ, [_VP, _I32, _I32, _I32, _I32]),
+    "kvx_shared_attention": (_I32, [_VP, ctypes.POINTER(AttnArgs), _VP, _SZ, _VP, _VP]),
     "kvx_status_str": (ctypes.c_char_p, [_I32]),
     "kvx_last_cuda_error": (_I32, []),
     "kvx_version": (_I32, []),
@@ -619,6 +682,101 @@ def move_heads(op: int, src: Optional[Layout], src_slots, src_head0: int, dst: O
                               _nbytes(ws) if ws_bytes is None else ws_bytes, _ptr(status),
                               _flags(flags), _stream(stream))
     _check(rc, "kvx_move_heads")
+
+
+def tables_workspace_size(n_reqs: int) -> int:
+    """kvx_tables_workspace_size: bytes of workspace for block_tables of up to n_reqs requests."""
+    return int(lib().kvx_tables_workspace_size(n_reqs))
+
+
+def block_tables(pool: Layout, page_size: int, new_lens, tables, free_pages, cursor, next_cursor,
+                 q_start, slots, ws, status, old_lens=None, prefix_pages=None, positions=None,
+                 ws_bytes=None, stream=None) -> None:
+    """kvx_block_tables: pages from ``free_pages`` (``cursor`` of them handed out before) for
+    requests that grow from ``old_lens`` (0 or None: new, behind the shared ``prefix_pages``) to
+    ``new_lens`` tokens; fills ``tables`` (int32 [n_reqs, max_pages], rows any stride apart) and
+    the ``slots`` and ``positions`` of the new tokens, ``q_start`` saying whose they are.  All
+    arrays are device int32 tensors; ``cursor`` may be None (0) and ``next_cursor`` the same word
+    as ``cursor``."""
+    _i32_arrays(new_lens=new_lens, tables=tables, free_pages=free_pages, cursor=cursor,
+                next_cursor=next_cursor, q_start=q_start, slots=slots, old_lens=old_lens,
+                prefix_pages=prefix_pages, positions=positions, status=status)
+    n = new_lens.numel()
+    if tables.dim() != 2 or tables.shape[0] < n or q_start.numel() < n + 1:
+        raise ValueError("tables needs a row, and q_start an entry and one more, for each request")
+    if old_lens is not None and old_lens.numel() < n:
+        raise ValueError("old_lens is shorter than new_lens")
+    room = slots.numel()
+    if positions is not None:
+        room = min(room, positions.numel())
+    a = TablesArgs(n, page_size, _ptr(old_lens), new_lens.data_ptr(), _ptr(prefix_pages),
+                   0 if prefix_pages is None else prefix_pages.numel(), tables.shape[1],
+                   tables.data_ptr(), tables.stride(0), free_pages.data_ptr(), free_pages.numel(),
+                   0, _ptr(cursor), next_cursor.data_ptr(), q_start.data_ptr(), slots.data_ptr(),
+                   _ptr(positions), room)
+    _check(lib().kvx_block_tables(_h(pool), a, _ptr(ws), _nbytes(ws) if ws_bytes is None else ws_bytes,
+                                  _ptr(status), _stream(stream)), "kvx_block_tables")
+
+
+def attention_workspace_size(pool: Layout, n_q: int, n_reqs: int, q_heads: int,
+                             prefix_len: int) -> int:
+    """kvx_attention_workspace_size: bytes of workspace for shared_attention calls of up to these
+    sizes on the layout."""
+    return int(lib().kvx_attention_workspace_size(_h(pool), n_q, n_reqs, q_heads, prefix_len))
+
+
+def shared_attention(pool: Layout, layer: int, q, out, tables, seq_lens, page_size: int, ws,
+                     status, q_start=None, prefix_pages=None, prefix_len: int = 0, lse=None,
+                     scale: Optional[float] = None, k_scale: float = 1.0, v_scale: float = 1.0,
+                     ws_bytes=None, stream=None) -> None:
+    """kvx_shared_attention: causal attention of ``q`` ([n_q, q_heads, head_dim], a head's
+    elements contiguous) over one layer of the pool, into ``out`` (and ``lse``, float32
+    [n_q, q_heads]).  Request b's positions below ``prefix_len`` are those of ``prefix_pages``,
+    read once for the whole batch, the rest those of ``tables[b]``; its query tokens are
+    ``q_start[b]`` up to ``q_start[b + 1]``, its last ``seq_lens[b]`` positions' end (None: one
+    token each).  ``scale`` is head_dim ** -0.5 by default."""
+    _i32_arrays(tables=tables, seq_lens=seq_lens, q_start=q_start, prefix_pages=prefix_pages,
+                status=status)
+    n_q, heads, dim = q.shape
+    n = seq_lens.numel()
+    if dim != pool.head_dim or out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("q and out are [n_q, q_heads, head_dim] of one type")
+    if (dim > 1 and n_q * heads > 0) and (q.stride(2) != 1 or out.stride(2) != 1):
+        raise ValueError("a head's elements must be contiguous in q and out")
+    if tables.dim() != 2 or tables.shape[0] < n or (q_start is not None and q_start.numel() < n + 1):
+        raise ValueError("tables needs a row, and q_start an entry and one more, for each request")
+    if lse is not None and (tuple(lse.shape) != (n_q, heads) or lse.element_size() != 4
+                            or not lse.is_floating_point() or not lse.is_contiguous()):
+        raise ValueError("lse is a contiguous float32 [n_q, q_heads]")
+    a = AttnArgs(layer, _q_dtype(q), heads, n_q, n, page_size, tables.shape[1], prefix_len,
+                 tables.stride(0), tables.data_ptr(), _ptr(prefix_pages),
+                 0 if prefix_pages is None else prefix_pages.numel(), 0, seq_lens.data_ptr(),
+                 _ptr(q_start), q.data_ptr(), q.stride(0), q.stride(1), out.data_ptr(),
+                 out.stride(0), out.stride(1), _ptr(lse),
+                 dim ** -0.5 if scale is None else scale, k_scale, v_scale, 0)
+    _check(lib().kvx_shared_attention(_h(pool), a, _ptr(ws),
+                                      _nbytes(ws) if ws_bytes is None else ws_bytes,
+                                      _ptr(status), _stream(stream)), "kvx_shared_attention")
+
+
+def _q_dtype(q) -> int:
+    import torch
+    got = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}.get(q.dtype)
+    if got is None:
+        raise ValueError("q and out are float16, bfloat16 or float32")
+    return got
+
+
+def _i32_arrays(**arrays) -> None:
+    """Index arrays are int32; lists (all but tables, whose rows may be apart) are contiguous."""
+    for name, x in arrays.items():
+        if x is None:
+            continue
+        if x.element_size() != 4 or x.is_floating_point():
+            raise ValueError(f"{name} must be int32")
+        if x.dim() and x.numel() > 1 and x.stride(-1) != 1 or (x.dim() > 1 and name != "tables"):
+            raise ValueError(f"{name} must be contiguous" + (" within a row" if name == "tables"
+                                                             else " and one-dimensional"))
 
 
 # ---- checked calls -------------------------------------------------------------------------

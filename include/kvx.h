@@ -537,6 +537,131 @@ KVX_API kvx_status kvx_stream_reshard(const kvx_layout_t *srcs, int32_t n_srcs,
                                       const kvx_stream_ctl *ctl, void *d_ws, size_t ws_bytes,
                                       int32_t *d_status, uint32_t flags, kvx_stream_t stream);
 
+/* ---- block tables and slot maps -------------------------------------------------------- */
+
+/* Most requests of one kvx_block_tables or kvx_shared_attention call. */
+#define KVX_MAX_TABLE_REQUESTS 65536
+
+/* Arguments of kvx_block_tables (read on the host at the call).  Every array is device memory
+ * of int32, 4-byte aligned, and no output overlaps another array, except that next_cursor may
+ * be cursor.  Page i of a pool is its slots i * page_size .. (i + 1) * page_size - 1. */
+typedef struct kvx_tables_args {
+  int32_t n_reqs;            /* 0 .. KVX_MAX_TABLE_REQUESTS */
+  int32_t page_size;         /* tokens per page (>= 1); the layout's own with KVX_HND_PAGED */
+  const int32_t *old_lens;   /* [n_reqs]: tokens that row b's pages hold already; 0: a new
+                                request.  NULL: every request is new */
+  const int32_t *new_lens;   /* [n_reqs]: tokens that row b has to hold, prefix included;
+                                0 with old 0: a row that only pads the batch */
+  const int32_t *prefix_pages; /* [n_prefix_pages]: full pages that every new request shares */
+  int32_t n_prefix_pages;    /* >= 0 (prefix_pages may be NULL at 0) */
+  int32_t max_pages;         /* entries a row of tables has room for (>= 1) */
+  int32_t *tables;           /* row b at tables + b * table_stride; old pages in, all pages out */
+  int64_t table_stride;      /* elements, >= max_pages */
+  const int32_t *free_pages; /* [n_free]: pages to hand out, in this order */
+  int32_t n_free;            /* >= 0 (free_pages may be NULL at 0) */
+  int32_t reserved;          /* must be 0 */
+  const int32_t *cursor;     /* [1]: entries of free_pages handed out before; NULL: 0 */
+  int32_t *next_cursor;      /* [1]: cursor + the pages that this call handed out */
+  int32_t *q_start;          /* [n_reqs + 1]: first new token of each request; the last: all */
+  int32_t *slots;            /* [max_tokens]: the pool slot of every new token */
+  int32_t *positions;        /* [max_tokens]: its position in its request; or NULL */
+  int64_t max_tokens;        /* 0 .. INT32_MAX: room in slots and positions */
+} kvx_tables_args;
+
+/* Block tables and slot maps of a batch from its lengths: what the slot lists of kvx_scatter /
+ * kvx_transfer and the tables of kvx_shared_attention are made of ([Mooncake] 7.4: the decode
+ * side's block table; [PD-budget] 5090 section: D hands out its own pages for a request).
+ * With page = page_size and, for request b,
+ *   start = old_b, or n_prefix_pages * page for a new request with new_b > 0 (else 0);
+ *   have = ceil(start / page), need = ceil(new_b / page), taken = need - have:
+ *  - a new request's row begins with prefix_pages; entries have .. need - 1 of row b become the
+ *    next `taken` entries of free_pages, requests in order; entries from need on stay;
+ *  - q_start[b] = the sum of new - start over the requests before b;
+ *  - for i < new_b - start: positions[q_start[b] + i] = start + i and slots[q_start[b] + i] =
+ *    row_b[(start + i) / page] * page + (start + i) % page.
+ * One call grows running requests by a token (or several) and lays out whole prompts; calls in
+ * one stream chain through the cursor, also when captured into a CUDA graph.
+ * On the stream: *d_status = KVX_OK; or, with nothing else written, KVX_ERR_INVALID_ARG (a
+ * length below 0, new < start, a cursor below 0) or KVX_ERR_OUT_OF_RANGE (more pages than a row
+ * or the free list holds, more tokens than max_tokens, a page id in use outside the pool); the
+ * larger code if both happened.  Repeats within free_pages are not looked for.
+ * Host errors: KVX_ERR_INVALID_ARG, KVX_ERR_ALIGNMENT, KVX_ERR_NO_WORKSPACE (d_ws 256-byte
+ * aligned, kvx_tables_workspace_size(n_reqs) bytes; no initialisation needed). */
+KVX_API size_t kvx_tables_workspace_size(int32_t n_reqs);
+KVX_API kvx_status kvx_block_tables(kvx_layout_t pool, const kvx_tables_args *args, void *d_ws,
+                                    size_t ws_bytes, int32_t *d_status, kvx_stream_t stream);
+
+/* ---- attention over a paged pool, a shared prefix computed once -------------------------- */
+
+/* Largest head_dim of kvx_shared_attention. */
+#define KVX_ATTN_MAX_HEAD_DIM 256
+
+/* Arguments of kvx_shared_attention (read on the host at the call); pointers are device memory. */
+typedef struct kvx_attn_args {
+  int32_t layer;             /* K is plane 2 * layer, V plane 2 * layer + 1 */
+  int32_t q_dtype;           /* type of q and out: the pool's (KVX_F16, KVX_BF16, KVX_F32); with
+                                a KVX_FP8 pool (E4M3 values) KVX_F16 or KVX_BF16 */
+  int32_t q_heads;           /* a multiple of the layout's kv_heads: query head h reads kv head
+                                h / (q_heads / kv_heads) */
+  int32_t n_q;               /* query tokens of all requests (>= 0) */
+  int32_t n_reqs;            /* 0 .. KVX_MAX_TABLE_REQUESTS */
+  int32_t page_size;         /* tokens per table entry (>= 1); the layout's with KVX_HND_PAGED */
+  int32_t max_pages;         /* entries of a row of tables (>= 1) */
+  int32_t prefix_len;        /* leading positions that all requests share (>= 0) */
+  int64_t table_stride;      /* elements between rows of tables, >= max_pages */
+  const int32_t *tables;     /* row b: request b's pages in order of position.  Entries of
+                                positions below prefix_len, and past the request's end, are not
+                                read */
+  const int32_t *prefix_pages; /* [n_prefix_pages]: the pages of positions 0 .. prefix_len - 1 */
+  int32_t n_prefix_pages;    /* >= ceil(prefix_len / page_size) */
+  int32_t reserved;          /* must be 0 */
+  const int32_t *seq_lens;   /* [n_reqs]: positions of request b in the pool, the prefix and its
+                                query tokens included; 0: a row that only pads the batch */
+  const int32_t *q_start;    /* [n_reqs + 1]: request b's query tokens are q_start[b] ..
+                                q_start[b + 1] - 1, the last positions of the request, in order;
+                                q_start[n_reqs] <= n_q.  NULL: one token each (n_q == n_reqs) */
+  const void *q;             /* [n_q][q_heads][head_dim], elements of a head contiguous */
+  int64_t q_token_stride, q_head_stride; /* elements */
+  void *out;                 /* as q */
+  int64_t out_token_stride, out_head_stride;
+  float *lse;                /* [n_q][q_heads] natural log of each row's sum of exponentials; or
+                                NULL */
+  float scale;               /* of the scores (usually head_dim ^ -0.5) */
+  float k_scale, v_scale;    /* what the pool's K and V elements are multiplied by (1 unless the
+                                pool is quantised) */
+  int32_t reserved2;         /* must be 0 */
+} kvx_attn_args;
+
+/* Causal attention of a batch over one layer of a paged pool, for decode steps, for several
+ * drafted tokens a request, and for prompts.  Query token i of request b (of n) with length len
+ * sees positions 0 .. len - n + i: those below prefix_len through prefix_pages, whose scores
+ * with the queries of all requests are computed together so that the prefix is read once for
+ * the batch, the others through row b.  With s_j = scale * k_scale * <q, K_j>:
+ *   out = v_scale * sum_j exp(s_j) V_j / sum_j exp(s_j),   lse = log sum_j exp(s_j).
+ * Sums are held in 32 bits; with 16-bit types the weights exp(s_j - max) are rounded to the
+ * pool's 16-bit type (BF16 or F16 as q for an FP8 pool) for the product with V.  Results do not
+ * depend on scheduling: the same call gives the same bits.
+ * A row that sees nothing (a length of 0, or fewer positions than query tokens), or whose every
+ * score is -inf, is 0 with lse -inf.  What masked positions and other slots hold, NaN and
+ * infinities included, does not reach a result.  Tokens of no request (at or past
+ * q_start[n_reqs]) get 0 and -inf.
+ * Any head_dim up to KVX_ATTN_MAX_HEAD_DIM, page size, stride and element-aligned address; rows
+ * of 16-bit and FP8 pools with head_dim 64 or 128 and 16-byte aligned heads take the tensor
+ * cores, all others a plain kernel.
+ * d_status: *d_status = KVX_OK, KVX_ERR_INVALID_ARG (a length below 0, q_start not rising from
+ * 0 to at most n_q) or KVX_ERR_OUT_OF_RANGE (a length beyond the table row, a page id outside
+ * the pool), the larger if both: out and lse are then unspecified, and nothing outside the pool
+ * was read.  Host errors: KVX_ERR_INVALID_ARG (also a kv_planes = 1 layout), KVX_ERR_ALIGNMENT
+ * (q or out not element aligned, other arrays not 4-byte aligned), KVX_ERR_OVERLAP (out in the
+ * pool), KVX_ERR_NO_WORKSPACE (d_ws 256-byte aligned, kvx_attention_workspace_size bytes, no
+ * initialisation needed).  Calls that overlap on the GPU need workspaces of their own.
+ * kvx_attention_workspace_size returns 0 if the arguments are out of range; a size covers every
+ * call with at most that many query tokens, requests, heads and prefix tokens on the layout. */
+KVX_API size_t kvx_attention_workspace_size(kvx_layout_t pool, int32_t n_q, int32_t n_reqs,
+                                            int32_t q_heads, int32_t prefix_len);
+KVX_API kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_args *args, void *d_ws,
+                                        size_t ws_bytes, int32_t *d_status, kvx_stream_t stream);
+
 /* ---- misc ---------------------------------------------------------------------------- */
 
 /* Which kernel moves linear chunks (rows contiguous on both sides).  KVX_ENGINE_BULK uses the
