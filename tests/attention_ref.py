@@ -5,8 +5,8 @@ their end, and queries taken as a slice of a wider tensor; :func:`reference` fol
 definition request by request over the tokens themselves (it never looks at the pool), and
 :func:`check` holds a result to bounds derived from the formats.
 
-Bounds.  With u the half spacing of the 16-bit type (2^-9 for bf16, 2^-12 * 2 for f16; 2^-24 for
-32 bits), a row's result differs from the exact one by at most
+Bounds.  With u the half spacing of the type at 1 (torch.finfo(type).eps / 2: 2^-8 for bf16's 8
+significant bits, 2^-11 for f16's 11, 2^-24 for 32-bit floats' 24), a row's result differs from the exact one by at most
   out: u |out| + (u + 2 ds + 2^-18) * sum_j p_j |v_j|   (+ f16: weights below 2^-14 of the greatest
        are spaced 2^-24 apart, so 2^-24 sum_j |v_j| more)
   lse: ds + 2^-18 + 2^-22 |lse|
@@ -22,7 +22,7 @@ import torch
 
 TYPES = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32,
          "fp8": torch.float8_e4m3fn}
-U = {torch.bfloat16: 2.0 ** -9, torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -24}
+U = {t: torch.finfo(t).eps / 2 for t in (torch.bfloat16, torch.float16, torch.float32)}
 
 
 class Case:
