@@ -1,9 +1,8 @@
 // kvx_attn.cu -- kvx_shared_attention: checks, the plan, the join, and the choice of kernels.
 //
-// Lengths and query starts are device data, so the split of the work is made on the device: a
-// one-CTA plan kernel cuts the prefix (rows of all tokens) and every request's own keys into
-// items of about equal key counts, so that their number suits the GPU, and the item kernels walk
-// that list with a grid that does not depend on it.
+// Lengths and query starts are device data, so the work is laid out on the device: a one-CTA
+// plan kernel adds up the key tiles of all units, and the kernels behind it walk that line with a
+// grid that does not depend on it.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -20,18 +19,6 @@ namespace kvx {
 namespace {
 
 constexpr int kPlanCta = 1024;
-
-__device__ __forceinline__ int64_t block_sum(int64_t x, int64_t *sm) {
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
-  __syncthreads();
-  if (lane == 0) sm[w] = x;
-  __syncthreads();
-  int64_t t = 0;
-  for (int i = 0; i < (int)(blockDim.x >> 5); ++i) t += sm[i];
-  return t;
-}
 
 // Exclusive block-wide sum; *total gets the whole.
 __device__ __forceinline__ int64_t block_excl(int64_t x, int64_t *total, int64_t *sm) {
@@ -88,16 +75,11 @@ __global__ void __launch_bounds__(kPlanCta) attn_plan_kernel(const AttnParams p)
   __shared__ int64_t sm[32];
   const int tid = threadIdx.x, n = p.n_reqs;
   int32_t bad = 0;
-  if (tid == 0) *p.status = KVX_OK;
   for (int t = tid; t < p.n_q; t += kPlanCta) p.owner[t] = -1, p.limit[t] = 0;
   __syncthreads();
-  // how many key tiles there are in all, over the row tiles that read them
-  int64_t work = 0;
   int32_t most = 0;
   for (int b = tid; b < n; b += kPlanCta) {
     const Req r = request(p, b, &bad);
-    const int64_t rows = (int64_t)r.n * p.group, tiles = (rows + p.row_tile - 1) / p.row_tile;
-    work += tiles * max(0, r.len - p.prefix_len);
     most = max(most, r.len);
     for (int i = 0; i < r.n; ++i) {
       p.owner[r.t0 + i] = b;
@@ -105,29 +87,18 @@ __global__ void __launch_bounds__(kPlanCta) attn_plan_kernel(const AttnParams p)
     }
   }
   for (int o = 16; o; o >>= 1) most = max(most, __shfl_xor_sync(~0u, most, o));
-  work = block_sum(work, sm);
-  __syncthreads();
   if ((tid & 31) == 0) sm[tid >> 5] = most;
   __syncthreads();
   for (int i = 0; i < 32; ++i) most = max(most, (int32_t)sm[i]);
-  const int32_t prefix = min(p.prefix_len, most);
-  const int64_t prows = (int64_t)p.n_q * p.group;
-  const int64_t ptiles = (prows + p.row_tile - 1) / p.row_tile;
-  work = (work + ptiles * prefix) * p.kv_heads;
-  int64_t chunk = (work + p.target - 1) / p.target;
-  chunk = max(chunk, (int64_t)kAttnMinSplit);
-  chunk = (chunk + kAttnSplitTile - 1) / kAttnSplitTile * kAttnSplitTile;
-  chunk = min(chunk, (int64_t)1 << 30);
-  // segs, their items and partial rows; seg 0 is the prefix
-  int64_t items = 0, parts = 0;
+  int64_t tiles = 0;
   for (int s0 = 0; s0 <= n; s0 += kPlanCta) {
     const int s = s0 + tid;
     AttnSeg g = {};
-    int64_t ni = 0, np = 0;
+    int64_t mine = 0;
     if (s <= n) {
-      if (s == 0) {
-        g.rows = (int32_t)prows;
-        g.key1 = prefix;
+      if (s == 0) {  // no further than some request reaches
+        g.rows = p.n_q * p.group;
+        g.key1 = min(p.prefix_len, most);
       } else {
         const Req r = request(p, s - 1, &bad);
         g.row0 = r.t0 * p.group;
@@ -135,58 +106,21 @@ __global__ void __launch_bounds__(kPlanCta) attn_plan_kernel(const AttnParams p)
         g.key0 = p.prefix_len;
         g.key1 = max(r.len, p.prefix_len);
       }
-      g.chunk = (int32_t)chunk;
-      if (g.rows > 0) g.splits = (int32_t)((g.key1 - g.key0 + chunk - 1) / chunk);
-      ni = (int64_t)((g.rows + p.row_tile - 1) / p.row_tile) * g.splits * p.kv_heads;
-      np = (int64_t)g.rows * g.splits * p.kv_heads;
+      if (g.rows > 0) g.key_tiles = (int32_t)(((int64_t)g.key1 - g.key0 + kAttnKeyTile - 1) / kAttnKeyTile);
+      mine = (int64_t)((g.rows + p.row_tile - 1) / p.row_tile) * g.key_tiles;
     }
-    int64_t ti, tp;
-    const int64_t bi = block_excl(ni, &ti, sm), bp = block_excl(np, &tp, sm);
-    g.part = parts + bp;
-    if (s <= n) {
-      p.segs[s] = g;
-      p.item_base[s] = (int32_t)(items + bi);
-    }
-    items += ti;
-    parts += tp;
-  }
-  // overlapping query ranges could ask for more than the workspace holds
-  if (items > p.max_items || parts > p.max_parts) {
-    bad = max(bad, (int32_t)KVX_ERR_INVALID_ARG);
-    items = 0;
+    int64_t total;
+    g.tile0 = tiles + block_excl(mine, &total, sm);
+    if (s <= n) p.segs[s] = g;
+    tiles += total;
   }
   const int any_range = __syncthreads_or(bad == KVX_ERR_OUT_OF_RANGE);
   const int any_arg = __syncthreads_or(bad == KVX_ERR_INVALID_ARG);
-  const int64_t made = (any_range || any_arg) ? 0 : items;
   if (tid == 0) {
-    p.head->n_items = (int32_t)made;
-    p.head->prefix_splits = p.segs[0].splits;
-    if (any_range) atomicMax(p.status, (int32_t)KVX_ERR_OUT_OF_RANGE);
-    else if (any_arg) atomicMax(p.status, (int32_t)KVX_ERR_INVALID_ARG);
-  }
-  // the item list: kv heads of one split and row tile side by side, so that neighbouring CTAs
-  // read neighbouring heads of the same rows
-  for (int64_t i = tid; i < made; i += kPlanCta) {
-    int lo = 0, hi = n;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (p.item_base[mid] <= i) lo = mid;
-      else hi = mid - 1;
-    }
-    const AttnSeg g = p.segs[lo];
-    int32_t k = (int32_t)(i - p.item_base[lo]);
-    const int32_t h = k % p.kv_heads;
-    k /= p.kv_heads;
-    const int32_t sp = k % g.splits, tile = k / g.splits;
-    AttnItem it;
-    it.row0 = g.row0 + tile * p.row_tile;
-    it.rows = min(p.row_tile, g.rows - tile * p.row_tile);
-    it.key0 = g.key0 + sp * g.chunk;
-    it.key1 = (int32_t)min((int64_t)g.key1, (int64_t)it.key0 + g.chunk);
-    it.table = lo - 1;
-    it.head = h;
-    it.part = g.part + ((int64_t)h * g.splits + sp) * g.rows + tile * p.row_tile;
-    p.items[i] = it;
+    p.head->tiles = tiles;
+    p.head->quota = max((int64_t)1, (tiles + p.groups - 1) / p.groups);
+    p.head->segs = any_range || any_arg ? 0 : n + 1;
+    *p.status = any_range ? KVX_ERR_OUT_OF_RANGE : any_arg ? KVX_ERR_INVALID_ARG : KVX_OK;
   }
 }
 
@@ -207,13 +141,26 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const AttnPa
   const int h = qh / p.group, r = t * p.group + qh - h * p.group;
   const int D = p.head_dim, b = p.owner[t];
   IO *out = reinterpret_cast<IO *>(p.out + t * p.out_tok + qh * p.out_head);
-  const AttnSeg sp = p.segs[0];
-  AttnSeg so = {};
-  if (b >= 0) so = p.segs[1 + b];
-  const int n0 = b >= 0 ? sp.splits : 0, n = p.head->n_items > 0 ? n0 + so.splits : 0;
+  // the pieces of the row: n0 of the prefix, then the request's own
+  int64_t first[2], more[2];
+  int count[2] = {0, 0};
+  for (int k = 0; k < 2; ++k) {
+    if (b < 0 || p.head->segs == 0) break;
+    const AttnSeg s = p.segs[k == 0 ? 0 : 1 + b];
+    if (s.key_tiles == 0) continue;
+    const int unit = (r - s.row0) / p.row_tile, row0 = s.row0 + unit * p.row_tile;
+    const int64_t w = s.tile0 + (int64_t)unit * s.key_tiles, quota = p.head->quota;
+    const int g0 = (int)(w / quota), g1 = (int)((w + s.key_tiles - 1) / quota);
+    count[k] = g1 - g0 + 1;
+    first[k] = attn_part(p, k == 0, true, 0, h, row0) + (r - row0);
+    more[k] = attn_part(p, k == 0, false, g0, h, row0) + (r - row0);
+  }
+  const int n0 = count[0], n = n0 + count[1];
+  const int64_t step = (int64_t)p.kv_heads * p.row_tile;
   auto part = [&](int i) {
-    return i < n0 ? sp.part + ((int64_t)h * sp.splits + i) * sp.rows + (r - sp.row0)
-                  : so.part + ((int64_t)h * so.splits + (i - n0)) * so.rows + (r - so.row0);
+    const int k = i < n0 ? 0 : 1;
+    i -= k ? n0 : 0;
+    return i == 0 ? first[k] : more[k] + i * step;
   };
   float top = -INFINITY;
   for (int i = lane; i < n; i += 32) top = fmaxf(top, p.part_m[part(i)]);
@@ -248,34 +195,22 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const AttnPa
 }
 
 struct Sizes {
-  int64_t segs_off, base_off, limit_off, owner_off, items_off, m_off, l_off, o_off, total;
-  int64_t max_items, max_parts;
-  int32_t target;
+  int64_t segs_off, limit_off, owner_off, m_off, l_off, o_off, total;
+  int32_t groups;
 };
 
-constexpr int kTargetItems = 152 * 8;
-
-// Bounds on what the plan makes: with c keys a split, sum over segs of tiles * ceil(keys / c) *
-// kv_heads <= target + tiles in all * kv_heads, and a tile has at most row_tile rows.
-Sizes sizes(int64_t n_q, int64_t n_reqs, int64_t q_heads, int64_t kv_heads, int64_t prefix,
-            int64_t D, int row_tile) {
+// How many groups of kv_heads CTAs: as many as are resident at once.
+Sizes sizes(int64_t n_q, int64_t n_reqs, int64_t q_heads, int64_t kv_heads, int64_t D, int row_tile) {
   Sizes z = {};
-  const int64_t group = q_heads / kv_heads;
-  const int64_t tiles = (n_q * group + row_tile - 1) / row_tile + n_reqs +
-                        (prefix > 0 ? (n_q * group + row_tile - 1) / row_tile : 0);
-  z.target = kTargetItems;
-  z.max_items = z.target + tiles * kv_heads;
-  z.max_parts = std::min(z.max_items * row_tile,
-                         z.target * (int64_t)row_tile + 2 * n_q * q_heads);
+  z.groups = (int32_t)std::max((int64_t)1, 152 * 2 / kv_heads);
+  const int64_t parts = 2 * n_q * q_heads + z.groups * kv_heads * row_tile;
   z.segs_off = sizeof(AttnHeader);
-  z.base_off = align_up(z.segs_off + (int64_t)sizeof(AttnSeg) * (n_reqs + 1), 256);
-  z.limit_off = align_up(z.base_off + 4 * (n_reqs + 2), 256);
+  z.limit_off = align_up(z.segs_off + (int64_t)sizeof(AttnSeg) * (n_reqs + 1), 256);
   z.owner_off = align_up(z.limit_off + 4 * n_q, 256);
-  z.items_off = align_up(z.owner_off + 4 * n_q, 256);
-  z.m_off = align_up(z.items_off + (int64_t)sizeof(AttnItem) * z.max_items, 256);
-  z.l_off = align_up(z.m_off + 4 * z.max_parts, 256);
-  z.o_off = align_up(z.l_off + 4 * z.max_parts, 256);
-  z.total = align_up(z.o_off + 4 * z.max_parts * D, 256);
+  z.m_off = align_up(z.owner_off + 4 * n_q, 256);
+  z.l_off = align_up(z.m_off + 4 * parts, 256);
+  z.o_off = align_up(z.l_off + 4 * parts, 256);
+  z.total = align_up(z.o_off + 4 * parts * D, 256);
   return z;
 }
 
@@ -284,6 +219,13 @@ bool shape_ok(const kvx_layout *l, int64_t n_q, int64_t n_reqs, int64_t q_heads,
          n_reqs >= 0 && n_reqs <= KVX_MAX_TABLE_REQUESTS && q_heads >= 1 &&
          q_heads % l->kv_heads == 0 && prefix >= 0 && n_q * q_heads <= (int64_t)1 << 30;
 }
+
+// Whether the tensor-core kernels take a layout.
+bool tensor_cores(const kvx_layout *l) {
+  return l->elem <= 2 && (l->head_dim == 64 || l->head_dim == 128) && l->vec == 16;
+}
+
+int row_tile(const kvx_layout *l) { return tensor_cores(l) ? kAttnNarrowRows : kAttnGeneralRows; }
 
 bool mult(const void *p, uintptr_t a) { return (uintptr_t)p % a == 0; }
 
@@ -295,8 +237,8 @@ static_assert(sizeof(kvx_attn_args) == 152, "the binding mirrors this structure"
 extern "C" size_t kvx_attention_workspace_size(kvx_layout_t pool, int32_t n_q, int32_t n_reqs,
                                                int32_t q_heads, int32_t prefix_len) {
   if (!kvx::shape_ok(pool, n_q, n_reqs, q_heads, prefix_len)) return 0;
-  return (size_t)kvx::sizes(n_q, n_reqs, q_heads, pool->kv_heads, prefix_len, pool->head_dim,
-                            kvx::kAttnGeneralRows).total;
+  return (size_t)kvx::sizes(n_q, n_reqs, q_heads, pool->kv_heads, pool->head_dim,
+                            kvx::row_tile(pool)).total;
 }
 
 extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_args *args,
@@ -337,8 +279,7 @@ extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_arg
     for (int i = 2 * a.layer; i < 2 * a.layer + 2; ++i)
       if (b0 < pool->plane[i] + pool->extent && pool->plane[i] < b1) return KVX_ERR_OVERLAP;
   }
-  const Sizes z = sizes(a.n_q, a.n_reqs, a.q_heads, pool->kv_heads, a.prefix_len, pool->head_dim,
-                        kAttnGeneralRows);
+  const Sizes z = sizes(a.n_q, a.n_reqs, a.q_heads, pool->kv_heads, pool->head_dim, row_tile(pool));
   if (!d_ws || !mult(d_ws, 256) || (int64_t)ws_bytes < z.total) return KVX_ERR_NO_WORKSPACE;
 
   AttnParams p;
@@ -378,17 +319,14 @@ extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_arg
   p.page_size = a.page_size;
   p.max_pages = a.max_pages;
   p.prefix_len = a.prefix_len;
-  p.row_tile = kAttnGeneralRows;
-  p.target = z.target;
-  p.max_items = (int32_t)z.max_items;
-  p.max_parts = z.max_parts;
+  p.row_tile = row_tile(pool);
+  p.q_even = ((uintptr_t)a.q | (uintptr_t)p.q_tok | (uintptr_t)p.q_head) % 4 == 0;
+  p.groups = z.groups;
   char *ws = static_cast<char *>(d_ws);
   p.head = reinterpret_cast<AttnHeader *>(ws);
   p.segs = reinterpret_cast<AttnSeg *>(ws + z.segs_off);
-  p.item_base = reinterpret_cast<int32_t *>(ws + z.base_off);
   p.limit = reinterpret_cast<int32_t *>(ws + z.limit_off);
   p.owner = reinterpret_cast<int32_t *>(ws + z.owner_off);
-  p.items = reinterpret_cast<AttnItem *>(ws + z.items_off);
   p.part_m = reinterpret_cast<float *>(ws + z.m_off);
   p.part_l = reinterpret_cast<float *>(ws + z.l_off);
   p.part_o = reinterpret_cast<float *>(ws + z.o_off);
@@ -398,7 +336,8 @@ extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_arg
   void *kargs[] = {&p};
   cudaError_t e = cudaLaunchKernel((const void *)attn_plan_kernel, dim3(1), dim3(kPlanCta), kargs, 0, s);
   if (e == cudaSuccess && a.n_q > 0) {
-    e = launch_attn_general(p, pool->dtype, a.q_dtype, 152 * 2, s);
+    e = tensor_cores(pool) ? launch_attn_narrow(p, pool->dtype, a.q_dtype, s)
+                           : launch_attn_general(p, pool->dtype, a.q_dtype, s);
     if (e == cudaSuccess) {
       const void *join = a.q_dtype == KVX_F32   ? (const void *)attn_join_kernel<float>
                          : a.q_dtype == KVX_F16 ? (const void *)attn_join_kernel<__half>

@@ -2,11 +2,18 @@
 //
 // Rows and parts.  A row is (query token t, query head); the G = q_heads / kv_heads rows of a
 // token that read one kv head lie together: row r of kv head h is token r / G, query head
-// h * G + r % G.  The keys of a row are cut into the common prefix and the request's own
-// positions, and each of the two into splits; a split of a run of rows is an item, which one CTA
-// works through with a running maximum and sum.  It leaves, per row, the unnormalised sum
-// o = sum_j e^(s_j - m) v_j in 32 bits, m and l = sum_j e^(s_j - m), and the join kernel adds the
-// parts of a row in a fixed order:
+// h * G + r % G.  A seg is a set of rows with the keys they all read: the prefix (rows of all
+// tokens) or one request's own positions (its rows).  A unit is row_tile rows of a seg, and its
+// keys are cut into tiles of kAttnKeyTile.  All units' key tiles in a line are dealt out evenly:
+// group g of kv_heads CTAs, one CTA a head, takes tiles [g * quota, (g + 1) * quota) of the line.
+// So every CTA has the same number of tiles whatever the lengths, and the CTAs of a group read
+// the heads of the same rows at the same time.
+//
+// A piece is what a CTA has of one unit.  It is worked through with a running maximum and sum and
+// leaves, per row, the unnormalised sum o = sum_j e^(s_j - m) v_j in 32 bits, m and
+// l = sum_j e^(s_j - m).  The piece that begins a unit leaves them at the rows' own place, one that
+// goes on with a unit (there is at most one in a group) at the group's place.  The join adds the
+// pieces of a row in the order of the line, so results do not depend on scheduling:
 //   M = max m_i,  out = sum_i e^(m_i - M) o_i / sum_i e^(m_i - M) l_i.
 // Scores are kept in units of log 2 (scale * k_scale * log2 e is folded into one factor), so the
 // exponential is exp2.
@@ -19,8 +26,7 @@
 
 namespace kvx {
 
-constexpr int kAttnSplitTile = 64;   // splits are cut at multiples of this many keys
-constexpr int kAttnMinSplit = 128;   // and are not made shorter than this
+constexpr int kAttnKeyTile = 64;
 
 // Where a layer's rows are: element row (page id, offset in page, kv head) starts at
 // plane + id * page_stride + offset * tok_stride + head * head_stride (bytes), in either kind of
@@ -33,30 +39,19 @@ struct AttnPool {
   int32_t page_shift;    // log2(page_size), or -1
 };
 
-// One seg: the prefix (rows of all tokens) or a request (its own rows, its own positions).
 struct AttnSeg {
-  int64_t part;    // first partial row; kv head h, split s, local row i is partial row
-                   // part + ((int64_t)h * splits + s) * rows + i
-  int32_t row0;    // first row
-  int32_t rows;
+  int64_t tile0;       // its first key tile in the line
+  int32_t row0, rows;
   int32_t key0, key1;
-  int32_t splits;  // 0: no keys
-  int32_t chunk;   // keys per split
-};
-
-struct AttnItem {
-  int64_t part;    // partial row of the item's first row
-  int32_t row0;    // first row, and how many (at most the kernel's tile)
-  int32_t rows;
-  int32_t key0, key1;
-  int32_t table;   // request whose row names the pages; -1: the prefix list
-  int32_t head;    // kv head
+  int32_t key_tiles;   // of each unit; 0: no keys (or no rows)
+  int32_t pad;
 };
 
 struct AttnHeader {
-  int32_t n_items;
-  int32_t prefix_splits;
-  int32_t pad[14];
+  int64_t tiles;       // in the line
+  int64_t quota;       // of a group
+  int32_t segs;        // 1 + n_reqs; 0: the arguments were refused
+  int32_t pad[11];
 };
 
 struct AttnParams {
@@ -73,18 +68,17 @@ struct AttnParams {
   float v_scale;
   int32_t n_q, n_reqs, q_heads, kv_heads, group, head_dim;
   int32_t page_size, max_pages, prefix_len;
-  int32_t row_tile;   // most rows of an item
-  int32_t target;     // items wanted
-  int32_t max_items;
+  int32_t row_tile;   // rows of a unit
+  int32_t groups;     // groups of kv_heads CTAs
+  int32_t q_even;     // q's heads start on 4-byte boundaries
   // workspace
   AttnHeader *head;
   AttnSeg *segs;      // [1 + n_reqs]: the prefix, then the requests
-  int32_t *item_base; // [2 + n_reqs]
   int32_t *limit;     // [n_q]: positions that a token sees
   int32_t *owner;     // [n_q]: its request, -1: none
-  AttnItem *items;
+  // part rows: [kv_heads][n_q * G] of the requests' first pieces, the same of the prefix's, and
+  // [groups][kv_heads][row_tile] of pieces that go on
   float *part_m, *part_l, *part_o;
-  int64_t max_parts;
   int32_t *status;
 };
 
@@ -112,6 +106,62 @@ __device__ __forceinline__ int64_t attn_key_offset(const AttnParams &p, int32_t 
   return attn_page(p, table, pg) * p.pool.page_stride + off * p.pool.tok_stride;
 }
 
+// First part row of a piece of a unit that starts at row0 (see AttnParams).
+__device__ __forceinline__ int64_t attn_part(const AttnParams &p, bool prefix, bool first, int g,
+                                             int h, int32_t row0) {
+  const int64_t all = (int64_t)p.n_q * p.group;
+  if (first) return ((prefix ? p.kv_heads : 0) + h) * all + row0;
+  return 2 * p.kv_heads * all + ((int64_t)g * p.kv_heads + h) * p.row_tile;
+}
+
+// The seg with tile w in it, among the n segs.
+__device__ __forceinline__ int attn_find_seg(const AttnSeg *segs, int n, int64_t w) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (segs[mid].tile0 <= w) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;  // the last one that starts at or before w: the empty ones before it share its start
+}
+
+// A piece: keys [key0, key1) for rows [row0, row0 + rows).
+struct AttnPiece {
+  int64_t part;
+  int32_t row0, rows, key0, key1, table;
+};
+
+// Calls f(piece) for every piece of group g, kv head h.
+template <typename F>
+__device__ __forceinline__ void attn_pieces(const AttnParams &p, int g, int h, F f) {
+  const int n = p.head->segs;
+  const int64_t quota = p.head->quota;
+  int64_t w = g * quota;
+  const int64_t end = min(p.head->tiles, w + quota);
+  if (n == 0 || w >= end) return;
+  int s = attn_find_seg(p.segs, n, w);
+  while (w < end) {
+    const AttnSeg seg = p.segs[s];
+    const int units = (seg.rows + p.row_tile - 1) / p.row_tile;
+    const int64_t tiles = (int64_t)units * seg.key_tiles;
+    while (w < end && w < seg.tile0 + tiles) {
+      const int64_t at = w - seg.tile0;
+      const int unit = (int)(at / seg.key_tiles), kt = (int)(at - (int64_t)unit * seg.key_tiles);
+      const int take = (int)min((int64_t)(seg.key_tiles - kt), end - w);
+      AttnPiece x;
+      x.row0 = seg.row0 + unit * p.row_tile;
+      x.rows = min(p.row_tile, seg.rows - unit * p.row_tile);
+      x.key0 = seg.key0 + kt * kAttnKeyTile;
+      x.key1 = (int32_t)min((int64_t)seg.key1, (int64_t)x.key0 + (int64_t)take * kAttnKeyTile);
+      x.table = s - 1;
+      x.part = attn_part(p, s == 0, kt == 0, g, h, x.row0);
+      f(x);
+      w += take;
+    }
+    ++s;
+  }
+}
+
 __device__ __forceinline__ void attn_wait_prior() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
@@ -119,8 +169,10 @@ __device__ __forceinline__ void attn_release_next() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-cudaError_t launch_attn_general(const AttnParams &p, int32_t dtype, int32_t io, int grid,
-                                cudaStream_t s);
+cudaError_t launch_attn_general(const AttnParams &p, int32_t dtype, int32_t io, cudaStream_t s);
 constexpr int kAttnGeneralRows = 16;
+// head_dim 64 or 128, 16-bit or 8-bit pool with 16-byte aligned heads.
+cudaError_t launch_attn_narrow(const AttnParams &p, int32_t dtype, int32_t io, cudaStream_t s);
+constexpr int kAttnNarrowRows = 64;
 
 }  // namespace kvx

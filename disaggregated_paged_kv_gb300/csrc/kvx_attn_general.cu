@@ -1,7 +1,7 @@
 // kvx_attn_general.cu -- the plain kernel of kvx_shared_attention: any type, head_dim and
 // alignment.
 //
-// A CTA of 128 threads works one item of up to 16 rows: the queries and 32 keys at a time sit in
+// A CTA of 128 threads works one piece of up to 16 rows: the queries and 32 keys at a time sit in
 // shared memory as 32-bit values; each warp scores four rows, a lane a key, and takes the
 // running maximum and sum of its rows with shuffles; then every thread adds the tile's weighted
 // values into its one or two columns of all 16 rows, held in registers.
@@ -36,9 +36,8 @@ __global__ void __launch_bounds__(kThreads) attn_general_kernel(const AttnParams
   __shared__ int64_t soff[kKeys];
   __shared__ int32_t slim[kRows];
   attn_wait_prior();
-  const int n_items = p.head->n_items;
-  for (int it = blockIdx.x; it < n_items; it += gridDim.x) {
-    const AttnItem item = p.items[it];
+  const int g = blockIdx.x / p.kv_heads, head = blockIdx.x - g * p.kv_heads;
+  attn_pieces(p, g, head, [&](const AttnPiece &item) {
     __syncthreads();
     for (int i = tid; i < kRows * D; i += kThreads) {
       const int r = i / D, d = i - r * D;
@@ -46,7 +45,7 @@ __global__ void __launch_bounds__(kThreads) attn_general_kernel(const AttnParams
       if (r < item.rows) {
         const int row = item.row0 + r, t = row / p.group;
         const IO *q = reinterpret_cast<const IO *>(p.q + t * p.q_tok +
-                                                   (item.head * p.group + row - t * p.group) * p.q_head);
+                                                   (head * p.group + row - t * p.group) * p.q_head);
         x = to_f(q[d]) * p.scale_log2;
       }
       sq[i] = x;
@@ -66,7 +65,7 @@ __global__ void __launch_bounds__(kThreads) attn_general_kernel(const AttnParams
     for (int k0 = item.key0; k0 < end; k0 += kKeys) {
       const int nk = min(kKeys, end - k0);
       __syncthreads();  // the tile before has been read
-      if (tid < nk) soff[tid] = attn_key_offset(p, item.table, k0 + tid) + item.head * p.pool.head_stride;
+      if (tid < nk) soff[tid] = attn_key_offset(p, item.table, k0 + tid) + head * p.pool.head_stride;
       __syncthreads();
       for (int i = tid; i < kKeys * D; i += kThreads) {
         const int j = i / D, d = i - j * D;
@@ -137,11 +136,11 @@ __global__ void __launch_bounds__(kThreads) attn_general_kernel(const AttnParams
         const int r = warp * (kRows / 4) + i;
         if (r < item.rows) p.part_m[item.part + r] = m[i], p.part_l[item.part + r] = l[i];
       }
-  }
+  });
 }
 
 template <typename KV, typename IO>
-cudaError_t launch(const AttnParams &p, int grid, cudaStream_t s) {
+cudaError_t launch(const AttnParams &p, cudaStream_t s) {
   const size_t smem = sizeof(float) * ((size_t)p.head_dim * (kRows + 2 * kKeys) + kKeys +
                                        kRows * kKeys + kRows);
   const void *fn = p.head_dim <= kThreads ? (const void *)attn_general_kernel<KV, IO, 1>
@@ -149,18 +148,17 @@ cudaError_t launch(const AttnParams &p, int grid, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 100 * 1024);
   if (e != cudaSuccess) return e;
   void *args[] = {const_cast<AttnParams *>(&p)};
-  return launch_pdl(fn, dim3(grid), dim3(kThreads), args, s, smem);
+  return launch_pdl(fn, dim3(p.groups * p.kv_heads), dim3(kThreads), args, s, smem);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_general(const AttnParams &p, int32_t dtype, int32_t io, int grid,
-                                cudaStream_t s) {
-  if (dtype == KVX_F32) return launch<float, float>(p, grid, s);
-  if (dtype == KVX_F16) return launch<__half, __half>(p, grid, s);
-  if (dtype == KVX_BF16) return launch<__nv_bfloat16, __nv_bfloat16>(p, grid, s);
-  if (io == KVX_F16) return launch<__nv_fp8_e4m3, __half>(p, grid, s);
-  return launch<__nv_fp8_e4m3, __nv_bfloat16>(p, grid, s);
+cudaError_t launch_attn_general(const AttnParams &p, int32_t dtype, int32_t io, cudaStream_t s) {
+  if (dtype == KVX_F32) return launch<float, float>(p, s);
+  if (dtype == KVX_F16) return launch<__half, __half>(p, s);
+  if (dtype == KVX_BF16) return launch<__nv_bfloat16, __nv_bfloat16>(p, s);
+  if (io == KVX_F16) return launch<__nv_fp8_e4m3, __half>(p, s);
+  return launch<__nv_fp8_e4m3, __nv_bfloat16>(p, s);
 }
 
 }  // namespace kvx
