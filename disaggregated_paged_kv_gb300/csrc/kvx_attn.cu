@@ -73,6 +73,7 @@ __device__ __forceinline__ Req request(const AttnParams &p, int b, int32_t *bad)
 
 __global__ void __launch_bounds__(kPlanCta) attn_plan_kernel(const AttnParams p) {
   __shared__ int64_t sm[32];
+  attn_wait_prior();
   const int tid = threadIdx.x, n = p.n_reqs;
   int32_t bad = 0;
   for (int t = tid; t < p.n_q; t += kPlanCta) p.owner[t] = -1, p.limit[t] = 0;
@@ -334,7 +335,7 @@ extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_arg
 
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   void *kargs[] = {&p};
-  cudaError_t e = cudaLaunchKernel((const void *)attn_plan_kernel, dim3(1), dim3(kPlanCta), kargs, 0, s);
+  cudaError_t e = launch_pdl((const void *)attn_plan_kernel, dim3(1), dim3(kPlanCta), kargs, s);
   if (e == cudaSuccess && a.n_q > 0) {
     e = tensor_cores(pool) ? launch_attn_narrow(p, pool->dtype, a.q_dtype, s)
                            : launch_attn_general(p, pool->dtype, a.q_dtype, s);

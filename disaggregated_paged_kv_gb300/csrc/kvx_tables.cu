@@ -7,6 +7,8 @@
 //                 the sums in the workspace, every one its verdict.
 //   tables_fill   a grid over the new tokens, in chunks of 4096: slots, positions and the table
 //                 entry of every page that begins among them, then the shared prefix entries.
+// Up to kTabThreads requests with room for no more than kOneTokens tokens (decode steps, drafts,
+// short prompts) are one CTA's work in one launch, tables_one.
 // Bound: the writes (8 bytes a token, 4 a page) for prompts, two launches' latency for a decode
 // step.
 #include <cstring>
@@ -21,7 +23,9 @@ namespace {
 constexpr int kTabThreads = 1024;
 constexpr int kTabMaxCtas = 32;
 constexpr int kFillThreads = 256;
-constexpr int kFillChunk = 4096;  // tokens a CTA writes at a time: 4 x 4 consecutive a thread
+constexpr int kFillChunk = 16 * kFillThreads;  // tokens a CTA writes at a time
+
+constexpr int kOneTokens = 8192;
 
 struct TabParams {
   kvx_tables_args a;
@@ -108,8 +112,37 @@ __device__ __forceinline__ bool page_ok(const TabParams &p, int32_t id) {
   return id >= 0 && id < p.num_pages;
 }
 
+// span_of, with the row's room checked and (page: read the table) the page that is filled further.
+__device__ __forceinline__ Span checked_span(const TabParams &p, int b, bool page, int32_t *bad) {
+  const Span s = span_of(p, b, bad);
+  if (max(s.need, s.have) > p.a.max_pages) {
+    *bad = max(*bad, (int32_t)KVX_ERR_OUT_OF_RANGE);
+  } else if (page && s.end > s.start && p.a.old_lens && p.a.old_lens[b] > 0 &&
+             s.start < s.have * p.a.page_size &&
+             !page_ok(p, p.a.tables[b * p.a.table_stride + s.have - 1])) {
+    *bad = max(*bad, (int32_t)KVX_ERR_OUT_OF_RANGE);
+  }
+  return s;
+}
+
+// Cursor, totals, and every page id that the call is going to use, by thread at of step.
+__device__ __forceinline__ void check_ids(const TabParams &p, int64_t cur, int64_t tokens,
+                                          int64_t pages, int64_t at, int64_t step, int32_t *bad) {
+  if (cur < 0) {
+    *bad = max(*bad, (int32_t)KVX_ERR_INVALID_ARG);
+  } else if (cur + pages > p.a.n_free || tokens > p.a.max_tokens) {
+    *bad = max(*bad, (int32_t)KVX_ERR_OUT_OF_RANGE);
+  } else {
+    for (int64_t i = at; i < pages; i += step)
+      if (!page_ok(p, p.a.free_pages[cur + i])) *bad = max(*bad, (int32_t)KVX_ERR_OUT_OF_RANGE);
+    for (int64_t i = at; i < p.a.n_prefix_pages; i += step)
+      if (!page_ok(p, p.a.prefix_pages[i])) *bad = max(*bad, (int32_t)KVX_ERR_OUT_OF_RANGE);
+  }
+}
+
 __global__ void __launch_bounds__(kTabThreads) tables_plan_kernel(const TabParams p) {
   __shared__ int64_t sm[32][2];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int n = p.a.n_reqs, tid = threadIdx.x;
   int32_t bad = 0;
   int64_t tokens = 0, pages = 0;
@@ -117,14 +150,9 @@ __global__ void __launch_bounds__(kTabThreads) tables_plan_kernel(const TabParam
     const int b = b0 + tid;
     int64_t cnt = 0, take = 0;
     if (b < n) {
-      const Span s = span_of(p, b, &bad);
+      const Span s = checked_span(p, b, blockIdx.x == 0, &bad);
       cnt = s.end - s.start;
       take = s.need - s.have;
-      if (max(s.need, s.have) > p.a.max_pages) bad = max(bad, (int32_t)KVX_ERR_OUT_OF_RANGE);
-      else if (blockIdx.x == 0 && cnt > 0 && s.start > 0 && p.a.old_lens && p.a.old_lens[b] > 0 &&
-               s.start < s.have * p.a.page_size &&
-               !page_ok(p, p.a.tables[b * p.a.table_stride + s.have - 1]))
-        bad = max(bad, (int32_t)KVX_ERR_OUT_OF_RANGE);  // the page that is filled further
     }
     int64_t tc, tp;
     block_scan2(cnt, take, &tc, &tp, sm);
@@ -137,16 +165,8 @@ __global__ void __launch_bounds__(kTabThreads) tables_plan_kernel(const TabParam
     pages += tp;
   }
   const int64_t cur = p.a.cursor ? p.a.cursor[0] : 0;
-  if (cur < 0) bad = max(bad, (int32_t)KVX_ERR_INVALID_ARG);
-  else if (cur + pages > p.a.n_free || tokens > p.a.max_tokens)
-    bad = max(bad, (int32_t)KVX_ERR_OUT_OF_RANGE);
-  else {
-    const int64_t step = (int64_t)p.ctas * kTabThreads, at = (int64_t)blockIdx.x * kTabThreads + tid;
-    for (int64_t i = at; i < pages; i += step)
-      if (!page_ok(p, p.a.free_pages[cur + i])) bad = max(bad, (int32_t)KVX_ERR_OUT_OF_RANGE);
-    for (int64_t i = at; i < p.a.n_prefix_pages; i += step)
-      if (!page_ok(p, p.a.prefix_pages[i])) bad = max(bad, (int32_t)KVX_ERR_OUT_OF_RANGE);
-  }
+  check_ids(p, cur, tokens, pages, (int64_t)blockIdx.x * kTabThreads + tid,
+            (int64_t)p.ctas * kTabThreads, &bad);
   const int any_range = __syncthreads_or(bad == KVX_ERR_OUT_OF_RANGE);
   const int any_arg = __syncthreads_or(bad == KVX_ERR_INVALID_ARG);
   if (tid == 0) {
@@ -170,34 +190,26 @@ __device__ __forceinline__ int find_request(const int32_t *base, int lo, int hi,
   return lo;
 }
 
-__global__ void __launch_bounds__(kFillThreads) tables_fill_kernel(const TabParams p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+// Slots, positions and new table entries of all tokens, and the shared prefix entries, by CTA cta
+// of ctas with Threads threads.  cur: the cursor before the call.
+template <int Threads>
+__device__ __forceinline__ void fill(const TabParams &p, const int32_t *tok_base,
+                                     const int32_t *page_base, int32_t tokens, int64_t cur, int cta,
+                                     int ctas) {
+  constexpr int kChunk = 16 * Threads;  // tokens at a time: 4 x 4 consecutive a thread
   const int n = p.a.n_reqs, tid = threadIdx.x;
-  int32_t bad = tid < p.ctas ? p.verdict[tid] : 0;
-  const int any_range = __syncthreads_or(bad == KVX_ERR_OUT_OF_RANGE);
-  const int any_arg = __syncthreads_or(bad == KVX_ERR_INVALID_ARG);
-  if (blockIdx.x == 0 && tid == 0)
-    *p.status = any_range ? KVX_ERR_OUT_OF_RANGE : any_arg ? KVX_ERR_INVALID_ARG : KVX_OK;
-  if (any_range || any_arg) return;
-  const int32_t tokens = (int32_t)p.totals[0];
-  // the cursor as it was: next_cursor may be the same word, so it is not read again here
-  const int64_t cur = p.totals[1] - (p.page_base[n]);
-  const int64_t gtid = (int64_t)blockIdx.x * kFillThreads + tid, gstep = (int64_t)gridDim.x * kFillThreads;
-  for (int64_t b = gtid; b <= n; b += gstep) p.a.q_start[b] = p.tok_base[b];
-  if (gtid == 0) *p.a.next_cursor = (int32_t)p.totals[1];
-
   int32_t none = 0;
-  for (int64_t c0 = (int64_t)blockIdx.x * kFillChunk; c0 < tokens; c0 += (int64_t)gridDim.x * kFillChunk) {
-    const int32_t last = (int32_t)min(c0 + kFillChunk, (int64_t)tokens) - 1;
-    const int lo = find_request(p.tok_base, 0, n - 1, (int32_t)c0);
-    const int hi = find_request(p.tok_base, lo, n - 1, last);
+  for (int64_t c0 = (int64_t)cta * kChunk; c0 < tokens; c0 += (int64_t)ctas * kChunk) {
+    const int32_t last = (int32_t)min(c0 + kChunk, (int64_t)tokens) - 1;
+    const int lo = find_request(tok_base, 0, n - 1, (int32_t)c0);
+    const int hi = find_request(tok_base, lo, n - 1, last);
 #pragma unroll
-    for (int g = 0; g < kFillChunk / (4 * kFillThreads); ++g) {
-      const int32_t i0 = (int32_t)c0 + (g * kFillThreads + tid) * 4;
+    for (int g = 0; g < kChunk / (4 * Threads); ++g) {
+      const int32_t i0 = (int32_t)c0 + (g * Threads + tid) * 4;
       if (i0 > last) break;
-      int b = find_request(p.tok_base, lo, hi, i0);
+      int b = find_request(tok_base, lo, hi, i0);
       Span s = span_of(p, b, &none);
-      int32_t q0 = p.tok_base[b], q1 = p.tok_base[b + 1];
+      int32_t q0 = tok_base[b], q1 = tok_base[b + 1];
       int64_t page = -1;
       int32_t id = 0, slot[4], at[4];
 #pragma unroll
@@ -206,7 +218,7 @@ __global__ void __launch_bounds__(kFillThreads) tables_fill_kernel(const TabPara
         if (i > last) break;
         while (i >= q1) {  // the next request that has new tokens
           ++b;
-          q0 = q1, q1 = p.tok_base[b + 1];
+          q0 = q1, q1 = tok_base[b + 1];
           if (i < q1) s = span_of(p, b, &none);
           page = -1;
         }
@@ -216,7 +228,7 @@ __global__ void __launch_bounds__(kFillThreads) tables_fill_kernel(const TabPara
         if (pg != page) {
           page = pg;
           id = pg < s.have ? p.a.tables[b * p.a.table_stride + pg]
-                           : p.a.free_pages[cur + p.page_base[b] + (pg - s.have)];
+                           : p.a.free_pages[cur + page_base[b] + (pg - s.have)];
         }
         if (off == 0) p.a.tables[b * p.a.table_stride + pg] = id;
         slot[k] = (int32_t)((int64_t)id * p.a.page_size + off);
@@ -241,11 +253,56 @@ __global__ void __launch_bounds__(kFillThreads) tables_fill_kernel(const TabPara
   }
   // the shared prefix at the head of every new request's row, a CTA per row
   if (p.a.n_prefix_pages > 0)
-    for (int b = blockIdx.x; b < n; b += gridDim.x) {
+    for (int b = cta; b < n; b += ctas) {
       if ((p.a.old_lens && p.a.old_lens[b] != 0) || p.a.new_lens[b] == 0) continue;
-      for (int j = tid; j < p.a.n_prefix_pages; j += kFillThreads)
+      for (int j = tid; j < p.a.n_prefix_pages; j += Threads)
         p.a.tables[b * p.a.table_stride + j] = p.a.prefix_pages[j];
     }
+}
+
+__global__ void __launch_bounds__(kFillThreads) tables_fill_kernel(const TabParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int n = p.a.n_reqs, tid = threadIdx.x;
+  const int32_t bad = tid < p.ctas ? p.verdict[tid] : 0;
+  const int any_range = __syncthreads_or(bad == KVX_ERR_OUT_OF_RANGE);
+  const int any_arg = __syncthreads_or(bad == KVX_ERR_INVALID_ARG);
+  if (blockIdx.x == 0 && tid == 0)
+    *p.status = any_range ? KVX_ERR_OUT_OF_RANGE : any_arg ? KVX_ERR_INVALID_ARG : KVX_OK;
+  if (any_range || any_arg) return;
+  const int64_t next = p.totals[1];
+  const int64_t gtid = (int64_t)blockIdx.x * kFillThreads + tid, gstep = (int64_t)gridDim.x * kFillThreads;
+  for (int64_t b = gtid; b <= n; b += gstep) p.a.q_start[b] = p.tok_base[b];
+  if (gtid == 0) *p.a.next_cursor = (int32_t)next;
+  // the cursor as it was: next_cursor may be the same word, so it is not read again here
+  fill<kFillThreads>(p, p.tok_base, p.page_base, (int32_t)p.totals[0], next - p.page_base[n],
+                     blockIdx.x, gridDim.x);
+}
+
+// The whole call in one CTA, a request a thread, the sums in shared memory.
+__global__ void __launch_bounds__(kTabThreads) tables_one_kernel(const TabParams p) {
+  __shared__ int64_t sm[32][2];
+  __shared__ int32_t tok_base[kTabThreads + 1], page_base[kTabThreads + 1];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int n = p.a.n_reqs, b = threadIdx.x;
+  const int64_t cur = p.a.cursor ? p.a.cursor[0] : 0;
+  int32_t bad = 0;
+  int64_t cnt = 0, take = 0, tokens, pages;
+  if (b < n) {
+    const Span s = checked_span(p, b, true, &bad);
+    cnt = s.end - s.start;
+    take = s.need - s.have;
+  }
+  block_scan2(cnt, take, &tokens, &pages, sm);
+  if (b < n) tok_base[b] = (int32_t)cnt, page_base[b] = (int32_t)take;
+  if (b == n % kTabThreads) tok_base[n] = (int32_t)tokens, page_base[n] = (int32_t)pages;
+  check_ids(p, cur, tokens, pages, b, kTabThreads, &bad);
+  const int any_range = __syncthreads_or(bad == KVX_ERR_OUT_OF_RANGE);
+  const int any_arg = __syncthreads_or(bad == KVX_ERR_INVALID_ARG);
+  if (b == 0) *p.status = any_range ? KVX_ERR_OUT_OF_RANGE : any_arg ? KVX_ERR_INVALID_ARG : KVX_OK;
+  if (any_range || any_arg) return;
+  for (int i = b; i <= n; i += kTabThreads) p.a.q_start[i] = tok_base[i];
+  if (b == 0) *p.a.next_cursor = (int32_t)(cur + pages);
+  fill<kTabThreads>(p, tok_base, page_base, (int32_t)tokens, cur, 0, 1);
 }
 
 bool aligned4(const void *p) { return ((uintptr_t)p & 3) == 0; }
@@ -303,15 +360,20 @@ extern "C" kvx_status kvx_block_tables(kvx_layout_t pool, const kvx_tables_args 
   p.ctas = (int32_t)(1 + ids / 8192 < kTabMaxCtas ? 1 + ids / 8192 : kTabMaxCtas);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   void *kargs[] = {&p};
-  cudaError_t e = cudaLaunchKernel((const void *)tables_plan_kernel, dim3(p.ctas), dim3(kTabThreads),
-                                   kargs, 0, s);
-  if (e == cudaSuccess) {
-    const int64_t chunks = (a.max_tokens + kFillChunk - 1) / kFillChunk;
-    const int64_t rows = a.n_prefix_pages > 0 ? a.n_reqs : 1;
-    int64_t grid = chunks > rows ? chunks : rows;
-    if (grid > 152 * 8) grid = 152 * 8;
-    if (grid < 1) grid = 1;
-    e = launch_pdl((const void *)tables_fill_kernel, dim3((unsigned)grid), dim3(kFillThreads), kargs, s);
+  cudaError_t e;
+  if (a.n_reqs <= kTabThreads && a.max_tokens <= kOneTokens &&
+      (int64_t)a.n_reqs * a.n_prefix_pages <= kOneTokens) {
+    e = launch_pdl((const void *)tables_one_kernel, dim3(1), dim3(kTabThreads), kargs, s);
+  } else {
+    e = launch_pdl((const void *)tables_plan_kernel, dim3(p.ctas), dim3(kTabThreads), kargs, s);
+    if (e == cudaSuccess) {
+      const int64_t chunks = (a.max_tokens + kFillChunk - 1) / kFillChunk;
+      const int64_t rows = a.n_prefix_pages > 0 ? a.n_reqs : 1;
+      const int64_t most = chunks > rows ? chunks : rows;
+      const int64_t grid = most < 1 ? 1 : most < 152 * 8 ? most : 152 * 8;
+      e = launch_pdl((const void *)tables_fill_kernel, dim3((unsigned)grid), dim3(kFillThreads),
+                     kargs, s);
+    }
   }
   if (e != cudaSuccess) {
     record_cuda_error(e);

@@ -283,10 +283,23 @@ def _nbytes(x) -> int:
     return int(x.numel() * x.element_size())
 
 
+_raw_stream = None  # torch's current stream as a number, without a Stream object around it
+
+
+def _current_stream() -> Optional[int]:
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        if not torch.cuda.is_initialized() or not hasattr(torch._C, "_cuda_getCurrentRawStream"):
+            return int(torch.cuda.current_stream().cuda_stream) or None
+        device, raw = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+        _raw_stream = lambda: raw(device())  # noqa: E731
+    return _raw_stream() or None
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        return int(torch.cuda.current_stream().cuda_stream) or None
+        return _current_stream()
     if isinstance(stream, int):
         return stream or None
     return int(stream.cuda_stream) or None
@@ -698,19 +711,17 @@ def block_tables(pool: Layout, page_size: int, new_lens, tables, free_pages, cur
     the ``slots`` and ``positions`` of the new tokens, ``q_start`` saying whose they are.  All
     arrays are device int32 tensors; ``cursor`` may be None (0) and ``next_cursor`` the same word
     as ``cursor``."""
-    _i32_arrays(new_lens=new_lens, tables=tables, free_pages=free_pages, cursor=cursor,
-                next_cursor=next_cursor, q_start=q_start, slots=slots, old_lens=old_lens,
-                prefix_pages=prefix_pages, positions=positions, status=status)
+    _i32_arrays((new_lens, free_pages, cursor, next_cursor, q_start, slots, old_lens, prefix_pages,
+                 positions, status), tables)
     n = new_lens.numel()
-    if tables.dim() != 2 or tables.shape[0] < n or q_start.numel() < n + 1:
-        raise ValueError("tables needs a row, and q_start an entry and one more, for each request")
-    if old_lens is not None and old_lens.numel() < n:
-        raise ValueError("old_lens is shorter than new_lens")
+    rows, width = tables.shape
+    if rows < n or q_start.numel() <= n or (old_lens is not None and old_lens.numel() < n):
+        raise ValueError("tables, q_start or old_lens has no room for every request")
     room = slots.numel()
     if positions is not None:
         room = min(room, positions.numel())
     a = TablesArgs(n, page_size, _ptr(old_lens), new_lens.data_ptr(), _ptr(prefix_pages),
-                   0 if prefix_pages is None else prefix_pages.numel(), tables.shape[1],
+                   0 if prefix_pages is None else prefix_pages.numel(), width,
                    tables.data_ptr(), tables.stride(0), free_pages.data_ptr(), free_pages.numel(),
                    0, _ptr(cursor), next_cursor.data_ptr(), q_start.data_ptr(), slots.data_ptr(),
                    _ptr(positions), room)
@@ -735,48 +746,49 @@ def shared_attention(pool: Layout, layer: int, q, out, tables, seq_lens, page_si
     read once for the whole batch, the rest those of ``tables[b]``; its query tokens are
     ``q_start[b]`` up to ``q_start[b + 1]``, its last ``seq_lens[b]`` positions' end (None: one
     token each).  ``scale`` is head_dim ** -0.5 by default."""
-    _i32_arrays(tables=tables, seq_lens=seq_lens, q_start=q_start, prefix_pages=prefix_pages,
-                status=status)
+    _i32_arrays((seq_lens, q_start, prefix_pages, status), tables)
     n_q, heads, dim = q.shape
     n = seq_lens.numel()
-    if dim != pool.head_dim or out.shape != q.shape or out.dtype != q.dtype:
+    rows, width = tables.shape
+    if q.dtype is not out.dtype or dim != pool.head_dim or out.shape != q.shape:
         raise ValueError("q and out are [n_q, q_heads, head_dim] of one type")
-    if (dim > 1 and n_q * heads > 0) and (q.stride(2) != 1 or out.stride(2) != 1):
+    q_tok, q_head, q_el = q.stride()
+    o_tok, o_head, o_el = out.stride()
+    if (q_el != 1 or o_el != 1) and dim > 1 and n_q * heads > 0:
         raise ValueError("a head's elements must be contiguous in q and out")
-    if tables.dim() != 2 or tables.shape[0] < n or (q_start is not None and q_start.numel() < n + 1):
-        raise ValueError("tables needs a row, and q_start an entry and one more, for each request")
-    if lse is not None and (tuple(lse.shape) != (n_q, heads) or lse.element_size() != 4
-                            or not lse.is_floating_point() or not lse.is_contiguous()):
+    if rows < n or (q_start is not None and q_start.numel() <= n):
+        raise ValueError("tables or q_start has no room for every request")
+    if lse is not None and (lse.shape != (n_q, heads) or str(lse.dtype) != "torch.float32"
+                            or not lse.is_contiguous()):
         raise ValueError("lse is a contiguous float32 [n_q, q_heads]")
-    a = AttnArgs(layer, _q_dtype(q), heads, n_q, n, page_size, tables.shape[1], prefix_len,
+    a = AttnArgs(layer, _q_dtype(q), heads, n_q, n, page_size, width, prefix_len,
                  tables.stride(0), tables.data_ptr(), _ptr(prefix_pages),
                  0 if prefix_pages is None else prefix_pages.numel(), 0, seq_lens.data_ptr(),
-                 _ptr(q_start), q.data_ptr(), q.stride(0), q.stride(1), out.data_ptr(),
-                 out.stride(0), out.stride(1), _ptr(lse),
-                 dim ** -0.5 if scale is None else scale, k_scale, v_scale, 0)
+                 _ptr(q_start), q.data_ptr(), q_tok, q_head, out.data_ptr(), o_tok, o_head,
+                 _ptr(lse), dim ** -0.5 if scale is None else scale, k_scale, v_scale, 0)
     _check(lib().kvx_shared_attention(_h(pool), a, _ptr(ws),
                                       _nbytes(ws) if ws_bytes is None else ws_bytes,
                                       _ptr(status), _stream(stream)), "kvx_shared_attention")
 
 
+_Q_DTYPES = {"torch.float16": F16, "torch.bfloat16": BF16, "torch.float32": F32}
+
+
 def _q_dtype(q) -> int:
-    import torch
-    got = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}.get(q.dtype)
+    got = _Q_DTYPES.get(str(q.dtype))
     if got is None:
         raise ValueError("q and out are float16, bfloat16 or float32")
     return got
 
 
-def _i32_arrays(**arrays) -> None:
-    """Index arrays are int32; lists (all but tables, whose rows may be apart) are contiguous."""
-    for name, x in arrays.items():
-        if x is None:
-            continue
-        if x.element_size() != 4 or x.is_floating_point():
-            raise ValueError(f"{name} must be int32")
-        if x.dim() and x.numel() > 1 and x.stride(-1) != 1 or (x.dim() > 1 and name != "tables"):
-            raise ValueError(f"{name} must be contiguous" + (" within a row" if name == "tables"
-                                                             else " and one-dimensional"))
+def _i32_arrays(lists, tables) -> None:
+    """Index arrays are int32; lists are contiguous, the rows of tables may be apart."""
+    i32 = tables.dtype
+    if str(i32) != "torch.int32" or tables.dim() != 2 or (tables.shape[1] > 1 and tables.stride(1) != 1):
+        raise ValueError("tables is an int32 [n_reqs, max_pages] with contiguous rows")
+    for x in lists:
+        if x is not None and (x.dtype is not i32 or not x.is_contiguous()):
+            raise ValueError("lengths, page lists, slots and status are contiguous int32 tensors")
 
 
 # ---- checked calls -------------------------------------------------------------------------
