@@ -71,57 +71,147 @@ __device__ __forceinline__ Req request(const AttnParams &p, int b, int32_t *bad)
   return r;
 }
 
+// The last b in [0, n) with base[b] <= x.
+__device__ __forceinline__ int last_at_or_before(const int32_t *base, int n, int32_t x) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (base[mid] <= x) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
 __global__ void __launch_bounds__(kPlanCta) attn_plan_kernel(const AttnParams p) {
   __shared__ int64_t sm[32];
   attn_wait_prior();
   const int tid = threadIdx.x, n = p.n_reqs;
-  int32_t bad = 0;
-  for (int t = tid; t < p.n_q; t += kPlanCta) p.owner[t] = -1, p.limit[t] = 0;
-  __syncthreads();
-  int32_t most = 0;
-  for (int b = tid; b < n; b += kPlanCta) {
-    const Req r = request(p, b, &bad);
-    most = max(most, r.len);
-    for (int i = 0; i < r.n; ++i) {
-      p.owner[r.t0 + i] = b;
-      p.limit[r.t0 + i] = max(0, r.len - r.n + i + 1);
+  int32_t bad = 0, most = 0;
+  // check; how far the longest request reaches; which requests are prompts
+  int64_t many = 0, plain = 0;
+  for (int b0 = 0; b0 < n; b0 += kPlanCta) {
+    const int b = b0 + tid;
+    int64_t mine = 0, total;
+    Req r = {};
+    bool prompt = false;
+    if (b < n) {
+      r = request(p, b, &bad);
+      most = max(most, r.len);
+      prompt = p.wide_groups > 0 && (int64_t)r.n * p.group > kAttnNarrowRows;
+      mine = prompt ? 0 : r.n;
     }
+    const int64_t at = plain + block_excl(mine, &total, sm);
+    if (b < n) {
+      // a request's first place in prefix_tok, as an offset from its first token; prompts: none
+      p.prompt[b] = prompt ? INT32_MIN : (int32_t)(at - r.t0);
+      many += prompt;
+    }
+    plain += total;
   }
   for (int o = 16; o; o >>= 1) most = max(most, __shfl_xor_sync(~0u, most, o));
-  if ((tid & 31) == 0) sm[tid >> 5] = most;
   __syncthreads();
+  if ((tid & 31) == 0) sm[tid >> 5] = most;
+  const int any_range = __syncthreads_or(bad == KVX_ERR_OUT_OF_RANGE);
+  const int any_arg = __syncthreads_or(bad == KVX_ERR_INVALID_ARG);
+  const int any_prompt = __syncthreads_or(many > 0);
   for (int i = 0; i < 32; ++i) most = max(most, (int32_t)sm[i]);
+  const bool refused = any_range || any_arg;
+  const int32_t prefix = min(p.prefix_len, most);  // no further than some request reaches
+  if (tid == 0) {
+    p.head->segs = refused ? 0 : n + 1;
+    *p.status = any_range ? KVX_ERR_OUT_OF_RANGE : any_arg ? KVX_ERR_INVALID_ARG : KVX_OK;
+  }
+  // what each token sees, and whose it is
+  int32_t none = 0;
+  const int32_t last = refused || n == 0 ? 0 : p.q_start ? p.q_start[n] : n;
+  for (int t = tid; t < p.n_q; t += kPlanCta) {
+    int b = -1, sees = 0;
+    if (t < last) {
+      b = p.q_start ? last_at_or_before(p.q_start, n, t) : t;
+      const Req r = request(p, b, &none);
+      sees = max(0, r.len - r.n + (t - r.t0) + 1);
+      const int32_t at = p.prompt[b];
+      if (at != INT32_MIN) p.prefix_tok[at + t] = t, p.prefix_at[t] = at + t;
+    }
+    p.owner[t] = b;
+    p.limit[t] = sees;
+  }
+  // the narrow line
   int64_t tiles = 0;
   for (int s0 = 0; s0 <= n; s0 += kPlanCta) {
     const int s = s0 + tid;
     AttnSeg g = {};
     int64_t mine = 0;
-    if (s <= n) {
-      if (s == 0) {  // no further than some request reaches
-        g.rows = p.n_q * p.group;
-        g.key1 = min(p.prefix_len, most);
-      } else {
-        const Req r = request(p, s - 1, &bad);
+    if (s <= n && !refused) {
+      if (s == 0) {
+        if (p.wide_groups == 0) {
+          g.rows = (int32_t)plain * p.group;
+          g.key1 = prefix;
+        }
+      } else if (p.prompt[s - 1] != INT32_MIN) {
+        const Req r = request(p, s - 1, &none);
         g.row0 = r.t0 * p.group;
         g.rows = r.n * p.group;
         g.key0 = p.prefix_len;
         g.key1 = max(r.len, p.prefix_len);
       }
-      if (g.rows > 0) g.key_tiles = (int32_t)(((int64_t)g.key1 - g.key0 + kAttnKeyTile - 1) / kAttnKeyTile);
-      mine = (int64_t)((g.rows + p.row_tile - 1) / p.row_tile) * g.key_tiles;
+      if (g.rows > 0) g.key_tiles = (int32_t)up((int64_t)g.key1 - g.key0, kAttnKeyTile);
+      mine = up(g.rows, p.row_tile) * g.key_tiles;
     }
     int64_t total;
     g.tile0 = tiles + block_excl(mine, &total, sm);
     if (s <= n) p.segs[s] = g;
     tiles += total;
   }
-  const int any_range = __syncthreads_or(bad == KVX_ERR_OUT_OF_RANGE);
-  const int any_arg = __syncthreads_or(bad == KVX_ERR_INVALID_ARG);
+  // the wide line: units first, then their tiles
+  int64_t units = 0, wide = 0;
+  if (p.wide_groups > 0 && !refused) {
+    for (int s0 = 0; s0 <= n; s0 += kPlanCta) {
+      const int s = s0 + tid;
+      int64_t mine = 0, total;
+      if (s == 0) mine = prefix > 0 ? up(plain * p.group, kAttnWideRows) : 0;
+      else if (s <= n && any_prompt && p.prompt[s - 1] == INT32_MIN)
+        mine = up((int64_t)request(p, s - 1, &none).n * p.group, kAttnWideRows);
+      const int64_t at = units + block_excl(mine, &total, sm);
+      if (s <= n) p.unit_base[s] = (int32_t)at;
+      units += total;
+      if (!any_prompt) break;
+    }
+    __syncthreads();
+    for (int64_t u0 = 0; u0 < units; u0 += kPlanCta) {
+      const int64_t u = u0 + tid;
+      AttnUnit x = {};
+      int64_t total;
+      if (u < units) {
+        const int s = any_prompt ? last_at_or_before(p.unit_base, n + 1, (int32_t)u) : 0;
+        const int tile = (int)(u - (s ? p.unit_base[s] : 0));
+        x.table = s - 1;
+        x.row0 = tile * kAttnWideRows;
+        if (s == 0) {
+          x.rows = (int32_t)min((int64_t)kAttnWideRows, plain * p.group - x.row0);
+          x.key1 = prefix;
+        } else {
+          const Req r = request(p, s - 1, &none);
+          x.rows = min(kAttnWideRows, r.n * p.group - x.row0);
+          // as far as its last row sees
+          x.key1 = max(0, r.len - r.n + (x.row0 + x.rows - 1) / p.group + 1);
+          x.row0 += r.t0 * p.group;
+        }
+        x.key_tiles = (int32_t)up(x.key1, kAttnWideKeys);
+      }
+      x.tile0 = wide + block_excl(x.key_tiles, &total, sm);
+      if (u < units) p.units[u] = x;
+      wide += total;
+    }
+  }
   if (tid == 0) {
     p.head->tiles = tiles;
-    p.head->quota = max((int64_t)1, (tiles + p.groups - 1) / p.groups);
-    p.head->segs = any_range || any_arg ? 0 : n + 1;
-    *p.status = any_range ? KVX_ERR_OUT_OF_RANGE : any_arg ? KVX_ERR_INVALID_ARG : KVX_OK;
+    p.head->quota = max((int64_t)1, up(tiles, p.groups));
+    p.head->units = (int32_t)units;
+    p.head->wide_tiles = wide;
+    p.head->wide_quota = p.wide_groups > 0 ? max((int64_t)1, up(wide, p.wide_groups)) : 1;
   }
 }
 
@@ -142,26 +232,47 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const AttnPa
   const int h = qh / p.group, r = t * p.group + qh - h * p.group;
   const int D = p.head_dim, b = p.owner[t];
   IO *out = reinterpret_cast<IO *>(p.out + t * p.out_tok + qh * p.out_head);
-  // the pieces of the row: n0 of the prefix, then the request's own
-  int64_t first[2], more[2];
+  // the pieces of the row: n0 of the prefix (or of the prompt), then the request's own
+  int64_t first[2], more[2], step[2];
   int count[2] = {0, 0};
-  for (int k = 0; k < 2; ++k) {
-    if (b < 0 || p.head->segs == 0) break;
-    const AttnSeg s = p.segs[k == 0 ? 0 : 1 + b];
-    if (s.key_tiles == 0) continue;
-    const int unit = (r - s.row0) / p.row_tile, row0 = s.row0 + unit * p.row_tile;
-    const int64_t w = s.tile0 + (int64_t)unit * s.key_tiles, quota = p.head->quota;
-    const int g0 = (int)(w / quota), g1 = (int)((w + s.key_tiles - 1) / quota);
-    count[k] = g1 - g0 + 1;
-    first[k] = attn_part(p, k == 0, true, 0, h, row0) + (r - row0);
-    more[k] = attn_part(p, k == 0, false, g0, h, row0) + (r - row0);
+  const AttnHeader head = *p.head;
+  if (b >= 0 && head.segs > 0) {
+    const bool prompt = p.prompt[b] == INT32_MIN;
+    if (p.wide_groups > 0) {
+      // the row's place among those of its kind of work, and with it its unit
+      const int s = prompt ? 1 + b : 0, lead = prompt ? (p.q_start ? p.q_start[b] : b) * p.group : 0;
+      const int wr = prompt ? r : p.prefix_at[t] * p.group + r % p.group;
+      const int u = (s ? p.unit_base[s] : 0) + (wr - lead) / kAttnWideRows;
+      if (u < head.units) {
+        const AttnUnit x = p.units[u];
+        const int64_t q = head.wide_quota;
+        if (x.key_tiles > 0 && x.table == s - 1) {
+          const int g0 = (int)(x.tile0 / q), g1 = (int)((x.tile0 + x.key_tiles - 1) / q);
+          if (prompt && g0 == g1) return;  // the wide kernel has written the result
+          count[0] = g1 - g0 + 1;
+          first[0] = attn_wide_part(p, true, 0, h) + r;
+          more[0] = attn_wide_part(p, false, g0, h) + (wr - x.row0);
+          step[0] = (int64_t)p.kv_heads * kAttnWideRows;
+        }
+      }
+    }
+    for (int k = p.wide_groups > 0 ? 1 : 0; k < 2; ++k) {
+      const AttnSeg s = p.segs[k == 0 ? 0 : 1 + b];
+      if (s.key_tiles == 0) continue;
+      const int unit = (r - s.row0) / p.row_tile, row0 = s.row0 + unit * p.row_tile;
+      const int64_t w = s.tile0 + (int64_t)unit * s.key_tiles;
+      const int g0 = (int)(w / head.quota), g1 = (int)((w + s.key_tiles - 1) / head.quota);
+      count[k] = g1 - g0 + 1;
+      first[k] = attn_part(p, k == 0, true, 0, h, row0) + (r - row0);
+      more[k] = attn_part(p, k == 0, false, g0, h, row0) + (r - row0);
+      step[k] = (int64_t)p.kv_heads * p.row_tile;
+    }
   }
   const int n0 = count[0], n = n0 + count[1];
-  const int64_t step = (int64_t)p.kv_heads * p.row_tile;
   auto part = [&](int i) {
     const int k = i < n0 ? 0 : 1;
     i -= k ? n0 : 0;
-    return i == 0 ? first[k] : more[k] + i * step;
+    return i == 0 ? first[k] : more[k] + i * step[k];
   };
   float top = -INFINITY;
   for (int i = lane; i < n; i += 32) top = fmaxf(top, p.part_m[part(i)]);
@@ -196,22 +307,40 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const AttnPa
 }
 
 struct Sizes {
-  int64_t segs_off, limit_off, owner_off, m_off, l_off, o_off, total;
-  int32_t groups;
+  int64_t segs_off, units_off, base_off, prompt_off, limit_off, owner_off, tok_off, at_off;
+  int64_t m_off, l_off, o_off, total;
+  int32_t groups, wide_groups;
 };
 
 // How many groups of kv_heads CTAs: as many as are resident at once.
-Sizes sizes(int64_t n_q, int64_t n_reqs, int64_t q_heads, int64_t kv_heads, int64_t D, int row_tile) {
+Sizes sizes(int64_t n_q, int64_t n_reqs, int64_t q_heads, int64_t kv_heads, int64_t D, int row_tile,
+            bool wide) {
   Sizes z = {};
+  const int64_t rows = n_q * (q_heads / kv_heads);
   z.groups = (int32_t)std::max((int64_t)1, 152 * 2 / kv_heads);
-  const int64_t parts = 2 * n_q * q_heads + z.groups * kv_heads * row_tile;
-  z.segs_off = sizeof(AttnHeader);
-  z.limit_off = align_up(z.segs_off + (int64_t)sizeof(AttnSeg) * (n_reqs + 1), 256);
-  z.owner_off = align_up(z.limit_off + 4 * n_q, 256);
-  z.m_off = align_up(z.owner_off + 4 * n_q, 256);
-  z.l_off = align_up(z.m_off + 4 * parts, 256);
-  z.o_off = align_up(z.l_off + 4 * parts, 256);
-  z.total = align_up(z.o_off + 4 * parts * D, 256);
+  z.wide_groups = wide ? (int32_t)std::max((int64_t)1, 152 / kv_heads) : 0;
+  const int64_t parts = 2 * n_q * q_heads + z.groups * kv_heads * row_tile +
+                        z.wide_groups * kv_heads * kAttnWideRows;
+  // prompts have more than kAttnNarrowRows rows each
+  const int64_t units = wide ? 2 * (rows / kAttnWideRows) + rows / kAttnNarrowRows + 2 : 0;
+  int64_t at = sizeof(AttnHeader);
+  auto take = [&](int64_t bytes) {
+    const int64_t here = at;
+    at = align_up(at + bytes, 256);
+    return here;
+  };
+  z.segs_off = take((int64_t)sizeof(AttnSeg) * (n_reqs + 1));
+  z.units_off = take((int64_t)sizeof(AttnUnit) * units);
+  z.base_off = take(4 * (n_reqs + 2));
+  z.prompt_off = take(4 * n_reqs);
+  z.limit_off = take(4 * n_q);
+  z.owner_off = take(4 * n_q);
+  z.tok_off = take(4 * n_q);
+  z.at_off = take(4 * n_q);
+  z.m_off = take(4 * parts);
+  z.l_off = take(4 * parts);
+  z.o_off = take(4 * parts * D);
+  z.total = at;
   return z;
 }
 
@@ -228,6 +357,11 @@ bool tensor_cores(const kvx_layout *l) {
 
 int row_tile(const kvx_layout *l) { return tensor_cores(l) ? kAttnNarrowRows : kAttnGeneralRows; }
 
+// Whether a call may have work for the wide kernel: more rows than the narrow kernel has in a unit.
+bool takes_wide(const kvx_layout *l, int64_t n_q, int64_t q_heads) {
+  return tensor_cores(l) && n_q * (q_heads / l->kv_heads) > kAttnNarrowRows;
+}
+
 bool mult(const void *p, uintptr_t a) { return (uintptr_t)p % a == 0; }
 
 static_assert(sizeof(kvx_attn_args) == 152, "the binding mirrors this structure");
@@ -239,7 +373,7 @@ extern "C" size_t kvx_attention_workspace_size(kvx_layout_t pool, int32_t n_q, i
                                                int32_t q_heads, int32_t prefix_len) {
   if (!kvx::shape_ok(pool, n_q, n_reqs, q_heads, prefix_len)) return 0;
   return (size_t)kvx::sizes(n_q, n_reqs, q_heads, pool->kv_heads, pool->head_dim,
-                            kvx::row_tile(pool)).total;
+                            kvx::row_tile(pool), kvx::takes_wide(pool, n_q, q_heads)).total;
 }
 
 extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_args *args,
@@ -280,7 +414,12 @@ extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_arg
     for (int i = 2 * a.layer; i < 2 * a.layer + 2; ++i)
       if (b0 < pool->plane[i] + pool->extent && pool->plane[i] < b1) return KVX_ERR_OVERLAP;
   }
-  const Sizes z = sizes(a.n_q, a.n_reqs, a.q_heads, pool->kv_heads, pool->head_dim, row_tile(pool));
+  // without prompts the wide kernel has the prefix alone; it takes the greatest score from the
+  // greatest product, so the factor between them has to be above 0
+  const bool wide = takes_wide(pool, a.n_q, a.q_heads) && (a.q_start || a.prefix_len > 0) &&
+                    a.scale * a.k_scale > 0.f;
+  const Sizes z = sizes(a.n_q, a.n_reqs, a.q_heads, pool->kv_heads, pool->head_dim, row_tile(pool),
+                        wide);
   if (!d_ws || !mult(d_ws, 256) || (int64_t)ws_bytes < z.total) return KVX_ERR_NO_WORKSPACE;
 
   AttnParams p;
@@ -323,9 +462,15 @@ extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_arg
   p.row_tile = row_tile(pool);
   p.q_even = ((uintptr_t)a.q | (uintptr_t)p.q_tok | (uintptr_t)p.q_head) % 4 == 0;
   p.groups = z.groups;
+  p.wide_groups = z.wide_groups;
   char *ws = static_cast<char *>(d_ws);
   p.head = reinterpret_cast<AttnHeader *>(ws);
   p.segs = reinterpret_cast<AttnSeg *>(ws + z.segs_off);
+  p.units = reinterpret_cast<AttnUnit *>(ws + z.units_off);
+  p.unit_base = reinterpret_cast<int32_t *>(ws + z.base_off);
+  p.prompt = reinterpret_cast<int32_t *>(ws + z.prompt_off);
+  p.prefix_tok = reinterpret_cast<int32_t *>(ws + z.tok_off);
+  p.prefix_at = reinterpret_cast<int32_t *>(ws + z.at_off);
   p.limit = reinterpret_cast<int32_t *>(ws + z.limit_off);
   p.owner = reinterpret_cast<int32_t *>(ws + z.owner_off);
   p.part_m = reinterpret_cast<float *>(ws + z.m_off);
@@ -339,6 +484,7 @@ extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_arg
   if (e == cudaSuccess && a.n_q > 0) {
     e = tensor_cores(pool) ? launch_attn_narrow(p, pool->dtype, a.q_dtype, s)
                            : launch_attn_general(p, pool->dtype, a.q_dtype, s);
+    if (e == cudaSuccess && wide) e = launch_attn_wide(p, pool->dtype, a.q_dtype, s);
     if (e == cudaSuccess) {
       const void *join = a.q_dtype == KVX_F32   ? (const void *)attn_join_kernel<float>
                          : a.q_dtype == KVX_F16 ? (const void *)attn_join_kernel<__half>

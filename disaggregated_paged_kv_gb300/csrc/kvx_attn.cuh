@@ -2,12 +2,17 @@
 //
 // Rows and parts.  A row is (query token t, query head); the G = q_heads / kv_heads rows of a
 // token that read one kv head lie together: row r of kv head h is token r / G, query head
-// h * G + r % G.  A seg is a set of rows with the keys they all read: the prefix (rows of all
-// tokens) or one request's own positions (its rows).  A unit is row_tile rows of a seg, and its
-// keys are cut into tiles of kAttnKeyTile.  All units' key tiles in a line are dealt out evenly:
-// group g of kv_heads CTAs, one CTA a head, takes tiles [g * quota, (g + 1) * quota) of the line.
-// So every CTA has the same number of tiles whatever the lengths, and the CTAs of a group read
-// the heads of the same rows at the same time.
+// h * G + r % G.  Three kinds of work, each a set of rows with the keys they all read:
+//   own      a request's rows and its positions behind the prefix;
+//   prefix   the rows of many requests and the prefix;
+//   prompt   a request with many rows of its own and all its positions, prefix included: its
+//            tiles of rows are full without the others', and one pass needs no join.
+// The narrow kernel (and the plain one) takes units of up to row_tile rows: own work, and the
+// prefix where there are few rows in all.  The wide kernel takes units of up to 256 rows: the
+// prefix and prompts.  A unit's keys are cut into tiles, all units' key tiles stand in a line, and
+// the line is dealt out evenly: group g of kv_heads CTAs, one CTA a head, takes tiles
+// [g * quota, (g + 1) * quota).  So every CTA has the same number of tiles whatever the lengths,
+// and the CTAs of a group read the heads of the same rows at the same time.
 //
 // A piece is what a CTA has of one unit.  It is worked through with a running maximum and sum and
 // leaves, per row, the unnormalised sum o = sum_j e^(s_j - m) v_j in 32 bits, m and
@@ -26,7 +31,11 @@
 
 namespace kvx {
 
-constexpr int kAttnKeyTile = 64;
+constexpr int kAttnKeyTile = 64;       // of the narrow and the plain kernel
+constexpr int kAttnGeneralRows = 16;   // rows of a unit, plain kernel
+constexpr int kAttnNarrowRows = 64;    // narrow kernel
+constexpr int kAttnWideKeys = 128;     // key tile of the wide kernel
+constexpr int kAttnWideRows = 256;     // rows of its units
 
 // Where a layer's rows are: element row (page id, offset in page, kv head) starts at
 // plane + id * page_stride + offset * tok_stride + head * head_stride (bytes), in either kind of
@@ -39,6 +48,7 @@ struct AttnPool {
   int32_t page_shift;    // log2(page_size), or -1
 };
 
+// Work of the narrow line: the prefix (first) or a request's own positions.
 struct AttnSeg {
   int64_t tile0;       // its first key tile in the line
   int32_t row0, rows;
@@ -47,11 +57,22 @@ struct AttnSeg {
   int32_t pad;
 };
 
+// A unit of the wide line.  table: the request of a prompt, -1: the prefix, whose rows are those
+// of the tokens of prefix_tok.
+struct AttnUnit {
+  int64_t tile0;
+  int32_t row0, rows;
+  int32_t key_tiles, key1;
+  int32_t table;
+  int32_t pad;
+};
+
 struct AttnHeader {
-  int64_t tiles;       // in the line
-  int64_t quota;       // of a group
-  int32_t segs;        // 1 + n_reqs; 0: the arguments were refused
-  int32_t pad[11];
+  int64_t tiles, quota;            // the narrow line, and a group's part of it
+  int64_t wide_tiles, wide_quota;
+  int32_t segs;                    // 1 + n_reqs; 0: the arguments were refused
+  int32_t units;
+  int32_t pad[6];
 };
 
 struct AttnParams {
@@ -68,16 +89,26 @@ struct AttnParams {
   float v_scale;
   int32_t n_q, n_reqs, q_heads, kv_heads, group, head_dim;
   int32_t page_size, max_pages, prefix_len;
-  int32_t row_tile;   // rows of a unit
-  int32_t groups;     // groups of kv_heads CTAs
-  int32_t q_even;     // q's heads start on 4-byte boundaries
+  int32_t row_tile;      // rows of a narrow unit
+  int32_t groups;        // groups of kv_heads CTAs, narrow line
+  int32_t wide_groups;   // of the wide line; 0: no wide kernel
+  int32_t q_even;        // q's heads start on 4-byte boundaries
+  int32_t q_vec;         // on 16-byte boundaries
+  int32_t out_vec;       // out's heads do
   // workspace
   AttnHeader *head;
-  AttnSeg *segs;      // [1 + n_reqs]: the prefix, then the requests
-  int32_t *limit;     // [n_q]: positions that a token sees
-  int32_t *owner;     // [n_q]: its request, -1: none
-  // part rows: [kv_heads][n_q * G] of the requests' first pieces, the same of the prefix's, and
-  // [groups][kv_heads][row_tile] of pieces that go on
+  AttnSeg *segs;         // [1 + n_reqs]: the prefix, then the requests
+  AttnUnit *units;
+  int32_t *unit_base;    // [2 + n_reqs]: first wide unit of the prefix and of each request
+  int32_t *prompt;       // [n_reqs]: INT32_MIN: prompt work; else what to add to a token for its
+                         // place in prefix_tok
+  int32_t *limit;        // [n_q]: positions that a token sees
+  int32_t *owner;        // [n_q]: its request, -1: none
+  int32_t *prefix_tok;   // [n_q]: tokens whose requests are not prompts, in order
+  int32_t *prefix_at;    // [n_q]: a token's place in prefix_tok
+  // part rows: [kv_heads][n_q * G] of own work's first pieces; the same of the prefix's and
+  // prompts' first pieces; then pieces that go on, [groups][kv_heads][row_tile] and
+  // [wide_groups][kv_heads][256]
   float *part_m, *part_l, *part_o;
   int32_t *status;
 };
@@ -106,23 +137,33 @@ __device__ __forceinline__ int64_t attn_key_offset(const AttnParams &p, int32_t 
   return attn_page(p, table, pg) * p.pool.page_stride + off * p.pool.tok_stride;
 }
 
-// First part row of a piece of a unit that starts at row0 (see AttnParams).
+// First part row of a piece of a narrow unit that starts at row0 (see AttnParams).
 __device__ __forceinline__ int64_t attn_part(const AttnParams &p, bool prefix, bool first, int g,
                                              int h, int32_t row0) {
   const int64_t all = (int64_t)p.n_q * p.group;
   if (first) return ((prefix ? p.kv_heads : 0) + h) * all + row0;
   return 2 * p.kv_heads * all + ((int64_t)g * p.kv_heads + h) * p.row_tile;
 }
+// The same of the wide line: the place of row 0 of head h for first pieces, of the unit's first
+// row for those that go on.
+__device__ __forceinline__ int64_t attn_wide_part(const AttnParams &p, bool first, int g, int h) {
+  const int64_t all = (int64_t)p.n_q * p.group;
+  if (first) return (p.kv_heads + h) * all;
+  return 2 * p.kv_heads * all + (int64_t)p.groups * p.kv_heads * p.row_tile +
+         ((int64_t)g * p.kv_heads + h) * kAttnWideRows;
+}
 
-// The seg with tile w in it, among the n segs.
-__device__ __forceinline__ int attn_find_seg(const AttnSeg *segs, int n, int64_t w) {
+// The last of n entries (of segs or units) that starts at or before tile w: empty ones before it
+// share its start.
+template <typename E>
+__device__ __forceinline__ int attn_find(const E *e, int n, int64_t w) {
   int lo = 0, hi = n - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (segs[mid].tile0 <= w) lo = mid;
+    if (e[mid].tile0 <= w) lo = mid;
     else hi = mid - 1;
   }
-  return lo;  // the last one that starts at or before w: the empty ones before it share its start
+  return lo;
 }
 
 // A piece: keys [key0, key1) for rows [row0, row0 + rows).
@@ -131,7 +172,7 @@ struct AttnPiece {
   int32_t row0, rows, key0, key1, table;
 };
 
-// Calls f(piece) for every piece of group g, kv head h.
+// Calls f(piece) for every piece of group g, kv head h of the narrow line.
 template <typename F>
 __device__ __forceinline__ void attn_pieces(const AttnParams &p, int g, int h, F f) {
   const int n = p.head->segs;
@@ -139,7 +180,7 @@ __device__ __forceinline__ void attn_pieces(const AttnParams &p, int g, int h, F
   int64_t w = g * quota;
   const int64_t end = min(p.head->tiles, w + quota);
   if (n == 0 || w >= end) return;
-  int s = attn_find_seg(p.segs, n, w);
+  int s = attn_find(p.segs, n, w);
   while (w < end) {
     const AttnSeg seg = p.segs[s];
     const int units = (seg.rows + p.row_tile - 1) / p.row_tile;
@@ -170,9 +211,8 @@ __device__ __forceinline__ void attn_release_next() {
 }
 
 cudaError_t launch_attn_general(const AttnParams &p, int32_t dtype, int32_t io, cudaStream_t s);
-constexpr int kAttnGeneralRows = 16;
 // head_dim 64 or 128, 16-bit or 8-bit pool with 16-byte aligned heads.
 cudaError_t launch_attn_narrow(const AttnParams &p, int32_t dtype, int32_t io, cudaStream_t s);
-constexpr int kAttnNarrowRows = 64;
+cudaError_t launch_attn_wide(const AttnParams &p, int32_t dtype, int32_t io, cudaStream_t s);
 
 }  // namespace kvx

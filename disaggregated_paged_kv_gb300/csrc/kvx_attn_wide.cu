@@ -1,0 +1,617 @@
+// kvx_attn_wide.cu -- shared attention for many rows a key: the prefix of a batch, and prompts.
+//
+// A CTA (one per SM) has a unit of two tiles of 128 rows and walks its keys in tiles of 128.  Both
+// products run on the 5th-generation tensor cores with their sums in tensor memory (512 columns):
+// S = Q K^T of either row tile (128 columns each) and O += P V (head_dim columns each); the weights
+// P overlay the first half of their S as 16-bit values and are the product's A operand from there.
+// The two row tiles alternate: while one's scores become weights, the tensor cores work for the
+// other.  Warps 0-3 and 4-7 do the softmax of the tiles (a thread a row, so no exchange between
+// threads), warps 8-11 bring in the queries and the keys and values by page look-up, warp 12
+// issues the products.
+//
+// Bound: 4 D operations a score on the tensor cores (1024 cycles for 128 x 128 scores at D = 128)
+// against one exponential and about five instructions a score on four warps.
+//
+// A row's sums refer to a maximum that is renewed only when a score passes it by 2^8: the factor
+// between the two cancels in the quotient, weights stay below 2^8 (in range for f16 and bf16), and
+// the sums in tensor memory are rescaled a few times in all instead of with every tile.
+#include <type_traits>
+
+#include "kvx_attn.cuh"
+#include "kvx_attn_mma.cuh"
+#include "kvx_launch.cuh"
+
+namespace kvx {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kKeys = kAttnWideKeys;
+constexpr int kStages = 4;      // of one K or V tile each
+constexpr float kRenew = 8.f;
+constexpr uint64_t kWaitNs = 2000000000ull;  // no wait of the kernel is that long unless it is lost
+
+template <int D>
+struct Smem {
+  alignas(1024) char q[2][128 * D * 2];
+  alignas(1024) char kv[kStages][kKeys * D * 2];
+  int64_t off[2][kKeys];
+  uint64_t q_full, q_empty, full[kStages], empty[kStages], s_full[2], p_full[2], o_full[2], o_empty[2], drained;
+  // of the piece, by its parity: the least position that a live row does not see, and whether
+  // infinities or NaN were taken out of the V tiles from there on
+  int32_t least[2], odd[2];
+  int32_t warp_least[4];
+  int32_t lost;
+  uint32_t tmem;
+};
+
+// ---- barriers ------------------------------------------------------------------------------
+__device__ __forceinline__ void bar_init(uint64_t *b, int n) {
+  asm volatile("mbarrier.init.shared.b64 [%0], %1;" ::"r"(smem_u32(b)), "r"(n) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint64_t *b) {
+  asm volatile("mbarrier.arrive.shared.b64 _, [%0];" ::"r"(smem_u32(b)) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint64_t *b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+               : "=r"(ok) : "r"(smem_u32(b)), "r"(parity) : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ uint64_t now_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+  return t;
+}
+// False when the wait is given up: too long, or some other wait of the CTA was.
+__device__ __forceinline__ bool bar_wait_slow(uint64_t *b, uint32_t parity, volatile int32_t *lost, int32_t *status) {
+  const uint64_t t0 = now_ns();
+  for (;;) {
+    for (int i = 0; i < 64; ++i)
+      if (bar_try(b, parity)) return true;
+    if (*lost) return false;
+    if (now_ns() - t0 > kWaitNs) {
+      *lost = 1;
+      atomicMax(status, (int32_t)KVX_ERR_TIMEOUT);
+      return false;
+    }
+  }
+}
+
+// ---- tensor memory and products --------------------------------------------------------------
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+  asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
+               "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
+               ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add) : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+  asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
+               "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
+               ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(add) : "memory");
+}
+// The barrier is arrived at when all products issued before are done.
+__device__ __forceinline__ void mma_commit(uint64_t *b) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+               ::"r"(smem_u32(b)) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tmem_ld32(uint32_t (&r)[32], uint32_t a) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(a) : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t (&r)[16], uint32_t a) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(a) : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      ::"r"(a), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// A matrix operand in shared memory: rows of 128 bytes, 16-byte chunks exchanged by the row's low
+// three bits (128-byte swizzle), groups of eight rows 1024 bytes apart.  lead: bytes between the
+// blocks of 64 columns, for the operand that is read across its rows.
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead) {
+  return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+         1ull << 46 | 2ull << 61;
+}
+
+// Byte place of 16-byte chunk c (of D / 8) of row r in a tile of 128 rows kept as such blocks.
+__device__ __forceinline__ uint32_t place(int r, int c) {
+  return (uint32_t)((c >> 3) * 128 * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+struct WidePiece {
+  int32_t row0, rows, key0, tiles, key1, table;
+  bool first, whole;
+};
+
+// Calls f(piece) for every piece of group g; f returns false to stop.
+template <typename F>
+__device__ __forceinline__ void wide_pieces(const AttnParams &p, int g, F f) {
+  const int n = p.head->units;
+  const int64_t quota = p.head->wide_quota;
+  int64_t w = g * quota;
+  const int64_t end = min(p.head->wide_tiles, w + quota);
+  if (n == 0 || w >= end) return;
+  for (int u = attn_find(p.units, n, w); w < end; ++u) {
+    const AttnUnit x = p.units[u];
+    if (w >= x.tile0 + x.key_tiles) continue;
+    const int kt = (int)(w - x.tile0);
+    WidePiece y;
+    y.row0 = x.row0, y.rows = x.rows, y.table = x.table;
+    y.tiles = (int)min((int64_t)(x.key_tiles - kt), end - w);
+    y.key0 = kt * kKeys;
+    y.key1 = (int32_t)min((int64_t)x.key1, (int64_t)y.key0 + (int64_t)y.tiles * kKeys);
+    y.first = kt == 0;
+    y.whole = y.first && y.tiles == x.key_tiles;
+    if (!f(y)) return;
+    w += y.tiles;
+  }
+}
+
+// The token of local row i of a piece; its row's member of the group is (row0 + i) % group.
+__device__ __forceinline__ int row_token(const AttnParams &p, const WidePiece &x, int i) {
+  const int t = (x.row0 + i) / p.group;
+  return x.table < 0 ? p.prefix_tok[t] : t;
+}
+
+template <typename T, bool FP8, int D>
+__global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const AttnParams p) {
+  extern __shared__ char raw_smem[];
+  Smem<D> &sm = *reinterpret_cast<Smem<D> *>(raw_smem + (-smem_u32(raw_smem) & 1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    bar_init(&sm.q_full, 128);
+    bar_init(&sm.q_empty, 1);
+    for (int i = 0; i < kStages; ++i) bar_init(&sm.full[i], 128), bar_init(&sm.empty[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      bar_init(&sm.s_full[i], 1), bar_init(&sm.p_full[i], 128);
+      bar_init(&sm.o_full[i], 1), bar_init(&sm.o_empty[i], 128);
+      sm.odd[i] = 0;
+    }
+    bar_init(&sm.drained, 1);
+    sm.lost = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 12) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sm.tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tm = sm.tmem;
+  const uint32_t tmS[2] = {tm, tm + 128}, tmO[2] = {tm + 256, tm + 256 + D};
+  attn_wait_prior();
+  const int g = blockIdx.x / p.kv_heads, h = blockIdx.x - g * p.kv_heads;
+  auto wait = [&](uint64_t *b, uint32_t parity) {
+    return bar_try(b, parity) || bar_wait_slow(b, parity, &sm.lost, p.status);
+  };
+
+  if (warp < 8) {
+    // ---- softmax of row tile t, a thread a row ----
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    const int t = warp >> 2, r = tid & 127;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+    uint32_t s_phase = 0, o_phase = 0, parity = 0;
+    wide_pieces(p, g, [&](const WidePiece &x) {
+      const int i = t * 128 + r;
+      const bool active = x.rows > t * 128;
+      const bool live = i < x.rows;
+      const int token = live ? row_token(p, x, i) : 0;
+      const int lim = live ? min(p.limit[token], x.key1) : 0;
+      const int member = (x.row0 + i) % p.group;
+      float m = -INFINITY;
+      float2 l2 = make_float2(0.f, 0.f);
+      if (active) {
+        for (int j = 0; j < x.tiles; ++j) {
+          if (!__all_sync(~0u, wait(&sm.s_full[t], s_phase))) return false;
+          s_phase ^= 1;
+          fence_after();
+          uint32_t s[4][32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(s[c], tmS[t] + lanes + c * 32);
+          tmem_wait_ld();
+          const int k0 = x.key0 + j * kKeys, seen = lim - k0;
+          if (seen < kKeys) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (c * 32 + k >= seen) s[c][k] = 0xff800000u;
+          }
+          float t0 = -INFINITY, t1 = -INFINITY, t2 = -INFINITY, t3 = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            t0 = fmaxf(t0, __uint_as_float(s[0][k])), t1 = fmaxf(t1, __uint_as_float(s[1][k]));
+            t2 = fmaxf(t2, __uint_as_float(s[2][k])), t3 = fmaxf(t3, __uint_as_float(s[3][k]));
+          }
+          const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * p.scale_log2;
+          const bool renew = top > m + kRenew || (m == -INFINITY && top > m);
+          if (__any_sync(~0u, renew)) {
+            const float f = !renew ? 1.f : m == -INFINITY ? 0.f : ex2(m - top);
+            if (renew) m = top;
+            l2.x *= f, l2.y *= f;
+            if (j > 0) {  // S of this tile is done, so are the products before it
+#pragma unroll
+              for (int c = 0; c < D / 16; ++c) {
+                uint32_t o[16];
+                tmem_ld16(o, tmO[t] + lanes + c * 16);
+                tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                tmem_st16(tmO[t] + lanes + c * 16, o);
+              }
+            }
+          }
+          const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t w[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float a = ex2(fmaf(__uint_as_float(s[c][2 * k]), p.scale_log2, -base));
+              const float b = ex2(fmaf(__uint_as_float(s[c][2 * k + 1]), p.scale_log2, -base));
+              l2.x += a, l2.y += b;
+              w[k] = pack2<T>(a, b);  // rounded to the values' type for the product; the sum is not
+            }
+            tmem_st16(tmS[t] + lanes + c * 16, w);
+          }
+          tmem_wait_st();
+          fence_before();
+          bar_arrive(&sm.p_full[t]);
+        }
+      }
+      if (!__all_sync(~0u, wait(&sm.o_full[t], o_phase))) return false;
+      o_phase ^= 1;
+      fence_after();
+      if (active) {
+        const float l = l2.x + l2.y;
+        const int qh = h * p.group + member;
+        const int64_t part = attn_wide_part(p, x.first, g, h) + (x.first ? (int64_t)token * p.group + member : i);
+        const bool direct = x.whole && x.table >= 0;
+        const float inv = l == 0.f ? 0.f : p.v_scale / l;
+        T *out = reinterpret_cast<T *>(p.out + (int64_t)token * p.out_tok + (int64_t)qh * p.out_head);
+        const int odd = *(volatile int32_t *)&sm.odd[parity], least = *(volatile int32_t *)&sm.least[parity];
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          __syncwarp();
+          tmem_ld32(o, tmO[t] + lanes + c * 32);
+          tmem_wait_ld();
+          if (!live) continue;
+          if (l == 0.f) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = 0;
+          } else if (odd) {
+            // infinities and NaN that were taken out of tiles that some row's mask falls into
+            for (int key = x.key0; key < lim; ++key) {
+              const char *v = p.pool.v + attn_key_offset(p, key < p.prefix_len ? -1 : x.table, key) +
+                              h * p.pool.head_stride;
+              const int tile1 = x.key0 + ((key - x.key0) / kKeys + 1) * kKeys;
+              if (tile1 <= least) continue;
+#pragma unroll
+              for (int k = 0; k < 32; ++k) {
+                float e;
+                if constexpr (FP8) {
+                  const uint32_t u = from_e4m3x2<__half>(reinterpret_cast<const uint8_t *>(v)[c * 32 + k]);
+                  e = __half2float(*reinterpret_cast<const __half *>(&u));
+                } else {
+                  e = (float)reinterpret_cast<const T *>(v)[c * 32 + k];
+                }
+                if (!isfinite(e)) o[k] = __float_as_uint(__uint_as_float(o[k]) + e);
+              }
+            }
+          }
+          if (direct) {
+            uint32_t w[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              w[k] = pack2<T>(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
+            if (p.out_vec) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                reinterpret_cast<uint4 *>(out + c * 32)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                reinterpret_cast<uint16_t *>(out)[c * 32 + 2 * k] = (uint16_t)w[k];
+                reinterpret_cast<uint16_t *>(out)[c * 32 + 2 * k + 1] = (uint16_t)(w[k] >> 16);
+              }
+            }
+          } else {
+            float4 *d = reinterpret_cast<float4 *>(p.part_o + part * D + c * 32);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              d[k] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                 __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+          }
+        }
+        if (live) {
+          if (direct) {
+            if (p.lse)
+              p.lse[(int64_t)token * p.q_heads + qh] =
+                  l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
+          } else {
+            p.part_m[part] = m;
+            p.part_l[part] = l;
+          }
+        }
+        fence_before();
+      }
+      bar_arrive(&sm.o_empty[t]);
+      parity ^= 1;
+      return true;
+    });
+  } else if (warp < 12) {
+    // ---- loads ----
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    const int i = tid - 256;
+    constexpr int kRaw = FP8 ? D / 16 : D / 8;         // 16-byte chunks of a row in the pool
+    constexpr int kStep = 128 / kRaw, kPer = kKeys / kStep;
+    const int c = i % kRaw, r0 = i / kRaw;
+    uint32_t stage = 0, phase = 1, q_phase = 1, parity = 0;
+    uint64_t *pend[2] = {nullptr, nullptr};  // barriers of copies on their way, the older first
+    auto arrive = [&](uint64_t *b) {
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      bar_arrive(b);
+    };
+    auto sent = [&](uint64_t *b) {  // the copies for b have been issued
+      cp_async_commit();
+      if (pend[0]) {
+        cp_async_wait<2>();
+        arrive(pend[0]);
+      }
+      pend[0] = pend[1], pend[1] = b;
+    };
+    auto flush = [&]() {
+      cp_async_wait<0>();
+      for (int k = 0; k < 2; ++k)
+        if (pend[k]) arrive(pend[k]);
+      pend[0] = pend[1] = nullptr;
+    };
+    // A wait that was given up is not waited for again (see bar_wait_slow): these threads then run
+    // through what is left without waiting, since they meet at barriers of their own.
+    wide_pieces(p, g, [&](const WidePiece &x) {
+      // from where on live rows differ in what they see
+      int least = INT32_MAX;
+      for (int k = i; k < x.rows; k += 128) {
+        const int v = p.limit[row_token(p, x, k)];
+        if (v > x.key0) least = min(least, v);
+      }
+      for (int o = 16; o; o >>= 1) least = min(least, __shfl_xor_sync(~0u, least, o));
+      asm volatile("bar.sync 1, 128;" ::: "memory");  // the piece before is done with sm.off
+      auto look = [&](int tile) -> int64_t {
+        const int pos = x.key0 + tile * kKeys + i;
+        return tile < x.tiles && pos < x.key1
+                   ? attn_key_offset(p, pos < p.prefix_len ? -1 : x.table, pos) + h * p.pool.head_stride : 0;
+      };
+      sm.off[0][i] = look(0);
+      int64_t next = look(1);
+      if (lane == 0) sm.warp_least[warp - 8] = least;
+      wait(&sm.q_empty, q_phase);
+      q_phase ^= 1;
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      least = min(min(sm.warp_least[0], sm.warp_least[1]), min(sm.warp_least[2], sm.warp_least[3]));
+      if (i == 0) sm.least[parity] = least, sm.odd[parity] = 0;
+      asm volatile("bar.sync 1, 128;" ::: "memory");  // odd is 0 before anyone sets it
+      // queries
+      {
+        constexpr int kC = D / 8, kS = 128 / kC;
+        const int cq = i % kC;
+        for (int r = i / kC; r < 256; r += kS) {
+          if (r >= 128 && x.rows <= 128) break;
+          const bool ok = r < x.rows;
+          const int token = ok ? row_token(p, x, r) : 0, member = (x.row0 + r) % p.group;
+          const char *src = p.q + (int64_t)token * p.q_tok + (int64_t)(h * p.group + (ok ? member : 0)) * p.q_head + cq * 16;
+          char *dst = sm.q[r >> 7] + place(r & 127, cq);
+          if (p.q_vec) {
+            cp_async16(smem_u32(dst), src, ok);
+          } else {
+            const uint16_t *u = reinterpret_cast<const uint16_t *>(src);
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = ok ? u[2 * k] | (uint32_t)u[2 * k + 1] << 16 : 0;
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        sent(&sm.q_full);
+      }
+      for (int j = 0; j < x.tiles; ++j) {
+        const int64_t *off = sm.off[j & 1];
+        const int k0 = x.key0 + j * kKeys;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          if (!bar_try(&sm.empty[stage], phase)) {
+            flush();  // nothing that is there is held back meanwhile
+            wait(&sm.empty[stage], phase);
+          }
+          char *dst = sm.kv[stage];
+          const char *plane = (kv ? p.pool.v : p.pool.k) + c * 16;
+          if constexpr (FP8) {
+            uint4 raw[kPer];
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {
+              const int r = r0 + k * kStep;
+              raw[k] = k0 + r < x.key1 ? __ldg(reinterpret_cast<const uint4 *>(plane + off[r])) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {
+              const int r = r0 + k * kStep;
+              const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+              uint32_t o[8];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                o[2 * e] = from_e4m3x2<T>((uint16_t)w[e]);
+                o[2 * e + 1] = from_e4m3x2<T>((uint16_t)(w[e] >> 16));
+              }
+              *reinterpret_cast<uint4 *>(dst + place(r, 2 * c)) = make_uint4(o[0], o[1], o[2], o[3]);
+              *reinterpret_cast<uint4 *>(dst + place(r, 2 * c + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {
+              const int r = r0 + k * kStep;
+              cp_async16(smem_u32(dst) + place(r, c), plane + off[r], k0 + r < x.key1);
+            }
+          }
+          if (kv && k0 + kKeys > least && least < x.key1) {
+            // see attn_narrow_kernel: values that are not finite, where some row's mask falls into
+            // the tile; a thread looks at the chunks that it has copied itself
+            cp_async_commit();
+            cp_async_wait<0>();
+            bool any = false;
+            for (int k = 0; k < kPer * (FP8 ? 2 : 1); ++k) {
+              const int r = r0 + (FP8 ? k >> 1 : k) * kStep;
+              uint4 *v = reinterpret_cast<uint4 *>(dst + place(r, FP8 ? 2 * c + (k & 1) : c));
+              uint32_t w[4] = {v->x, v->y, v->z, v->w};
+              bool here = false;
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (odd2<T>(w[e])) {
+                  if (odd2<T>(w[e] & 0xffffu)) w[e] &= 0xffff0000u;
+                  if (odd2<T>(w[e] & 0xffff0000u)) w[e] &= 0xffffu;
+                  here = true;
+                }
+              if (here) *v = make_uint4(w[0], w[1], w[2], w[3]);
+              any |= here;
+            }
+            if (any) *(volatile int32_t *)&sm.odd[parity] = 1;
+          }
+          sent(&sm.full[stage]);
+          if (++stage == kStages) stage = 0, phase ^= 1;
+        }
+        // the offsets of the next tile, over those of the tile before, which everyone has used
+        sm.off[(j + 1) & 1][i] = next;
+        next = look(j + 2);
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+      }
+      flush();
+      parity ^= 1;
+      return true;
+    });
+    flush();
+  } else {
+    // ---- products ----
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (warp == 12 && lane == 0) {
+      constexpr uint32_t kFmt = std::is_same<T, __half>::value ? 0u : 1u;
+      constexpr uint32_t kBase = 1u << 4 | kFmt << 7 | kFmt << 10 | (128u >> 4) << 24;
+      constexpr uint32_t kDescS = kBase | (uint32_t)(kKeys >> 3) << 17;
+      constexpr uint32_t kDescO = kBase | (uint32_t)(D >> 3) << 17 | 1u << 16;  // V read across its rows
+      uint32_t stage = 0, phase = 0, q_phase = 0, p_phase[2] = {0, 0}, oe_phase = 1;
+      uint64_t qd[2];
+      for (int t = 0; t < 2; ++t) qd[t] = operand(smem_u32(sm.q[t]), 0);
+      auto scores = [&](int t, uint32_t kst) {
+        const uint64_t kd = operand(smem_u32(sm.kv[kst]), 0);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint64_t step = (uint64_t)((k >> 2) * (128 * 128 >> 4) + (k & 3) * 2);
+          mma_ss(tmS[t], qd[t] + step, kd + step, kDescS, k > 0);
+        }
+      };
+      wide_pieces(p, g, [&](const WidePiece &x) {
+        const int tiles = x.tiles, nt = x.rows > 128 ? 2 : 1;
+        if (!wait(&sm.q_full, q_phase) || !wait(&sm.full[stage], phase)) return false;
+        q_phase ^= 1;
+        fence_after();
+        for (int t = 0; t < nt; ++t) {
+          scores(t, stage);
+          mma_commit(&sm.s_full[t]);
+        }
+        mma_commit(&sm.empty[stage]);
+        if (++stage == kStages) stage = 0, phase ^= 1;
+        if (tiles == 1) mma_commit(&sm.q_empty);
+        for (int j = 0; j < tiles; ++j) {
+          const uint32_t vst = stage;
+          if (!wait(&sm.full[vst], phase)) return false;
+          if (++stage == kStages) stage = 0, phase ^= 1;
+          const bool more = j + 1 < tiles;
+          if (more && !wait(&sm.full[stage], phase)) return false;
+          const uint64_t vd = operand(smem_u32(sm.kv[vst]), 128 * 128);
+          for (int t = 0; t < nt; ++t) {
+            if (j == 0 && !wait(&sm.o_empty[t], oe_phase)) return false;
+            if (!wait(&sm.p_full[t], p_phase[t])) return false;
+            p_phase[t] ^= 1;
+            fence_after();
+#pragma unroll
+            for (int k = 0; k < kKeys / 16; ++k)
+              mma_ts(tmO[t], tmS[t] + k * 8, vd + (uint64_t)(k * (16 * 128 >> 4)), kDescO, j > 0 || k > 0);
+            if (more) {
+              scores(t, stage);
+              mma_commit(&sm.s_full[t]);
+            } else {
+              mma_commit(&sm.o_full[t]);
+            }
+          }
+          mma_commit(&sm.empty[vst]);
+          if (more) {
+            mma_commit(&sm.empty[stage]);
+            if (++stage == kStages) stage = 0, phase ^= 1;
+            if (j + 2 == tiles) mma_commit(&sm.q_empty);
+          }
+        }
+        if (nt == 1) {  // keeps the tiles in step
+          if (!wait(&sm.o_empty[1], oe_phase)) return false;
+          mma_commit(&sm.o_full[1]);
+        }
+        oe_phase ^= 1;
+        return true;
+      });
+      if (*(volatile int32_t *)&sm.lost) {  // products in flight end before their memory is given up
+        mma_commit(&sm.drained);
+        for (int i = 0; i < 1 << 16 && !bar_try(&sm.drained, 0); ++i) {}
+      }
+    }
+    __syncwarp();
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == 12)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm) : "memory");
+}
+
+template <typename T, bool FP8, int D>
+cudaError_t launch(const AttnParams &p, cudaStream_t s) {
+  const void *fn = (const void *)attn_wide_kernel<T, FP8, D>;
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<D>) + 1024);
+  if (e != cudaSuccess) return e;
+  void *args[] = {const_cast<AttnParams *>(&p)};
+  return launch_pdl(fn, dim3(p.wide_groups * p.kv_heads), dim3(kThreads), args, s, sizeof(Smem<D>) + 1024);
+}
+
+template <typename T, bool FP8>
+cudaError_t launch_d(const AttnParams &p, cudaStream_t s) {
+  return p.head_dim == 64 ? launch<T, FP8, 64>(p, s) : launch<T, FP8, 128>(p, s);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_wide(const AttnParams &p, int32_t dtype, int32_t io, cudaStream_t s) {
+  if (dtype == KVX_F16) return launch_d<__half, false>(p, s);
+  if (dtype == KVX_BF16) return launch_d<__nv_bfloat16, false>(p, s);
+  if (io == KVX_F16) return launch_d<__half, true>(p, s);
+  return launch_d<__nv_bfloat16, true>(p, s);
+}
+
+}  // namespace kvx
