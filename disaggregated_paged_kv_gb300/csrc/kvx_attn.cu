@@ -32,13 +32,15 @@ __device__ __forceinline__ int64_t block_excl(int64_t x, int64_t *total, int64_t
   __syncthreads();
   if (lane == 31) sm[w] = y;
   __syncthreads();
-  int64_t before = 0, t = 0;
-  for (int i = 0; i < nw; ++i) {
-    if (i < w) before += sm[i];
-    t += sm[i];
+  int64_t z = lane < nw ? sm[lane] : 0;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t u = __shfl_up_sync(~0u, z, d);
+    if (lane >= d) z += u;
   }
-  *total = t;
-  return before + y - x;
+  *total = __shfl_sync(~0u, z, 31);
+  const int64_t before = __shfl_sync(~0u, z, (w + 31) & 31);
+  return (w ? before : 0) + y - x;
 }
 
 // A request's query tokens and length as the kernels use them: clamped into what can be
@@ -274,33 +276,53 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const AttnPa
     i -= k ? n0 : 0;
     return i == 0 ? first[k] : more[k] + i * step[k];
   };
+  // lane i has part i (of 32 at a time); all lanes then add the parts, four columns a lane
   float top = -INFINITY;
   for (int i = lane; i < n; i += 32) top = fmaxf(top, p.part_m[part(i)]);
 #pragma unroll
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
   const float base = top == -INFINITY ? 0.f : top;
-  float l = 0.f;
-  for (int i = 0; i < n; ++i) {
-    const int64_t x = part(i);
-    l = fmaf(exp2f(p.part_m[x] - base), p.part_l[x], l);
-  }
-  const float inv = l == 0.f ? 0.f : p.v_scale / l;
-  for (int d0 = 0; d0 < D; d0 += 128) {
-    float acc[4] = {};
-    for (int i = 0; i < n; ++i) {
-      const int64_t x = part(i);
-      const float f = exp2f(p.part_m[x] - base);
+  constexpr int kCols = KVX_ATTN_MAX_HEAD_DIM / 32;
+  float l = 0.f, acc[kCols] = {};
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const int left = min(32, n - i0);
+    int64_t at = 0;
+    float f = 0.f;
+    if (lane < left) {
+      at = part(i0 + lane);
+      f = exp2f(p.part_m[at] - base);
+      l = fmaf(f, p.part_l[at], l);
+    }
+    if (D == 128) {
+#pragma unroll 4
+      for (int i = 0; i < left; ++i) {
+        const int64_t x = __shfl_sync(~0u, at, i);
+        const float w = __shfl_sync(~0u, f, i);
+        const float4 v = *reinterpret_cast<const float4 *>(p.part_o + x * 128 + lane * 4);
+        acc[0] = fmaf(w, v.x, acc[0]), acc[1] = fmaf(w, v.y, acc[1]);
+        acc[2] = fmaf(w, v.z, acc[2]), acc[3] = fmaf(w, v.w, acc[3]);
+      }
+    } else {
+#pragma unroll 2
+      for (int i = 0; i < left; ++i) {
+        const int64_t x = __shfl_sync(~0u, at, i);
+        const float w = __shfl_sync(~0u, f, i);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int d = d0 + c * 32 + lane;
-        if (d < D) acc[c] = fmaf(f, p.part_o[x * D + d], acc[c]);
+        for (int c = 0; c < kCols; ++c)
+          if (c * 32 + lane < D) acc[c] = fmaf(w, p.part_o[x * D + c * 32 + lane], acc[c]);
       }
     }
+  }
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int d = d0 + c * 32 + lane;
-      if (d < D) put(out + d, l == 0.f ? 0.f : acc[c] * inv);
-    }
+  for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
+  const float inv = l == 0.f ? 0.f : p.v_scale / l;
+  if (D == 128) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) put(out + lane * 4 + c, l == 0.f ? 0.f : acc[c] * inv);
+  } else {
+#pragma unroll
+    for (int c = 0; c < kCols; ++c)
+      if (c * 32 + lane < D) put(out + c * 32 + lane, l == 0.f ? 0.f : acc[c] * inv);
   }
   if (p.lse && lane == 0)
     p.lse[w] = l == 0.f ? -INFINITY : (base + log2f(l)) * 0.693147180559945309f;

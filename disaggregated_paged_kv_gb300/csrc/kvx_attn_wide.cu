@@ -35,6 +35,7 @@ struct Smem {
   alignas(1024) char q[2][128 * D * 2];
   alignas(1024) char kv[kStages][kKeys * D * 2];
   int64_t off[2][kKeys];
+  int64_t q_off[256];  // where the rows' queries are; -1: no row
   uint64_t q_full, q_empty, full[kStages], empty[kStages], s_full[2], p_full[2], o_full[2], o_empty[2], drained;
   // of the piece, by its parity: the least position that a live row does not see, and whether
   // infinities or NaN were taken out of the V tiles from there on
@@ -394,9 +395,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const AttnParams
     wide_pieces(p, g, [&](const WidePiece &x) {
       // from where on live rows differ in what they see
       int least = INT32_MAX;
-      for (int k = i; k < x.rows; k += 128) {
-        const int v = p.limit[row_token(p, x, k)];
-        if (v > x.key0) least = min(least, v);
+      int64_t q_off[2] = {-1, -1};
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int r = i + k * 128;
+        if (r < x.rows) {
+          const int token = row_token(p, x, r), v = p.limit[token];
+          if (v > x.key0) least = min(least, v);
+          q_off[k] = token * p.q_tok + (h * p.group + (x.row0 + r) % p.group) * p.q_head;
+        }
       }
       for (int o = 16; o; o >>= 1) least = min(least, __shfl_xor_sync(~0u, least, o));
       asm volatile("bar.sync 1, 128;" ::: "memory");  // the piece before is done with sm.off
@@ -406,6 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const AttnParams
                    ? attn_key_offset(p, pos < p.prefix_len ? -1 : x.table, pos) + h * p.pool.head_stride : 0;
       };
       sm.off[0][i] = look(0);
+      sm.q_off[i] = q_off[0], sm.q_off[i + 128] = q_off[1];
       int64_t next = look(1);
       if (lane == 0) sm.warp_least[warp - 8] = least;
       wait(&sm.q_empty, q_phase);
@@ -418,11 +426,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const AttnParams
       {
         constexpr int kC = D / 8, kS = 128 / kC;
         const int cq = i % kC;
-        for (int r = i / kC; r < 256; r += kS) {
-          if (r >= 128 && x.rows <= 128) break;
-          const bool ok = r < x.rows;
-          const int token = ok ? row_token(p, x, r) : 0, member = (x.row0 + r) % p.group;
-          const char *src = p.q + (int64_t)token * p.q_tok + (int64_t)(h * p.group + (ok ? member : 0)) * p.q_head + cq * 16;
+#pragma unroll 8
+        for (int r = i / kC; r < (x.rows > 128 ? 256 : 128); r += kS) {
+          const int64_t o = sm.q_off[r];
+          const bool ok = o >= 0;
+          const char *src = p.q + (ok ? o : 0) + cq * 16;
           char *dst = sm.q[r >> 7] + place(r & 127, cq);
           if (p.q_vec) {
             cp_async16(smem_u32(dst), src, ok);
@@ -441,19 +449,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const AttnParams
         const int k0 = x.key0 + j * kKeys;
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
-          if (!bar_try(&sm.empty[stage], phase)) {
-            flush();  // nothing that is there is held back meanwhile
-            wait(&sm.empty[stage], phase);
-          }
-          char *dst = sm.kv[stage];
           const char *plane = (kv ? p.pool.v : p.pool.k) + c * 16;
-          if constexpr (FP8) {
-            uint4 raw[kPer];
+          uint4 raw[FP8 ? kPer : 1];
+          if constexpr (FP8) {  // on their way while the stage is waited for
 #pragma unroll
             for (int k = 0; k < kPer; ++k) {
               const int r = r0 + k * kStep;
               raw[k] = k0 + r < x.key1 ? __ldg(reinterpret_cast<const uint4 *>(plane + off[r])) : make_uint4(0, 0, 0, 0);
             }
+          }
+          if (!bar_try(&sm.empty[stage], phase)) {
+            flush();  // nothing that is there is held back meanwhile
+            wait(&sm.empty[stage], phase);
+          }
+          char *dst = sm.kv[stage];
+          if constexpr (FP8) {
 #pragma unroll
             for (int k = 0; k < kPer; ++k) {
               const int r = r0 + k * kStep;
