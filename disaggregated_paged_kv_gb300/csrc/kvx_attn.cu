@@ -506,7 +506,7 @@ extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_arg
   if (e == cudaSuccess && a.n_q > 0) {
     e = tensor_cores(pool) ? launch_attn_narrow(p, pool->dtype, a.q_dtype, s)
                            : launch_attn_general(p, pool->dtype, a.q_dtype, s);
-    if (e == cudaSuccess && wide) e = launch_attn_wide(p, pool->dtype, a.q_dtype, s);
+    if (e == cudaSuccess && wide) e = launch_attn_wide(p, pool->dtype, a.q_dtype, hnd, s);
     if (e == cudaSuccess) {
       const void *join = a.q_dtype == KVX_F32   ? (const void *)attn_join_kernel<float>
                          : a.q_dtype == KVX_F16 ? (const void *)attn_join_kernel<__half>

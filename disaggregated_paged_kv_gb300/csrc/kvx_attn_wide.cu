@@ -15,6 +15,9 @@
 // A row's sums refer to a maximum that is renewed only when a score passes it by 2^8: the factor
 // between the two cancels in the quotient, weights stay below 2^8 (in range for f16 and bf16), and
 // the sums in tensor memory are rescaled a few times in all instead of with every tile.
+#include <cuda.h>
+
+#include <cstring>
 #include <type_traits>
 
 #include "kvx_attn.cuh"
@@ -26,23 +29,34 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kKeys = kAttnWideKeys;
-constexpr int kStages = 4;      // of one K or V tile each
 constexpr float kRenew = 8.f;
 constexpr uint64_t kWaitNs = 2000000000ull;  // no wait of the kernel is that long unless it is lost
 
-template <int D>
+template <bool FP8, int D>
 struct Smem {
+  static constexpr int kStages = FP8 ? 3 : 4;  // of one K or V tile each, as 16-bit values
+  static constexpr int kRawStages = FP8 ? 3 : 1;
   alignas(1024) char q[2][128 * D * 2];
   alignas(1024) char kv[kStages][kKeys * D * 2];
-  int64_t off[2][kKeys];
-  int64_t q_off[256];  // where the rows' queries are; -1: no row
-  uint64_t q_full, q_empty, full[kStages], empty[kStages], s_full[2], p_full[2], o_full[2], o_empty[2], drained;
+  alignas(128) char raw[kRawStages][FP8 ? kKeys * D : 128];  // 8-bit tiles as they come
+  int64_t off[kKeys];
+  uint64_t q_full, full[kStages], empty[kStages], raw_full[kRawStages];
+  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], drained;
   // of the piece, by its parity: the least position that a live row does not see, and whether
   // infinities or NaN were taken out of the V tiles from there on
   int32_t least[2], odd[2];
   int32_t warp_least[4];
   int32_t lost;
   uint32_t tmem;
+};
+
+// How tiles come by tensor copies: boxes of `rows` consecutive tokens of one page and head.  A
+// plane is seen as rows of elements: [slot][kv heads * head_dim], or [page][kv head][token] rows of
+// head_dim for head-major pages.
+struct WideTma {
+  int32_t rows;       // 0: no tensor copies (pages too short, or too many rows for an index)
+  int32_t head_x;     // a head's first column: head * head_x
+  int64_t page_y, head_y;  // row of (page, head, token): page * page_y + head * head_y + token
 };
 
 // ---- barriers ------------------------------------------------------------------------------
@@ -57,6 +71,13 @@ __device__ __forceinline__ bool bar_try(uint64_t *b, uint32_t parity) {
   asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
                : "=r"(ok) : "r"(smem_u32(b)), "r"(parity) : "memory");
   return ok != 0;
+}
+__device__ __forceinline__ void bar_expect(uint64_t *b, int bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared.b64 _, [%0], %1;" ::"r"(smem_u32(b)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void tma_load(void *dst, const CUtensorMap *map, int x, int y, uint64_t *b) {
+  asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+               ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_u32(b)) : "memory");
 }
 __device__ __forceinline__ uint64_t now_ns() {
   uint64_t t;
@@ -176,13 +197,17 @@ __device__ __forceinline__ int row_token(const AttnParams &p, const WidePiece &x
 }
 
 template <typename T, bool FP8, int D>
-__global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(kThreads, 1)
+attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ WideTma tma,
+                 const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
   extern __shared__ char raw_smem[];
-  Smem<D> &sm = *reinterpret_cast<Smem<D> *>(raw_smem + (-smem_u32(raw_smem) & 1023));
+  using S = Smem<FP8, D>;
+  constexpr int kStages = S::kStages;
+  S &sm = *reinterpret_cast<S *>(raw_smem + (-smem_u32(raw_smem) & 1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
-    bar_init(&sm.q_full, 128);
-    bar_init(&sm.q_empty, 1);
+    bar_init(&sm.q_full, 256);
+    for (int i = 0; i < S::kRawStages; ++i) bar_init(&sm.raw_full[i], 1);
     for (int i = 0; i < kStages; ++i) bar_init(&sm.full[i], 128), bar_init(&sm.empty[i], 1);
     for (int i = 0; i < 2; ++i) {
       bar_init(&sm.s_full[i], 1), bar_init(&sm.p_full[i], 128);
@@ -221,6 +246,30 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const AttnParams
       const int token = live ? row_token(p, x, i) : 0;
       const int lim = live ? min(p.limit[token], x.key1) : 0;
       const int member = (x.row0 + i) % p.group;
+      if (active) {  // this row's queries; the products of the piece before are done with the last
+        const char *src = p.q + token * p.q_tok + (int64_t)(h * p.group + member) * p.q_head;
+#pragma unroll 1
+        for (int c0 = 0; c0 < D / 8; c0 += 8) {
+          uint4 w[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            w[c] = make_uint4(0, 0, 0, 0);
+            if (live && p.q_vec) w[c] = *reinterpret_cast<const uint4 *>(src + (c0 + c) * 16);
+          }
+          if (live && !p.q_vec) {
+            const uint16_t *u = reinterpret_cast<const uint16_t *>(src) + c0 * 8;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              w[c].x = u[8 * c] | (uint32_t)u[8 * c + 1] << 16, w[c].y = u[8 * c + 2] | (uint32_t)u[8 * c + 3] << 16;
+              w[c].z = u[8 * c + 4] | (uint32_t)u[8 * c + 5] << 16, w[c].w = u[8 * c + 6] | (uint32_t)u[8 * c + 7] << 16;
+            }
+          }
+#pragma unroll
+          for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(sm.q[t] + place(r, c0 + c)) = w[c];
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      }
+      bar_arrive(&sm.q_full);
       float m = -INFINITY;
       float2 l2 = make_float2(0.f, 0.f);
       if (active) {
@@ -293,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const AttnParams
         const float inv = l == 0.f ? 0.f : p.v_scale / l;
         T *out = reinterpret_cast<T *>(p.out + (int64_t)token * p.out_tok + (int64_t)qh * p.out_head);
         const int odd = *(volatile int32_t *)&sm.odd[parity], least = *(volatile int32_t *)&sm.least[parity];
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
           __syncwarp();
@@ -340,11 +389,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const AttnParams
               }
             }
           } else {
-            float4 *d = reinterpret_cast<float4 *>(p.part_o + part * D + c * 32);
+            float *d = p.part_o + part * D + c * 32;
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              d[k] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
-                                 __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+            for (int k = 0; k < 32; k += 8)  // whole sectors
+              asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(d + k), "r"(o[k]),
+                           "r"(o[k + 1]), "r"(o[k + 2]), "r"(o[k + 3]), "r"(o[k + 4]), "r"(o[k + 5]),
+                           "r"(o[k + 6]), "r"(o[k + 7]) : "memory");
           }
         }
         if (live) {
@@ -370,11 +420,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const AttnParams
     constexpr int kRaw = FP8 ? D / 16 : D / 8;         // 16-byte chunks of a row in the pool
     constexpr int kStep = 128 / kRaw, kPer = kKeys / kStep;
     const int c = i % kRaw, r0 = i / kRaw;
-    uint32_t stage = 0, phase = 1, q_phase = 1, parity = 0;
+    uint32_t stage = 0, phase = 1, parity = 0, raw_in = 0, raw_out = 0, raw_phase = 0;
     uint64_t *pend[2] = {nullptr, nullptr};  // barriers of copies on their way, the older first
     auto arrive = [&](uint64_t *b) {
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       bar_arrive(b);
+    };
+    auto flush = [&]() {
+      if (pend[0]) {
+        cp_async_wait<1>();
+        arrive(pend[0]);
+      }
+      if (pend[1]) {
+        cp_async_wait<0>();
+        arrive(pend[1]);
+      }
+      pend[0] = pend[1] = nullptr;
     };
     auto sent = [&](uint64_t *b) {  // the copies for b have been issued
       cp_async_commit();
@@ -384,78 +445,115 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const AttnParams
       }
       pend[0] = pend[1], pend[1] = b;
     };
-    auto flush = [&]() {
-      cp_async_wait<0>();
-      for (int k = 0; k < 2; ++k)
-        if (pend[k]) arrive(pend[k]);
-      pend[0] = pend[1] = nullptr;
-    };
     // A wait that was given up is not waited for again (see bar_wait_slow): these threads then run
     // through what is left without waiting, since they meet at barriers of their own.
     wide_pieces(p, g, [&](const WidePiece &x) {
       // from where on live rows differ in what they see
       int least = INT32_MAX;
-      int64_t q_off[2] = {-1, -1};
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int r = i + k * 128;
-        if (r < x.rows) {
-          const int token = row_token(p, x, r), v = p.limit[token];
-          if (v > x.key0) least = min(least, v);
-          q_off[k] = token * p.q_tok + (h * p.group + (x.row0 + r) % p.group) * p.q_head;
-        }
+        const int v = r < x.rows ? p.limit[row_token(p, x, r)] : 0;
+        if (v > x.key0) least = min(least, v);
       }
       for (int o = 16; o; o >>= 1) least = min(least, __shfl_xor_sync(~0u, least, o));
-      asm volatile("bar.sync 1, 128;" ::: "memory");  // the piece before is done with sm.off
-      auto look = [&](int tile) -> int64_t {
-        const int pos = x.key0 + tile * kKeys + i;
-        return tile < x.tiles && pos < x.key1
-                   ? attn_key_offset(p, pos < p.prefix_len ? -1 : x.table, pos) + h * p.pool.head_stride : 0;
-      };
-      sm.off[0][i] = look(0);
-      sm.q_off[i] = q_off[0], sm.q_off[i + 128] = q_off[1];
-      int64_t next = look(1);
       if (lane == 0) sm.warp_least[warp - 8] = least;
-      wait(&sm.q_empty, q_phase);
-      q_phase ^= 1;
       asm volatile("bar.sync 1, 128;" ::: "memory");
       least = min(min(sm.warp_least[0], sm.warp_least[1]), min(sm.warp_least[2], sm.warp_least[3]));
+      if (least >= x.key1) least = INT32_MAX;
       if (i == 0) sm.least[parity] = least, sm.odd[parity] = 0;
       asm volatile("bar.sync 1, 128;" ::: "memory");  // odd is 0 before anyone sets it
-      // queries
-      {
-        constexpr int kC = D / 8, kS = 128 / kC;
-        const int cq = i % kC;
-#pragma unroll 8
-        for (int r = i / kC; r < (x.rows > 128 ? 256 : 128); r += kS) {
-          const int64_t o = sm.q_off[r];
-          const bool ok = o >= 0;
-          const char *src = p.q + (ok ? o : 0) + cq * 16;
-          char *dst = sm.q[r >> 7] + place(r & 127, cq);
-          if (p.q_vec) {
-            cp_async16(smem_u32(dst), src, ok);
+
+      // a tile that tensor copies can bring: whole, the same for all live rows, and no box of it
+      // partly in the prefix
+      auto regular = [&](int j) {
+        const int k0 = x.key0 + j * kKeys;
+        return tma.rows > 0 && k0 + kKeys <= x.key1 && k0 + kKeys <= least &&
+               (k0 >= p.prefix_len || k0 + kKeys <= p.prefix_len || p.prefix_len % tma.rows == 0);
+      };
+      const int boxes = tma.rows > 0 ? kKeys / tma.rows : 1;
+      // page look-ups: lane l of the first warp has boxes l, l + 32, ... of a regular tile
+      auto row_of = [&](int pos) -> int {
+        int pg, off;
+        if (p.pool.page_shift >= 0) pg = pos >> p.pool.page_shift, off = pos & (p.page_size - 1);
+        else pg = pos / p.page_size, off = pos - pg * p.page_size;
+        return (int)(attn_page(p, pos < p.prefix_len ? -1 : x.table, pg) * tma.page_y + h * tma.head_y + off);
+      };
+      auto look = [&](int j) -> int64_t {  // of any tile, key by key
+        const int pos = x.key0 + j * kKeys + i;
+        return pos < x.key1
+                   ? attn_key_offset(p, pos < p.prefix_len ? -1 : x.table, pos) + h * p.pool.head_stride : 0;
+      };
+      auto box0 = [&](int j) -> int {  // row of this lane's first box
+        return warp == 8 && j < x.tiles && regular(j) && lane < boxes
+                   ? row_of(x.key0 + j * kKeys + lane * tma.rows) : 0;
+      };
+      // The raw or 16-bit tile (kv: 0 K, 1 V) of tile j, by the first warp.
+      auto tensor = [&](int j, int kv, int row, char *dst, uint64_t *bar) {
+        const CUtensorMap *map = kv ? &v_map : &k_map;
+        if (lane == 0) bar_expect(bar, kKeys * D * (FP8 ? 1 : 2));
+        __syncwarp();
+        for (int b = lane; b < boxes; b += 32) {
+          if (b != lane) row = row_of(x.key0 + j * kKeys + b * tma.rows);
+          if constexpr (FP8) {
+            tma_load(dst + b * tma.rows * D, map, h * tma.head_x, row, bar);
           } else {
-            const uint16_t *u = reinterpret_cast<const uint16_t *>(src);
-            uint32_t w[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) w[k] = ok ? u[2 * k] | (uint32_t)u[2 * k + 1] << 16 : 0;
-            *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int half = 0; half < D / 64; ++half)
+              tma_load(dst + half * kKeys * 128 + b * tma.rows * 128, map, h * tma.head_x + half * 64, row, bar);
           }
         }
-        sent(&sm.q_full);
-      }
-      for (int j = 0; j < x.tiles; ++j) {
-        const int64_t *off = sm.off[j & 1];
-        const int k0 = x.key0 + j * kKeys;
+      };
+      auto convert = [&](const uint4 &v, char *dst, int r) {  // 16 8-bit values to their places
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t o[8];
 #pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          o[2 * e] = from_e4m3x2<T>((uint16_t)w[e]);
+          o[2 * e + 1] = from_e4m3x2<T>((uint16_t)(w[e] >> 16));
+        }
+        *reinterpret_cast<uint4 *>(dst + place(r, 2 * c)) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4 *>(dst + place(r, 2 * c + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+      };
+
+      // 8-bit tiles come by tensor copies some stages ahead of their conversion
+      int ahead = 0, ahead_row = box0(0);
+      auto fetch = [&](int upto) {  // up to tile and half number `upto`
+        for (; ahead < min(upto, 2 * x.tiles); ++ahead) {
+          if (regular(ahead >> 1)) {
+            if (warp == 8) tensor(ahead >> 1, ahead & 1, ahead_row, sm.raw[raw_in], &sm.raw_full[raw_in]);
+            if (++raw_in == S::kRawStages) raw_in = 0;
+          }
+          if (ahead & 1) ahead_row = box0((ahead + 1) >> 1);
+        }
+      };
+      int next_row = FP8 ? 0 : box0(0);
+      for (int j = 0; j < x.tiles; ++j) {
+        const int k0 = x.key0 + j * kKeys;
+        const bool reg = regular(j);
+        const int row = next_row;
+        if constexpr (!FP8) next_row = box0(j + 1);
+        if (!reg) {
+          // key by key; the tile that used these offsets before is done with by everyone
+          const int64_t o = look(j);
+          asm volatile("bar.sync 1, 128;" ::: "memory");
+          sm.off[i] = o;
+          asm volatile("bar.sync 1, 128;" ::: "memory");
+        }
+        const int64_t *off = sm.off;
+#pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {
           const char *plane = (kv ? p.pool.v : p.pool.k) + c * 16;
           uint4 raw[FP8 ? kPer : 1];
-          if constexpr (FP8) {  // on their way while the stage is waited for
+          if constexpr (FP8) {
+            if (reg) {
+              fetch(2 * j + kv + S::kRawStages);
+            } else {
 #pragma unroll
-            for (int k = 0; k < kPer; ++k) {
-              const int r = r0 + k * kStep;
-              raw[k] = k0 + r < x.key1 ? __ldg(reinterpret_cast<const uint4 *>(plane + off[r])) : make_uint4(0, 0, 0, 0);
+              for (int k = 0; k < kPer; ++k) {
+                const int r = r0 + k * kStep;
+                raw[k] = k0 + r < x.key1 ? __ldg(reinterpret_cast<const uint4 *>(plane + off[r])) : make_uint4(0, 0, 0, 0);
+              }
             }
           }
           if (!bar_try(&sm.empty[stage], phase)) {
@@ -464,19 +562,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const AttnParams
           }
           char *dst = sm.kv[stage];
           if constexpr (FP8) {
+            if (reg) {
+              wait(&sm.raw_full[raw_out], raw_phase);
 #pragma unroll
-            for (int k = 0; k < kPer; ++k) {
-              const int r = r0 + k * kStep;
-              const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
-              uint32_t o[8];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                o[2 * e] = from_e4m3x2<T>((uint16_t)w[e]);
-                o[2 * e + 1] = from_e4m3x2<T>((uint16_t)(w[e] >> 16));
-              }
-              *reinterpret_cast<uint4 *>(dst + place(r, 2 * c)) = make_uint4(o[0], o[1], o[2], o[3]);
-              *reinterpret_cast<uint4 *>(dst + place(r, 2 * c + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+              for (int k = 0; k < kPer; ++k)
+                raw[k] = *reinterpret_cast<const uint4 *>(sm.raw[raw_out] + (r0 + k * kStep) * D + c * 16);
+              asm volatile("bar.sync 1, 128;" ::: "memory");  // the raw stage may be filled again
+              if (++raw_out == S::kRawStages) raw_out = 0, raw_phase ^= 1;
             }
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) convert(raw[k], dst, r0 + k * kStep);
+          } else if (reg) {
+            flush();
+            if (warp == 8) tensor(j, kv, row, dst, &sm.full[stage]);
+            if (i != 0) bar_arrive(&sm.full[stage]);
           } else {
 #pragma unroll
             for (int k = 0; k < kPer; ++k) {
@@ -484,12 +583,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const AttnParams
               cp_async16(smem_u32(dst) + place(r, c), plane + off[r], k0 + r < x.key1);
             }
           }
-          if (kv && k0 + kKeys > least && least < x.key1) {
+          if (kv && k0 + kKeys > least) {
             // see attn_narrow_kernel: values that are not finite, where some row's mask falls into
             // the tile; a thread looks at the chunks that it has copied itself
             cp_async_commit();
             cp_async_wait<0>();
             bool any = false;
+#pragma unroll 1
             for (int k = 0; k < kPer * (FP8 ? 2 : 1); ++k) {
               const int r = r0 + (FP8 ? k >> 1 : k) * kStep;
               uint4 *v = reinterpret_cast<uint4 *>(dst + place(r, FP8 ? 2 * c + (k & 1) : c));
@@ -507,19 +607,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const AttnParams
             }
             if (any) *(volatile int32_t *)&sm.odd[parity] = 1;
           }
-          sent(&sm.full[stage]);
+          if (FP8) arrive(&sm.full[stage]);
+          else if (!reg) sent(&sm.full[stage]);
           if (++stage == kStages) stage = 0, phase ^= 1;
         }
-        // the offsets of the next tile, over those of the tile before, which everyone has used
-        sm.off[(j + 1) & 1][i] = next;
-        next = look(j + 2);
-        asm volatile("bar.sync 1, 128;" ::: "memory");
       }
       flush();
+      asm volatile("bar.sync 1, 128;" ::: "memory");  // everyone has read warp_least
       parity ^= 1;
       return true;
     });
-    flush();
   } else {
     // ---- products ----
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
@@ -550,7 +647,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const AttnParams
         }
         mma_commit(&sm.empty[stage]);
         if (++stage == kStages) stage = 0, phase ^= 1;
-        if (tiles == 1) mma_commit(&sm.q_empty);
         for (int j = 0; j < tiles; ++j) {
           const uint32_t vst = stage;
           if (!wait(&sm.full[vst], phase)) return false;
@@ -577,7 +673,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const AttnParams
           if (more) {
             mma_commit(&sm.empty[stage]);
             if (++stage == kStages) stage = 0, phase ^= 1;
-            if (j + 2 == tiles) mma_commit(&sm.q_empty);
           }
         }
         if (nt == 1) {  // keeps the tiles in step
@@ -601,27 +696,80 @@ __global__ void __launch_bounds__(kThreads, 1) attn_wide_kernel(const AttnParams
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm) : "memory");
 }
 
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
+                              CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                              CUtensorMapFloatOOBfill);
+
+EncodeFn encoder() {
+  static const EncodeFn fn = [] {
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess) {
+      (void)cudaGetLastError();
+      f = nullptr;
+    }
+    return reinterpret_cast<EncodeFn>(f);
+  }();
+  return fn;
+}
+
+// The planes as rows of elements (see WideTma).  Boxes need pages of at least kMinBox tokens in a
+// row; without them, or with more rows than an index counts, the tiles come key by key.
+constexpr int kMinBox = 4;
+
+void make_tma(const AttnParams &p, bool fp8, bool hnd, WideTma *t, CUtensorMap *km, CUtensorMap *vm) {
+  int rows = kKeys;
+  while (p.page_size % rows != 0) rows >>= 1;
+  const int64_t pages = p.pool.num_pages, D = p.head_dim;
+  const int64_t all = hnd ? pages * p.kv_heads * p.page_size : pages * p.page_size;
+  *t = WideTma{};
+  if (rows < kMinBox || all > INT32_MAX || !encoder()) return;
+  const cuuint64_t dims[2] = {(cuuint64_t)(hnd ? D : D * p.kv_heads), (cuuint64_t)all};
+  const cuuint64_t strides[1] = {(cuuint64_t)p.pool.tok_stride};
+  const cuuint32_t box[2] = {(cuuint32_t)(fp8 ? D : 64), (cuuint32_t)rows}, one[2] = {1, 1};
+  for (int kv = 0; kv < 2; ++kv)
+    if (encoder()(kv ? vm : km, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2,
+                  const_cast<char *>(kv ? p.pool.v : p.pool.k), dims, strides, box, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  fp8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return;
+  t->rows = rows;
+  t->head_x = hnd ? 0 : (int32_t)D;
+  t->page_y = hnd ? (int64_t)p.kv_heads * p.page_size : p.page_size;
+  t->head_y = hnd ? p.page_size : 0;
+}
+
 template <typename T, bool FP8, int D>
-cudaError_t launch(const AttnParams &p, cudaStream_t s) {
+cudaError_t launch(const AttnParams &p, bool hnd, cudaStream_t s) {
   const void *fn = (const void *)attn_wide_kernel<T, FP8, D>;
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<D>) + 1024);
+  constexpr int kSmem = (int)sizeof(Smem<FP8, D>) + 1024;
+  static_assert(kSmem <= 227 * 1024, "shared memory of one SM");
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  void *args[] = {const_cast<AttnParams *>(&p)};
-  return launch_pdl(fn, dim3(p.wide_groups * p.kv_heads), dim3(kThreads), args, s, sizeof(Smem<D>) + 1024);
+  WideTma tma;
+  CUtensorMap km, vm;
+  std::memset(&km, 0, sizeof(km));
+  std::memset(&vm, 0, sizeof(vm));
+  make_tma(p, FP8, hnd, &tma, &km, &vm);
+  void *args[] = {const_cast<AttnParams *>(&p), &tma, &km, &vm};
+  return launch_pdl(fn, dim3(p.wide_groups * p.kv_heads), dim3(kThreads), args, s, kSmem);
 }
 
 template <typename T, bool FP8>
-cudaError_t launch_d(const AttnParams &p, cudaStream_t s) {
-  return p.head_dim == 64 ? launch<T, FP8, 64>(p, s) : launch<T, FP8, 128>(p, s);
+cudaError_t launch_d(const AttnParams &p, bool hnd, cudaStream_t s) {
+  return p.head_dim == 64 ? launch<T, FP8, 64>(p, hnd, s) : launch<T, FP8, 128>(p, hnd, s);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_wide(const AttnParams &p, int32_t dtype, int32_t io, cudaStream_t s) {
-  if (dtype == KVX_F16) return launch_d<__half, false>(p, s);
-  if (dtype == KVX_BF16) return launch_d<__nv_bfloat16, false>(p, s);
-  if (io == KVX_F16) return launch_d<__half, true>(p, s);
-  return launch_d<__nv_bfloat16, true>(p, s);
+cudaError_t launch_attn_wide(const AttnParams &p, int32_t dtype, int32_t io, bool hnd, cudaStream_t s) {
+  if (dtype == KVX_F16) return launch_d<__half, false>(p, hnd, s);
+  if (dtype == KVX_BF16) return launch_d<__nv_bfloat16, false>(p, hnd, s);
+  if (io == KVX_F16) return launch_d<__half, true>(p, hnd, s);
+  return launch_d<__nv_bfloat16, true>(p, hnd, s);
 }
 
 }  // namespace kvx

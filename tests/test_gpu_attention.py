@@ -100,6 +100,32 @@ def test_many_requests(dtype, D):
     run(ar.make(dtype, "planes", 16, 2, 7, D, lens=lens, prefix=1000, layers=1, layer=0))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "fp8"])
+@pytest.mark.parametrize("kind,page", [("planes", 1), ("planes", 4), ("slots", 8), ("hnd", 16),
+                                       ("planes", 24), ("slots", 64), ("hnd", 128), ("hnd", 3)])
+@pytest.mark.parametrize("prefix", [384, 517])
+def test_many_rows_by_page_size(dtype, kind, page, prefix):
+    """Tiles of many rows over whole pages, parts of pages, and a prefix that ends inside one."""
+    lens = [prefix + 1 + 29 * (i % 5) for i in range(40)]
+    run(ar.make(dtype, kind, page, 2, 4, 64 if page == 8 else 128, lens=lens, prefix=prefix,
+                layers=2, layer=1, seed=page))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("kind,page,prefix", [("planes", 16, 300), ("hnd", 32, 512), ("slots", 2, 260),
+                                              ("planes", 64, 0)])
+def test_prompts_by_page_size(dtype, kind, page, prefix):
+    """Prompts walk from the prefix's pages into their own inside a tile of keys."""
+    q = [200, 1, 77, 150]
+    run(ar.make(dtype, kind, page, 2, 4, 128, lens=[prefix + 200, prefix + 50, prefix + 377, prefix + 150],
+                qlens=q, prefix=prefix, seed=page))
+
+
+def test_prompts_among_padding_and_single_tokens():
+    run(ar.make("f16", "planes", 16, 2, 8, 64, lens=[0, 700, 301, 0, 640, 333, 299],
+                qlens=[1, 300, 1, 40, 5, 33, 60], prefix=300))
+
+
 def test_long_and_short_together():
     run(ar.make("bf16", "planes", 16, 1, 4, 128, lens=[9000, 1, 30, 4000], prefix=0, layers=1, layer=0))
 
