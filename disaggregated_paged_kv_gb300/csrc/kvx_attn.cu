@@ -482,7 +482,10 @@ extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_arg
   p.max_pages = a.max_pages;
   p.prefix_len = a.prefix_len;
   p.row_tile = row_tile(pool);
-  p.q_even = ((uintptr_t)a.q | (uintptr_t)p.q_tok | (uintptr_t)p.q_head) % 4 == 0;
+  const uintptr_t q_at = (uintptr_t)a.q | (uintptr_t)p.q_tok | (uintptr_t)p.q_head;
+  p.q_even = q_at % 4 == 0;
+  p.q_vec = q_at % 16 == 0;
+  p.out_vec = ((uintptr_t)a.out | (uintptr_t)p.out_tok | (uintptr_t)p.out_head) % 16 == 0;
   p.groups = z.groups;
   p.wide_groups = z.wide_groups;
   char *ws = static_cast<char *>(d_ws);

@@ -50,13 +50,13 @@ struct Smem {
   uint32_t tmem;
 };
 
-// How tiles come by tensor copies: boxes of `rows` consecutive tokens of one page and head.  A
-// plane is seen as rows of elements: [slot][kv heads * head_dim], or [page][kv head][token] rows of
-// head_dim for head-major pages.
+// How tiles come by tensor copies: boxes of `rows` (a multiple of 8) consecutive tokens of one page
+// and head.  A plane is seen as [group of 8 tokens][block of 64 16-bit columns][token][column] (8-bit
+// pools: [token][column]), so that a box arrives as the matrix operand's own arrangement.
 struct WideTma {
   int32_t rows;       // 0: no tensor copies (pages too short, or too many rows for an index)
-  int32_t head_x;     // a head's first column: head * head_x
-  int64_t page_y, head_y;  // row of (page, head, token): page * page_y + head * head_y + token
+  int32_t head_x;     // a head's first block (8-bit pools: column): head * head_x
+  int64_t page_y, head_y;  // first token of (page, head): page * page_y + head * head_y
 };
 
 // ---- barriers ------------------------------------------------------------------------------
@@ -74,6 +74,10 @@ __device__ __forceinline__ bool bar_try(uint64_t *b, uint32_t parity) {
 }
 __device__ __forceinline__ void bar_expect(uint64_t *b, int bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared.b64 _, [%0], %1;" ::"r"(smem_u32(b)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void tma_load4(void *dst, const CUtensorMap *map, int z, int y, uint64_t *b) {
+  asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+               ::"r"(smem_u32(dst)), "l"(map), "r"(0), "r"(0), "r"(z), "r"(y), "r"(smem_u32(b)) : "memory");
 }
 __device__ __forceinline__ void tma_load(void *dst, const CUtensorMap *map, int x, int y, uint64_t *b) {
   asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
@@ -148,17 +152,19 @@ __device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t (&r)[16]) {
       : "memory");
 }
 
-// A matrix operand in shared memory: rows of 128 bytes, 16-byte chunks exchanged by the row's low
-// three bits (128-byte swizzle), groups of eight rows 1024 bytes apart.  lead: bytes between the
-// blocks of 64 columns, for the operand that is read across its rows.
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead) {
-  return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+// A matrix operand in shared memory, D 16-bit columns a row: groups of eight rows, in them blocks of
+// 64 columns, in them eight rows of 128 bytes whose 16-byte chunks are exchanged by the row (128-byte
+// swizzle).  So eight rows are D * 16 bytes, blocks 1024 bytes apart.
+template <int D>
+__device__ __forceinline__ uint64_t operand(uint32_t addr) {
+  return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(1024 >> 4) << 16 | (uint64_t)(D * 16 >> 4) << 32 |
          1ull << 46 | 2ull << 61;
 }
 
-// Byte place of 16-byte chunk c (of D / 8) of row r in a tile of 128 rows kept as such blocks.
+// Byte place of 16-byte chunk c (of D / 8) of row r.
+template <int D>
 __device__ __forceinline__ uint32_t place(int r, int c) {
-  return (uint32_t)((c >> 3) * 128 * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+  return (uint32_t)((r >> 3) * (D * 16) + (c >> 3) * 1024 + (r & 7) * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
 struct WidePiece {
@@ -265,7 +271,7 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ W
             }
           }
 #pragma unroll
-          for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(sm.q[t] + place(r, c0 + c)) = w[c];
+          for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(sm.q[t] + place<D>(r, c0 + c)) = w[c];
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
@@ -471,8 +477,8 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ W
         return tma.rows > 0 && k0 + kKeys <= x.key1 && k0 + kKeys <= least &&
                (k0 >= p.prefix_len || k0 + kKeys <= p.prefix_len || p.prefix_len % tma.rows == 0);
       };
-      const int boxes = tma.rows > 0 ? kKeys / tma.rows : 1;
-      // page look-ups: lane l of the first warp has boxes l, l + 32, ... of a regular tile
+      const int boxes = tma.rows > 0 ? kKeys / tma.rows : 1, pw = warp - 8;
+      // page look-ups: lane l of warp w has box 4 l + w of a regular tile
       auto row_of = [&](int pos) -> int {
         int pg, off;
         if (p.pool.page_shift >= 0) pg = pos >> p.pool.page_shift, off = pos & (p.page_size - 1);
@@ -484,24 +490,17 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ W
         return pos < x.key1
                    ? attn_key_offset(p, pos < p.prefix_len ? -1 : x.table, pos) + h * p.pool.head_stride : 0;
       };
-      auto box0 = [&](int j) -> int {  // row of this lane's first box
-        return warp == 8 && j < x.tiles && regular(j) && lane < boxes
-                   ? row_of(x.key0 + j * kKeys + lane * tma.rows) : 0;
+      auto box0 = [&](int j) -> int {  // row of this lane's box
+        return j < x.tiles && regular(j) && lane * 4 + pw < boxes
+                   ? row_of(x.key0 + j * kKeys + (lane * 4 + pw) * tma.rows) : 0;
       };
-      // The raw or 16-bit tile (kv: 0 K, 1 V) of tile j, by the first warp.
-      auto tensor = [&](int j, int kv, int row, char *dst, uint64_t *bar) {
+      // this lane's box of K (kv 0) or V (1); a lane of each warp at most has work for short tiles
+      auto tensor = [&](int kv, int row, char *dst, uint64_t *bar) {
         const CUtensorMap *map = kv ? &v_map : &k_map;
-        if (lane == 0) bar_expect(bar, kKeys * D * (FP8 ? 1 : 2));
-        __syncwarp();
-        for (int b = lane; b < boxes; b += 32) {
-          if (b != lane) row = row_of(x.key0 + j * kKeys + b * tma.rows);
-          if constexpr (FP8) {
-            tma_load(dst + b * tma.rows * D, map, h * tma.head_x, row, bar);
-          } else {
-#pragma unroll
-            for (int half = 0; half < D / 64; ++half)
-              tma_load(dst + half * kKeys * 128 + b * tma.rows * 128, map, h * tma.head_x + half * 64, row, bar);
-          }
+        const int b = lane * 4 + pw;
+        if (b < boxes) {
+          if constexpr (FP8) tma_load(dst + b * tma.rows * D, map, h * tma.head_x, row, bar);
+          else tma_load4(dst + b * tma.rows * D * 2, map, h * tma.head_x, row >> 3, bar);
         }
       };
       auto convert = [&](const uint4 &v, char *dst, int r) {  // 16 8-bit values to their places
@@ -512,8 +511,8 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ W
           o[2 * e] = from_e4m3x2<T>((uint16_t)w[e]);
           o[2 * e + 1] = from_e4m3x2<T>((uint16_t)(w[e] >> 16));
         }
-        *reinterpret_cast<uint4 *>(dst + place(r, 2 * c)) = make_uint4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<uint4 *>(dst + place(r, 2 * c + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+        *reinterpret_cast<uint4 *>(dst + place<D>(r, 2 * c)) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4 *>(dst + place<D>(r, 2 * c + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
       };
 
       // 8-bit tiles come by tensor copies some stages ahead of their conversion
@@ -521,7 +520,8 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ W
       auto fetch = [&](int upto) {  // up to tile and half number `upto`
         for (; ahead < min(upto, 2 * x.tiles); ++ahead) {
           if (regular(ahead >> 1)) {
-            if (warp == 8) tensor(ahead >> 1, ahead & 1, ahead_row, sm.raw[raw_in], &sm.raw_full[raw_in]);
+            if (i == 0) bar_expect(&sm.raw_full[raw_in], kKeys * D);
+            tensor(ahead & 1, ahead_row, sm.raw[raw_in], &sm.raw_full[raw_in]);
             if (++raw_in == S::kRawStages) raw_in = 0;
           }
           if (ahead & 1) ahead_row = box0((ahead + 1) >> 1);
@@ -574,13 +574,16 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ W
             for (int k = 0; k < kPer; ++k) convert(raw[k], dst, r0 + k * kStep);
           } else if (reg) {
             flush();
-            if (warp == 8) tensor(j, kv, row, dst, &sm.full[stage]);
+            // one arrival for the tile's bytes and one for each thread's boxes: those of a thread may
+            // arrive before the bytes are announced, the stage is not full before the thread is
+            if (i == 0) bar_expect(&sm.full[stage], kKeys * D * 2);
+            tensor(kv, row, dst, &sm.full[stage]);
             if (i != 0) bar_arrive(&sm.full[stage]);
           } else {
 #pragma unroll
             for (int k = 0; k < kPer; ++k) {
               const int r = r0 + k * kStep;
-              cp_async16(smem_u32(dst) + place(r, c), plane + off[r], k0 + r < x.key1);
+              cp_async16(smem_u32(dst) + place<D>(r, c), plane + off[r], k0 + r < x.key1);
             }
           }
           if (kv && k0 + kKeys > least) {
@@ -592,7 +595,7 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ W
 #pragma unroll 1
             for (int k = 0; k < kPer * (FP8 ? 2 : 1); ++k) {
               const int r = r0 + (FP8 ? k >> 1 : k) * kStep;
-              uint4 *v = reinterpret_cast<uint4 *>(dst + place(r, FP8 ? 2 * c + (k & 1) : c));
+              uint4 *v = reinterpret_cast<uint4 *>(dst + place<D>(r, FP8 ? 2 * c + (k & 1) : c));
               uint32_t w[4] = {v->x, v->y, v->z, v->w};
               bool here = false;
 #pragma unroll
@@ -627,12 +630,12 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ W
       constexpr uint32_t kDescO = kBase | (uint32_t)(D >> 3) << 17 | 1u << 16;  // V read across its rows
       uint32_t stage = 0, phase = 0, q_phase = 0, p_phase[2] = {0, 0}, oe_phase = 1;
       uint64_t qd[2];
-      for (int t = 0; t < 2; ++t) qd[t] = operand(smem_u32(sm.q[t]), 0);
+      for (int t = 0; t < 2; ++t) qd[t] = operand<D>(smem_u32(sm.q[t]));
       auto scores = [&](int t, uint32_t kst) {
-        const uint64_t kd = operand(smem_u32(sm.kv[kst]), 0);
+        const uint64_t kd = operand<D>(smem_u32(sm.kv[kst]));
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          const uint64_t step = (uint64_t)((k >> 2) * (128 * 128 >> 4) + (k & 3) * 2);
+          const uint64_t step = (uint64_t)((k >> 2) * (1024 >> 4) + (k & 3) * 2);
           mma_ss(tmS[t], qd[t] + step, kd + step, kDescS, k > 0);
         }
       };
@@ -653,7 +656,7 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ W
           if (++stage == kStages) stage = 0, phase ^= 1;
           const bool more = j + 1 < tiles;
           if (more && !wait(&sm.full[stage], phase)) return false;
-          const uint64_t vd = operand(smem_u32(sm.kv[vst]), 128 * 128);
+          const uint64_t vd = operand<D>(smem_u32(sm.kv[vst]));
           for (int t = 0; t < nt; ++t) {
             if (j == 0 && !wait(&sm.o_empty[t], oe_phase)) return false;
             if (!wait(&sm.p_full[t], p_phase[t])) return false;
@@ -661,7 +664,7 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ W
             fence_after();
 #pragma unroll
             for (int k = 0; k < kKeys / 16; ++k)
-              mma_ts(tmO[t], tmS[t] + k * 8, vd + (uint64_t)(k * (16 * 128 >> 4)), kDescO, j > 0 || k > 0);
+              mma_ts(tmO[t], tmS[t] + k * 8, vd + (uint64_t)(k * (2 * D * 16 >> 4)), kDescO, j > 0 || k > 0);
             if (more) {
               scores(t, stage);
               mma_commit(&sm.s_full[t]);
@@ -715,29 +718,30 @@ EncodeFn encoder() {
   return fn;
 }
 
-// The planes as rows of elements (see WideTma).  Boxes need pages of at least kMinBox tokens in a
-// row; without them, or with more rows than an index counts, the tiles come key by key.
-constexpr int kMinBox = 4;
-
+// The planes as WideTma says.  Boxes are whole groups of 8 tokens of a page; with other pages, or
+// more rows than an index counts, the tiles come key by key.
 void make_tma(const AttnParams &p, bool fp8, bool hnd, WideTma *t, CUtensorMap *km, CUtensorMap *vm) {
-  int rows = kKeys;
-  while (p.page_size % rows != 0) rows >>= 1;
+  *t = WideTma{};
   const int64_t pages = p.pool.num_pages, D = p.head_dim;
   const int64_t all = hnd ? pages * p.kv_heads * p.page_size : pages * p.page_size;
-  *t = WideTma{};
-  if (rows < kMinBox || all > INT32_MAX || !encoder()) return;
-  const cuuint64_t dims[2] = {(cuuint64_t)(hnd ? D : D * p.kv_heads), (cuuint64_t)all};
-  const cuuint64_t strides[1] = {(cuuint64_t)p.pool.tok_stride};
-  const cuuint32_t box[2] = {(cuuint32_t)(fp8 ? D : 64), (cuuint32_t)rows}, one[2] = {1, 1};
+  if (p.page_size % 8 != 0 || all > INT32_MAX || !encoder()) return;
+  int rows = kKeys;
+  while (p.page_size % rows != 0) rows >>= 1;
+  const cuuint64_t pitch = (cuuint64_t)p.pool.tok_stride;
+  const cuuint64_t columns = (cuuint64_t)(hnd ? D : D * p.kv_heads);
+  const cuuint64_t dims8[2] = {columns, (cuuint64_t)all}, strides8[1] = {pitch};
+  const cuuint32_t box8[2] = {(cuuint32_t)D, (cuuint32_t)rows};
+  const cuuint64_t dims[4] = {64, 8, columns / 64, (cuuint64_t)(all / 8)}, strides[3] = {pitch, 128, pitch * 8};
+  const cuuint32_t box[4] = {64, 8, (cuuint32_t)(D / 64), (cuuint32_t)(rows / 8)}, one[4] = {1, 1, 1, 1};
   for (int kv = 0; kv < 2; ++kv)
-    if (encoder()(kv ? vm : km, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2,
-                  const_cast<char *>(kv ? p.pool.v : p.pool.k), dims, strides, box, one,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE,
+    if (encoder()(kv ? vm : km, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16,
+                  fp8 ? 2 : 4, const_cast<char *>(kv ? p.pool.v : p.pool.k), fp8 ? dims8 : dims,
+                  fp8 ? strides8 : strides, fp8 ? box8 : box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   fp8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return;
   t->rows = rows;
-  t->head_x = hnd ? 0 : (int32_t)D;
+  t->head_x = hnd ? 0 : (int32_t)(fp8 ? D : D / 64);
   t->page_y = hnd ? (int64_t)p.kv_heads * p.page_size : p.page_size;
   t->head_y = hnd ? p.page_size : 0;
 }
