@@ -11,6 +11,7 @@
 #include <cuda_fp16.h>
 
 #include "kvx_attn.cuh"
+#include "kvx_attn_tma.cuh"
 #include "kvx_internal.cuh"
 #include "kvx_launch.cuh"
 #include "kvx_layout.cuh"
@@ -43,36 +44,6 @@ __device__ __forceinline__ int64_t block_excl(int64_t x, int64_t *total, int64_t
   return (w ? before : 0) + y - x;
 }
 
-// A request's query tokens and length as the kernels use them: clamped into what can be
-// addressed, whatever the arrays hold.
-struct Req {
-  int32_t t0, n, len;
-};
-
-__device__ __forceinline__ Req request(const AttnParams &p, int b, int32_t *bad) {
-  Req r;
-  r.t0 = b;
-  r.n = 1;
-  if (p.q_start) {
-    const int32_t a = p.q_start[b], z = p.q_start[b + 1];
-    if (a < 0 || z < a || z > p.n_q || (b == 0 && a != 0)) {
-      *bad = max(*bad, (int32_t)KVX_ERR_INVALID_ARG);
-      r.t0 = 0, r.n = 0;
-    } else {
-      r.t0 = a, r.n = z - a;
-    }
-  }
-  r.len = p.seq_lens[b];
-  if (r.len < 0) {
-    *bad = max(*bad, (int32_t)KVX_ERR_INVALID_ARG);
-    r.len = 0;
-  } else if (r.len > (int64_t)p.max_pages * p.page_size) {
-    *bad = max(*bad, (int32_t)KVX_ERR_OUT_OF_RANGE);
-    r.len = 0;
-  }
-  return r;
-}
-
 // The last b in [0, n) with base[b] <= x.
 __device__ __forceinline__ int last_at_or_before(const int32_t *base, int n, int32_t x) {
   int lo = 0, hi = n - 1;
@@ -84,8 +55,6 @@ __device__ __forceinline__ int last_at_or_before(const int32_t *base, int n, int
   return lo;
 }
 
-__device__ __forceinline__ int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
 __global__ void __launch_bounds__(kPlanCta) attn_plan_kernel(const AttnParams p) {
   __shared__ int64_t sm[32];
   attn_wait_prior();
@@ -96,10 +65,10 @@ __global__ void __launch_bounds__(kPlanCta) attn_plan_kernel(const AttnParams p)
   for (int b0 = 0; b0 < n; b0 += kPlanCta) {
     const int b = b0 + tid;
     int64_t mine = 0, total;
-    Req r = {};
+    AttnReq r = {};
     bool prompt = false;
     if (b < n) {
-      r = request(p, b, &bad);
+      r = attn_request(p, b, &bad);
       most = max(most, r.len);
       prompt = p.wide_groups > 0 && (int64_t)r.n * p.group > kAttnNarrowRows;
       mine = prompt ? 0 : r.n;
@@ -122,8 +91,7 @@ __global__ void __launch_bounds__(kPlanCta) attn_plan_kernel(const AttnParams p)
   const bool refused = any_range || any_arg;
   const int32_t prefix = min(p.prefix_len, most);  // no further than some request reaches
   if (tid == 0) {
-    p.head->segs = refused ? 0 : n + 1;
-    *p.status = any_range ? KVX_ERR_OUT_OF_RANGE : any_arg ? KVX_ERR_INVALID_ARG : KVX_OK;
+    p.head->refused = any_range ? KVX_ERR_OUT_OF_RANGE : any_arg ? KVX_ERR_INVALID_ARG : KVX_OK;
   }
   // what each token sees, and whose it is
   int32_t none = 0;
@@ -132,7 +100,7 @@ __global__ void __launch_bounds__(kPlanCta) attn_plan_kernel(const AttnParams p)
     int b = -1, sees = 0;
     if (t < last) {
       b = p.q_start ? last_at_or_before(p.q_start, n, t) : t;
-      const Req r = request(p, b, &none);
+      const AttnReq r = attn_request(p, b, &none);
       sees = max(0, r.len - r.n + (t - r.t0) + 1);
       const int32_t at = p.prompt[b];
       if (at != INT32_MIN) p.prefix_tok[at + t] = t, p.prefix_at[t] = at + t;
@@ -153,14 +121,14 @@ __global__ void __launch_bounds__(kPlanCta) attn_plan_kernel(const AttnParams p)
           g.key1 = prefix;
         }
       } else if (p.prompt[s - 1] != INT32_MIN) {
-        const Req r = request(p, s - 1, &none);
+        const AttnReq r = attn_request(p, s - 1, &none);
         g.row0 = r.t0 * p.group;
         g.rows = r.n * p.group;
-        g.key0 = p.prefix_len;
-        g.key1 = max(r.len, p.prefix_len);
+        g.low = p.prefix_len;
+        g.key1 = r.len;
       }
-      if (g.rows > 0) g.key_tiles = (int32_t)up((int64_t)g.key1 - g.key0, kAttnKeyTile);
-      mine = up(g.rows, p.row_tile) * g.key_tiles;
+      attn_tile_seg(&g);
+      mine = attn_up(g.rows, p.row_tile) * g.key_tiles;
     }
     int64_t total;
     g.tile0 = tiles + block_excl(mine, &total, sm);
@@ -173,9 +141,9 @@ __global__ void __launch_bounds__(kPlanCta) attn_plan_kernel(const AttnParams p)
     for (int s0 = 0; s0 <= n; s0 += kPlanCta) {
       const int s = s0 + tid;
       int64_t mine = 0, total;
-      if (s == 0) mine = prefix > 0 ? up(plain * p.group, kAttnWideRows) : 0;
+      if (s == 0) mine = prefix > 0 ? attn_up(plain * p.group, kAttnWideRows) : 0;
       else if (s <= n && any_prompt && p.prompt[s - 1] == INT32_MIN)
-        mine = up((int64_t)request(p, s - 1, &none).n * p.group, kAttnWideRows);
+        mine = attn_up((int64_t)attn_request(p, s - 1, &none).n * p.group, kAttnWideRows);
       const int64_t at = units + block_excl(mine, &total, sm);
       if (s <= n) p.unit_base[s] = (int32_t)at;
       units += total;
@@ -195,26 +163,45 @@ __global__ void __launch_bounds__(kPlanCta) attn_plan_kernel(const AttnParams p)
           x.rows = (int32_t)min((int64_t)kAttnWideRows, plain * p.group - x.row0);
           x.key1 = prefix;
         } else {
-          const Req r = request(p, s - 1, &none);
+          const AttnReq r = attn_request(p, s - 1, &none);
           x.rows = min(kAttnWideRows, r.n * p.group - x.row0);
           // as far as its last row sees
           x.key1 = max(0, r.len - r.n + (x.row0 + x.rows - 1) / p.group + 1);
           x.row0 += r.t0 * p.group;
         }
-        x.key_tiles = (int32_t)up(x.key1, kAttnWideKeys);
+        x.key_tiles = (int32_t)attn_up(x.key1, kAttnWideKeys);
       }
       x.tile0 = wide + block_excl(x.key_tiles, &total, sm);
       if (u < units) p.units[u] = x;
       wide += total;
     }
   }
+  const int64_t quota = max((int64_t)1, attn_up(tiles, p.groups));
+  const int64_t wide_quota = p.wide_groups > 0 ? max((int64_t)1, attn_up(wide, p.wide_groups)) : 1;
   if (tid == 0) {
     p.head->tiles = tiles;
-    p.head->quota = max((int64_t)1, up(tiles, p.groups));
+    p.head->quota = quota;
     p.head->units = (int32_t)units;
     p.head->wide_tiles = wide;
-    p.head->wide_quota = p.wide_groups > 0 ? max((int64_t)1, up(wide, p.wide_groups)) : 1;
+    p.head->wide_quota = wide_quota;
   }
+  __syncthreads();
+  // tokens of prompts whose rows the wide kernel writes itself, being in one piece
+  if (any_prompt && !refused)
+    for (int t = tid; t < last; t += kPlanCta) {
+      const int b = p.owner[t];
+      if (p.prompt[b] != INT32_MIN) continue;
+      const int at = (t - p.q_start[b]) * p.group;
+      bool whole = true;
+      for (int u = at / kAttnWideRows; u <= (at + p.group - 1) / kAttnWideRows; ++u) {
+        const AttnUnit x = p.units[p.unit_base[1 + b] + u];
+        whole = whole && x.key_tiles > 0 && x.tile0 / wide_quota == (x.tile0 + x.key_tiles - 1) / wide_quota;
+      }
+      if (whole) p.owner[t] = kAttnWritten;
+    }
+  for (int g = tid; g < p.groups + p.wide_groups; g += kPlanCta)
+    p.start[g] = g < p.groups ? attn_find(p.segs, n + 1, g * quota)
+                 : units > 0  ? attn_find(p.units, (int)units, (g - p.groups) * wide_quota) : 0;
 }
 
 __device__ __forceinline__ void put(float *o, float x) { *o = x; }
@@ -223,34 +210,62 @@ __device__ __forceinline__ void put(__nv_bfloat16 *o, float x) { *o = __float2bf
 
 constexpr int kJoinWarps = 4;
 
-// One warp joins the parts of one (token, query head), prefix splits first, in order.
-template <typename IO>
-__global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const AttnParams p) {
+// Which group's part of a line a tile is in; 32-bit arithmetic where it is enough.
+__device__ __forceinline__ int group_of(int64_t tile, int64_t quota) {
+  if (((tile | quota) >> 31) == 0) return (int)((uint32_t)tile / (uint32_t)quota);
+  return (int)(tile / quota);
+}
+
+// A block joins the parts of `heads` query heads of one token, a warp a head at a time, prefix splits
+// first, in order.  DK: head_dim, 0: any.
+template <typename IO, int DK>
+__global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid_constant__ AttnParams p, int heads) {
   attn_wait_prior();
-  const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
-  if (w >= (int64_t)p.n_q * p.q_heads) return;
-  const int t = (int)(w / p.q_heads), qh = (int)(w - (int64_t)t * p.q_heads);
-  const int h = qh / p.group, r = t * p.group + qh - h * p.group;
-  const int D = p.head_dim, b = p.owner[t];
-  IO *out = reinterpret_cast<IO *>(p.out + t * p.out_tok + qh * p.out_head);
-  // the pieces of the row: n0 of the prefix (or of the prompt), then the request's own
-  int64_t first[2], more[2], step[2];
-  int count[2] = {0, 0};
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = blockIdx.x;
   const AttnHeader head = *p.head;
-  if (b >= 0 && head.segs > 0) {
-    const bool prompt = p.prompt[b] == INT32_MIN;
-    if (p.wide_groups > 0) {
-      // the row's place among those of its kind of work, and with it its unit
-      const int s = prompt ? 1 + b : 0, lead = prompt ? (p.q_start ? p.q_start[b] : b) * p.group : 0;
-      const int wr = prompt ? r : p.prefix_at[t] * p.group + r % p.group;
-      const int u = (s ? p.unit_base[s] : 0) + (wr - lead) / kAttnWideRows;
-      if (u < head.units) {
-        const AttnUnit x = p.units[u];
-        const int64_t q = head.wide_quota;
-        if (x.key_tiles > 0 && x.table == s - 1) {
-          const int g0 = (int)(x.tile0 / q), g1 = (int)((x.tile0 + x.key_tiles - 1) / q);
-          if (prompt && g0 == g1) return;  // the wide kernel has written the result
+  if (blockIdx.x == 0 && blockIdx.y == 0) {  // the call's verdict
+    int32_t e = head.refused;
+    for (int i = threadIdx.x; i < p.n_errors; i += kJoinWarps * 32) e = max(e, p.errors[i]);
+    for (int o = 16; o; o >>= 1) e = max(e, __shfl_xor_sync(~0u, e, o));
+    __shared__ int32_t worst[kJoinWarps];
+    if (lane == 0) worst[warp] = e;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int i = 1; i < kJoinWarps; ++i) e = max(e, worst[i]);
+      *p.status = e;
+    }
+  }
+  if (t >= p.n_q) return;
+  const int b = p.planned ? p.owner[t] : t;
+  if (b == kAttnWritten) return;
+  const int D = DK ? DK : p.head_dim;
+  const bool some = b >= 0 && !head.refused;
+  const bool prompt = some && p.planned && p.prompt[b] == INT32_MIN;
+  AttnSeg seg[2] = {};
+  if (some && p.wide_groups == 0) seg[0] = p.segs[0];
+  if (some) seg[1] = p.segs[1 + b];
+  const int units = p.planned ? head.units : attn_plain_units(p);
+  // of the wide line: the token's unit 0, and its first row's place among those of its kind of work
+  int unit0 = 0, lead = 0, wide_row = t * p.group;
+  if (some && p.wide_groups > 0 && p.planned) {
+    if (prompt) unit0 = p.unit_base[1 + b], lead = p.q_start ? p.q_start[b] * p.group : b * p.group;
+    else wide_row = p.prefix_at[t] * p.group;
+  }
+  const int qh1 = min(p.q_heads, (int)(blockIdx.y + 1) * heads);
+  for (int qh = blockIdx.y * heads + warp; qh < qh1; qh += kJoinWarps) {
+    const int h = qh / p.group, member = qh - h * p.group, r = t * p.group + member;
+    // the pieces of the row: n0 of the prefix (or of the prompt), then the request's own
+    int64_t first[2], more[2], step[2];
+    int count[2] = {0, 0};
+    if (some && p.wide_groups > 0) {
+      const int wr = wide_row + member, u = unit0 + (wr - lead) / kAttnWideRows;
+      if (u < units) {
+        const AttnUnit x = p.planned ? p.units[u] : attn_plain_unit(p, u);
+        const int64_t q = p.planned ? head.wide_quota
+                                    : max((int64_t)1, attn_up((int64_t)units * x.key_tiles, p.wide_groups));
+        if (x.key_tiles > 0 && x.table == (prompt ? b : -1)) {
+          const int g0 = group_of(x.tile0, q), g1 = group_of(x.tile0 + x.key_tiles - 1, q);
+          if (prompt && g0 == g1) continue;  // the wide kernel has written the result
           count[0] = g1 - g0 + 1;
           first[0] = attn_wide_part(p, true, 0, h) + r;
           more[0] = attn_wide_part(p, false, g0, h) + (wr - x.row0);
@@ -258,79 +273,149 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const AttnPa
         }
       }
     }
-    for (int k = p.wide_groups > 0 ? 1 : 0; k < 2; ++k) {
-      const AttnSeg s = p.segs[k == 0 ? 0 : 1 + b];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const AttnSeg &s = seg[k];
       if (s.key_tiles == 0) continue;
       const int unit = (r - s.row0) / p.row_tile, row0 = s.row0 + unit * p.row_tile;
       const int64_t w = s.tile0 + (int64_t)unit * s.key_tiles;
-      const int g0 = (int)(w / head.quota), g1 = (int)((w + s.key_tiles - 1) / head.quota);
+      const int g0 = group_of(w, head.quota), g1 = group_of(w + s.key_tiles - 1, head.quota);
       count[k] = g1 - g0 + 1;
       first[k] = attn_part(p, k == 0, true, 0, h, row0) + (r - row0);
       more[k] = attn_part(p, k == 0, false, g0, h, row0) + (r - row0);
       step[k] = (int64_t)p.kv_heads * p.row_tile;
     }
-  }
-  const int n0 = count[0], n = n0 + count[1];
-  auto part = [&](int i) {
-    const int k = i < n0 ? 0 : 1;
-    i -= k ? n0 : 0;
-    return i == 0 ? first[k] : more[k] + i * step[k];
-  };
-  // lane i has part i (of 32 at a time); all lanes then add the parts, four columns a lane
-  float top = -INFINITY;
-  for (int i = lane; i < n; i += 32) top = fmaxf(top, p.part_m[part(i)]);
+    const int n0 = count[0], n = n0 + count[1];
+    auto part = [&](int i) {
+      const int k = i < n0 ? 0 : 1;
+      i -= k ? n0 : 0;
+      return i == 0 ? first[k] : more[k] + i * step[k];
+    };
+    // lane i has part i (of 32 at a time); all lanes then add the parts, neighbouring columns a lane
+    float top = -INFINITY, l = 0.f;
+    constexpr int kCols = DK ? DK / 32 : KVX_ATTN_MAX_HEAD_DIM / 32;
+    float acc[kCols] = {};
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      const int left = min(32, n - i0);
+      int64_t at = 0;
+      float m = -INFINITY, pl = 0.f;
+      if (lane < left) {
+        at = part(i0 + lane);
+        m = p.part_m[at];
+        pl = p.part_l[at];
+      }
+      float now = m;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-  const float base = top == -INFINITY ? 0.f : top;
-  constexpr int kCols = KVX_ATTN_MAX_HEAD_DIM / 32;
-  float l = 0.f, acc[kCols] = {};
-  for (int i0 = 0; i0 < n; i0 += 32) {
-    const int left = min(32, n - i0);
-    int64_t at = 0;
-    float f = 0.f;
-    if (lane < left) {
-      at = part(i0 + lane);
-      f = exp2f(p.part_m[at] - base);
-      l = fmaf(f, p.part_l[at], l);
-    }
-    if (D == 128) {
+      for (int o = 16; o; o >>= 1) now = fmaxf(now, __shfl_xor_sync(~0u, now, o));
+      now = fmaxf(now, top);
+      const float base = now == -INFINITY ? 0.f : now;
+      if (i0 > 0) {  // more than 32 parts: what the first ones gave refers to the greatest so far
+        const float f = top == -INFINITY ? 0.f : exp2f(top - base);
+        l *= f;
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) acc[c] *= f;
+      }
+      top = now;
+      const float f = exp2f(m - base);
+      l = fmaf(f, pl, l);
 #pragma unroll 4
       for (int i = 0; i < left; ++i) {
-        const int64_t x = __shfl_sync(~0u, at, i);
+        const float *o = p.part_o + __shfl_sync(~0u, at, i) * D;
         const float w = __shfl_sync(~0u, f, i);
-        const float4 v = *reinterpret_cast<const float4 *>(p.part_o + x * 128 + lane * 4);
-        acc[0] = fmaf(w, v.x, acc[0]), acc[1] = fmaf(w, v.y, acc[1]);
-        acc[2] = fmaf(w, v.z, acc[2]), acc[3] = fmaf(w, v.w, acc[3]);
-      }
-    } else {
-#pragma unroll 2
-      for (int i = 0; i < left; ++i) {
-        const int64_t x = __shfl_sync(~0u, at, i);
-        const float w = __shfl_sync(~0u, f, i);
+        if constexpr (DK == 128) {
+          const float4 v = *reinterpret_cast<const float4 *>(o + lane * 4);
+          acc[0] = fmaf(w, v.x, acc[0]), acc[1] = fmaf(w, v.y, acc[1]);
+          acc[2] = fmaf(w, v.z, acc[2]), acc[3] = fmaf(w, v.w, acc[3]);
+        } else if constexpr (DK == 64) {
+          const float2 v = *reinterpret_cast<const float2 *>(o + lane * 2);
+          acc[0] = fmaf(w, v.x, acc[0]), acc[1] = fmaf(w, v.y, acc[1]);
+        } else {
 #pragma unroll
-        for (int c = 0; c < kCols; ++c)
-          if (c * 32 + lane < D) acc[c] = fmaf(w, p.part_o[x * D + c * 32 + lane], acc[c]);
+          for (int c = 0; c < kCols; ++c)
+            if (c * 32 + lane < D) acc[c] = fmaf(w, o[c * 32 + lane], acc[c]);
+        }
       }
     }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
+    const float inv = l == 0.f ? 0.f : p.v_scale / l;
+    IO *out = reinterpret_cast<IO *>(p.out + t * p.out_tok + qh * p.out_head);
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) {
+      const int d = DK ? lane * kCols + c : c * 32 + lane;
+      if (DK || d < D) put(out + d, l == 0.f ? 0.f : acc[c] * inv);
+    }
+    if (p.lse && lane == 0)
+      p.lse[(int64_t)t * p.q_heads + qh] =
+          l == 0.f ? -INFINITY : ((top == -INFINITY ? 0.f : top) + log2f(l)) * 0.693147180559945309f;
   }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
-  const float inv = l == 0.f ? 0.f : p.v_scale / l;
-  if (D == 128) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) put(out + lane * 4 + c, l == 0.f ? 0.f : acc[c] * inv);
-  } else {
-#pragma unroll
-    for (int c = 0; c < kCols; ++c)
-      if (c * 32 + lane < D) put(out + c * 32 + lane, l == 0.f ? 0.f : acc[c] * inv);
-  }
-  if (p.lse && lane == 0)
-    p.lse[w] = l == 0.f ? -INFINITY : (base + log2f(l)) * 0.693147180559945309f;
 }
 
+template <typename IO>
+const void *join_kernel(int D) {
+  return D == 64    ? (const void *)attn_join_kernel<IO, 64>
+         : D == 128 ? (const void *)attn_join_kernel<IO, 128>
+                    : (const void *)attn_join_kernel<IO, 0>;
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
+                              CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                              CUtensorMapFloatOOBfill);
+
+EncodeFn encoder() {
+  static const EncodeFn fn = [] {
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess) {
+      (void)cudaGetLastError();
+      f = nullptr;
+    }
+    return reinterpret_cast<EncodeFn>(f);
+  }();
+  return fn;
+}
+
+}  // namespace
+
+void attn_make_tma(const AttnParams &p, int keys, bool fp8, bool hnd, AttnTma *t, CUtensorMap *km,
+                   CUtensorMap *vm) {
+  *t = AttnTma{};
+  std::memset(km, 0, sizeof(*km));
+  std::memset(vm, 0, sizeof(*vm));
+  const int64_t pages = p.pool.num_pages, D = p.head_dim;
+  const int64_t all = hnd ? pages * p.kv_heads * p.page_size : pages * p.page_size;
+  if (p.page_size % 8 != 0 || all > INT32_MAX || !encoder()) return;
+  int rows = keys;
+  while (p.page_size % rows != 0) rows >>= 1;
+  const cuuint64_t pitch = (cuuint64_t)p.pool.tok_stride;
+  const cuuint64_t columns = (cuuint64_t)(hnd ? D : D * p.kv_heads);
+  const cuuint64_t dims8[2] = {columns, (cuuint64_t)all}, strides8[1] = {pitch};
+  const cuuint32_t box8[2] = {(cuuint32_t)D, (cuuint32_t)rows};
+  const cuuint64_t dims[4] = {64, 8, columns / 64, (cuuint64_t)(all / 8)}, strides[3] = {pitch, 128, pitch * 8};
+  const cuuint32_t box[4] = {64, 8, (cuuint32_t)(D / 64), (cuuint32_t)(rows / 8)}, one[4] = {1, 1, 1, 1};
+  for (int kv = 0; kv < 2; ++kv)
+    if (encoder()(kv ? vm : km, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16,
+                  fp8 ? 2 : 4, const_cast<char *>(kv ? p.pool.v : p.pool.k), fp8 ? dims8 : dims,
+                  fp8 ? strides8 : strides, fp8 ? box8 : box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  fp8 && D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return;
+  t->rows = rows;
+  t->head_x = hnd ? 0 : (int32_t)(fp8 ? D : D / 64);
+  t->page_y = hnd ? (int64_t)p.kv_heads * p.page_size : p.page_size;
+  t->head_y = hnd ? p.page_size : 0;
+}
+
+namespace {
+
+// Calls with one query token a request do without the plan kernel up to this many requests.
+constexpr int kPlanReqs = 2048;
+
 struct Sizes {
-  int64_t segs_off, units_off, base_off, prompt_off, limit_off, owner_off, tok_off, at_off;
-  int64_t m_off, l_off, o_off, total;
+  int64_t segs_off, units_off, start_off, base_off, prompt_off, limit_off, owner_off, tok_off, at_off;
+  int64_t m_off, l_off, o_off, errors_off, errors, total;
   int32_t groups, wide_groups;
 };
 
@@ -341,6 +426,7 @@ Sizes sizes(int64_t n_q, int64_t n_reqs, int64_t q_heads, int64_t kv_heads, int6
   const int64_t rows = n_q * (q_heads / kv_heads);
   z.groups = (int32_t)std::max((int64_t)1, 152 * 2 / kv_heads);
   z.wide_groups = wide ? (int32_t)std::max((int64_t)1, 152 / kv_heads) : 0;
+  z.errors = z.groups * kv_heads + z.wide_groups * kv_heads;
   const int64_t parts = 2 * n_q * q_heads + z.groups * kv_heads * row_tile +
                         z.wide_groups * kv_heads * kAttnWideRows;
   // prompts have more than kAttnNarrowRows rows each
@@ -353,12 +439,14 @@ Sizes sizes(int64_t n_q, int64_t n_reqs, int64_t q_heads, int64_t kv_heads, int6
   };
   z.segs_off = take((int64_t)sizeof(AttnSeg) * (n_reqs + 1));
   z.units_off = take((int64_t)sizeof(AttnUnit) * units);
+  z.start_off = take(4 * (z.groups + z.wide_groups));
   z.base_off = take(4 * (n_reqs + 2));
   z.prompt_off = take(4 * n_reqs);
   z.limit_off = take(4 * n_q);
   z.owner_off = take(4 * n_q);
   z.tok_off = take(4 * n_q);
   z.at_off = take(4 * n_q);
+  z.errors_off = take(4 * z.errors);
   z.m_off = take(4 * parts);
   z.l_off = take(4 * parts);
   z.o_off = take(4 * parts * D);
@@ -487,11 +575,15 @@ extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_arg
   p.q_vec = q_at % 16 == 0;
   p.out_vec = ((uintptr_t)a.out | (uintptr_t)p.out_tok | (uintptr_t)p.out_head) % 16 == 0;
   p.groups = z.groups;
+  // a single token a request, and not so many requests that every CTA's adding them up tells
+  p.planned = a.n_q == 0 || a.q_start || a.n_reqs > kPlanReqs;
+  p.after_wide = wide;
   p.wide_groups = z.wide_groups;
   char *ws = static_cast<char *>(d_ws);
   p.head = reinterpret_cast<AttnHeader *>(ws);
   p.segs = reinterpret_cast<AttnSeg *>(ws + z.segs_off);
   p.units = reinterpret_cast<AttnUnit *>(ws + z.units_off);
+  p.start = reinterpret_cast<int32_t *>(ws + z.start_off);
   p.unit_base = reinterpret_cast<int32_t *>(ws + z.base_off);
   p.prompt = reinterpret_cast<int32_t *>(ws + z.prompt_off);
   p.prefix_tok = reinterpret_cast<int32_t *>(ws + z.tok_off);
@@ -501,23 +593,33 @@ extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_arg
   p.part_m = reinterpret_cast<float *>(ws + z.m_off);
   p.part_l = reinterpret_cast<float *>(ws + z.l_off);
   p.part_o = reinterpret_cast<float *>(ws + z.o_off);
+  p.errors = reinterpret_cast<int32_t *>(ws + z.errors_off);
+  p.n_errors = a.n_q > 0 ? (int32_t)z.errors : 0;
   p.status = d_status;
 
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   void *kargs[] = {&p};
-  cudaError_t e = launch_pdl((const void *)attn_plan_kernel, dim3(1), dim3(kPlanCta), kargs, s);
-  if (e == cudaSuccess && a.n_q > 0) {
-    e = tensor_cores(pool) ? launch_attn_narrow(p, pool->dtype, a.q_dtype, s)
-                           : launch_attn_general(p, pool->dtype, a.q_dtype, s);
+  // The wide kernel goes first: the narrow one does not wait for it, and takes over its SMs one by
+  // one as its CTAs end.
+  cudaError_t e = cudaSuccess;
+  if (p.planned) e = launch_pdl((const void *)attn_plan_kernel, dim3(1), dim3(kPlanCta), kargs, s);
+  if (a.n_q > 0) {
     if (e == cudaSuccess && wide) e = launch_attn_wide(p, pool->dtype, a.q_dtype, hnd, s);
-    if (e == cudaSuccess) {
-      const void *join = a.q_dtype == KVX_F32   ? (const void *)attn_join_kernel<float>
-                         : a.q_dtype == KVX_F16 ? (const void *)attn_join_kernel<__half>
-                                                : (const void *)attn_join_kernel<__nv_bfloat16>;
-      const int64_t rows = (int64_t)a.n_q * a.q_heads;
-      e = launch_pdl(join, dim3((unsigned)((rows + kJoinWarps - 1) / kJoinWarps)),
-                     dim3(kJoinWarps * 32), kargs, s);
-    }
+    if (e == cudaSuccess)
+      e = tensor_cores(pool) ? launch_attn_narrow(p, pool->dtype, a.q_dtype, hnd, s)
+                             : launch_attn_general(p, pool->dtype, a.q_dtype, s);
+  }
+  if (e == cudaSuccess) {
+    const void *join = a.q_dtype == KVX_F32   ? join_kernel<float>(pool->head_dim)
+                       : a.q_dtype == KVX_F16 ? join_kernel<__half>(pool->head_dim)
+                                              : join_kernel<__nv_bfloat16>(pool->head_dim);
+    // a warp a row while that fills the GPU; then a block a token, which reads what is the token's once
+    int heads = kJoinWarps;
+    if ((int64_t)a.n_q * a.q_heads > (int64_t)kJoinWarps * 152 * 16 || a.q_heads > kJoinWarps * 65535)
+      heads = a.q_heads;
+    void *jargs[] = {&p, &heads};
+    e = launch_pdl(join, dim3((unsigned)std::max(1, a.n_q), (unsigned)((a.q_heads + heads - 1) / heads)),
+                   dim3(kJoinWarps * 32), jargs, s);
   }
   if (e != cudaSuccess) {
     record_cuda_error(e);

@@ -37,6 +37,8 @@ constexpr int kAttnNarrowRows = 64;    // narrow kernel
 constexpr int kAttnWideKeys = 128;     // key tile of the wide kernel
 constexpr int kAttnWideRows = 256;     // rows of its units
 
+constexpr int kAttnWritten = -2;
+
 // Where a layer's rows are: element row (page id, offset in page, kv head) starts at
 // plane + id * page_stride + offset * tok_stride + head * head_stride (bytes), in either kind of
 // layout.
@@ -52,9 +54,9 @@ struct AttnPool {
 struct AttnSeg {
   int64_t tile0;       // its first key tile in the line
   int32_t row0, rows;
-  int32_t key0, key1;
+  int32_t low;         // its first position; tiles begin at multiples of their length, so that they
+  int32_t key0, key1;  // hold whole pages: key0 is the first tile's begin, at most low
   int32_t key_tiles;   // of each unit; 0: no keys (or no rows)
-  int32_t pad;
 };
 
 // A unit of the wide line.  table: the request of a prompt, -1: the prefix, whose rows are those
@@ -70,7 +72,7 @@ struct AttnUnit {
 struct AttnHeader {
   int64_t tiles, quota;            // the narrow line, and a group's part of it
   int64_t wide_tiles, wide_quota;
-  int32_t segs;                    // 1 + n_reqs; 0: the arguments were refused
+  int32_t refused;                 // 0, or the kvx_status that the arguments were refused with
   int32_t units;
   int32_t pad[6];
 };
@@ -92,6 +94,9 @@ struct AttnParams {
   int32_t row_tile;      // rows of a narrow unit
   int32_t groups;        // groups of kv_heads CTAs, narrow line
   int32_t wide_groups;   // of the wide line; 0: no wide kernel
+  int32_t planned;       // 1: the plan kernel has laid the work out.  0: one query token a request,
+                         // and every kernel works its part out from the lengths
+  int32_t after_wide;    // the narrow kernel runs beside the end of the wide kernel
   int32_t q_even;        // q's heads start on 4-byte boundaries
   int32_t q_vec;         // on 16-byte boundaries
   int32_t out_vec;       // out's heads do
@@ -99,42 +104,107 @@ struct AttnParams {
   AttnHeader *head;
   AttnSeg *segs;         // [1 + n_reqs]: the prefix, then the requests
   AttnUnit *units;
+  int32_t *start;        // [groups + wide_groups]: the seg, or unit, that a group begins in
   int32_t *unit_base;    // [2 + n_reqs]: first wide unit of the prefix and of each request
   int32_t *prompt;       // [n_reqs]: INT32_MIN: prompt work; else what to add to a token for its
                          // place in prefix_tok
   int32_t *limit;        // [n_q]: positions that a token sees
-  int32_t *owner;        // [n_q]: its request, -1: none
+  int32_t *owner;        // [n_q]: its request, -1: none, kAttnWritten: nothing is left to be joined
   int32_t *prefix_tok;   // [n_q]: tokens whose requests are not prompts, in order
   int32_t *prefix_at;    // [n_q]: a token's place in prefix_tok
   // part rows: [kv_heads][n_q * G] of own work's first pieces; the same of the prefix's and
   // prompts' first pieces; then pieces that go on, [groups][kv_heads][row_tile] and
   // [wide_groups][kv_heads][256]
   float *part_m, *part_l, *part_o;
+  int32_t *errors;       // [n_errors]: one word of each CTA of the kernels before the join
+  int32_t n_errors;
   int32_t *status;
 };
 
 // The page id of position pos for an item's table, checked: an id outside the pool is reported
-// and read as page 0.
-__device__ __forceinline__ int32_t attn_page(const AttnParams &p, int32_t table, int64_t pg) {
+// in *error (of the CTA) and read as page 0.
+__device__ __forceinline__ int32_t attn_page(const AttnParams &p, int32_t table, int64_t pg, int32_t *error) {
   const int32_t id = table < 0 ? p.prefix_pages[pg] : p.tables[table * p.table_stride + pg];
   if ((uint32_t)id >= (uint64_t)p.pool.num_pages) {
-    atomicMax(p.status, (int32_t)KVX_ERR_OUT_OF_RANGE);
+    *(volatile int32_t *)error = KVX_ERR_OUT_OF_RANGE;
     return 0;
   }
   return id;
 }
 
-// Byte offset in a plane of position pos, kv head 0.
-__device__ __forceinline__ int64_t attn_key_offset(const AttnParams &p, int32_t table, int32_t pos) {
-  int32_t pg, off;
+// Page and offset of a position.
+__device__ __forceinline__ void attn_split(const AttnParams &p, int32_t pos, int32_t *pg, int32_t *off) {
   if (p.pool.page_shift >= 0) {
-    pg = pos >> p.pool.page_shift;
-    off = pos & (p.page_size - 1);
+    *pg = pos >> p.pool.page_shift;
+    *off = pos & (p.page_size - 1);
   } else {
-    pg = pos / p.page_size;
-    off = pos - pg * p.page_size;
+    *pg = pos / p.page_size;
+    *off = pos - *pg * p.page_size;
   }
-  return attn_page(p, table, pg) * p.pool.page_stride + off * p.pool.tok_stride;
+}
+
+// Byte offset in a plane of position pos, kv head 0.
+__device__ __forceinline__ int64_t attn_key_offset(const AttnParams &p, int32_t table, int32_t pos, int32_t *error) {
+  int32_t pg, off;
+  attn_split(p, pos, &pg, &off);
+  return attn_page(p, table, pg, error) * p.pool.page_stride + off * p.pool.tok_stride;
+}
+
+// A request's query tokens and length as the kernels use them: clamped into what can be
+// addressed, whatever the arrays hold.
+struct AttnReq {
+  int32_t t0, n, len;
+};
+
+__device__ __forceinline__ AttnReq attn_request(const AttnParams &p, int b, int32_t *bad) {
+  AttnReq r;
+  r.t0 = b;
+  r.n = 1;
+  if (p.q_start) {
+    const int32_t a = p.q_start[b], z = p.q_start[b + 1];
+    if (a < 0 || z < a || z > p.n_q || (b == 0 && a != 0)) {
+      *bad = max(*bad, (int32_t)KVX_ERR_INVALID_ARG);
+      r.t0 = 0, r.n = 0;
+    } else {
+      r.t0 = a, r.n = z - a;
+    }
+  }
+  r.len = p.seq_lens[b];
+  if (r.len < 0) {
+    *bad = max(*bad, (int32_t)KVX_ERR_INVALID_ARG);
+    r.len = 0;
+  } else if (r.len > (int64_t)p.max_pages * p.page_size) {
+    *bad = max(*bad, (int32_t)KVX_ERR_OUT_OF_RANGE);
+    r.len = 0;
+  }
+  return r;
+}
+
+// Positions that token t sees.
+__device__ __forceinline__ int32_t attn_limit(const AttnParams &p, int32_t t) {
+  return p.planned ? p.limit[t] : max(0, p.seq_lens[t]);
+}
+
+__host__ __device__ __forceinline__ int64_t attn_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+__device__ __forceinline__ void attn_tile_seg(AttnSeg *g) {
+  g->key0 = g->low / kAttnKeyTile * kAttnKeyTile;
+  if (g->rows > 0 && g->key1 > g->low)
+    g->key_tiles = (int32_t)attn_up((int64_t)g->key1 - g->key0, kAttnKeyTile);
+}
+
+// Seg s of a call without a plan (its tile0 aside).
+__device__ __forceinline__ AttnSeg attn_plain_seg(const AttnParams &p, int s, int32_t *bad) {
+  AttnSeg g = {};
+  if (s == 0) {
+    if (p.wide_groups == 0) g.rows = p.n_q * p.group, g.key1 = p.prefix_len;
+  } else {
+    const AttnReq r = attn_request(p, s - 1, bad);
+    g.row0 = r.t0 * p.group, g.rows = p.group;
+    g.low = p.prefix_len, g.key1 = r.len;
+  }
+  attn_tile_seg(&g);
+  return g;
 }
 
 // First part row of a piece of a narrow unit that starts at row0 (see AttnParams).
@@ -166,32 +236,109 @@ __device__ __forceinline__ int attn_find(const E *e, int n, int64_t w) {
   return lo;
 }
 
-// A piece: keys [key0, key1) for rows [row0, row0 + rows).
+// A piece: keys [key0, key1), those below low left out, for rows [row0, row0 + rows).
 struct AttnPiece {
   int64_t part;
-  int32_t row0, rows, key0, key1, table;
+  int32_t row0, rows, low, key0, key1, table;
 };
 
-// Calls f(piece) for every piece of group g, kv head h of the narrow line.
+// Where a CTA's part of the narrow line begins.
+struct AttnLine {
+  int64_t w, end;     // its tiles
+  int64_t tile0;      // first tile of seg
+  int32_t seg;
+};
+
+// Group g's part, found by the CTA's Threads threads: by a search in the plan, or without one by adding
+// up all lengths (the first CTA then leaves what the join needs).  sm: two words a warp and four more.
+template <int Threads>
+__device__ __forceinline__ AttnLine attn_line(const AttnParams &p, int g, int64_t *sm) {
+  AttnLine l = {};
+  if (p.planned) {
+    const int64_t quota = p.head->quota;
+    l.seg = p.start[g];
+    if (p.head->refused) return l;
+    l.w = g * quota;
+    l.end = min(p.head->tiles, l.w + quota);
+    if (l.w < l.end) l.tile0 = p.segs[l.seg].tile0;
+    return l;
+  }
+  constexpr int kWarps = Threads / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = 1 + p.n_reqs;
+  const int per = (n + Threads - 1) / Threads, s0 = min(tid * per, n), s1 = min(s0 + per, n);
+  int32_t bad = 0;
+  int64_t mine = 0;
+  for (int s = s0; s < s1; ++s) {
+    const AttnSeg g = attn_plain_seg(p, s, &bad);
+    mine += attn_up(g.rows, p.row_tile) * g.key_tiles;
+  }
+  int64_t x = mine;
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t y = __shfl_up_sync(~0u, x, d);
+    if (lane >= d) x += y;
+  }
+  for (int o = 16; o; o >>= 1) bad = max(bad, __shfl_xor_sync(~0u, bad, o));
+  if (lane == 31) sm[warp] = x, sm[kWarps + warp] = bad;
+  __syncthreads();
+  int64_t total = 0, before = 0;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    if (i < warp) before += sm[i];
+    total += sm[i];
+    bad = max(bad, (int32_t)sm[kWarps + i]);
+  }
+  before += x - mine;
+  const int64_t quota = max((int64_t)1, attn_up(total, p.groups));
+  if (blockIdx.x == 0) {
+    int64_t at = before;
+    for (int s = s0; s < s1; ++s) {
+      AttnSeg g = attn_plain_seg(p, s, &bad);
+      g.tile0 = at;
+      p.segs[s] = g;
+      at += attn_up(g.rows, p.row_tile) * g.key_tiles;
+    }
+    if (tid == 0) p.head->tiles = total, p.head->quota = quota, p.head->refused = bad;
+  }
+  l.w = g * quota;
+  l.end = min(total, l.w + quota);
+  if (bad || l.w >= l.end) {
+    l.end = l.w;
+    return l;
+  }
+  if (before <= l.w && l.w < before + mine) {
+    int64_t at = before;
+    for (int s = s0; s < s1; ++s) {
+      const AttnSeg g = attn_plain_seg(p, s, &bad);
+      const int64_t next = at + attn_up(g.rows, p.row_tile) * g.key_tiles;
+      if (l.w < next) {
+        sm[2 * kWarps] = s, sm[2 * kWarps + 1] = at;
+        break;
+      }
+      at = next;
+    }
+  }
+  __syncthreads();
+  l.seg = (int32_t)sm[2 * kWarps];
+  l.tile0 = sm[2 * kWarps + 1];
+  return l;
+}
+
+// Calls f(piece) for every piece of group g, kv head h of the narrow line, l being its part.
 template <typename F>
-__device__ __forceinline__ void attn_pieces(const AttnParams &p, int g, int h, F f) {
-  const int n = p.head->segs;
-  const int64_t quota = p.head->quota;
-  int64_t w = g * quota;
-  const int64_t end = min(p.head->tiles, w + quota);
-  if (n == 0 || w >= end) return;
-  int s = attn_find(p.segs, n, w);
-  while (w < end) {
-    const AttnSeg seg = p.segs[s];
-    const int units = (seg.rows + p.row_tile - 1) / p.row_tile;
-    const int64_t tiles = (int64_t)units * seg.key_tiles;
-    while (w < end && w < seg.tile0 + tiles) {
-      const int64_t at = w - seg.tile0;
+__device__ __forceinline__ void attn_pieces(const AttnParams &p, int g, int h, const AttnLine &l, F f) {
+  int64_t w = l.w, tile0 = l.tile0;
+  int32_t none = 0;
+  for (int s = l.seg; w < l.end; ++s) {
+    const AttnSeg seg = p.planned ? p.segs[s] : attn_plain_seg(p, s, &none);
+    const int64_t tiles = attn_up(seg.rows, p.row_tile) * seg.key_tiles;
+    while (w < l.end && w < tile0 + tiles) {
+      const int64_t at = w - tile0;
       const int unit = (int)(at / seg.key_tiles), kt = (int)(at - (int64_t)unit * seg.key_tiles);
-      const int take = (int)min((int64_t)(seg.key_tiles - kt), end - w);
+      const int take = (int)min((int64_t)(seg.key_tiles - kt), l.end - w);
       AttnPiece x;
       x.row0 = seg.row0 + unit * p.row_tile;
       x.rows = min(p.row_tile, seg.rows - unit * p.row_tile);
+      x.low = seg.low;
       x.key0 = seg.key0 + kt * kAttnKeyTile;
       x.key1 = (int32_t)min((int64_t)seg.key1, (int64_t)x.key0 + (int64_t)take * kAttnKeyTile);
       x.table = s - 1;
@@ -199,8 +346,23 @@ __device__ __forceinline__ void attn_pieces(const AttnParams &p, int g, int h, F
       f(x);
       w += take;
     }
-    ++s;
+    tile0 += tiles;
   }
+}
+
+// The wide line of a call without a plan: the prefix and all rows.
+__device__ __forceinline__ int attn_plain_units(const AttnParams &p) {
+  return p.prefix_len > 0 ? (int)attn_up((int64_t)p.n_q * p.group, kAttnWideRows) : 0;
+}
+__device__ __forceinline__ AttnUnit attn_plain_unit(const AttnParams &p, int u) {
+  AttnUnit x = {};
+  x.row0 = u * kAttnWideRows;
+  x.rows = min(kAttnWideRows, p.n_q * p.group - x.row0);
+  x.key1 = p.prefix_len;
+  x.key_tiles = (int32_t)attn_up(p.prefix_len, kAttnWideKeys);
+  x.tile0 = (int64_t)u * x.key_tiles;
+  x.table = -1;
+  return x;
 }
 
 __device__ __forceinline__ void attn_wait_prior() {
@@ -212,7 +374,7 @@ __device__ __forceinline__ void attn_release_next() {
 
 cudaError_t launch_attn_general(const AttnParams &p, int32_t dtype, int32_t io, cudaStream_t s);
 // head_dim 64 or 128, 16-bit or 8-bit pool with 16-byte aligned heads.
-cudaError_t launch_attn_narrow(const AttnParams &p, int32_t dtype, int32_t io, cudaStream_t s);
+cudaError_t launch_attn_narrow(const AttnParams &p, int32_t dtype, int32_t io, bool hnd, cudaStream_t s);
 cudaError_t launch_attn_wide(const AttnParams &p, int32_t dtype, int32_t io, bool hnd, cudaStream_t s);
 
 }  // namespace kvx

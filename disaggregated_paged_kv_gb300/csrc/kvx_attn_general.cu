@@ -37,7 +37,11 @@ __global__ void __launch_bounds__(kThreads) attn_general_kernel(const AttnParams
   __shared__ int32_t slim[kRows];
   attn_wait_prior();
   const int g = blockIdx.x / p.kv_heads, head = blockIdx.x - g * p.kv_heads;
-  attn_pieces(p, g, head, [&](const AttnPiece &item) {
+  __shared__ int64_t scan[2 * (kThreads / 32) + 4];
+  __shared__ int32_t error;
+  if (tid == 0) error = 0;
+  const AttnLine line = attn_line<kThreads>(p, g, scan);
+  attn_pieces(p, g, head, line, [&](const AttnPiece &item) {
     __syncthreads();
     for (int i = tid; i < kRows * D; i += kThreads) {
       const int r = i / D, d = i - r * D;
@@ -50,7 +54,7 @@ __global__ void __launch_bounds__(kThreads) attn_general_kernel(const AttnParams
       }
       sq[i] = x;
     }
-    if (tid < kRows) slim[tid] = tid < item.rows ? p.limit[(item.row0 + tid) / p.group] : 0;
+    if (tid < kRows) slim[tid] = tid < item.rows ? attn_limit(p, (item.row0 + tid) / p.group) : 0;
     float acc[kRows][NC], m[kRows / 4], l[kRows / 4];
 #pragma unroll
     for (int r = 0; r < kRows; ++r)
@@ -62,10 +66,10 @@ __global__ void __launch_bounds__(kThreads) attn_general_kernel(const AttnParams
     int most = 0, least = INT32_MAX;
     for (int r = 0; r < item.rows; ++r) most = max(most, slim[r]), least = min(least, slim[r]);
     const int end = min(item.key1, most);
-    for (int k0 = item.key0; k0 < end; k0 += kKeys) {
+    for (int k0 = max(item.key0, item.low); k0 < end; k0 += kKeys) {
       const int nk = min(kKeys, end - k0);
       __syncthreads();  // the tile before has been read
-      if (tid < nk) soff[tid] = attn_key_offset(p, item.table, k0 + tid) + head * p.pool.head_stride;
+      if (tid < nk) soff[tid] = attn_key_offset(p, item.table, k0 + tid, &error) + head * p.pool.head_stride;
       __syncthreads();
       for (int i = tid; i < kKeys * D; i += kThreads) {
         const int j = i / D, d = i - j * D;
@@ -137,6 +141,8 @@ __global__ void __launch_bounds__(kThreads) attn_general_kernel(const AttnParams
         if (r < item.rows) p.part_m[item.part + r] = m[i], p.part_l[item.part + r] = l[i];
       }
   });
+  __syncthreads();
+  if (tid == 0) p.errors[blockIdx.x] = error;
 }
 
 template <typename KV, typename IO>

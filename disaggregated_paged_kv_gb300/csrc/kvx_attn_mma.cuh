@@ -87,6 +87,17 @@ __device__ __forceinline__ bool odd2(uint32_t x) {
   return (x & m) == m || ((x >> 16) & m) == m;
 }
 
+// What a row of bf16 queries is multiplied by on its way to f16, a power of two that brings its greatest
+// magnitude (given by its bits) to 2^14 .. 2^15; *factor, of its scores, is divided by it.  Both are
+// exact.  A row with an infinity or NaN stays as it is.
+__device__ __forceinline__ float half_scale(uint32_t bits, float *factor) {
+  const int e = (int)(bits >> 7);
+  if (e == 255) return 1.f;
+  const int up = min(268 - e, 253);
+  *factor *= __int_as_float((254 - up) << 23);
+  return __int_as_float(up << 23);
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -1,0 +1,89 @@
+// kvx_attn_tma.cuh -- how the tensor-core attention kernels bring key and value tiles to shared
+// memory: barriers with bounded waits, tensor copies of whole pages, and the tiles' arrangement.
+#pragma once
+
+#include <cuda.h>
+
+#include <cstdint>
+
+#include "kvx_attn.cuh"
+#include "kvx_attn_mma.cuh"
+
+namespace kvx {
+
+// How tiles come by tensor copies: boxes of `rows` (a multiple of 8) consecutive tokens of one page
+// and head.  A plane is seen as [group of 8 tokens][block of 64 16-bit columns][token][column] (8-bit
+// pools: [token][column]), so that a box arrives as the matrix operand's own arrangement.
+struct AttnTma {
+  int32_t rows;       // 0: no tensor copies (pages too short, or too many rows for an index)
+  int32_t head_x;     // a head's first block (8-bit pools: column): head * head_x
+  int64_t page_y, head_y;  // first token of (page, head): page * page_y + head * head_y
+};
+
+// A tile of D 16-bit columns a row: groups of eight rows, in them blocks of 64 columns, in them eight
+// rows of 128 bytes whose 16-byte chunks are exchanged by the row (128-byte swizzle), so that eight rows
+// of one chunk lie in different banks.  Byte place of 16-byte chunk c (of D / 8) of row r.
+template <int D>
+__device__ __forceinline__ uint32_t place(int r, int c) {
+  return (uint32_t)((r >> 3) * (D * 16) + (c >> 3) * 1024 + (r & 7) * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+// The same of an 8-bit tile as it comes: rows of D bytes, chunks exchanged by the row.
+template <int D>
+__device__ __forceinline__ uint32_t place8(int r, int c) {
+  return D == 128 ? (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)) : (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+}
+
+// No wait of a kernel is this long unless it is lost.
+constexpr uint64_t kAttnWaitNs = 2000000000ull;
+
+// ---- barriers ------------------------------------------------------------------------------
+__device__ __forceinline__ void bar_init(uint64_t *b, int n) {
+  asm volatile("mbarrier.init.shared.b64 [%0], %1;" ::"r"(smem_u32(b)), "r"(n) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint64_t *b) {
+  asm volatile("mbarrier.arrive.shared.b64 _, [%0];" ::"r"(smem_u32(b)) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint64_t *b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+               : "=r"(ok) : "r"(smem_u32(b)), "r"(parity) : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ void bar_expect(uint64_t *b, int bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared.b64 _, [%0], %1;" ::"r"(smem_u32(b)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void tma_load4(void *dst, const CUtensorMap *map, int z, int y, uint64_t *b) {
+  asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+               ::"r"(smem_u32(dst)), "l"(map), "r"(0), "r"(0), "r"(z), "r"(y), "r"(smem_u32(b)) : "memory");
+}
+__device__ __forceinline__ void tma_load(void *dst, const CUtensorMap *map, int x, int y, uint64_t *b) {
+  asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+               ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_u32(b)) : "memory");
+}
+__device__ __forceinline__ uint64_t now_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+  return t;
+}
+// False when the wait is given up: too long, or some other wait of the CTA was.
+__device__ __forceinline__ bool bar_wait_slow(uint64_t *b, uint32_t parity, volatile int32_t *lost, int32_t *error) {
+  const uint64_t t0 = now_ns();
+  for (;;) {
+    for (int i = 0; i < 64; ++i)
+      if (bar_try(b, parity)) return true;
+    if (*lost) return false;
+    if (now_ns() - t0 > kAttnWaitNs) {
+      *lost = 1;
+      *(volatile int32_t *)error = KVX_ERR_TIMEOUT;
+      return false;
+    }
+  }
+}
+
+// The planes of a call as AttnTma says, for tiles of `keys` keys.  Boxes are whole groups of 8 tokens of a
+// page; with other pages, or more rows than an index counts, the tiles come key by key (t->rows 0).
+void attn_make_tma(const AttnParams &p, int keys, bool fp8, bool hnd, AttnTma *t, CUtensorMap *km,
+                   CUtensorMap *vm);
+
+}  // namespace kvx

@@ -17,11 +17,11 @@
 // the sums in tensor memory are rescaled a few times in all instead of with every tile.
 #include <cuda.h>
 
-#include <cstring>
 #include <type_traits>
 
 #include "kvx_attn.cuh"
 #include "kvx_attn_mma.cuh"
+#include "kvx_attn_tma.cuh"
 #include "kvx_launch.cuh"
 
 namespace kvx {
@@ -30,7 +30,6 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kKeys = kAttnWideKeys;
 constexpr float kRenew = 8.f;
-constexpr uint64_t kWaitNs = 2000000000ull;  // no wait of the kernel is that long unless it is lost
 
 template <bool FP8, int D>
 struct Smem {
@@ -38,7 +37,7 @@ struct Smem {
   static constexpr int kRawStages = FP8 ? 3 : 1;
   alignas(1024) char q[2][128 * D * 2];
   alignas(1024) char kv[kStages][kKeys * D * 2];
-  alignas(128) char raw[kRawStages][FP8 ? kKeys * D : 128];  // 8-bit tiles as they come
+  alignas(1024) char raw[kRawStages][FP8 ? kKeys * D : 128];  // 8-bit tiles as they come
   int64_t off[kKeys];
   uint64_t q_full, full[kStages], empty[kStages], raw_full[kRawStages];
   uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], drained;
@@ -46,62 +45,9 @@ struct Smem {
   // infinities or NaN were taken out of the V tiles from there on
   int32_t least[2], odd[2];
   int32_t warp_least[4];
-  int32_t lost;
+  int32_t lost, error;
   uint32_t tmem;
 };
-
-// How tiles come by tensor copies: boxes of `rows` (a multiple of 8) consecutive tokens of one page
-// and head.  A plane is seen as [group of 8 tokens][block of 64 16-bit columns][token][column] (8-bit
-// pools: [token][column]), so that a box arrives as the matrix operand's own arrangement.
-struct WideTma {
-  int32_t rows;       // 0: no tensor copies (pages too short, or too many rows for an index)
-  int32_t head_x;     // a head's first block (8-bit pools: column): head * head_x
-  int64_t page_y, head_y;  // first token of (page, head): page * page_y + head * head_y
-};
-
-// ---- barriers ------------------------------------------------------------------------------
-__device__ __forceinline__ void bar_init(uint64_t *b, int n) {
-  asm volatile("mbarrier.init.shared.b64 [%0], %1;" ::"r"(smem_u32(b)), "r"(n) : "memory");
-}
-__device__ __forceinline__ void bar_arrive(uint64_t *b) {
-  asm volatile("mbarrier.arrive.shared.b64 _, [%0];" ::"r"(smem_u32(b)) : "memory");
-}
-__device__ __forceinline__ bool bar_try(uint64_t *b, uint32_t parity) {
-  uint32_t ok;
-  asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
-               : "=r"(ok) : "r"(smem_u32(b)), "r"(parity) : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ void bar_expect(uint64_t *b, int bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared.b64 _, [%0], %1;" ::"r"(smem_u32(b)), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void tma_load4(void *dst, const CUtensorMap *map, int z, int y, uint64_t *b) {
-  asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
-               ::"r"(smem_u32(dst)), "l"(map), "r"(0), "r"(0), "r"(z), "r"(y), "r"(smem_u32(b)) : "memory");
-}
-__device__ __forceinline__ void tma_load(void *dst, const CUtensorMap *map, int x, int y, uint64_t *b) {
-  asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-               ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_u32(b)) : "memory");
-}
-__device__ __forceinline__ uint64_t now_ns() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-  return t;
-}
-// False when the wait is given up: too long, or some other wait of the CTA was.
-__device__ __forceinline__ bool bar_wait_slow(uint64_t *b, uint32_t parity, volatile int32_t *lost, int32_t *status) {
-  const uint64_t t0 = now_ns();
-  for (;;) {
-    for (int i = 0; i < 64; ++i)
-      if (bar_try(b, parity)) return true;
-    if (*lost) return false;
-    if (now_ns() - t0 > kWaitNs) {
-      *lost = 1;
-      atomicMax(status, (int32_t)KVX_ERR_TIMEOUT);
-      return false;
-    }
-  }
-}
 
 // ---- tensor memory and products --------------------------------------------------------------
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
@@ -161,12 +107,6 @@ __device__ __forceinline__ uint64_t operand(uint32_t addr) {
          1ull << 46 | 2ull << 61;
 }
 
-// Byte place of 16-byte chunk c (of D / 8) of row r.
-template <int D>
-__device__ __forceinline__ uint32_t place(int r, int c) {
-  return (uint32_t)((r >> 3) * (D * 16) + (c >> 3) * 1024 + (r & 7) * 128 + (((c & 7) ^ (r & 7)) << 4));
-}
-
 struct WidePiece {
   int32_t row0, rows, key0, tiles, key1, table;
   bool first, whole;
@@ -175,13 +115,16 @@ struct WidePiece {
 // Calls f(piece) for every piece of group g; f returns false to stop.
 template <typename F>
 __device__ __forceinline__ void wide_pieces(const AttnParams &p, int g, F f) {
-  const int n = p.head->units;
-  const int64_t quota = p.head->wide_quota;
+  const int n = p.planned ? p.head->units : attn_plain_units(p);
+  if (n == 0) return;
+  const int64_t tiles = p.planned ? p.head->wide_tiles : (int64_t)n * attn_plain_unit(p, 0).key_tiles;
+  const int64_t quota = p.planned ? p.head->wide_quota : max((int64_t)1, attn_up(tiles, p.wide_groups));
   int64_t w = g * quota;
-  const int64_t end = min(p.head->wide_tiles, w + quota);
-  if (n == 0 || w >= end) return;
-  for (int u = attn_find(p.units, n, w); w < end; ++u) {
-    const AttnUnit x = p.units[u];
+  const int64_t end = min(tiles, w + quota);
+  if (w >= end) return;
+  int u = p.planned ? p.start[p.groups + g] : (int)(w / attn_plain_unit(p, 0).key_tiles);
+  for (; w < end; ++u) {
+    const AttnUnit x = p.planned ? p.units[u] : attn_plain_unit(p, u);
     if (w >= x.tile0 + x.key_tiles) continue;
     const int kt = (int)(w - x.tile0);
     WidePiece y;
@@ -199,15 +142,16 @@ __device__ __forceinline__ void wide_pieces(const AttnParams &p, int g, F f) {
 // The token of local row i of a piece; its row's member of the group is (row0 + i) % group.
 __device__ __forceinline__ int row_token(const AttnParams &p, const WidePiece &x, int i) {
   const int t = (x.row0 + i) / p.group;
-  return x.table < 0 ? p.prefix_tok[t] : t;
+  return x.table < 0 && p.planned ? p.prefix_tok[t] : t;
 }
 
-template <typename T, bool FP8, int D>
+template <typename IO, bool FP8, int D>
 __global__ void __launch_bounds__(kThreads, 1)
-attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ WideTma tma,
+attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnTma tma,
                  const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
   extern __shared__ char raw_smem[];
   using S = Smem<FP8, D>;
+  using T = typename std::conditional<FP8, __half, IO>::type;  // of the products
   constexpr int kStages = S::kStages;
   S &sm = *reinterpret_cast<S *>(raw_smem + (-smem_u32(raw_smem) & 1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -221,7 +165,7 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ W
       sm.odd[i] = 0;
     }
     bar_init(&sm.drained, 1);
-    sm.lost = 0;
+    sm.lost = sm.error = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 12) {
@@ -234,9 +178,10 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ W
   const uint32_t tm = sm.tmem;
   const uint32_t tmS[2] = {tm, tm + 128}, tmO[2] = {tm + 256, tm + 256 + D};
   attn_wait_prior();
+  attn_release_next();  // the narrow kernel may take over SMs as CTAs end; what it reads is there
   const int g = blockIdx.x / p.kv_heads, h = blockIdx.x - g * p.kv_heads;
   auto wait = [&](uint64_t *b, uint32_t parity) {
-    return bar_try(b, parity) || bar_wait_slow(b, parity, &sm.lost, p.status);
+    return bar_try(b, parity) || bar_wait_slow(b, parity, &sm.lost, &sm.error);
   };
 
   if (warp < 8) {
@@ -250,9 +195,28 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ W
       const bool active = x.rows > t * 128;
       const bool live = i < x.rows;
       const int token = live ? row_token(p, x, i) : 0;
-      const int lim = live ? min(p.limit[token], x.key1) : 0;
+      const int lim = live ? min(attn_limit(p, token), x.key1) : 0;
       const int member = (x.row0 + i) % p.group;
+      float scale = p.scale_log2;
       if (active) {  // this row's queries; the products of the piece before are done with the last
+        float f = 1.f;
+        if constexpr (FP8 && std::is_same<IO, __nv_bfloat16>::value) {  // see attn_narrow_kernel
+          const uint16_t *u = reinterpret_cast<const uint16_t *>(p.q + token * p.q_tok + (int64_t)(h * p.group + member) * p.q_head);
+          uint32_t most = 0;
+          if (live) {
+            if (p.q_vec) {
+#pragma unroll 8
+              for (int c = 0; c < D / 8; ++c) {
+                const uint4 w = reinterpret_cast<const uint4 *>(u)[c];
+                most = max(most, max(max(max(w.x & 0x7fffu, w.x >> 16 & 0x7fffu), max(w.y & 0x7fffu, w.y >> 16 & 0x7fffu)),
+                                     max(max(w.z & 0x7fffu, w.z >> 16 & 0x7fffu), max(w.w & 0x7fffu, w.w >> 16 & 0x7fffu))));
+              }
+            } else {
+              for (int d = 0; d < D; ++d) most = max(most, u[d] & 0x7fffu);
+            }
+          }
+          f = half_scale(most, &scale);
+        }
         const char *src = p.q + token * p.q_tok + (int64_t)(h * p.group + member) * p.q_head;
 #pragma unroll 1
         for (int c0 = 0; c0 < D / 8; c0 += 8) {
@@ -271,7 +235,16 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ W
             }
           }
 #pragma unroll
-          for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(sm.q[t] + place<D>(r, c0 + c)) = w[c];
+          for (int c = 0; c < 8; ++c) {
+            if constexpr (FP8 && std::is_same<IO, __nv_bfloat16>::value) {
+              uint32_t v[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                v[e] = pack2<__half>(__uint_as_float(v[e] << 16) * f, __uint_as_float(v[e] & 0xffff0000u) * f);
+              w[c] = make_uint4(v[0], v[1], v[2], v[3]);
+            }
+            *reinterpret_cast<uint4 *>(sm.q[t] + place<D>(r, c0 + c)) = w[c];
+          }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
@@ -301,7 +274,7 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ W
             t0 = fmaxf(t0, __uint_as_float(s[0][k])), t1 = fmaxf(t1, __uint_as_float(s[1][k]));
             t2 = fmaxf(t2, __uint_as_float(s[2][k])), t3 = fmaxf(t3, __uint_as_float(s[3][k]));
           }
-          const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * p.scale_log2;
+          const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * scale;
           const bool renew = top > m + kRenew || (m == -INFINITY && top > m);
           if (__any_sync(~0u, renew)) {
             const float f = !renew ? 1.f : m == -INFINITY ? 0.f : ex2(m - top);
@@ -325,8 +298,8 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ W
             uint32_t w[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
-              const float a = ex2(fmaf(__uint_as_float(s[c][2 * k]), p.scale_log2, -base));
-              const float b = ex2(fmaf(__uint_as_float(s[c][2 * k + 1]), p.scale_log2, -base));
+              const float a = ex2(fmaf(__uint_as_float(s[c][2 * k]), scale, -base));
+              const float b = ex2(fmaf(__uint_as_float(s[c][2 * k + 1]), scale, -base));
               l2.x += a, l2.y += b;
               w[k] = pack2<T>(a, b);  // rounded to the values' type for the product; the sum is not
             }
@@ -346,7 +319,7 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ W
         const int64_t part = attn_wide_part(p, x.first, g, h) + (x.first ? (int64_t)token * p.group + member : i);
         const bool direct = x.whole && x.table >= 0;
         const float inv = l == 0.f ? 0.f : p.v_scale / l;
-        T *out = reinterpret_cast<T *>(p.out + (int64_t)token * p.out_tok + (int64_t)qh * p.out_head);
+        IO *out = reinterpret_cast<IO *>(p.out + (int64_t)token * p.out_tok + (int64_t)qh * p.out_head);
         const int odd = *(volatile int32_t *)&sm.odd[parity], least = *(volatile int32_t *)&sm.least[parity];
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
@@ -361,7 +334,7 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ W
           } else if (odd) {
             // infinities and NaN that were taken out of tiles that some row's mask falls into
             for (int key = x.key0; key < lim; ++key) {
-              const char *v = p.pool.v + attn_key_offset(p, key < p.prefix_len ? -1 : x.table, key) +
+              const char *v = p.pool.v + attn_key_offset(p, key < p.prefix_len ? -1 : x.table, key, &sm.error) +
                               h * p.pool.head_stride;
               const int tile1 = x.key0 + ((key - x.key0) / kKeys + 1) * kKeys;
               if (tile1 <= least) continue;
@@ -382,7 +355,7 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ W
             uint32_t w[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k)
-              w[k] = pack2<T>(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
+              w[k] = pack2<IO>(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
             if (p.out_vec) {
 #pragma unroll
               for (int k = 0; k < 4; ++k)
@@ -459,7 +432,7 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ W
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int r = i + k * 128;
-        const int v = r < x.rows ? p.limit[row_token(p, x, r)] : 0;
+        const int v = r < x.rows ? attn_limit(p, row_token(p, x, r)) : 0;
         if (v > x.key0) least = min(least, v);
       }
       for (int o = 16; o; o >>= 1) least = min(least, __shfl_xor_sync(~0u, least, o));
@@ -481,14 +454,13 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ W
       // page look-ups: lane l of warp w has box 4 l + w of a regular tile
       auto row_of = [&](int pos) -> int {
         int pg, off;
-        if (p.pool.page_shift >= 0) pg = pos >> p.pool.page_shift, off = pos & (p.page_size - 1);
-        else pg = pos / p.page_size, off = pos - pg * p.page_size;
-        return (int)(attn_page(p, pos < p.prefix_len ? -1 : x.table, pg) * tma.page_y + h * tma.head_y + off);
+        attn_split(p, pos, &pg, &off);
+        return (int)(attn_page(p, pos < p.prefix_len ? -1 : x.table, pg, &sm.error) * tma.page_y + h * tma.head_y + off);
       };
       auto look = [&](int j) -> int64_t {  // of any tile, key by key
         const int pos = x.key0 + j * kKeys + i;
         return pos < x.key1
-                   ? attn_key_offset(p, pos < p.prefix_len ? -1 : x.table, pos) + h * p.pool.head_stride : 0;
+                   ? attn_key_offset(p, pos < p.prefix_len ? -1 : x.table, pos, &sm.error) + h * p.pool.head_stride : 0;
       };
       auto box0 = [&](int j) -> int {  // row of this lane's box
         return j < x.tiles && regular(j) && lane * 4 + pw < boxes
@@ -566,7 +538,7 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ W
               wait(&sm.raw_full[raw_out], raw_phase);
 #pragma unroll
               for (int k = 0; k < kPer; ++k)
-                raw[k] = *reinterpret_cast<const uint4 *>(sm.raw[raw_out] + (r0 + k * kStep) * D + c * 16);
+                raw[k] = *reinterpret_cast<const uint4 *>(sm.raw[raw_out] + place8<D>(r0 + k * kStep, c));
               asm volatile("bar.sync 1, 128;" ::: "memory");  // the raw stage may be filled again
               if (++raw_out == S::kRawStages) raw_out = 0, raw_phase ^= 1;
             }
@@ -695,76 +667,28 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ W
   fence_before();
   __syncthreads();
   fence_after();
+  if (tid == 0) p.errors[p.groups * p.kv_heads + blockIdx.x] = sm.error;
   if (warp == 12)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm) : "memory");
 }
 
-using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
-                              CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
-                              CUtensorMapFloatOOBfill);
-
-EncodeFn encoder() {
-  static const EncodeFn fn = [] {
-    void *f = nullptr;
-    cudaDriverEntryPointQueryResult r;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
-        r != cudaDriverEntryPointSuccess) {
-      (void)cudaGetLastError();
-      f = nullptr;
-    }
-    return reinterpret_cast<EncodeFn>(f);
-  }();
-  return fn;
-}
-
-// The planes as WideTma says.  Boxes are whole groups of 8 tokens of a page; with other pages, or
-// more rows than an index counts, the tiles come key by key.
-void make_tma(const AttnParams &p, bool fp8, bool hnd, WideTma *t, CUtensorMap *km, CUtensorMap *vm) {
-  *t = WideTma{};
-  const int64_t pages = p.pool.num_pages, D = p.head_dim;
-  const int64_t all = hnd ? pages * p.kv_heads * p.page_size : pages * p.page_size;
-  if (p.page_size % 8 != 0 || all > INT32_MAX || !encoder()) return;
-  int rows = kKeys;
-  while (p.page_size % rows != 0) rows >>= 1;
-  const cuuint64_t pitch = (cuuint64_t)p.pool.tok_stride;
-  const cuuint64_t columns = (cuuint64_t)(hnd ? D : D * p.kv_heads);
-  const cuuint64_t dims8[2] = {columns, (cuuint64_t)all}, strides8[1] = {pitch};
-  const cuuint32_t box8[2] = {(cuuint32_t)D, (cuuint32_t)rows};
-  const cuuint64_t dims[4] = {64, 8, columns / 64, (cuuint64_t)(all / 8)}, strides[3] = {pitch, 128, pitch * 8};
-  const cuuint32_t box[4] = {64, 8, (cuuint32_t)(D / 64), (cuuint32_t)(rows / 8)}, one[4] = {1, 1, 1, 1};
-  for (int kv = 0; kv < 2; ++kv)
-    if (encoder()(kv ? vm : km, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16,
-                  fp8 ? 2 : 4, const_cast<char *>(kv ? p.pool.v : p.pool.k), fp8 ? dims8 : dims,
-                  fp8 ? strides8 : strides, fp8 ? box8 : box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  fp8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return;
-  t->rows = rows;
-  t->head_x = hnd ? 0 : (int32_t)(fp8 ? D : D / 64);
-  t->page_y = hnd ? (int64_t)p.kv_heads * p.page_size : p.page_size;
-  t->head_y = hnd ? p.page_size : 0;
-}
-
-template <typename T, bool FP8, int D>
+template <typename IO, bool FP8, int D>
 cudaError_t launch(const AttnParams &p, bool hnd, cudaStream_t s) {
-  const void *fn = (const void *)attn_wide_kernel<T, FP8, D>;
+  const void *fn = (const void *)attn_wide_kernel<IO, FP8, D>;
   constexpr int kSmem = (int)sizeof(Smem<FP8, D>) + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory of one SM");
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  WideTma tma;
+  AttnTma tma;
   CUtensorMap km, vm;
-  std::memset(&km, 0, sizeof(km));
-  std::memset(&vm, 0, sizeof(vm));
-  make_tma(p, FP8, hnd, &tma, &km, &vm);
+  attn_make_tma(p, kKeys, FP8, hnd, &tma, &km, &vm);
   void *args[] = {const_cast<AttnParams *>(&p), &tma, &km, &vm};
   return launch_pdl(fn, dim3(p.wide_groups * p.kv_heads), dim3(kThreads), args, s, kSmem);
 }
 
-template <typename T, bool FP8>
+template <typename IO, bool FP8>
 cudaError_t launch_d(const AttnParams &p, bool hnd, cudaStream_t s) {
-  return p.head_dim == 64 ? launch<T, FP8, 64>(p, hnd, s) : launch<T, FP8, 128>(p, hnd, s);
+  return p.head_dim == 64 ? launch<IO, FP8, 64>(p, hnd, s) : launch<IO, FP8, 128>(p, hnd, s);
 }
 
 }  // namespace
