@@ -126,7 +126,7 @@ struct Consumer {
     float o[D / 8][4] = {}, m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
     int odd = 0;
     for (int k0 = x.key0; k0 < x.key1; k0 += kTileKeys) {
-      if (!bar_try(&sm.full[stage], phase)) bar_wait_slow(&sm.full[stage], phase, &sm.lost, &sm.error);
+      bar_wait(&sm.full[stage], phase, &sm.lost, &sm.error);
       const uint32_t kb = smem_u32(sm.kv[stage][0]), vb = smem_u32(sm.kv[stage][1]);
       const bool mixed = k0 + kTileKeys > least;
 #pragma unroll
@@ -422,7 +422,7 @@ attn_narrow_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
         const int row_now = row;
         const int64_t off_now = off;
         look(j + 1);
-        if (!bar_try(&sm.empty[stage], phase)) bar_wait_slow(&sm.empty[stage], phase, &sm.lost, &sm.error);
+        bar_wait(&sm.empty[stage], phase, &sm.lost, &sm.error);
         if (regular(j)) {
           // (a box may arrive before the tile's bytes are announced: the stage is not full before
           // thread 0 has arrived)

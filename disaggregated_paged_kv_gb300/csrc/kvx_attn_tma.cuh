@@ -34,8 +34,8 @@ __device__ __forceinline__ uint32_t place8(int r, int c) {
   return D == 128 ? (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)) : (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
 }
 
-// No wait of a kernel is this long unless it is lost.
-constexpr uint64_t kAttnWaitNs = 2000000000ull;
+// No wait of a kernel takes as many polls unless it is lost.
+constexpr uint32_t kAttnPolls = 1u << 19;
 
 // ---- barriers ------------------------------------------------------------------------------
 __device__ __forceinline__ void bar_init(uint64_t *b, int n) {
@@ -61,24 +61,18 @@ __device__ __forceinline__ void tma_load(void *dst, const CUtensorMap *map, int 
   asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
                ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_u32(b)) : "memory");
 }
-__device__ __forceinline__ uint64_t now_ns() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-  return t;
-}
-// False when the wait is given up: too long, or some other wait of the CTA was.
-__device__ __forceinline__ bool bar_wait_slow(uint64_t *b, uint32_t parity, volatile int32_t *lost, int32_t *error) {
-  const uint64_t t0 = now_ns();
-  for (;;) {
-    for (int i = 0; i < 64; ++i)
-      if (bar_try(b, parity)) return true;
-    if (*lost) return false;
-    if (now_ns() - t0 > kAttnWaitNs) {
-      *lost = 1;
+// Waits for a phase.  False when the wait is given up: after kAttnPolls polls (a poll waits some
+// microseconds itself), or because some other wait of the CTA was.
+__device__ __forceinline__ bool bar_wait(uint64_t *b, uint32_t parity, int32_t *lost, int32_t *error) {
+  for (uint32_t n = 0; !bar_try(b, parity); ++n) {
+    if (*(volatile int32_t *)lost) return false;
+    if (n == kAttnPolls) {
+      *(volatile int32_t *)lost = 1;
       *(volatile int32_t *)error = KVX_ERR_TIMEOUT;
       return false;
     }
   }
+  return true;
 }
 
 // The planes of a call as AttnTma says, for tiles of `keys` keys.  Boxes are whole groups of 8 tokens of a

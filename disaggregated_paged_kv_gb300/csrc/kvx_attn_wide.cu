@@ -50,20 +50,27 @@ struct Smem {
 };
 
 // ---- tensor memory and products --------------------------------------------------------------
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
-  asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
-               "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
-               ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add) : "memory");
+// One lane of the warp issues (lead != 0 there); the others pass by.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add, uint32_t lead) {
+  asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 p, %4, 0;\nsetp.ne.u32 q, %5, 0;\n"
+               "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
+               ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add), "r"(lead) : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
-  asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
-               "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
-               ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(add) : "memory");
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add, uint32_t lead) {
+  asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 p, %4, 0;\nsetp.ne.u32 q, %5, 0;\n"
+               "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
+               ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(add), "r"(lead) : "memory");
 }
 // The barrier is arrived at when all products issued before are done.
-__device__ __forceinline__ void mma_commit(uint64_t *b) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-               ::"r"(smem_u32(b)) : "memory");
+__device__ __forceinline__ void mma_commit(uint64_t *b, uint32_t lead) {
+  asm volatile("{\n.reg .pred q;\nsetp.ne.u32 q, %1, 0;\n"
+               "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}"
+               ::"r"(smem_u32(b)), "r"(lead) : "memory");
+}
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t r;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+  return r;
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -175,19 +182,19 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tm = sm.tmem;
-  const uint32_t tmS[2] = {tm, tm + 128}, tmO[2] = {tm + 256, tm + 256 + D};
+  constexpr uint32_t tm = 0;  // all 512 columns are this CTA's, so they begin at the first
   attn_wait_prior();
   attn_release_next();  // the narrow kernel may take over SMs as CTAs end; what it reads is there
   const int g = blockIdx.x / p.kv_heads, h = blockIdx.x - g * p.kv_heads;
   auto wait = [&](uint64_t *b, uint32_t parity) {
-    return bar_try(b, parity) || bar_wait_slow(b, parity, &sm.lost, &sm.error);
+    return bar_wait(b, parity, &sm.lost, &sm.error);
   };
 
   if (warp < 8) {
     // ---- softmax of row tile t, a thread a row ----
     asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
     const int t = warp >> 2, r = tid & 127;
+    const uint32_t tmS = tm + t * 128, tmO = tm + 256 + t * D;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     uint32_t s_phase = 0, o_phase = 0, parity = 0;
     wide_pieces(p, g, [&](const WidePiece &x) {
@@ -258,7 +265,7 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
           fence_after();
           uint32_t s[4][32];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(s[c], tmS[t] + lanes + c * 32);
+          for (int c = 0; c < 4; ++c) tmem_ld32(s[c], tmS + lanes + c * 32);
           tmem_wait_ld();
           const int k0 = x.key0 + j * kKeys, seen = lim - k0;
           if (seen < kKeys) {
@@ -284,11 +291,11 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
 #pragma unroll
               for (int c = 0; c < D / 16; ++c) {
                 uint32_t o[16];
-                tmem_ld16(o, tmO[t] + lanes + c * 16);
+                tmem_ld16(o, tmO + lanes + c * 16);
                 tmem_wait_ld();
 #pragma unroll
                 for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                tmem_st16(tmO[t] + lanes + c * 16, o);
+                tmem_st16(tmO + lanes + c * 16, o);
               }
             }
           }
@@ -303,7 +310,7 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
               l2.x += a, l2.y += b;
               w[k] = pack2<T>(a, b);  // rounded to the values' type for the product; the sum is not
             }
-            tmem_st16(tmS[t] + lanes + c * 16, w);
+            tmem_st16(tmS + lanes + c * 16, w);
           }
           tmem_wait_st();
           fence_before();
@@ -325,7 +332,7 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
           __syncwarp();
-          tmem_ld32(o, tmO[t] + lanes + c * 32);
+          tmem_ld32(o, tmO + lanes + c * 32);
           tmem_wait_ld();
           if (!live) continue;
           if (l == 0.f) {
@@ -424,7 +431,7 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
       }
       pend[0] = pend[1], pend[1] = b;
     };
-    // A wait that was given up is not waited for again (see bar_wait_slow): these threads then run
+    // A wait that was given up is not waited for again (see bar_wait): these threads then run
     // through what is left without waiting, since they meet at barriers of their own.
     wide_pieces(p, g, [&](const WidePiece &x) {
       // from where on live rows differ in what they see
@@ -595,81 +602,84 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
   } else {
     // ---- products ----
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    if (warp == 12 && lane == 0) {
+    if (warp == 12) {  // all lanes walk along, so that what they agree on stays in uniform registers
+      const uint32_t lead = elect_lane();
+      auto wait_all = [&](uint64_t *b, uint32_t parity) { return __all_sync(~0u, wait(b, parity)) != 0; };
       constexpr uint32_t kFmt = std::is_same<T, __half>::value ? 0u : 1u;
       constexpr uint32_t kBase = 1u << 4 | kFmt << 7 | kFmt << 10 | (128u >> 4) << 24;
       constexpr uint32_t kDescS = kBase | (uint32_t)(kKeys >> 3) << 17;
       constexpr uint32_t kDescO = kBase | (uint32_t)(D >> 3) << 17 | 1u << 16;  // V read across its rows
-      uint32_t stage = 0, phase = 0, q_phase = 0, p_phase[2] = {0, 0}, oe_phase = 1;
-      uint64_t qd[2];
-      for (int t = 0; t < 2; ++t) qd[t] = operand<D>(smem_u32(sm.q[t]));
+      // (everything is a function of t by arithmetic and the loops over t are unrolled: one thread issues
+      // a product every 64 cycles and has no time for tables in memory)
+      uint32_t stage = 0, phase = 0, q_phase = 0, p_phase = 0, oe_phase = 1;
+      const uint64_t q0 = operand<D>(smem_u32(sm.q[0])), kv0 = operand<D>(smem_u32(sm.kv[0]));
+      constexpr uint64_t kTileStep = 128 * D * 2 >> 4;
       auto scores = [&](int t, uint32_t kst) {
-        const uint64_t kd = operand<D>(smem_u32(sm.kv[kst]));
+        const uint64_t qd = q0 + t * kTileStep, kd = kv0 + kst * kTileStep;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint64_t step = (uint64_t)((k >> 2) * (1024 >> 4) + (k & 3) * 2);
-          mma_ss(tmS[t], qd[t] + step, kd + step, kDescS, k > 0);
+          mma_ss(tm + t * 128, qd + step, kd + step, kDescS, k > 0, lead);
         }
       };
       wide_pieces(p, g, [&](const WidePiece &x) {
-        const int tiles = x.tiles, nt = x.rows > 128 ? 2 : 1;
-        if (!wait(&sm.q_full, q_phase) || !wait(&sm.full[stage], phase)) return false;
+        const int tiles = x.tiles;
+        const bool two = x.rows > 128;
+        if (!wait_all(&sm.q_full, q_phase) || !wait_all(&sm.full[stage], phase)) return false;
         q_phase ^= 1;
         fence_after();
-        for (int t = 0; t < nt; ++t) {
-          scores(t, stage);
-          mma_commit(&sm.s_full[t]);
-        }
-        mma_commit(&sm.empty[stage]);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if (t == 0 || two) {
+            scores(t, stage);
+            mma_commit(&sm.s_full[t], lead);
+          }
+        mma_commit(&sm.empty[stage], lead);
         if (++stage == kStages) stage = 0, phase ^= 1;
         for (int j = 0; j < tiles; ++j) {
           const uint32_t vst = stage;
-          if (!wait(&sm.full[vst], phase)) return false;
+          if (!wait_all(&sm.full[vst], phase)) return false;
           if (++stage == kStages) stage = 0, phase ^= 1;
           const bool more = j + 1 < tiles;
-          if (more && !wait(&sm.full[stage], phase)) return false;
-          const uint64_t vd = operand<D>(smem_u32(sm.kv[vst]));
-          for (int t = 0; t < nt; ++t) {
-            if (j == 0 && !wait(&sm.o_empty[t], oe_phase)) return false;
-            if (!wait(&sm.p_full[t], p_phase[t])) return false;
-            p_phase[t] ^= 1;
-            fence_after();
+          if (more && !wait_all(&sm.full[stage], phase)) return false;
+          const uint64_t vd = kv0 + vst * kTileStep;
 #pragma unroll
-            for (int k = 0; k < kKeys / 16; ++k)
-              mma_ts(tmO[t], tmS[t] + k * 8, vd + (uint64_t)(k * (2 * D * 16 >> 4)), kDescO, j > 0 || k > 0);
-            if (more) {
-              scores(t, stage);
-              mma_commit(&sm.s_full[t]);
-            } else {
-              mma_commit(&sm.o_full[t]);
+          for (int t = 0; t < 2; ++t) {
+            if (j == 0 && !wait_all(&sm.o_empty[t], oe_phase)) return false;
+            if (t == 0 || two) {
+              if (!wait_all(&sm.p_full[t], p_phase >> t & 1)) return false;
+              fence_after();
+#pragma unroll
+              for (int k = 0; k < kKeys / 16; ++k)
+                mma_ts(tm + 256 + t * D, tm + t * 128 + k * 8, vd + (uint64_t)(k * (2 * D * 16 >> 4)), kDescO,
+                       j > 0 || k > 0, lead);
+              if (more) scores(t, stage);
             }
+            if (!more) mma_commit(&sm.o_full[t], lead);
+            else if (t == 0 || two) mma_commit(&sm.s_full[t], lead);
           }
-          mma_commit(&sm.empty[vst]);
+          p_phase ^= two ? 3 : 1;
+          mma_commit(&sm.empty[vst], lead);
           if (more) {
-            mma_commit(&sm.empty[stage]);
+            mma_commit(&sm.empty[stage], lead);
             if (++stage == kStages) stage = 0, phase ^= 1;
           }
-        }
-        if (nt == 1) {  // keeps the tiles in step
-          if (!wait(&sm.o_empty[1], oe_phase)) return false;
-          mma_commit(&sm.o_full[1]);
         }
         oe_phase ^= 1;
         return true;
       });
       if (*(volatile int32_t *)&sm.lost) {  // products in flight end before their memory is given up
-        mma_commit(&sm.drained);
+        mma_commit(&sm.drained, lead);
         for (int i = 0; i < 1 << 16 && !bar_try(&sm.drained, 0); ++i) {}
       }
     }
-    __syncwarp();
   }
   fence_before();
   __syncthreads();
   fence_after();
   if (tid == 0) p.errors[p.groups * p.kv_heads + blockIdx.x] = sm.error;
   if (warp == 12)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(sm.tmem) : "memory");
 }
 
 template <typename IO, bool FP8, int D>
