@@ -121,10 +121,14 @@ struct AttnParams {
   int32_t *status;
 };
 
-// The page id of position pos for an item's table, checked: an id outside the pool is reported
-// in *error (of the CTA) and read as page 0.
-__device__ __forceinline__ int32_t attn_page(const AttnParams &p, int32_t table, int64_t pg, int32_t *error) {
-  const int32_t id = table < 0 ? p.prefix_pages[pg] : p.tables[table * p.table_stride + pg];
+// The page id of entry pg of a table (-1: the prefix list), as it stands there.
+__device__ __forceinline__ int32_t attn_entry(const AttnParams &p, int32_t table, int64_t pg) {
+  return table < 0 ? p.prefix_pages[pg] : p.tables[table * p.table_stride + pg];
+}
+
+// A page id checked: one outside the pool is reported in *error (of the CTA) and read as page 0.
+// (Apart from the load, so that a look-up ahead of its use is not waited for at the check.)
+__device__ __forceinline__ int32_t attn_checked(const AttnParams &p, int32_t id, int32_t *error) {
   if ((uint32_t)id >= (uint64_t)p.pool.num_pages) {
     *(volatile int32_t *)error = KVX_ERR_OUT_OF_RANGE;
     return 0;
@@ -147,7 +151,7 @@ __device__ __forceinline__ void attn_split(const AttnParams &p, int32_t pos, int
 __device__ __forceinline__ int64_t attn_key_offset(const AttnParams &p, int32_t table, int32_t pos, int32_t *error) {
   int32_t pg, off;
   attn_split(p, pos, &pg, &off);
-  return attn_page(p, table, pg, error) * p.pool.page_stride + off * p.pool.tok_stride;
+  return attn_checked(p, attn_entry(p, table, pg), error) * p.pool.page_stride + off * p.pool.tok_stride;
 }
 
 // A request's query tokens and length as the kernels use them: clamped into what can be

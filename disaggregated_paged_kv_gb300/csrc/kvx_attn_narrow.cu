@@ -400,28 +400,20 @@ attn_narrow_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
       auto regular = [&](int j) {
         return tma.rows > 0 && x.key0 + j * kTileKeys >= x.low && x.key0 + (j + 1) * kTileKeys <= x.key1;
       };
-      // look-ups a tile ahead: the row of this lane's box, or the offset of key 16 pw + lane % 16
-      int row = 0;
-      int64_t off = 0;
-      auto look = [&](int j) {
-        if (j >= tiles) return;
-        if (regular(j)) {
-          if (box < boxes) {
-            int pg, o;
-            attn_split(p, x.key0 + j * kTileKeys + box * tma.rows, &pg, &o);
-            row = (int)(attn_page(p, x.table, pg, &sm.error) * tma.page_y + h * tma.head_y + o);
-          }
-        } else {
-          const int pos = x.key0 + j * kTileKeys + pw * 16 + (lane & 15);
-          off = pos >= x.low && pos < x.key1
-                    ? attn_key_offset(p, x.table, pos, &sm.error) + h * p.pool.head_stride : -1;
-        }
+      // look-ups a tile ahead: the page of this lane's box, or of key 16 pw + lane % 16
+      auto look = [&](int j) -> int32_t {
+        if (j >= tiles) return 0;
+        const bool reg = regular(j);
+        const int pos = x.key0 + j * kTileKeys + (reg ? box * tma.rows : pw * 16 + (lane & 15));
+        if (reg ? box >= boxes : pos < x.low || pos >= x.key1) return 0;
+        int pg, o;
+        attn_split(p, pos, &pg, &o);
+        return attn_entry(p, x.table, pg);
       };
-      look(0);
+      int32_t next = look(0);
       for (int j = 0; j < tiles; ++j) {
-        const int row_now = row;
-        const int64_t off_now = off;
-        look(j + 1);
+        const int32_t id = next;
+        next = look(j + 1);
         bar_wait(&sm.empty[stage], phase, &sm.lost, &sm.error);
         if (regular(j)) {
           // (a box may arrive before the tile's bytes are announced: the stage is not full before
@@ -429,17 +421,26 @@ attn_narrow_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
           if (tid == kConsumers) bar_expect(&sm.full[stage], 2 * S::kTile);
           if (box < boxes) {
             char *dst = sm.kv[stage][kv] + box * tma.rows * D * (FP8 ? 1 : 2);
-            if constexpr (FP8) tma_load(dst, kv ? &v_map : &k_map, h * tma.head_x, row_now, &sm.full[stage]);
-            else tma_load4(dst, kv ? &v_map : &k_map, h * tma.head_x, row_now >> 3, &sm.full[stage]);
+            int pg, o;
+            attn_split(p, x.key0 + j * kTileKeys + box * tma.rows, &pg, &o);
+            const int row = (int)(attn_checked(p, id, &sm.error) * tma.page_y + h * tma.head_y + o);
+            if constexpr (FP8) tma_load(dst, kv ? &v_map : &k_map, h * tma.head_x, row, &sm.full[stage]);
+            else tma_load4(dst, kv ? &v_map : &k_map, h * tma.head_x, row >> 3, &sm.full[stage]);
           }
           if (tid != kConsumers) bar_arrive(&sm.full[stage]);
         } else {
-          const int c = lane % kRaw;
+          const int c = lane % kRaw, pos = x.key0 + j * kTileKeys + pw * 16 + (lane & 15);
+          int64_t off = -1;
+          if (pos >= x.low && pos < x.key1) {
+            int pg, o;
+            attn_split(p, pos, &pg, &o);
+            off = attn_checked(p, id, &sm.error) * p.pool.page_stride + o * p.pool.tok_stride + h * p.pool.head_stride;
+          }
           const uint32_t kd = smem_u32(sm.kv[stage][0]), vd = smem_u32(sm.kv[stage][1]);
 #pragma unroll
           for (int i = 0; i < 16 / kPer; ++i) {
             const int r = i * kPer + lane / kRaw;
-            const int64_t at = __shfl_sync(~0u, off_now, r);
+            const int64_t at = __shfl_sync(~0u, off, r);
             const bool ok = at >= 0;
             cp_async16(kd + spot<FP8, D>(pw * 16 + r, c), p.pool.k + (ok ? at : 0) + c * 16, ok);
             cp_async16(vd + spot<FP8, D>(pw * 16 + r, c), p.pool.v + (ok ? at : 0) + c * 16, ok);

@@ -33,14 +33,14 @@ constexpr float kRenew = 8.f;
 
 template <bool FP8, int D>
 struct Smem {
-  static constexpr int kStages = FP8 ? 3 : 4;  // of one K or V tile each, as 16-bit values
+  static constexpr int kStages = FP8 ? 3 : 5;  // of one K or V tile each, as 16-bit values
   static constexpr int kRawStages = FP8 ? 3 : 1;
   alignas(1024) char q[2][128 * D * 2];
   alignas(1024) char kv[kStages][kKeys * D * 2];
   alignas(1024) char raw[kRawStages][FP8 ? kKeys * D : 128];  // 8-bit tiles as they come
   int64_t off[kKeys];
   uint64_t q_full, full[kStages], empty[kStages], raw_full[kRawStages];
-  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], drained;
+  uint64_t s_full[2], p_full[2][2], o_full[2], o_empty[2], drained;
   // of the piece, by its parity: the least position that a live row does not see, and whether
   // infinities or NaN were taken out of the V tiles from there on
   int32_t least[2], odd[2];
@@ -105,6 +105,36 @@ __device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t (&r)[16]) {
       : "memory");
 }
 
+// Two 32-bit floats at a time.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+  return r;
+}
+
 // A matrix operand in shared memory, D 16-bit columns a row: groups of eight rows, in them blocks of
 // 64 columns, in them eight rows of 128 bytes whose 16-byte chunks are exchanged by the row (128-byte
 // swizzle).  So eight rows are D * 16 bytes, blocks 1024 bytes apart.
@@ -167,7 +197,7 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
     for (int i = 0; i < S::kRawStages; ++i) bar_init(&sm.raw_full[i], 1);
     for (int i = 0; i < kStages; ++i) bar_init(&sm.full[i], 128), bar_init(&sm.empty[i], 1);
     for (int i = 0; i < 2; ++i) {
-      bar_init(&sm.s_full[i], 1), bar_init(&sm.p_full[i], 128);
+      bar_init(&sm.s_full[i], 1), bar_init(&sm.p_full[i][0], 128), bar_init(&sm.p_full[i][1], 128);
       bar_init(&sm.o_full[i], 1), bar_init(&sm.o_empty[i], 128);
       sm.odd[i] = 0;
     }
@@ -257,7 +287,7 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
       }
       bar_arrive(&sm.q_full);
       float m = -INFINITY;
-      float2 l2 = make_float2(0.f, 0.f);
+      uint64_t l2 = pair(0.f, 0.f);
       if (active) {
         for (int j = 0; j < x.tiles; ++j) {
           if (!__all_sync(~0u, wait(&sm.s_full[t], s_phase))) return false;
@@ -277,16 +307,16 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
           }
           float t0 = -INFINITY, t1 = -INFINITY, t2 = -INFINITY, t3 = -INFINITY;
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            t0 = fmaxf(t0, __uint_as_float(s[0][k])), t1 = fmaxf(t1, __uint_as_float(s[1][k]));
-            t2 = fmaxf(t2, __uint_as_float(s[2][k])), t3 = fmaxf(t3, __uint_as_float(s[3][k]));
+          for (int k = 0; k < 32; k += 2) {
+            t0 = max3(t0, s[0][k], s[0][k + 1]), t1 = max3(t1, s[1][k], s[1][k + 1]);
+            t2 = max3(t2, s[2][k], s[2][k + 1]), t3 = max3(t3, s[3][k], s[3][k + 1]);
           }
           const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * scale;
           const bool renew = top > m + kRenew || (m == -INFINITY && top > m);
           if (__any_sync(~0u, renew)) {
             const float f = !renew ? 1.f : m == -INFINITY ? 0.f : ex2(m - top);
             if (renew) m = top;
-            l2.x *= f, l2.y *= f;
+            l2 = mul2(l2, pair(f, f));
             if (j > 0) {  // S of this tile is done, so are the products before it
 #pragma unroll
               for (int c = 0; c < D / 16; ++c) {
@@ -299,29 +329,35 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
               }
             }
           }
-          const float base = m == -INFINITY ? 0.f : m;
+          const float base = m == -INFINITY ? 0.f : -m;
+          const uint64_t scale2 = pair(scale, scale), base2 = pair(base, base);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint32_t w[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
-              const float a = ex2(fmaf(__uint_as_float(s[c][2 * k]), scale, -base));
-              const float b = ex2(fmaf(__uint_as_float(s[c][2 * k + 1]), scale, -base));
-              l2.x += a, l2.y += b;
+              float a, b;
+              unpair(fma2(pair(__uint_as_float(s[c][2 * k]), __uint_as_float(s[c][2 * k + 1])), scale2, base2), a, b);
+              a = ex2(a), b = ex2(b);
+              l2 = add2(l2, pair(a, b));
               w[k] = pack2<T>(a, b);  // rounded to the values' type for the product; the sum is not
             }
             tmem_st16(tmS + lanes + c * 16, w);
+            if (c & 1) {  // the products with the first 64 keys need not wait for the others
+              tmem_wait_st();
+              fence_before();
+              bar_arrive(&sm.p_full[t][c >> 1]);
+            }
           }
-          tmem_wait_st();
-          fence_before();
-          bar_arrive(&sm.p_full[t]);
         }
       }
       if (!__all_sync(~0u, wait(&sm.o_full[t], o_phase))) return false;
       o_phase ^= 1;
       fence_after();
       if (active) {
-        const float l = l2.x + l2.y;
+        float l, l_odd;
+        unpair(l2, l, l_odd);
+        l += l_odd;
         const int qh = h * p.group + member;
         const int64_t part = attn_wide_part(p, x.first, g, h) + (x.first ? (int64_t)token * p.group + member : i);
         const bool direct = x.whole && x.table >= 0;
@@ -459,28 +495,31 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
       };
       const int boxes = tma.rows > 0 ? kKeys / tma.rows : 1, pw = warp - 8;
       // page look-ups: lane l of warp w has box 4 l + w of a regular tile
-      auto row_of = [&](int pos) -> int {
+      const int box = lane * 4 + pw;
+      auto box_page = [&](int j) -> int32_t {  // as it stands in the table; checked when it is used
+        if (j >= x.tiles || !regular(j) || box >= boxes) return 0;
         int pg, off;
+        const int pos = x.key0 + j * kKeys + box * tma.rows;
         attn_split(p, pos, &pg, &off);
-        return (int)(attn_page(p, pos < p.prefix_len ? -1 : x.table, pg, &sm.error) * tma.page_y + h * tma.head_y + off);
+        return attn_entry(p, pos < p.prefix_len ? -1 : x.table, pg);
+      };
+      auto box_row = [&](int j, int32_t id) -> int {
+        int pg, off;
+        attn_split(p, x.key0 + j * kKeys + box * tma.rows, &pg, &off);
+        return (int)(attn_checked(p, id, &sm.error) * tma.page_y + h * tma.head_y + off);
       };
       auto look = [&](int j) -> int64_t {  // of any tile, key by key
         const int pos = x.key0 + j * kKeys + i;
         return pos < x.key1
                    ? attn_key_offset(p, pos < p.prefix_len ? -1 : x.table, pos, &sm.error) + h * p.pool.head_stride : 0;
       };
-      auto box0 = [&](int j) -> int {  // row of this lane's box
-        return j < x.tiles && regular(j) && lane * 4 + pw < boxes
-                   ? row_of(x.key0 + j * kKeys + (lane * 4 + pw) * tma.rows) : 0;
-      };
       // this lane's box of K (kv 0) or V (1); a lane of each warp at most has work for short tiles
-      auto tensor = [&](int kv, int row, char *dst, uint64_t *bar) {
+      auto tensor = [&](int j, int kv, int32_t id, char *dst, uint64_t *bar) {
+        if (box >= boxes) return;
         const CUtensorMap *map = kv ? &v_map : &k_map;
-        const int b = lane * 4 + pw;
-        if (b < boxes) {
-          if constexpr (FP8) tma_load(dst + b * tma.rows * D, map, h * tma.head_x, row, bar);
-          else tma_load4(dst + b * tma.rows * D * 2, map, h * tma.head_x, row >> 3, bar);
-        }
+        const int row = box_row(j, id);
+        if constexpr (FP8) tma_load(dst + box * tma.rows * D, map, h * tma.head_x, row, bar);
+        else tma_load4(dst + box * tma.rows * D * 2, map, h * tma.head_x, row >> 3, bar);
       };
       auto convert = [&](const uint4 &v, char *dst, int r) {  // 16 8-bit values to their places
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -495,23 +534,24 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
       };
 
       // 8-bit tiles come by tensor copies some stages ahead of their conversion
-      int ahead = 0, ahead_row = box0(0);
+      int ahead = 0;
+      int32_t ahead_page = FP8 ? box_page(0) : 0, ahead_next = FP8 ? box_page(1) : 0;
       auto fetch = [&](int upto) {  // up to tile and half number `upto`
         for (; ahead < min(upto, 2 * x.tiles); ++ahead) {
           if (regular(ahead >> 1)) {
             if (i == 0) bar_expect(&sm.raw_full[raw_in], kKeys * D);
-            tensor(ahead & 1, ahead_row, sm.raw[raw_in], &sm.raw_full[raw_in]);
+            tensor(ahead >> 1, ahead & 1, ahead_page, sm.raw[raw_in], &sm.raw_full[raw_in]);
             if (++raw_in == S::kRawStages) raw_in = 0;
           }
-          if (ahead & 1) ahead_row = box0((ahead + 1) >> 1);
+          if (ahead & 1) ahead_page = ahead_next, ahead_next = box_page((ahead + 3) >> 1);
         }
       };
-      int next_row = FP8 ? 0 : box0(0);
+      int32_t next_page = FP8 ? 0 : box_page(0);
       for (int j = 0; j < x.tiles; ++j) {
         const int k0 = x.key0 + j * kKeys;
         const bool reg = regular(j);
-        const int row = next_row;
-        if constexpr (!FP8) next_row = box0(j + 1);
+        const int32_t page = next_page;
+        if constexpr (!FP8) next_page = box_page(j + 1);
         if (!reg) {
           // key by key; the tile that used these offsets before is done with by everyone
           const int64_t o = look(j);
@@ -556,7 +596,7 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
             // one arrival for the tile's bytes and one for each thread's boxes: those of a thread may
             // arrive before the bytes are announced, the stage is not full before the thread is
             if (i == 0) bar_expect(&sm.full[stage], kKeys * D * 2);
-            tensor(kv, row, dst, &sm.full[stage]);
+            tensor(j, kv, page, dst, &sm.full[stage]);
             if (i != 0) bar_arrive(&sm.full[stage]);
           } else {
 #pragma unroll
@@ -647,12 +687,15 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
           for (int t = 0; t < 2; ++t) {
             if (j == 0 && !wait_all(&sm.o_empty[t], oe_phase)) return false;
             if (t == 0 || two) {
-              if (!wait_all(&sm.p_full[t], p_phase >> t & 1)) return false;
-              fence_after();
 #pragma unroll
-              for (int k = 0; k < kKeys / 16; ++k)
+              for (int k = 0; k < kKeys / 16; ++k) {
+                if (k % (kKeys / 32) == 0) {
+                  if (!wait_all(&sm.p_full[t][k / (kKeys / 32)], p_phase >> t & 1)) return false;
+                  fence_after();
+                }
                 mma_ts(tm + 256 + t * D, tm + t * 128 + k * 8, vd + (uint64_t)(k * (2 * D * 16 >> 4)), kDescO,
                        j > 0 || k > 0, lead);
+              }
               if (more) scores(t, stage);
             }
             if (!more) mma_commit(&sm.o_full[t], lead);
