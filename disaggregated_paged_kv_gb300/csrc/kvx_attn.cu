@@ -57,8 +57,18 @@ __device__ __forceinline__ int last_at_or_before(const int32_t *base, int n, int
 
 __global__ void __launch_bounds__(kPlanCta) attn_plan_kernel(const AttnParams p) {
   __shared__ int64_t sm[32];
+  // the first requests' own first token, count, length and place (see AttnParams::prompt): calls of up to
+  // kPlanCta requests read them from here
+  __shared__ int32_t s_t0[kPlanCta + 1], s_len[kPlanCta], s_prompt[kPlanCta];
   attn_wait_prior();
   const int tid = threadIdx.x, n = p.n_reqs;
+  const bool small = n <= kPlanCta;
+  auto req = [&](int b) -> AttnReq {
+    if (small) return AttnReq{s_t0[b], s_t0[b + 1] - s_t0[b], s_len[b]};
+    int32_t none = 0;
+    return attn_request(p, b, &none);
+  };
+  auto place_of = [&](int b) -> int32_t { return small ? s_prompt[b] : p.prompt[b]; };
   int32_t bad = 0, most = 0;
   // check; how far the longest request reaches; which requests are prompts
   int64_t many = 0, plain = 0;
@@ -77,6 +87,10 @@ __global__ void __launch_bounds__(kPlanCta) attn_plan_kernel(const AttnParams p)
     if (b < n) {
       // a request's first place in prefix_tok, as an offset from its first token; prompts: none
       p.prompt[b] = prompt ? INT32_MIN : (int32_t)(at - r.t0);
+      if (small) {
+        s_t0[b] = r.t0, s_len[b] = r.len, s_prompt[b] = p.prompt[b];
+        if (b == n - 1) s_t0[n] = r.t0 + r.n;
+      }
       many += prompt;
     }
     plain += total;
@@ -94,15 +108,14 @@ __global__ void __launch_bounds__(kPlanCta) attn_plan_kernel(const AttnParams p)
     p.head->refused = any_range ? KVX_ERR_OUT_OF_RANGE : any_arg ? KVX_ERR_INVALID_ARG : KVX_OK;
   }
   // what each token sees, and whose it is
-  int32_t none = 0;
   const int32_t last = refused || n == 0 ? 0 : p.q_start ? p.q_start[n] : n;
   for (int t = tid; t < p.n_q; t += kPlanCta) {
     int b = -1, sees = 0;
     if (t < last) {
-      b = p.q_start ? last_at_or_before(p.q_start, n, t) : t;
-      const AttnReq r = attn_request(p, b, &none);
+      b = p.q_start ? last_at_or_before(small ? s_t0 : p.q_start, n, t) : t;
+      const AttnReq r = req(b);
       sees = max(0, r.len - r.n + (t - r.t0) + 1);
-      const int32_t at = p.prompt[b];
+      const int32_t at = place_of(b);
       if (at != INT32_MIN) p.prefix_tok[at + t] = t, p.prefix_at[t] = at + t;
     }
     p.owner[t] = b;
@@ -120,15 +133,15 @@ __global__ void __launch_bounds__(kPlanCta) attn_plan_kernel(const AttnParams p)
           g.rows = (int32_t)plain * p.group;
           g.key1 = prefix;
         }
-      } else if (p.prompt[s - 1] != INT32_MIN) {
-        const AttnReq r = attn_request(p, s - 1, &none);
+      } else if (place_of(s - 1) != INT32_MIN) {
+        const AttnReq r = req(s - 1);
         g.row0 = r.t0 * p.group;
         g.rows = r.n * p.group;
         g.low = p.prefix_len;
         g.key1 = r.len;
       }
-      attn_tile_seg(&g);
-      mine = attn_up(g.rows, p.row_tile) * g.key_tiles;
+      attn_tile_seg(p, &g);
+      mine = attn_length(p, g);
     }
     int64_t total;
     g.tile0 = tiles + block_excl(mine, &total, sm);
@@ -142,8 +155,8 @@ __global__ void __launch_bounds__(kPlanCta) attn_plan_kernel(const AttnParams p)
       const int s = s0 + tid;
       int64_t mine = 0, total;
       if (s == 0) mine = prefix > 0 ? attn_up(plain * p.group, kAttnWideRows) : 0;
-      else if (s <= n && any_prompt && p.prompt[s - 1] == INT32_MIN)
-        mine = attn_up((int64_t)attn_request(p, s - 1, &none).n * p.group, kAttnWideRows);
+      else if (s <= n && any_prompt && place_of(s - 1) == INT32_MIN)
+        mine = attn_up((int64_t)req(s - 1).n * p.group, kAttnWideRows);
       const int64_t at = units + block_excl(mine, &total, sm);
       if (s <= n) p.unit_base[s] = (int32_t)at;
       units += total;
@@ -163,7 +176,7 @@ __global__ void __launch_bounds__(kPlanCta) attn_plan_kernel(const AttnParams p)
           x.rows = (int32_t)min((int64_t)kAttnWideRows, plain * p.group - x.row0);
           x.key1 = prefix;
         } else {
-          const AttnReq r = attn_request(p, s - 1, &none);
+          const AttnReq r = req(s - 1);
           x.rows = min(kAttnWideRows, r.n * p.group - x.row0);
           // as far as its last row sees
           x.key1 = max(0, r.len - r.n + (x.row0 + x.rows - 1) / p.group + 1);
@@ -176,7 +189,7 @@ __global__ void __launch_bounds__(kPlanCta) attn_plan_kernel(const AttnParams p)
       wide += total;
     }
   }
-  const int64_t quota = max((int64_t)1, attn_up(tiles, p.groups));
+  const int64_t quota = max((int64_t)p.most_cost, attn_up(tiles, p.groups));
   const int64_t wide_quota = p.wide_groups > 0 ? max((int64_t)1, attn_up(wide, p.wide_groups)) : 1;
   if (tid == 0) {
     p.head->tiles = tiles;
@@ -278,8 +291,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid
       const AttnSeg &s = seg[k];
       if (s.key_tiles == 0) continue;
       const int unit = (r - s.row0) / p.row_tile, row0 = s.row0 + unit * p.row_tile;
-      const int64_t w = s.tile0 + (int64_t)unit * s.key_tiles;
-      const int g0 = group_of(w, head.quota), g1 = group_of(w + s.key_tiles - 1, head.quota);
+      const int64_t w = s.tile0 + (int64_t)unit * s.key_tiles * s.cost;
+      const int g0 = group_of(w, head.quota), g1 = group_of(w + (int64_t)(s.key_tiles - 1) * s.cost, head.quota);
       count[k] = g1 - g0 + 1;
       first[k] = attn_part(p, k == 0, true, 0, h, row0) + (r - row0);
       more[k] = attn_part(p, k == 0, false, g0, h, row0) + (r - row0);
@@ -318,7 +331,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid
       top = now;
       const float f = exp2f(m - base);
       l = fmaf(f, pl, l);
-#pragma unroll 4
+#pragma unroll 8
       for (int i = 0; i < left; ++i) {
         const float *o = p.part_o + __shfl_sync(~0u, at, i) * D;
         const float w = __shfl_sync(~0u, f, i);
@@ -412,6 +425,10 @@ namespace {
 
 // Calls with one query token a request do without the plan kernel up to this many requests.
 constexpr int kPlanReqs = 2048;
+
+// Operations from which the wide kernel takes the prefix and prompts (about 1200 TFLOP/s behind some 12
+// us) instead of the narrow one, 64 rows at a time (about 290 TFLOP/s, no launch of its own).
+constexpr double kWideWork = 4.5e9;
 
 struct Sizes {
   int64_t segs_off, units_off, start_off, base_off, prompt_off, limit_off, owner_off, tok_off, at_off;
@@ -524,9 +541,12 @@ extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_arg
     for (int i = 2 * a.layer; i < 2 * a.layer + 2; ++i)
       if (b0 < pool->plane[i] + pool->extent && pool->plane[i] < b1) return KVX_ERR_OVERLAP;
   }
-  // without prompts the wide kernel has the prefix alone; it takes the greatest score from the
-  // greatest product, so the factor between them has to be above 0
-  const bool wide = takes_wide(pool, a.n_q, a.q_heads) && (a.q_start || a.prefix_len > 0) &&
+  // What the wide kernel may have: the prefix, and with several tokens a request prompts, whose keys
+  // only the tables bound.  Below kWideWork operations its launch costs more than it saves.  It takes
+  // the greatest score from the greatest product, so the factor between them has to be above 0.
+  const double wide_keys = a.q_start ? (double)a.max_pages * a.page_size : (double)a.prefix_len;
+  const bool wide = takes_wide(pool, a.n_q, a.q_heads) &&
+                    4.0 * pool->head_dim * a.q_heads * a.n_q * wide_keys >= kWideWork &&
                     a.scale * a.k_scale > 0.f;
   const Sizes z = sizes(a.n_q, a.n_reqs, a.q_heads, pool->kv_heads, pool->head_dim, row_tile(pool),
                         wide);
@@ -578,6 +598,8 @@ extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_arg
   // a single token a request, and not so many requests that every CTA's adding them up tells
   p.planned = a.n_q == 0 || a.q_start || a.n_reqs > kPlanReqs;
   p.after_wide = wide;
+  const int32_t most_rows = p.planned ? INT32_MAX : wide ? p.group : std::max(p.group, a.n_q * p.group);
+  p.most_cost = attn_cost(most_rows, row_tile(pool));
   p.wide_groups = z.wide_groups;
   char *ws = static_cast<char *>(d_ws);
   p.head = reinterpret_cast<AttnHeader *>(ws);
@@ -607,7 +629,7 @@ extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_arg
     if (e == cudaSuccess && wide) e = launch_attn_wide(p, pool->dtype, a.q_dtype, hnd, s);
     if (e == cudaSuccess)
       e = tensor_cores(pool) ? launch_attn_narrow(p, pool->dtype, a.q_dtype, hnd, s)
-                             : launch_attn_general(p, pool->dtype, a.q_dtype, s);
+                             : launch_attn_general(p, pool->dtype, a.q_dtype, pool->vec == 16 && pool->seg_bytes % 16 == 0, s);
   }
   if (e == cudaSuccess) {
     const void *join = a.q_dtype == KVX_F32   ? join_kernel<float>(pool->head_dim)

@@ -9,10 +9,10 @@
 //            tiles of rows are full without the others', and one pass needs no join.
 // The narrow kernel (and the plain one) takes units of up to row_tile rows: own work, and the
 // prefix where there are few rows in all.  The wide kernel takes units of up to 256 rows: the
-// prefix and prompts.  A unit's keys are cut into tiles, all units' key tiles stand in a line, and
-// the line is dealt out evenly: group g of kv_heads CTAs, one CTA a head, takes tiles
-// [g * quota, (g + 1) * quota).  So every CTA has the same number of tiles whatever the lengths,
-// and the CTAs of a group read the heads of the same rows at the same time.
+// prefix and prompts.  A unit's keys are cut into tiles, all units' key tiles stand in a line, each as
+// long as its cost, and the line is dealt out evenly: group g of kv_heads CTAs, one CTA a head, takes
+// the tiles that begin in [g * quota, (g + 1) * quota).  So every CTA has about the same work whatever
+// the lengths, and the CTAs of a group read the heads of the same rows at the same time.
 //
 // A piece is what a CTA has of one unit.  It is worked through with a running maximum and sum and
 // leaves, per row, the unnormalised sum o = sum_j e^(s_j - m) v_j in 32 bits, m and
@@ -52,11 +52,13 @@ struct AttnPool {
 
 // Work of the narrow line: the prefix (first) or a request's own positions.
 struct AttnSeg {
-  int64_t tile0;       // its first key tile in the line
+  int64_t tile0;       // where its first key tile begins in the line
   int32_t row0, rows;
+  int32_t cost;        // of a tile
   int32_t low;         // its first position; tiles begin at multiples of their length, so that they
   int32_t key0, key1;  // hold whole pages: key0 is the first tile's begin, at most low
   int32_t key_tiles;   // of each unit; 0: no keys (or no rows)
+  int32_t pad;
 };
 
 // A unit of the wide line.  table: the request of a prompt, -1: the prefix, whose rows are those
@@ -93,6 +95,7 @@ struct AttnParams {
   int32_t page_size, max_pages, prefix_len;
   int32_t row_tile;      // rows of a narrow unit
   int32_t groups;        // groups of kv_heads CTAs, narrow line
+  int32_t most_cost;     // at least the cost of any tile of the call: no quota is below it
   int32_t wide_groups;   // of the wide line; 0: no wide kernel
   int32_t planned;       // 1: the plan kernel has laid the work out.  0: one query token a request,
                          // and every kernel works its part out from the lengths
@@ -191,7 +194,21 @@ __device__ __forceinline__ int32_t attn_limit(const AttnParams &p, int32_t t) {
 
 __host__ __device__ __forceinline__ int64_t attn_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-__device__ __forceinline__ void attn_tile_seg(AttnSeg *g) {
+// What a tile of a unit with that many rows costs: with up to 16 rows it is the bytes, with more the
+// products, which four warps share between 16-row groups.  (Tiles of 64 rows take 2 to 4 times the time of
+// tiles of 16 rows, depending on what else the SM has.)
+__host__ __device__ __forceinline__ int32_t attn_cost(int32_t rows, int32_t row_tile) {
+  const int32_t r = rows < row_tile ? rows : row_tile;
+  return r <= 16 ? 1 : r <= 32 ? 2 : 4;
+}
+
+// The length of a seg in the line.
+__device__ __forceinline__ int64_t attn_length(const AttnParams &p, const AttnSeg &g) {
+  return attn_up(g.rows, p.row_tile) * g.key_tiles * g.cost;
+}
+
+__device__ __forceinline__ void attn_tile_seg(const AttnParams &p, AttnSeg *g) {
+  g->cost = attn_cost(g->rows, p.row_tile);
   g->key0 = g->low / kAttnKeyTile * kAttnKeyTile;
   if (g->rows > 0 && g->key1 > g->low)
     g->key_tiles = (int32_t)attn_up((int64_t)g->key1 - g->key0, kAttnKeyTile);
@@ -207,7 +224,7 @@ __device__ __forceinline__ AttnSeg attn_plain_seg(const AttnParams &p, int s, in
     g.row0 = r.t0 * p.group, g.rows = p.group;
     g.low = p.prefix_len, g.key1 = r.len;
   }
-  attn_tile_seg(&g);
+  attn_tile_seg(p, &g);
   return g;
 }
 
@@ -273,8 +290,7 @@ __device__ __forceinline__ AttnLine attn_line(const AttnParams &p, int g, int64_
   int32_t bad = 0;
   int64_t mine = 0;
   for (int s = s0; s < s1; ++s) {
-    const AttnSeg g = attn_plain_seg(p, s, &bad);
-    mine += attn_up(g.rows, p.row_tile) * g.key_tiles;
+    mine += attn_length(p, attn_plain_seg(p, s, &bad));
   }
   int64_t x = mine;
   for (int d = 1; d < 32; d <<= 1) {
@@ -292,14 +308,14 @@ __device__ __forceinline__ AttnLine attn_line(const AttnParams &p, int g, int64_
     bad = max(bad, (int32_t)sm[kWarps + i]);
   }
   before += x - mine;
-  const int64_t quota = max((int64_t)1, attn_up(total, p.groups));
+  const int64_t quota = max((int64_t)p.most_cost, attn_up(total, p.groups));
   if (blockIdx.x == 0) {
     int64_t at = before;
     for (int s = s0; s < s1; ++s) {
       AttnSeg g = attn_plain_seg(p, s, &bad);
       g.tile0 = at;
       p.segs[s] = g;
-      at += attn_up(g.rows, p.row_tile) * g.key_tiles;
+      at += attn_length(p, g);
     }
     if (tid == 0) p.head->tiles = total, p.head->quota = quota, p.head->refused = bad;
   }
@@ -312,8 +328,7 @@ __device__ __forceinline__ AttnLine attn_line(const AttnParams &p, int g, int64_
   if (before <= l.w && l.w < before + mine) {
     int64_t at = before;
     for (int s = s0; s < s1; ++s) {
-      const AttnSeg g = attn_plain_seg(p, s, &bad);
-      const int64_t next = at + attn_up(g.rows, p.row_tile) * g.key_tiles;
+      const int64_t next = at + attn_length(p, attn_plain_seg(p, s, &bad));
       if (l.w < next) {
         sm[2 * kWarps] = s, sm[2 * kWarps + 1] = at;
         break;
@@ -335,10 +350,12 @@ __device__ __forceinline__ void attn_pieces(const AttnParams &p, int g, int h, c
   for (int s = l.seg; w < l.end; ++s) {
     const AttnSeg seg = p.planned ? p.segs[s] : attn_plain_seg(p, s, &none);
     const int64_t tiles = attn_up(seg.rows, p.row_tile) * seg.key_tiles;
-    while (w < l.end && w < tile0 + tiles) {
-      const int64_t at = w - tile0;
+    // the seg's tiles that begin in this group's part: at .. last - 1
+    int64_t at = attn_up(max(w - tile0, (int64_t)0), seg.cost);
+    const int64_t last = min(tiles, attn_up(l.end - tile0, seg.cost));
+    while (at < last) {
       const int unit = (int)(at / seg.key_tiles), kt = (int)(at - (int64_t)unit * seg.key_tiles);
-      const int take = (int)min((int64_t)(seg.key_tiles - kt), l.end - w);
+      const int take = (int)min((int64_t)(seg.key_tiles - kt), last - at);
       AttnPiece x;
       x.row0 = seg.row0 + unit * p.row_tile;
       x.rows = min(p.row_tile, seg.rows - unit * p.row_tile);
@@ -348,9 +365,10 @@ __device__ __forceinline__ void attn_pieces(const AttnParams &p, int g, int h, c
       x.table = s - 1;
       x.part = attn_part(p, s == 0, kt == 0, g, h, x.row0);
       f(x);
-      w += take;
+      at += take;
     }
-    tile0 += tiles;
+    tile0 += tiles * seg.cost;
+    w = max(w, tile0);
   }
 }
 
@@ -376,7 +394,8 @@ __device__ __forceinline__ void attn_release_next() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-cudaError_t launch_attn_general(const AttnParams &p, int32_t dtype, int32_t io, cudaStream_t s);
+// vec: heads are whole 16-byte pieces on 16-byte boundaries.
+cudaError_t launch_attn_general(const AttnParams &p, int32_t dtype, int32_t io, bool vec, cudaStream_t s);
 // head_dim 64 or 128, 16-bit or 8-bit pool with 16-byte aligned heads.
 cudaError_t launch_attn_narrow(const AttnParams &p, int32_t dtype, int32_t io, bool hnd, cudaStream_t s);
 cudaError_t launch_attn_wide(const AttnParams &p, int32_t dtype, int32_t io, bool hnd, cudaStream_t s);
