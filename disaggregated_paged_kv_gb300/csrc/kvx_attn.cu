@@ -189,8 +189,9 @@ __global__ void __launch_bounds__(kPlanCta) attn_plan_kernel(const AttnParams p)
       wide += total;
     }
   }
-  const int64_t quota = max((int64_t)p.most_cost, attn_up(tiles, p.groups));
-  const int64_t wide_quota = p.wide_groups > 0 ? max((int64_t)1, attn_up(wide, p.wide_groups)) : 1;
+  const AttnShare share = attn_share(p, tiles, wide);
+  const int64_t quota = max((int64_t)1, attn_up(tiles, share.groups));
+  const int64_t wide_quota = p.wide_groups > 0 ? max((int64_t)1, attn_up(wide, share.wide_groups)) : 1;
   if (tid == 0) {
     p.head->tiles = tiles;
     p.head->quota = quota;
@@ -222,12 +223,6 @@ __device__ __forceinline__ void put(__half *o, float x) { *o = __float2half_rn(x
 __device__ __forceinline__ void put(__nv_bfloat16 *o, float x) { *o = __float2bfloat16_rn(x); }
 
 constexpr int kJoinWarps = 4;
-
-// Which group's part of a line a tile is in; 32-bit arithmetic where it is enough.
-__device__ __forceinline__ int group_of(int64_t tile, int64_t quota) {
-  if (((tile | quota) >> 31) == 0) return (int)((uint32_t)tile / (uint32_t)quota);
-  return (int)(tile / quota);
-}
 
 // A block joins the parts of `heads` query heads of one token, a warp a head at a time, prefix splits
 // first, in order.  DK: head_dim, 0: any.
@@ -267,21 +262,23 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid
   const int qh1 = min(p.q_heads, (int)(blockIdx.y + 1) * heads);
   for (int qh = blockIdx.y * heads + warp; qh < qh1; qh += kJoinWarps) {
     const int h = qh / p.group, member = qh - h * p.group, r = t * p.group + member;
-    // the pieces of the row: n0 of the prefix (or of the prompt), then the request's own
-    int64_t first[2], more[2], step[2];
-    int count[2] = {0, 0};
+    // the pieces of the row: n0 of the prefix (or of the prompt), then the request's own.  The first is at
+    // the row's own place, piece i of group g at more + g * step; g is g0 + i, or where a group's part is
+    // shorter than a tile that of the i-th tile
+    int64_t first[2], more[2], step[2], begin[2];
+    int count[2] = {0, 0}, g0s[2], costs[2] = {0, 0};
     if (some && p.wide_groups > 0) {
       const int wr = wide_row + member, u = unit0 + (wr - lead) / kAttnWideRows;
       if (u < units) {
         const AttnUnit x = p.planned ? p.units[u] : attn_plain_unit(p, u);
-        const int64_t q = p.planned ? head.wide_quota
-                                    : max((int64_t)1, attn_up((int64_t)units * x.key_tiles, p.wide_groups));
+        const int64_t q = head.wide_quota;
         if (x.key_tiles > 0 && x.table == (prompt ? b : -1)) {
-          const int g0 = group_of(x.tile0, q), g1 = group_of(x.tile0 + x.key_tiles - 1, q);
+          const int g0 = (int)attn_div(x.tile0, q), g1 = (int)attn_div(x.tile0 + x.key_tiles - 1, q);
           if (prompt && g0 == g1) continue;  // the wide kernel has written the result
           count[0] = g1 - g0 + 1;
+          g0s[0] = g0;
           first[0] = attn_wide_part(p, true, 0, h) + r;
-          more[0] = attn_wide_part(p, false, g0, h) + (wr - x.row0);
+          more[0] = attn_wide_part(p, false, 0, h) + (wr - x.row0);
           step[0] = (int64_t)p.kv_heads * kAttnWideRows;
         }
       }
@@ -292,17 +289,23 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid
       if (s.key_tiles == 0) continue;
       const int unit = (r - s.row0) / p.row_tile, row0 = s.row0 + unit * p.row_tile;
       const int64_t w = s.tile0 + (int64_t)unit * s.key_tiles * s.cost;
-      const int g0 = group_of(w, head.quota), g1 = group_of(w + (int64_t)(s.key_tiles - 1) * s.cost, head.quota);
-      count[k] = g1 - g0 + 1;
+      g0s[k] = (int)attn_div(w, head.quota);
+      count[k] = s.key_tiles;
+      if (s.cost <= head.quota)
+        count[k] = (int)attn_div(w + (int64_t)(s.key_tiles - 1) * s.cost, head.quota) - g0s[k] + 1;
+      else
+        costs[k] = s.cost, begin[k] = w;
       first[k] = attn_part(p, k == 0, true, 0, h, row0) + (r - row0);
-      more[k] = attn_part(p, k == 0, false, g0, h, row0) + (r - row0);
+      more[k] = attn_part(p, k == 0, false, 0, h, row0) + (r - row0);
       step[k] = (int64_t)p.kv_heads * p.row_tile;
     }
     const int n0 = count[0], n = n0 + count[1];
     auto part = [&](int i) {
       const int k = i < n0 ? 0 : 1;
       i -= k ? n0 : 0;
-      return i == 0 ? first[k] : more[k] + i * step[k];
+      if (i == 0) return first[k];
+      const int g = costs[k] ? (int)attn_div(begin[k] + (int64_t)i * costs[k], head.quota) : g0s[k] + i;
+      return more[k] + g * step[k];
     };
     // lane i has part i (of 32 at a time); all lanes then add the parts, neighbouring columns a lane
     float top = -INFINITY, l = 0.f;
@@ -441,8 +444,8 @@ Sizes sizes(int64_t n_q, int64_t n_reqs, int64_t q_heads, int64_t kv_heads, int6
             bool wide) {
   Sizes z = {};
   const int64_t rows = n_q * (q_heads / kv_heads);
-  z.groups = (int32_t)std::max((int64_t)1, 152 * 2 / kv_heads);
-  z.wide_groups = wide ? (int32_t)std::max((int64_t)1, 152 / kv_heads) : 0;
+  z.groups = (int32_t)std::max((int64_t)1, kAttnSms * 2 / kv_heads);
+  z.wide_groups = wide ? (int32_t)std::max((int64_t)1, kAttnSms / kv_heads) : 0;
   z.errors = z.groups * kv_heads + z.wide_groups * kv_heads;
   const int64_t parts = 2 * n_q * q_heads + z.groups * kv_heads * row_tile +
                         z.wide_groups * kv_heads * kAttnWideRows;
@@ -590,17 +593,16 @@ extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_arg
   p.max_pages = a.max_pages;
   p.prefix_len = a.prefix_len;
   p.row_tile = row_tile(pool);
+  p.key_bytes = pool->elem;
   const uintptr_t q_at = (uintptr_t)a.q | (uintptr_t)p.q_tok | (uintptr_t)p.q_head;
   p.q_even = q_at % 4 == 0;
   p.q_vec = q_at % 16 == 0;
   p.out_vec = ((uintptr_t)a.out | (uintptr_t)p.out_tok | (uintptr_t)p.out_head) % 16 == 0;
   p.groups = z.groups;
+  p.wide_groups = z.wide_groups;
   // a single token a request, and not so many requests that every CTA's adding them up tells
   p.planned = a.n_q == 0 || a.q_start || a.n_reqs > kPlanReqs;
   p.after_wide = wide;
-  const int32_t most_rows = p.planned ? INT32_MAX : wide ? p.group : std::max(p.group, a.n_q * p.group);
-  p.most_cost = attn_cost(most_rows, row_tile(pool));
-  p.wide_groups = z.wide_groups;
   char *ws = static_cast<char *>(d_ws);
   p.head = reinterpret_cast<AttnHeader *>(ws);
   p.segs = reinterpret_cast<AttnSeg *>(ws + z.segs_off);
@@ -637,7 +639,7 @@ extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_arg
                                               : join_kernel<__nv_bfloat16>(pool->head_dim);
     // a warp a row while that fills the GPU; then a block a token, which reads what is the token's once
     int heads = kJoinWarps;
-    if ((int64_t)a.n_q * a.q_heads > (int64_t)kJoinWarps * 152 * 16 || a.q_heads > kJoinWarps * 65535)
+    if ((int64_t)a.n_q * a.q_heads > (int64_t)kJoinWarps * kAttnSms * 16 || a.q_heads > kJoinWarps * 65535)
       heads = a.q_heads;
     void *jargs[] = {&p, &heads};
     e = launch_pdl(join, dim3((unsigned)std::max(1, a.n_q), (unsigned)((a.q_heads + heads - 1) / heads)),

@@ -93,9 +93,9 @@ struct AttnParams {
   float v_scale;
   int32_t n_q, n_reqs, q_heads, kv_heads, group, head_dim;
   int32_t page_size, max_pages, prefix_len;
+  int32_t key_bytes;     // of an element of the pool
   int32_t row_tile;      // rows of a narrow unit
   int32_t groups;        // groups of kv_heads CTAs, narrow line
-  int32_t most_cost;     // at least the cost of any tile of the call: no quota is below it
   int32_t wide_groups;   // of the wide line; 0: no wide kernel
   int32_t planned;       // 1: the plan kernel has laid the work out.  0: one query token a request,
                          // and every kernel works its part out from the lengths
@@ -192,7 +192,12 @@ __device__ __forceinline__ int32_t attn_limit(const AttnParams &p, int32_t t) {
   return p.planned ? p.limit[t] : max(0, p.seq_lens[t]);
 }
 
-__host__ __device__ __forceinline__ int64_t attn_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+// a / b for a >= 0, b > 0; in 32 bits, an order of magnitude sooner, where that is enough.
+__device__ __forceinline__ int64_t attn_div(int64_t a, int64_t b) {
+  if (((a | b) >> 31) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+__device__ __forceinline__ int64_t attn_up(int64_t a, int64_t b) { return attn_div(a + b - 1, b); }
 
 // What a tile of a unit with that many rows costs: with up to 16 rows it is the bytes, with more the
 // products, which four warps share between 16-row groups.  (Tiles of 64 rows take 2 to 4 times the time of
@@ -202,9 +207,13 @@ __host__ __device__ __forceinline__ int32_t attn_cost(int32_t rows, int32_t row_
   return r <= 16 ? 1 : r <= 32 ? 2 : 4;
 }
 
+__device__ __forceinline__ int64_t attn_units(const AttnParams &p, int32_t rows) {
+  return rows <= p.row_tile ? rows > 0 : attn_up(rows, p.row_tile);
+}
+
 // The length of a seg in the line.
 __device__ __forceinline__ int64_t attn_length(const AttnParams &p, const AttnSeg &g) {
-  return attn_up(g.rows, p.row_tile) * g.key_tiles * g.cost;
+  return attn_units(p, g.rows) * g.key_tiles * g.cost;
 }
 
 __device__ __forceinline__ void attn_tile_seg(const AttnParams &p, AttnSeg *g) {
@@ -263,6 +272,99 @@ struct AttnPiece {
   int32_t row0, rows, low, key0, key1, table;
 };
 
+// How many groups of each line have work.  Both lines at once, on SMs of their own, where that is
+// estimated to end sooner than one after the other on all: the narrow line is bound by the bytes, which
+// half of the SMs read nearly as fast as all of them (311 against 260 us for 1.57 GB), the wide line by its
+// SMs.  Every kernel that needs it works it out by itself, in whole numbers, from the same totals.
+struct AttnShare {
+  int32_t groups, wide_groups;
+};
+
+// The shapes of the GPU, and measured times in ns: of a CTA's tile of 128 keys and 256 rows; of 16 bytes
+// of a narrow tile, two CTAs on the SM; of 1 MB at the memory's rate; and what a launch takes before and
+// after its tiles.
+constexpr int kAttnSms = 152;
+constexpr int64_t kAttnWideNs = 2300, kAttnNarrowPs = 470, kAttnMbNs = 160, kAttnStartNs = 9000;
+
+__device__ __forceinline__ AttnShare attn_share(const AttnParams &p, int64_t own, int64_t wide) {
+  AttnShare s = {p.groups, p.wide_groups};
+  if (p.wide_groups < 2 || own == 0 || wide == 0) return s;
+  const int64_t bytes = (int64_t)kAttnKeyTile * p.head_dim * p.key_bytes * 2;  // of a narrow tile
+  const int64_t floor_ns = (own * p.kv_heads * bytes >> 20) * kAttnMbNs;
+  // (short lines, and those that the SMs bound, gain nothing)
+  if (floor_ns < 4 * kAttnStartNs || floor_ns < attn_up(own, p.groups) * (bytes / 16 * kAttnNarrowPs) / 1000) return s;
+  auto narrow_ns = [&](int64_t groups) {
+    const int64_t sm = attn_up(own, groups) * (bytes / 16 * kAttnNarrowPs) / 1000;
+    return kAttnStartNs + (sm > floor_ns ? sm : floor_ns);
+  };
+  auto wide_ns = [&](int64_t groups) { return kAttnStartNs + attn_up(wide, groups) * kAttnWideNs; };
+  int64_t best = wide_ns(p.wide_groups) + narrow_ns(p.groups);
+  int at = p.wide_groups;
+  for (int g = 1 + (threadIdx.x & 31); g < p.wide_groups; g += 32) {
+    const int left = (kAttnSms - g * p.kv_heads) * 2 / p.kv_heads;
+    if (left < 1) continue;
+    const int64_t a = wide_ns(g), b = narrow_ns(left), both = a > b ? a : b;
+    if (both < best) best = both, at = g;
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    const int64_t b = __shfl_xor_sync(~0u, best, o);
+    const int g = __shfl_xor_sync(~0u, at, o);
+    if (b < best || (b == best && g < at)) best = b, at = g;
+  }
+  if (at < p.wide_groups) s.wide_groups = at, s.groups = min(p.groups, (kAttnSms - at * p.kv_heads) * 2 / p.kv_heads);
+  return s;
+}
+
+// The wide line of a call without a plan: the prefix and all rows.
+__device__ __forceinline__ int attn_plain_units(const AttnParams &p) {
+  return p.prefix_len > 0 ? (int)attn_up((int64_t)p.n_q * p.group, kAttnWideRows) : 0;
+}
+__device__ __forceinline__ AttnUnit attn_plain_unit(const AttnParams &p, int u) {
+  AttnUnit x = {};
+  x.row0 = u * kAttnWideRows;
+  x.rows = min(kAttnWideRows, p.n_q * p.group - x.row0);
+  x.key1 = p.prefix_len;
+  x.key_tiles = (int32_t)attn_up(p.prefix_len, kAttnWideKeys);
+  x.tile0 = (int64_t)u * x.key_tiles;
+  x.table = -1;
+  return x;
+}
+__device__ __forceinline__ int64_t attn_plain_wide(const AttnParams &p) {
+  return p.wide_groups ? (int64_t)attn_plain_units(p) * attn_plain_unit(p, 0).key_tiles : 0;
+}
+
+// The length of the narrow line of a call without a plan, added up by the CTA's Threads threads; *before,
+// *mine: where the thread's segs begin and how long they are; returns the verdict on the arguments in
+// *bad.  sm: two words a warp.
+template <int Threads>
+__device__ __forceinline__ int64_t attn_plain_total(const AttnParams &p, int64_t *sm, int64_t *before,
+                                                    int64_t *mine, int32_t *bad) {
+  constexpr int kWarps = Threads / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = 1 + p.n_reqs;
+  const int per = (n + Threads - 1) / Threads, s0 = min(tid * per, n), s1 = min(s0 + per, n);
+  *bad = 0;
+  *mine = 0;
+  for (int s = s0; s < s1; ++s) *mine += attn_length(p, attn_plain_seg(p, s, bad));
+  int64_t x = *mine;
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t y = __shfl_up_sync(~0u, x, d);
+    if (lane >= d) x += y;
+  }
+  for (int o = 16; o; o >>= 1) *bad = max(*bad, __shfl_xor_sync(~0u, *bad, o));
+  if (lane == 31) sm[warp] = x, sm[kWarps + warp] = *bad;
+  __syncthreads();
+  int64_t total = 0;
+  *before = x - *mine;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    if (i < warp) *before += sm[i];
+    total += sm[i];
+    *bad = max(*bad, (int32_t)sm[kWarps + i]);
+  }
+  return total;
+}
+
 // Where a CTA's part of the narrow line begins.
 struct AttnLine {
   int64_t w, end;     // its tiles
@@ -285,30 +387,13 @@ __device__ __forceinline__ AttnLine attn_line(const AttnParams &p, int g, int64_
     return l;
   }
   constexpr int kWarps = Threads / 32;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = 1 + p.n_reqs;
+  const int tid = threadIdx.x, n = 1 + p.n_reqs;
   const int per = (n + Threads - 1) / Threads, s0 = min(tid * per, n), s1 = min(s0 + per, n);
-  int32_t bad = 0;
-  int64_t mine = 0;
-  for (int s = s0; s < s1; ++s) {
-    mine += attn_length(p, attn_plain_seg(p, s, &bad));
-  }
-  int64_t x = mine;
-  for (int d = 1; d < 32; d <<= 1) {
-    const int64_t y = __shfl_up_sync(~0u, x, d);
-    if (lane >= d) x += y;
-  }
-  for (int o = 16; o; o >>= 1) bad = max(bad, __shfl_xor_sync(~0u, bad, o));
-  if (lane == 31) sm[warp] = x, sm[kWarps + warp] = bad;
-  __syncthreads();
-  int64_t total = 0, before = 0;
-#pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
-    if (i < warp) before += sm[i];
-    total += sm[i];
-    bad = max(bad, (int32_t)sm[kWarps + i]);
-  }
-  before += x - mine;
-  const int64_t quota = max((int64_t)p.most_cost, attn_up(total, p.groups));
+  int32_t bad;
+  int64_t before, mine;
+  const int64_t total = attn_plain_total<Threads>(p, sm, &before, &mine, &bad), wide = attn_plain_wide(p);
+  const AttnShare share = attn_share(p, total, wide);
+  const int64_t quota = max((int64_t)1, attn_up(total, share.groups));
   if (blockIdx.x == 0) {
     int64_t at = before;
     for (int s = s0; s < s1; ++s) {
@@ -317,7 +402,10 @@ __device__ __forceinline__ AttnLine attn_line(const AttnParams &p, int g, int64_
       p.segs[s] = g;
       at += attn_length(p, g);
     }
-    if (tid == 0) p.head->tiles = total, p.head->quota = quota, p.head->refused = bad;
+    if (tid == 0) {
+      p.head->tiles = total, p.head->quota = quota, p.head->refused = bad;
+      p.head->wide_quota = share.wide_groups ? max((int64_t)1, attn_up(wide, share.wide_groups)) : 1;
+    }
   }
   l.w = g * quota;
   l.end = min(total, l.w + quota);
@@ -349,12 +437,12 @@ __device__ __forceinline__ void attn_pieces(const AttnParams &p, int g, int h, c
   int32_t none = 0;
   for (int s = l.seg; w < l.end; ++s) {
     const AttnSeg seg = p.planned ? p.segs[s] : attn_plain_seg(p, s, &none);
-    const int64_t tiles = attn_up(seg.rows, p.row_tile) * seg.key_tiles;
+    const int64_t tiles = attn_units(p, seg.rows) * seg.key_tiles;
     // the seg's tiles that begin in this group's part: at .. last - 1
     int64_t at = attn_up(max(w - tile0, (int64_t)0), seg.cost);
     const int64_t last = min(tiles, attn_up(l.end - tile0, seg.cost));
     while (at < last) {
-      const int unit = (int)(at / seg.key_tiles), kt = (int)(at - (int64_t)unit * seg.key_tiles);
+      const int unit = (int)attn_div(at, seg.key_tiles), kt = (int)(at - (int64_t)unit * seg.key_tiles);
       const int take = (int)min((int64_t)(seg.key_tiles - kt), last - at);
       AttnPiece x;
       x.row0 = seg.row0 + unit * p.row_tile;
@@ -370,21 +458,6 @@ __device__ __forceinline__ void attn_pieces(const AttnParams &p, int g, int h, c
     tile0 += tiles * seg.cost;
     w = max(w, tile0);
   }
-}
-
-// The wide line of a call without a plan: the prefix and all rows.
-__device__ __forceinline__ int attn_plain_units(const AttnParams &p) {
-  return p.prefix_len > 0 ? (int)attn_up((int64_t)p.n_q * p.group, kAttnWideRows) : 0;
-}
-__device__ __forceinline__ AttnUnit attn_plain_unit(const AttnParams &p, int u) {
-  AttnUnit x = {};
-  x.row0 = u * kAttnWideRows;
-  x.rows = min(kAttnWideRows, p.n_q * p.group - x.row0);
-  x.key1 = p.prefix_len;
-  x.key_tiles = (int32_t)attn_up(p.prefix_len, kAttnWideKeys);
-  x.tile0 = (int64_t)u * x.key_tiles;
-  x.table = -1;
-  return x;
 }
 
 __device__ __forceinline__ void attn_wait_prior() {

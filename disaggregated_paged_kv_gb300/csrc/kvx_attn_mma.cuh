@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -85,6 +86,13 @@ template <typename T>
 __device__ __forceinline__ bool odd2(uint32_t x) {
   constexpr uint32_t m = sizeof(T) == 2 && std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
   return (x & m) == m || ((x >> 16) & m) == m;
+}
+
+// Weights for a product in T are e^(s - m) 2^shift, so that in f16, whose numbers end at 2^16 and 2^-24, they
+// reach as far below the greatest as they can.  room: the power of two by which a score may pass m.
+template <typename T>
+__device__ __forceinline__ constexpr float weight_shift(float room) {
+  return std::is_same<T, __half>::value ? 15.f - room : 0.f;
 }
 
 // What a row of bf16 queries is multiplied by on its way to f16, a power of two that brings its greatest

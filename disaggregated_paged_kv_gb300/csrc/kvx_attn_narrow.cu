@@ -58,6 +58,7 @@ template <typename IO, bool FP8, int D>
 struct Consumer {
   using T = typename std::conditional<FP8, __half, IO>::type;  // of the products
   using S = Smem<FP8, D>;
+  static constexpr float kShift = weight_shift<T>(0.f);
   const AttnParams &p;
   S &sm;
   const int h, lane, warp;
@@ -187,7 +188,7 @@ struct Consumer {
           for (int n = 0; n < D / 8; ++n) o[n][0] *= f0, o[n][1] *= f0, o[n][2] *= f1, o[n][3] *= f1;
           m0 = t0, m1 = t1;
         }
-        const float base0 = m0 == -INFINITY ? 0.f : m0, base1 = m1 == -INFINITY ? 0.f : m1;
+        const float base0 = m0 == -INFINITY ? 0.f : m0 - kShift, base1 = m1 == -INFINITY ? 0.f : m1 - kShift;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           uint32_t a[4];
@@ -341,7 +342,7 @@ struct Consumer {
           for (int e = 0; e < 2; ++e)
             *reinterpret_cast<float2 *>(d + (n + e) * 8 + 2 * c4) = make_float2(o[n + e][2 * up], o[n + e][2 * up + 1]);
       }
-      if (c4 == 0) p.part_m[at] = up ? m1 : m0, p.part_l[at] = up ? l1 : l0;
+      if (c4 == 0) p.part_m[at] = (up ? m1 : m0) - kShift, p.part_l[at] = up ? l1 : l0;
     }
   }
 

@@ -12,9 +12,9 @@
 // Bound: 4 D operations a score on the tensor cores (1024 cycles for 128 x 128 scores at D = 128)
 // against one exponential and about five instructions a score on four warps.
 //
-// A row's sums refer to a maximum that is renewed only when a score passes it by 2^8: the factor
-// between the two cancels in the quotient, weights stay below 2^8 (in range for f16 and bf16), and
-// the sums in tensor memory are rescaled a few times in all instead of with every tile.
+// A row's sums refer to a maximum that is renewed only when a score passes it by 2^8 (f16: 2^2): the factor
+// between the two cancels in the quotient, weights stay in range (see weight_shift), and the sums in
+// tensor memory are rescaled a few times in all instead of with every tile.
 #include <cuda.h>
 
 #include <type_traits>
@@ -29,7 +29,6 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kKeys = kAttnWideKeys;
-constexpr float kRenew = 8.f;
 
 template <bool FP8, int D>
 struct Smem {
@@ -46,6 +45,7 @@ struct Smem {
   int32_t least[2], odd[2];
   int32_t warp_least[4];
   int32_t lost, error;
+  int64_t scan[2 * (kThreads / 32)];
   uint32_t tmem;
 };
 
@@ -149,17 +149,10 @@ struct WidePiece {
   bool first, whole;
 };
 
-// Calls f(piece) for every piece of group g; f returns false to stop.
+// Calls f(piece) for every piece of group g, whose part of the line is [w, end), beginning in unit u; f
+// returns false to stop.
 template <typename F>
-__device__ __forceinline__ void wide_pieces(const AttnParams &p, int g, F f) {
-  const int n = p.planned ? p.head->units : attn_plain_units(p);
-  if (n == 0) return;
-  const int64_t tiles = p.planned ? p.head->wide_tiles : (int64_t)n * attn_plain_unit(p, 0).key_tiles;
-  const int64_t quota = p.planned ? p.head->wide_quota : max((int64_t)1, attn_up(tiles, p.wide_groups));
-  int64_t w = g * quota;
-  const int64_t end = min(tiles, w + quota);
-  if (w >= end) return;
-  int u = p.planned ? p.start[p.groups + g] : (int)(w / attn_plain_unit(p, 0).key_tiles);
+__device__ __forceinline__ void wide_pieces(const AttnParams &p, int u, int64_t w, int64_t end, F f) {
   for (; w < end; ++u) {
     const AttnUnit x = p.planned ? p.units[u] : attn_plain_unit(p, u);
     if (w >= x.tile0 + x.key_tiles) continue;
@@ -189,9 +182,33 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
   extern __shared__ char raw_smem[];
   using S = Smem<FP8, D>;
   using T = typename std::conditional<FP8, __half, IO>::type;  // of the products
+  // (f16: little room above the maximum, so that the weights keep their range below it)
+  constexpr float kRenew = std::is_same<T, __half>::value ? 2.f : 8.f, kShift = weight_shift<T>(kRenew);
   constexpr int kStages = S::kStages;
   S &sm = *reinterpret_cast<S *>(raw_smem + (-smem_u32(raw_smem) & 1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  attn_wait_prior();
+  attn_release_next();  // the narrow kernel may take SMs that this one does not use; what it reads is there
+  // this CTA's part of the line, and whether it has one
+  const int g = blockIdx.x / p.kv_heads, h = blockIdx.x - g * p.kv_heads;
+  int64_t w0, w1, quota;
+  if (p.planned) {
+    quota = p.head->wide_quota;
+    w1 = p.head->units ? p.head->wide_tiles : 0;
+  } else {
+    int64_t before, mine;
+    int32_t bad;
+    w1 = attn_plain_wide(p);
+    const int64_t own = attn_plain_total<kThreads>(p, sm.scan, &before, &mine, &bad);
+    quota = max((int64_t)1, attn_up(w1, attn_share(p, own, w1).wide_groups));
+  }
+  w0 = g * quota;
+  w1 = min(w1, w0 + quota);
+  if (w0 >= w1) {
+    if (tid == 0) p.errors[p.groups * p.kv_heads + blockIdx.x] = 0;
+    return;
+  }
+  const int unit0 = p.planned ? p.start[p.groups + g] : (int)(w0 / attn_plain_unit(p, 0).key_tiles);
   if (tid == 0) {
     bar_init(&sm.q_full, 256);
     for (int i = 0; i < S::kRawStages; ++i) bar_init(&sm.raw_full[i], 1);
@@ -213,9 +230,6 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
   __syncthreads();
   fence_after();
   constexpr uint32_t tm = 0;  // all 512 columns are this CTA's, so they begin at the first
-  attn_wait_prior();
-  attn_release_next();  // the narrow kernel may take over SMs as CTAs end; what it reads is there
-  const int g = blockIdx.x / p.kv_heads, h = blockIdx.x - g * p.kv_heads;
   auto wait = [&](uint64_t *b, uint32_t parity) {
     return bar_wait(b, parity, &sm.lost, &sm.error);
   };
@@ -227,7 +241,7 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
     const uint32_t tmS = tm + t * 128, tmO = tm + 256 + t * D;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     uint32_t s_phase = 0, o_phase = 0, parity = 0;
-    wide_pieces(p, g, [&](const WidePiece &x) {
+    wide_pieces(p, unit0, w0, w1, [&](const WidePiece &x) {
       const int i = t * 128 + r;
       const bool active = x.rows > t * 128;
       const bool live = i < x.rows;
@@ -312,10 +326,10 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
             t2 = max3(t2, s[2][k], s[2][k + 1]), t3 = max3(t3, s[3][k], s[3][k + 1]);
           }
           const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * scale;
-          const bool renew = top > m + kRenew || (m == -INFINITY && top > m);
+          const bool renew = top > m + (kRenew + kShift) || (m == -INFINITY && top > m);
           if (__any_sync(~0u, renew)) {
-            const float f = !renew ? 1.f : m == -INFINITY ? 0.f : ex2(m - top);
-            if (renew) m = top;
+            const float f = !renew ? 1.f : m == -INFINITY ? 0.f : ex2(m - (top - kShift));
+            if (renew) m = top - kShift;
             l2 = mul2(l2, pair(f, f));
             if (j > 0) {  // S of this tile is done, so are the products before it
 #pragma unroll
@@ -469,7 +483,7 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
     };
     // A wait that was given up is not waited for again (see bar_wait): these threads then run
     // through what is left without waiting, since they meet at barriers of their own.
-    wide_pieces(p, g, [&](const WidePiece &x) {
+    wide_pieces(p, unit0, w0, w1, [&](const WidePiece &x) {
       // from where on live rows differ in what they see
       int least = INT32_MAX;
 #pragma unroll
@@ -662,7 +676,7 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
           mma_ss(tm + t * 128, qd + step, kd + step, kDescS, k > 0, lead);
         }
       };
-      wide_pieces(p, g, [&](const WidePiece &x) {
+      wide_pieces(p, unit0, w0, w1, [&](const WidePiece &x) {
         const int tiles = x.tiles;
         const bool two = x.rows > 128;
         if (!wait_all(&sm.q_full, q_phase) || !wait_all(&sm.full[stage], phase)) return false;

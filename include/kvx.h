@@ -638,8 +638,8 @@ typedef struct kvx_attn_args {
  * with the queries of all requests are computed together so that the prefix is read once for
  * the batch, the others through row b.  With s_j = scale * k_scale * <q, K_j>:
  *   out = v_scale * sum_j exp(s_j) V_j / sum_j exp(s_j),   lse = log sum_j exp(s_j).
- * Sums are held in 32 bits; with 16-bit types the weights exp(s_j - max) are rounded to the
- * pool's 16-bit type (BF16 or F16 as q for an FP8 pool) for the product with V.  Results do not
+ * Sums are held in 32 bits; with 16- and 8-bit pools the weights exp(s_j - max) are rounded to the
+ * pool's 16-bit type (F16 for an FP8 pool, its queries too) for the product with V.  Results do not
  * depend on scheduling: the same call gives the same bits.
  * A row that sees nothing (a length of 0, or fewer positions than query tokens), or whose every
  * score is -inf, is 0 with lse -inf.  What masked positions and other slots hold, NaN and

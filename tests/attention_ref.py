@@ -31,13 +31,15 @@ class Case:
 
 def make(dtype="bf16", kind="planes", page=16, H=2, G=4, D=128, lens=(40,), qlens=None, prefix=0,
          layers=2, layer=1, io=None, q_gap=2, spread=1.5, seed=0, scale=None, k_scale=None,
-         v_scale=None, slot_pad=0, offset=0, edit=None):
+         v_scale=None, slot_pad=0, offset=0, edit=None, room=0, starts=False):
     """lens: positions of each request, prefix included (0: a padding row); qlens: query tokens of
-    each (None: single tokens).  slot_pad / offset: extra elements per slot and before plane 0."""
+    each (None: single tokens).  slot_pad / offset: extra elements per slot and before plane 0.
+    room: tokens that a table row has entries for, at least (garbage past the request's end).  starts: give
+    the query starts although every request has a single token."""
     g = torch.Generator().manual_seed(seed)
     c = Case()
     c.dtype, c.kind, c.page, c.H, c.G, c.D, c.prefix = dtype, kind, page, H, G, D, prefix
-    c.lens, c.single = list(lens), qlens is None
+    c.lens, c.single = list(lens), qlens is None and not starts
     c.qlens = [1] * len(lens) if qlens is None else list(qlens)
     c.layer, c.layers = layer, layers
     t = TYPES[dtype]
@@ -65,7 +67,7 @@ def make(dtype="bf16", kind="planes", page=16, H=2, G=4, D=128, lens=(40,), qlen
     pages = shared + sum(mine) + 2
     perm = torch.randperm(pages, generator=g).int()
     c.prefix_pages = perm[:shared].clone()
-    width = max([1] + [-(-n // page) for n in c.lens]) + 2
+    width = max([1, -(-room // page)] + [-(-n // page) for n in c.lens]) + 2
     c.tables = torch.full((B, width + 1), 2 ** 31 - 7, dtype=torch.int32)[:, :width]
     at = shared
     for b, n in enumerate(c.lens):

@@ -126,6 +126,157 @@ def test_prompts_among_padding_and_single_tokens():
                 qlens=[1, 300, 1, 40, 5, 33, 60], prefix=300))
 
 
+# Calls of many rows go to the kernel of 128-row tiles from some 4.5e9 operations on.  With query starts the
+# tables' room stands for the keys, so that small cases get there; without, the prefix has to be that long.
+ROOM = 300_000
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "fp8"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G", [1, 4, 7])
+def test_wide_prefix(dtype, D, G):
+    lens = [1000 + 1 + 13 * (i % 9) for i in range(90)]
+    run(ar.make(dtype, "planes", 16, 2, G, D, lens=lens, prefix=1000, layers=1, layer=0, room=ROOM,
+                starts=True))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "fp8"])
+@pytest.mark.parametrize("kind,page", [("planes", 1), ("planes", 4), ("slots", 8), ("hnd", 16),
+                                       ("planes", 24), ("slots", 64), ("hnd", 128), ("hnd", 3)])
+@pytest.mark.parametrize("prefix", [384, 517])
+def test_wide_by_page_size(dtype, kind, page, prefix):
+    lens = [prefix + 1 + 29 * (i % 5) for i in range(40)]
+    run(ar.make(dtype, kind, page, 2, 4, 64 if page == 8 else 128, lens=lens, prefix=prefix,
+                layers=2, layer=1, seed=page, room=ROOM, starts=True))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "fp8"])
+@pytest.mark.parametrize("kind,page,prefix", [("planes", 16, 300), ("hnd", 32, 512), ("slots", 2, 260),
+                                              ("planes", 64, 0)])
+@pytest.mark.parametrize("G", [4, 7])
+def test_wide_prompts(dtype, kind, page, prefix, G):
+    run(ar.make(dtype, kind, page, 2, G, 128, lens=[prefix + 200, prefix + 50, prefix + 377, prefix + 150],
+                qlens=[200, 1, 77, 150], prefix=prefix, seed=page, room=ROOM))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_wide_with_padding_short_and_single(dtype, D):
+    run(ar.make(dtype, "planes", 16, 2, 8, D, lens=[0, 700, 301, 0, 640, 333, 299, 20, 300],
+                qlens=[1, 300, 1, 40, 5, 33, 60, 20, 1], prefix=300, room=ROOM))
+    run(ar.make(dtype, "planes", 16, 1, 4, D, lens=[3, 0, 100, 20, 260], qlens=[6, 2, 100, 40, 300],
+                prefix=250, room=ROOM))
+    run(ar.make(dtype, "planes", 16, 2, 4, D, lens=[0] * 30 + [260, 5, 256, 90] * 6, prefix=256, room=ROOM,
+                starts=True))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "fp8"])
+def test_wide_sharp_and_rising_scores(dtype):
+    run(ar.make(dtype, "planes", 16, 2, 8, 64, lens=[700, 650], qlens=[150, 100], prefix=390, spread=30.0,
+                room=ROOM))
+
+    def edit(c):
+        c.q[:] = 1.0
+        for x in [c.common] + c.kv:
+            x[:, 0] = ((torch.arange(len(x)) / 4.0).to(x.dtype))[:, None, None]
+    run(ar.make(dtype, "planes", 16, 1, 4, 64, lens=[600], qlens=[90], prefix=0, edit=edit, room=ROOM,
+                k_scale=1.0))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "fp8"])
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+def test_wide_garbage_behind_the_mask(dtype, value):
+    """As test_garbage_behind_the_mask, in tiles of 128 rows."""
+    if dtype == "fp8" and not math.isnan(value):
+        pytest.skip("E4M3 has no infinities")
+
+    def edit(c):
+        c.kv[0][c.lens[0] - 150:, 1] = torch.tensor(value).to(c.kv[0].dtype)
+        c.kv[1][c.lens[1] - 1:, 0] = torch.tensor(value).to(c.kv[1].dtype)
+    c = ar.make(dtype, "planes", 16, 1, 4, 64, lens=[230, 140, 29], qlens=[200, 90, 1], prefix=20, edit=edit,
+                room=ROOM)
+    out, lse = ar.Run(c).call().results()
+    want, wlse, tol, tol_l = ar.reference(c)
+    sees = torch.zeros(c.T, dtype=torch.bool)
+    sees[c.start[1] - 150:c.start[1]] = True       # V
+    last = torch.zeros_like(sees)
+    last[c.start[2] - 1] = True                    # K
+    ok = ~sees & ~last
+    assert bool(((out - want).abs()[ok] <= tol[ok]).all())
+    assert bool(((lse - wlse).abs()[~last] <= tol_l[~last]).all())
+    assert not bool(torch.isfinite(out[sees]).any())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+def test_wide_garbage_in_the_prefix(dtype):
+    """Prefix positions that some requests do not reach hold NaN values."""
+    def edit(c):
+        for x in [c.common] + c.kv:
+            x[300:, 1] = torch.tensor(math.nan).to(x.dtype)
+    c = ar.make(dtype, "planes", 16, 1, 4, 64, lens=[290, 300, 301, 600] * 10, prefix=500, edit=edit,
+                room=ROOM, starts=True)
+    out, lse = ar.Run(c).call().results()
+    want, wlse, tol, tol_l = ar.reference(c)
+    for i, n in enumerate(c.lens):
+        if n <= 300:
+            assert bool(((out - want).abs()[i] <= tol[i]).all())
+        else:
+            assert bool(torch.isnan(out[i]).all())
+    assert bool(((lse - wlse).abs() <= tol_l).all())
+
+
+@pytest.mark.parametrize("dtype,kind", [("bf16", "planes"), ("f16", "hnd"), ("fp8", "slots")])
+@pytest.mark.parametrize("own", [3, 700])
+def test_wide_decode_step(dtype, kind, own):
+    """Single tokens without query starts, a prefix long enough for the wide kernel."""
+    lens = [4610 + 1 + (own * i) % (2 * own) for i in range(128)]
+    lens[5] = 0
+    lens[77] = 4000
+    run(ar.make(dtype, kind, 16, 1, 32, 64, lens=lens, prefix=4610, layers=1, layer=0))
+
+
+@pytest.mark.parametrize("scale", [-0.125, 0.0])
+def test_scales_that_turn_scores_round(scale):
+    run(ar.make("bf16", "planes", 16, 2, 4, 64, lens=[200 + i for i in range(40)], prefix=190, scale=scale,
+                room=ROOM, starts=True))
+
+
+def test_wide_queries_and_results_off_16_bytes():
+    c = ar.make("bf16", "planes", 16, 1, 4, 64, lens=[300, 330], qlens=[60, 90], prefix=200, room=ROOM)
+    r = ar.Run(c)
+    wide = torch.empty(c.T, 4 * 64 + 11, dtype=torch.bfloat16, device="cuda")
+    q = wide[:, 3:3 + 256].unflatten(1, (4, 64))
+    q.copy_(r.q)
+    r.q = q
+    r.out = torch.empty_like(wide)[:, 1:1 + 256].unflatten(1, (4, 64))
+    ar.check(c, r.call().results())
+
+
+def test_wide_same_bits_again():
+    c = ar.make("bf16", lens=[700, 650, 1300], qlens=[130, 5, 99], prefix=600, layers=1, layer=0, room=ROOM)
+    r = ar.Run(c)
+    a = r.call().results()
+    r.out.fill_(0)
+    r.ws.fill_(255)
+    b = r.call().results()
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_wide_device_refusals():
+    for edit, want in [
+        (lambda r: r.lens.fill_(-1), "INVALID_ARG"),
+        (lambda r: r.lens.fill_(2 ** 30), "OUT_OF_RANGE"),
+        (lambda r: r.tables.fill_(-1), "OUT_OF_RANGE"),
+        (lambda r: r.prefix_pages.fill_(2 ** 31 - 1), "OUT_OF_RANGE"),
+    ]:
+        for dtype in ("bf16", "fp8"):
+            for kw in (dict(lens=[300 + i for i in range(70)], starts=True),
+                       dict(lens=[400, 450], qlens=[100, 150])):
+                r = ar.Run(ar.make(dtype, D=128, prefix=250, layers=1, layer=0, room=ROOM, **kw))
+                edit(r)
+                assert _status(r) == getattr(r.kvx, "ERR_" + want)
+
+
 def test_long_and_short_together():
     run(ar.make("bf16", "planes", 16, 1, 4, 128, lens=[9000, 1, 30, 4000], prefix=0, layers=1, layer=0))
 
