@@ -224,6 +224,32 @@ __device__ __forceinline__ void put(__nv_bfloat16 *o, float x) { *o = __float2bf
 
 constexpr int kJoinWarps = 4;
 
+// The pieces of a row.  The first is at the row's own place, piece i, of group g, at more + g * step; g is
+// g0 + i, or (cost > 0) where a group's part is shorter than a tile that of the i-th tile.
+struct RowPieces {
+  int64_t first, more, step, begin;
+  int32_t count, g0, cost;
+};
+
+__device__ __forceinline__ RowPieces narrow_pieces(const AttnParams &p, const AttnSeg &s, int64_t quota,
+                                                   bool prefix, int h, int32_t r) {
+  RowPieces x = {};
+  if (s.key_tiles == 0) return x;
+  const int unit = s.rows <= p.row_tile ? 0 : (r - s.row0) / p.row_tile, row0 = s.row0 + unit * p.row_tile;
+  x.begin = s.tile0 + (int64_t)unit * s.key_tiles * s.cost;
+  x.g0 = (int)attn_div(x.begin, quota);
+  if (s.cost <= quota) {
+    x.count = (int)attn_div(x.begin + (int64_t)(s.key_tiles - 1) * s.cost, quota) - x.g0 + 1;
+  } else {
+    x.count = s.key_tiles;
+    x.cost = s.cost;
+  }
+  x.first = attn_part(p, prefix, true, 0, h, row0) + (r - row0);
+  x.more = attn_part(p, prefix, false, 0, h, row0) + (r - row0);
+  x.step = (int64_t)p.kv_heads * p.row_tile;
+  return x;
+}
+
 // A block joins the parts of `heads` query heads of one token, a warp a head at a time, prefix splits
 // first, in order.  DK: head_dim, 0: any.
 template <typename IO, int DK>
@@ -262,50 +288,34 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid
   const int qh1 = min(p.q_heads, (int)(blockIdx.y + 1) * heads);
   for (int qh = blockIdx.y * heads + warp; qh < qh1; qh += kJoinWarps) {
     const int h = qh / p.group, member = qh - h * p.group, r = t * p.group + member;
-    // the pieces of the row: n0 of the prefix (or of the prompt), then the request's own.  The first is at
-    // the row's own place, piece i of group g at more + g * step; g is g0 + i, or where a group's part is
-    // shorter than a tile that of the i-th tile
-    int64_t first[2], more[2], step[2], begin[2];
-    int count[2] = {0, 0}, g0s[2], costs[2] = {0, 0};
+    // the pieces of the row: those of the prefix (or of the prompt), then the request's own
+    RowPieces pre = {}, own = {};
     if (some && p.wide_groups > 0) {
       const int wr = wide_row + member, u = unit0 + (wr - lead) / kAttnWideRows;
       if (u < units) {
         const AttnUnit x = p.planned ? p.units[u] : attn_plain_unit(p, u);
-        const int64_t q = head.wide_quota;
         if (x.key_tiles > 0 && x.table == (prompt ? b : -1)) {
-          const int g0 = (int)attn_div(x.tile0, q), g1 = (int)attn_div(x.tile0 + x.key_tiles - 1, q);
-          if (prompt && g0 == g1) continue;  // the wide kernel has written the result
-          count[0] = g1 - g0 + 1;
-          g0s[0] = g0;
-          first[0] = attn_wide_part(p, true, 0, h) + r;
-          more[0] = attn_wide_part(p, false, 0, h) + (wr - x.row0);
-          step[0] = (int64_t)p.kv_heads * kAttnWideRows;
+          pre.g0 = (int)attn_div(x.tile0, head.wide_quota);
+          pre.count = (int)attn_div(x.tile0 + x.key_tiles - 1, head.wide_quota) - pre.g0 + 1;
+          if (prompt && pre.count == 1) continue;  // the wide kernel has written the result
+          pre.first = attn_wide_part(p, true, 0, h) + r;
+          pre.more = attn_wide_part(p, false, 0, h) + (wr - x.row0);
+          pre.step = (int64_t)p.kv_heads * kAttnWideRows;
         }
       }
+    } else {
+      pre = narrow_pieces(p, seg[0], head.quota, true, h, r);
     }
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const AttnSeg &s = seg[k];
-      if (s.key_tiles == 0) continue;
-      const int unit = (r - s.row0) / p.row_tile, row0 = s.row0 + unit * p.row_tile;
-      const int64_t w = s.tile0 + (int64_t)unit * s.key_tiles * s.cost;
-      g0s[k] = (int)attn_div(w, head.quota);
-      count[k] = s.key_tiles;
-      if (s.cost <= head.quota)
-        count[k] = (int)attn_div(w + (int64_t)(s.key_tiles - 1) * s.cost, head.quota) - g0s[k] + 1;
-      else
-        costs[k] = s.cost, begin[k] = w;
-      first[k] = attn_part(p, k == 0, true, 0, h, row0) + (r - row0);
-      more[k] = attn_part(p, k == 0, false, 0, h, row0) + (r - row0);
-      step[k] = (int64_t)p.kv_heads * p.row_tile;
-    }
-    const int n0 = count[0], n = n0 + count[1];
+    own = narrow_pieces(p, seg[1], head.quota, false, h, r);
+    const int n0 = pre.count, n = n0 + own.count;
     auto part = [&](int i) {
-      const int k = i < n0 ? 0 : 1;
+      const bool k = i >= n0;
       i -= k ? n0 : 0;
-      if (i == 0) return first[k];
-      const int g = costs[k] ? (int)attn_div(begin[k] + (int64_t)i * costs[k], head.quota) : g0s[k] + i;
-      return more[k] + g * step[k];
+      if (i == 0) return k ? own.first : pre.first;
+      const int cost = k ? own.cost : pre.cost;
+      int g = (k ? own.g0 : pre.g0) + i;
+      if (cost) g = (int)attn_div((k ? own.begin : pre.begin) + (int64_t)i * cost, head.quota);
+      return (k ? own.more : pre.more) + g * (k ? own.step : pre.step);
     };
     // lane i has part i (of 32 at a time); all lanes then add the parts, neighbouring columns a lane
     float top = -INFINITY, l = 0.f;
@@ -430,8 +440,11 @@ namespace {
 constexpr int kPlanReqs = 2048;
 
 // Operations from which the wide kernel takes the prefix and prompts (about 1200 TFLOP/s behind some 12
-// us) instead of the narrow one, 64 rows at a time (about 290 TFLOP/s, no launch of its own).
-constexpr double kWideWork = 4.5e9;
+// us) instead of the narrow one, 64 rows at a time (about 290 TFLOP/s, no launch of its own): kWideWork; but
+// already kWideBeside where the requests' own rows may come to kWideBytes, so that the two kernels can run
+// side by side (see attn_share).  64 requests of 1000-2000 tokens behind 2048 shared ones (2.1e9): 95 us
+// with the narrow kernel alone, 83 us side by side.
+constexpr double kWideWork = 4.5e9, kWideBeside = 0.7e9, kWideBytes = 2e8;
 
 struct Sizes {
   int64_t segs_off, units_off, start_off, base_off, prompt_off, limit_off, owner_off, tok_off, at_off;
@@ -547,9 +560,11 @@ extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_arg
   // What the wide kernel may have: the prefix, and with several tokens a request prompts, whose keys
   // only the tables bound.  Below kWideWork operations its launch costs more than it saves.  It takes
   // the greatest score from the greatest product, so the factor between them has to be above 0.
+  const double room = (double)a.max_pages * a.page_size;
+  const bool beside = (room - a.prefix_len) * a.n_reqs * pool->row_bytes * 2 >= kWideBytes;
   const double wide_keys = a.q_start ? (double)a.max_pages * a.page_size : (double)a.prefix_len;
   const bool wide = takes_wide(pool, a.n_q, a.q_heads) &&
-                    4.0 * pool->head_dim * a.q_heads * a.n_q * wide_keys >= kWideWork &&
+                    4.0 * pool->head_dim * a.q_heads * a.n_q * wide_keys >= (beside ? kWideBeside : kWideWork) &&
                     a.scale * a.k_scale > 0.f;
   const Sizes z = sizes(a.n_q, a.n_reqs, a.q_heads, pool->kv_heads, pool->head_dim, row_tile(pool),
                         wide);

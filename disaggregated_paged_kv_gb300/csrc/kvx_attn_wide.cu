@@ -187,28 +187,6 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
   constexpr int kStages = S::kStages;
   S &sm = *reinterpret_cast<S *>(raw_smem + (-smem_u32(raw_smem) & 1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  attn_wait_prior();
-  attn_release_next();  // the narrow kernel may take SMs that this one does not use; what it reads is there
-  // this CTA's part of the line, and whether it has one
-  const int g = blockIdx.x / p.kv_heads, h = blockIdx.x - g * p.kv_heads;
-  int64_t w0, w1, quota;
-  if (p.planned) {
-    quota = p.head->wide_quota;
-    w1 = p.head->units ? p.head->wide_tiles : 0;
-  } else {
-    int64_t before, mine;
-    int32_t bad;
-    w1 = attn_plain_wide(p);
-    const int64_t own = attn_plain_total<kThreads>(p, sm.scan, &before, &mine, &bad);
-    quota = max((int64_t)1, attn_up(w1, attn_share(p, own, w1).wide_groups));
-  }
-  w0 = g * quota;
-  w1 = min(w1, w0 + quota);
-  if (w0 >= w1) {
-    if (tid == 0) p.errors[p.groups * p.kv_heads + blockIdx.x] = 0;
-    return;
-  }
-  const int unit0 = p.planned ? p.start[p.groups + g] : (int)(w0 / attn_plain_unit(p, 0).key_tiles);
   if (tid == 0) {
     bar_init(&sm.q_full, 256);
     for (int i = 0; i < S::kRawStages; ++i) bar_init(&sm.raw_full[i], 1);
@@ -229,6 +207,30 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
   fence_before();
   __syncthreads();
   fence_after();
+  attn_wait_prior();
+  attn_release_next();  // the narrow kernel may take SMs that this one does not use; what it reads is there
+  // this CTA's part of the line, and whether it has one
+  const int g = blockIdx.x / p.kv_heads, h = blockIdx.x - g * p.kv_heads;
+  int64_t w0, w1, quota;
+  if (p.planned) {
+    quota = p.head->wide_quota;
+    w1 = p.head->units ? p.head->wide_tiles : 0;
+  } else {
+    int64_t before, mine;
+    int32_t bad;
+    w1 = attn_plain_wide(p);
+    const int64_t own = attn_plain_total<kThreads>(p, sm.scan, &before, &mine, &bad);
+    quota = max((int64_t)1, attn_up(w1, attn_share(p, own, w1).wide_groups));
+  }
+  w0 = g * quota;
+  w1 = min(w1, w0 + quota);
+  if (w0 >= w1) {
+    if (tid == 0) p.errors[p.groups * p.kv_heads + blockIdx.x] = 0;
+    if (warp == 12)
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(sm.tmem) : "memory");
+    return;
+  }
+  const int unit0 = p.planned ? p.start[p.groups + g] : (int)(w0 / attn_plain_unit(p, 0).key_tiles);
   constexpr uint32_t tm = 0;  // all 512 columns are this CTA's, so they begin at the first
   auto wait = [&](uint64_t *b, uint32_t parity) {
     return bar_wait(b, parity, &sm.lost, &sm.error);
