@@ -238,7 +238,7 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
 
   if (warp < 8) {
     // ---- softmax of row tile t, a thread a row ----
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     const int t = warp >> 2, r = tid & 127;
     const uint32_t tmS = tm + t * 128, tmO = tm + 256 + t * D;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
@@ -453,7 +453,7 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
     });
   } else if (warp < 12) {
     // ---- loads ----
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     const int i = tid - 256;
     constexpr int kRaw = FP8 ? D / 16 : D / 8;         // 16-byte chunks of a row in the pool
     constexpr int kStep = 128 / kRaw, kPer = kKeys / kStep;
@@ -657,7 +657,7 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
     });
   } else {
     // ---- products ----
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 12) {  // all lanes walk along, so that what they agree on stays in uniform registers
       const uint32_t lead = elect_lane();
       auto wait_all = [&](uint64_t *b, uint32_t parity) { return __all_sync(~0u, wait(b, parity)) != 0; };
