@@ -280,25 +280,24 @@ struct AttnShare {
   int32_t groups, wide_groups;
 };
 
-// The shapes of the GPU, and measured times in ns: of a CTA's tile of 128 keys and 256 rows; of 16 bytes
-// of a narrow tile, two CTAs on the SM; of 1 MB at the memory's rate; and what a launch takes before and
-// after its tiles.
+// The GPU's SMs, and measured times in ns: of a CTA's tile of 128 keys and 256 rows; of a narrow CTA's unit
+// of cost, two CTAs on the SM, at least, and of 16 bytes of a tile; of a request's begin and end; of 1 MB at
+// the memory's rate; and what a launch takes before and after its tiles.
 constexpr int kAttnSms = 152;
-constexpr int64_t kAttnWideNs = 2300, kAttnNarrowPs = 470, kAttnMbNs = 160, kAttnStartNs = 9000;
+constexpr int64_t kAttnWideNs = 2100, kAttnNarrowNs = 900, kAttnNarrowPs = 470, kAttnPieceNs = 3000, kAttnMbNs = 160,
+                  kAttnStartNs = 10000;
 
 __device__ __forceinline__ AttnShare attn_share(const AttnParams &p, int64_t own, int64_t wide) {
   AttnShare s = {p.groups, p.wide_groups};
   if (p.wide_groups < 2 || own == 0 || wide == 0) return s;
   const int64_t bytes = (int64_t)kAttnKeyTile * p.head_dim * p.key_bytes * 2;  // of a narrow tile
   const int64_t floor_ns = (own * p.kv_heads * bytes >> 20) * kAttnMbNs;
-  // (short lines, and those that the SMs bound, gain nothing)
-  if (floor_ns < 4 * kAttnStartNs || floor_ns < attn_up(own, p.groups) * (bytes / 16 * kAttnNarrowPs) / 1000) return s;
+  const int64_t unit_ns = max(kAttnNarrowNs, bytes / 16 * kAttnNarrowPs / 1000);
   auto narrow_ns = [&](int64_t groups) {
-    const int64_t sm = attn_up(own, groups) * (bytes / 16 * kAttnNarrowPs) / 1000;
-    return kAttnStartNs + (sm > floor_ns ? sm : floor_ns);
+    return kAttnStartNs + max(attn_up(own, groups) * unit_ns + attn_up(p.n_reqs, groups) * kAttnPieceNs, floor_ns);
   };
   auto wide_ns = [&](int64_t groups) { return kAttnStartNs + attn_up(wide, groups) * kAttnWideNs; };
-  int64_t best = wide_ns(p.wide_groups) + narrow_ns(p.groups);
+  int64_t best = (wide_ns(p.wide_groups) + narrow_ns(p.groups)) * 9 / 10;  // a tenth sooner, or not at all
   int at = p.wide_groups;
   for (int g = 1 + (threadIdx.x & 31); g < p.wide_groups; g += 32) {
     const int left = (kAttnSms - g * p.kv_heads) * 2 / p.kv_heads;
