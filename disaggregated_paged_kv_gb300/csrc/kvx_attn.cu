@@ -60,6 +60,7 @@ __global__ void __launch_bounds__(kPlanCta) attn_plan_kernel(const AttnParams p)
   // the first requests' own first token, count, length and place (see AttnParams::prompt): calls of up to
   // kPlanCta requests read them from here
   __shared__ int32_t s_t0[kPlanCta + 1], s_len[kPlanCta], s_prompt[kPlanCta];
+  attn_release_next();  // what follows may take its place, and waits for this kernel's end itself
   attn_wait_prior();
   const int tid = threadIdx.x, n = p.n_reqs;
   const bool small = n <= kPlanCta;

@@ -60,20 +60,24 @@ __global__ void __launch_bounds__(kThreads) attn_general_kernel(const __grid_con
   if (tid == 0) error = 0;
   const int g = blockIdx.x / p.kv_heads, head = blockIdx.x - g * p.kv_heads;
   const AttnLine line = attn_line<kThreads>(p, g, scan);
-  // columns past D are 0 throughout
-  for (int i = tid; i < (kRows + 2 * kKeys) * P; i += kThreads) sq[i] = 0.f;
+  if (D % 4 != 0)  // columns past D are 0 throughout
+    for (int i = tid; i < (kRows + 2 * kKeys) * P; i += kThreads) sq[i] = 0.f;
   attn_pieces(p, g, head, line, [&](const AttnPiece &item) {
     __syncthreads();
-    for (int i = tid; i < kRows * D; i += kThreads) {
-      const int r = i / D, d = i - r * D;
-      float x = 0.f;
-      if (r < item.rows) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {  // all rows' elements of a column are on their way together
+      const int d = tid + c * kThreads;
+      float x[kRows];
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
         const int row = item.row0 + r, t = row / p.group;
         const IO *q = reinterpret_cast<const IO *>(p.q + t * p.q_tok +
                                                    (int64_t)(head * p.group + row - t * p.group) * p.q_head);
-        x = to_f(q[d]) * p.scale_log2;
+        x[r] = r < item.rows && d < D ? to_f(q[d]) * p.scale_log2 : 0.f;
       }
-      sq[r * P + d] = x;
+      if (d < D)
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) sq[r * P + d] = x[r];
     }
     if (tid < kRows) slim[tid] = tid < item.rows ? attn_limit(p, (item.row0 + tid) / p.group) : 0;
     float acc[kRows][NC], m[kRows / 4], l[kRows / 4];

@@ -377,6 +377,7 @@ attn_narrow_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
   const int g = blockIdx.x / p.kv_heads, h = blockIdx.x - g * p.kv_heads;
   __syncthreads();
   const AttnLine line = attn_line<kThreads>(p, g, sm.scan);
+  attn_release_next();  // the join takes its place as CTAs end, and waits for the last
 
   if (warp < 4) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");

@@ -486,6 +486,17 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
     // A wait that was given up is not waited for again (see bar_wait): these threads then run
     // through what is left without waiting, since they meet at barriers of their own.
     wide_pieces(p, unit0, w0, w1, [&](const WidePiece &x) {
+      const int boxes = tma.rows > 0 ? kKeys / tma.rows : 1, pw = warp - 8;
+      // page look-ups: lane l of warp w has box 4 l + w of a regular tile
+      const int box = lane * 4 + pw;
+      auto box_page = [&](int j) -> int32_t {  // as it stands in the table; checked when it is used
+        int pg, off;
+        const int pos = x.key0 + j * kKeys + box * tma.rows;
+        if (pos >= x.key1 || box >= boxes) return 0;
+        attn_split(p, pos, &pg, &off);
+        return attn_entry(p, pos < p.prefix_len ? -1 : x.table, pg);
+      };
+      const int32_t page0 = box_page(0);
       // from where on live rows differ in what they see
       int least = INT32_MAX;
 #pragma unroll
@@ -508,16 +519,6 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
         const int k0 = x.key0 + j * kKeys;
         return tma.rows > 0 && k0 + kKeys <= x.key1 && k0 + kKeys <= least &&
                (k0 >= p.prefix_len || k0 + kKeys <= p.prefix_len || p.prefix_len % tma.rows == 0);
-      };
-      const int boxes = tma.rows > 0 ? kKeys / tma.rows : 1, pw = warp - 8;
-      // page look-ups: lane l of warp w has box 4 l + w of a regular tile
-      const int box = lane * 4 + pw;
-      auto box_page = [&](int j) -> int32_t {  // as it stands in the table; checked when it is used
-        if (j >= x.tiles || !regular(j) || box >= boxes) return 0;
-        int pg, off;
-        const int pos = x.key0 + j * kKeys + box * tma.rows;
-        attn_split(p, pos, &pg, &off);
-        return attn_entry(p, pos < p.prefix_len ? -1 : x.table, pg);
       };
       auto box_row = [&](int j, int32_t id) -> int {
         int pg, off;
@@ -551,7 +552,7 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
 
       // 8-bit tiles come by tensor copies some stages ahead of their conversion
       int ahead = 0;
-      int32_t ahead_page = FP8 ? box_page(0) : 0, ahead_next = FP8 ? box_page(1) : 0;
+      int32_t ahead_page = page0, ahead_next = FP8 ? box_page(1) : 0;
       auto fetch = [&](int upto) {  // up to tile and half number `upto`
         for (; ahead < min(upto, 2 * x.tiles); ++ahead) {
           if (regular(ahead >> 1)) {
@@ -562,7 +563,7 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
           if (ahead & 1) ahead_page = ahead_next, ahead_next = box_page((ahead + 3) >> 1);
         }
       };
-      int32_t next_page = FP8 ? 0 : box_page(0);
+      int32_t next_page = page0;
       for (int j = 0; j < x.tiles; ++j) {
         const int k0 = x.key0 + j * kKeys;
         const bool reg = regular(j);
