@@ -277,6 +277,56 @@ def test_wide_device_refusals():
                 assert _status(r) == getattr(r.kvx, "ERR_" + want)
 
 
+def test_offsets_past_32_bits():
+    """Pages at the end of planes of over 4 GiB, in token rows, head-major pages and a slot-major pool."""
+    kvx = ar.Run(ar.make("bf16", lens=[50])).kvx
+    c = ar.make("bf16", "planes", 16, 2, 4, 128, lens=[300, 333] + [290 + i for i in range(20)], prefix=280,
+                layers=1, layer=0)
+    R = c.H * c.D * 2
+    slots = (9 << 30) // (2 * R) // 16 * 16                    # two planes of 4.5 GiB
+    far = slots // 16 - c.pages
+    small = c.pool.view(torch.bfloat16).view(2, c.pages, 16, c.H, c.D).cuda()
+    for kind in ("planes", "hnd", "slots"):
+        pool = torch.empty(2 * slots * c.H * c.D, dtype=torch.bfloat16, device="cuda")
+        if kind == "planes":
+            pool.view(2, slots // 16, 16, c.H, c.D)[:, far:] = small
+            more = dict(plane_stride=slots * R)
+        elif kind == "hnd":
+            pool.view(2, slots // 16, c.H, 16, c.D)[:, far:] = small.transpose(2, 3)
+            more = dict(plane_stride=slots * R, kind=kvx.HND_PAGED, page_size=16)
+        else:
+            pool.view(slots // 16, 16, 2, c.H, c.D)[far:] = small.permute(1, 2, 0, 3, 4)
+            more = dict(plane_stride=R, slot_stride=2 * R)
+        for starts in (False, True):  # narrow kernel; with room in the tables the wide one too
+            r = ar.Run(c)
+            r.pool = None
+            r.layout = kvx.Layout(1, c.H, c.D, kvx.BF16, slots, base=pool, keepalive=pool, **more)
+            wide = torch.full((len(c.lens), 20000 if starts else c.tables.shape[1]), -1, dtype=torch.int32,
+                              device="cuda")
+            for b, n in enumerate(c.lens):
+                k = -(-n // 16)
+                wide[b, :k] = c.tables[b, :k].cuda() + far
+            r.tables = wide
+            r.prefix_pages = r.prefix_pages + far
+            ar.check(c, r.call(q_start=r.q_start if starts else None).results())
+            r.layout.close()
+        del pool
+
+
+@pytest.mark.parametrize("n", [1100, 2100])
+@pytest.mark.parametrize("starts", [False, True])
+def test_many_small_requests(n, starts):
+    """More requests than the plan keeps at hand, and (single tokens) more than calls without one take."""
+    run(ar.make("f16", "planes", 4, 1, 2, 64, lens=[(7 * i) % 23 for i in range(n)], prefix=6, layers=1,
+                layer=0, starts=starts))
+
+
+def test_more_kv_heads_than_multiprocessors():
+    run(ar.make("bf16", "planes", 8, 160, 1, 64, lens=[40, 33, 90], prefix=24, layers=1, layer=0))
+    run(ar.make("bf16", "planes", 8, 160, 2, 64, lens=[140, 133], qlens=[40, 37], prefix=24, layers=1,
+                layer=0, room=20000))
+
+
 def test_long_and_short_together():
     run(ar.make("bf16", "planes", 16, 1, 4, 128, lens=[9000, 1, 30, 4000], prefix=0, layers=1, layer=0))
 
