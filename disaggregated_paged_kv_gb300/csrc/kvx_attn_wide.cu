@@ -661,7 +661,11 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 12) {  // all lanes walk along, so that what they agree on stays in uniform registers
       const uint32_t lead = elect_lane();
-      auto wait_all = [&](uint64_t *b, uint32_t parity) { return __all_sync(~0u, wait(b, parity)) != 0; };
+      // (a wait that was given up is not waited for again, and what is then computed is of no account)
+      auto wait_all = [&](uint64_t *b, uint32_t parity) {
+        wait(b, parity);
+        __syncwarp();
+      };
       constexpr uint32_t kFmt = std::is_same<T, __half>::value ? 0u : 1u;
       constexpr uint32_t kBase = 1u << 4 | kFmt << 7 | kFmt << 10 | (128u >> 4) << 24;
       constexpr uint32_t kDescS = kBase | (uint32_t)(kKeys >> 3) << 17;
@@ -679,10 +683,13 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
           mma_ss(tm + t * 128, qd + step, kd + step, kDescS, k > 0, lead);
         }
       };
+      // About five products wait in the tensor cores' queue, 350 cycles: no two waits stand together, and
+      // stages are given back as soon as their last product has been issued.
       wide_pieces(p, unit0, w0, w1, [&](const WidePiece &x) {
         const int tiles = x.tiles;
         const bool two = x.rows > 128;
-        if (!wait_all(&sm.q_full, q_phase) || !wait_all(&sm.full[stage], phase)) return false;
+        wait_all(&sm.q_full, q_phase);
+        wait_all(&sm.full[stage], phase);
         q_phase ^= 1;
         fence_after();
 #pragma unroll
@@ -693,37 +700,42 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
           }
         mma_commit(&sm.empty[stage], lead);
         if (++stage == kStages) stage = 0, phase ^= 1;
+        wait_all(&sm.full[stage], phase);
         for (int j = 0; j < tiles; ++j) {
           const uint32_t vst = stage;
-          if (!wait_all(&sm.full[vst], phase)) return false;
           if (++stage == kStages) stage = 0, phase ^= 1;
+          const uint32_t kst = stage, k_phase = phase;  // of the next tile's keys
           const bool more = j + 1 < tiles;
-          if (more && !wait_all(&sm.full[stage], phase)) return false;
+          if (more && ++stage == kStages) stage = 0, phase ^= 1;  // now its values
           const uint64_t vd = kv0 + vst * kTileStep;
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            if (j == 0 && !wait_all(&sm.o_empty[t], oe_phase)) return false;
+            if (j == 0) wait_all(&sm.o_empty[t], oe_phase);
             if (t == 0 || two) {
 #pragma unroll
               for (int k = 0; k < kKeys / 16; ++k) {
                 if (k % (kKeys / 32) == 0) {
-                  if (!wait_all(&sm.p_full[t][k / (kKeys / 32)], p_phase >> t & 1)) return false;
+                  wait_all(&sm.p_full[t][k / (kKeys / 32)], p_phase >> t & 1);
                   fence_after();
                 }
                 mma_ts(tm + 256 + t * D, tm + t * 128 + k * 8, vd + (uint64_t)(k * (2 * D * 16 >> 4)), kDescO,
                        j > 0 || k > 0, lead);
               }
-              if (more) scores(t, stage);
             }
-            if (!more) mma_commit(&sm.o_full[t], lead);
-            else if (t == 0 || two) mma_commit(&sm.s_full[t], lead);
+            if (t == 1) mma_commit(&sm.empty[vst], lead);
+            if (more) {
+              if (t == 0) wait_all(&sm.full[kst], k_phase);
+              else wait_all(&sm.full[stage], phase);
+              if (t == 0 || two) {
+                scores(t, kst);
+                mma_commit(&sm.s_full[t], lead);
+              }
+            } else {
+              mma_commit(&sm.o_full[t], lead);
+            }
           }
           p_phase ^= two ? 3 : 1;
-          mma_commit(&sm.empty[vst], lead);
-          if (more) {
-            mma_commit(&sm.empty[stage], lead);
-            if (++stage == kStages) stage = 0, phase ^= 1;
-          }
+          if (more) mma_commit(&sm.empty[kst], lead);
         }
         oe_phase ^= 1;
         return true;
