@@ -74,9 +74,19 @@ __device__ __forceinline__ uint32_t elect_lane() {
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// All loads before are there; the registers go through, so that no use of them comes before.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0]),"+r"(r[1]),"+r"(r[2]),"+r"(r[3]),"+r"(r[4]),"+r"(r[5]),"+r"(r[6]),"+r"(r[7]),
+               "+r"(r[8]),"+r"(r[9]),"+r"(r[10]),"+r"(r[11]),"+r"(r[12]),"+r"(r[13]),"+r"(r[14]),"+r"(r[15]),
+               "+r"(r[16]),"+r"(r[17]),"+r"(r[18]),"+r"(r[19]),"+r"(r[20]),"+r"(r[21]),"+r"(r[22]),"+r"(r[23]),
+               "+r"(r[24]),"+r"(r[25]),"+r"(r[26]),"+r"(r[27]),"+r"(r[28]),"+r"(r[29]),"+r"(r[30]),"+r"(r[31]) :: "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0]),"+r"(r[1]),"+r"(r[2]),"+r"(r[3]),"+r"(r[4]),"+r"(r[5]),"+r"(r[6]),"+r"(r[7]),
+               "+r"(r[8]),"+r"(r[9]),"+r"(r[10]),"+r"(r[11]),"+r"(r[12]),"+r"(r[13]),"+r"(r[14]),"+r"(r[15]) :: "memory");
+}
 __device__ __forceinline__ void tmem_ld32(uint32_t (&r)[32], uint32_t a) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
@@ -312,8 +322,9 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
           uint32_t s[4][32];
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_ld32(s[c], tmS + lanes + c * 32);
-          tmem_wait_ld();
-          const int k0 = x.key0 + j * kKeys, seen = lim - k0;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_wait_ld(s[c]);
+          const int seen = lim - (x.key0 + j * kKeys);
           if (seen < kKeys) {
 #pragma unroll
             for (int c = 0; c < 4; ++c)
@@ -338,7 +349,7 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
               for (int c = 0; c < D / 16; ++c) {
                 uint32_t o[16];
                 tmem_ld16(o, tmO + lanes + c * 16);
-                tmem_wait_ld();
+                tmem_wait_ld(o);
 #pragma unroll
                 for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
                 tmem_st16(tmO + lanes + c * 16, o);
@@ -385,7 +396,7 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
           uint32_t o[32];
           __syncwarp();
           tmem_ld32(o, tmO + lanes + c * 32);
-          tmem_wait_ld();
+          tmem_wait_ld(o);
           if (!live) continue;
           if (l == 0.f) {
 #pragma unroll
