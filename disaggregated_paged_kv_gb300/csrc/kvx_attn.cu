@@ -443,8 +443,8 @@ constexpr int kPlanReqs = 2048;
 // Operations from which the wide kernel takes the prefix and prompts (about 1200 TFLOP/s behind some 12
 // us) instead of the narrow one, 64 rows at a time (about 290 TFLOP/s, no launch of its own): kWideWork; but
 // already kWideBeside where the requests' own rows may come to kWideBytes, so that the two kernels can run
-// side by side (see attn_share).  64 requests of 1000-2000 tokens behind 2048 shared ones (2.1e9): 95 us
-// with the narrow kernel alone, 83 us side by side.
+// side by side (see attn_share).  64 requests of 1000-2000 tokens behind 2048 shared ones (2.1e9): 102
+// us with the narrow kernel alone, 93 us side by side.
 constexpr double kWideWork = 4.5e9, kWideBeside = 0.7e9, kWideBytes = 2e8;
 
 struct Sizes {
