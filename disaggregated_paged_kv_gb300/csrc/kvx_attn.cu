@@ -237,7 +237,7 @@ __device__ __forceinline__ RowPieces narrow_pieces(const AttnParams &p, const At
   RowPieces x = {};
   if (s.key_tiles == 0) return x;
   const int unit = s.rows <= p.row_tile ? 0 : (r - s.row0) / p.row_tile, row0 = s.row0 + unit * p.row_tile;
-  x.begin = s.tile0 + (int64_t)unit * s.key_tiles * s.cost;
+  x.begin = s.tile0 + unit * attn_unit_length(p, s);
   x.g0 = (int)attn_div(x.begin, quota);
   if (s.cost <= quota) {
     x.count = (int)attn_div(x.begin + (int64_t)(s.key_tiles - 1) * s.cost, quota) - x.g0 + 1;
@@ -447,6 +447,12 @@ constexpr int kPlanReqs = 2048;
 // us with the narrow kernel alone, 93 us side by side.
 constexpr double kWideWork = 4.5e9, kWideBeside = 0.7e9, kWideBytes = 2e8;
 
+// A narrow unit's begin and end take about as long as some tiles of 16 rows.  Counted as 0, 2, 3 and 4 of
+// them: 95 requests of up to 25 own tokens behind 1360 shared ones 121, 66, 57 and 53 us; 96 FP8 decode
+// requests 60, 52, 59 and 60 us; 256 decode requests of 4096 own tokens 350, 344, 342 and 366 us.  The plain
+// kernel's tiles take so long that they do not tell.
+constexpr int32_t kNarrowUnitCost = 2;
+
 struct Sizes {
   int64_t segs_off, units_off, start_off, base_off, prompt_off, limit_off, owner_off, tok_off, at_off;
   int64_t m_off, l_off, o_off, errors_off, errors, total;
@@ -609,6 +615,7 @@ extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_arg
   p.max_pages = a.max_pages;
   p.prefix_len = a.prefix_len;
   p.row_tile = row_tile(pool);
+  p.unit_cost = tensor_cores(pool) ? kNarrowUnitCost : 0;
   p.key_bytes = pool->elem;
   const uintptr_t q_at = (uintptr_t)a.q | (uintptr_t)p.q_tok | (uintptr_t)p.q_head;
   p.q_even = q_at % 4 == 0;

@@ -95,6 +95,7 @@ struct AttnParams {
   int32_t page_size, max_pages, prefix_len;
   int32_t key_bytes;     // of an element of the pool
   int32_t row_tile;      // rows of a narrow unit
+  int32_t unit_cost;     // what a unit's begin and end cost, in tiles of up to 16 rows
   int32_t groups;        // groups of kv_heads CTAs, narrow line
   int32_t wide_groups;   // of the wide line; 0: no wide kernel
   int32_t planned;       // 1: the plan kernel has laid the work out.  0: one query token a request,
@@ -211,9 +212,13 @@ __device__ __forceinline__ int64_t attn_units(const AttnParams &p, int32_t rows)
   return rows <= p.row_tile ? rows > 0 : attn_up(rows, p.row_tile);
 }
 
-// The length of a seg in the line.
+// The length of a unit and of a seg in the line.  A unit's begin and end (its queries, joining its warps,
+// its results) come behind its tiles.
+__device__ __forceinline__ int64_t attn_unit_length(const AttnParams &p, const AttnSeg &g) {
+  return g.key_tiles > 0 ? (int64_t)g.key_tiles * g.cost + p.unit_cost : 0;
+}
 __device__ __forceinline__ int64_t attn_length(const AttnParams &p, const AttnSeg &g) {
-  return attn_units(p, g.rows) * g.key_tiles * g.cost;
+  return attn_units(p, g.rows) * attn_unit_length(p, g);
 }
 
 __device__ __forceinline__ void attn_tile_seg(const AttnParams &p, AttnSeg *g) {
@@ -281,20 +286,20 @@ struct AttnShare {
 };
 
 // The GPU's SMs, and measured times in ns: of a CTA's tile of 128 keys and 256 rows; of a narrow CTA's unit
-// of cost, two CTAs on the SM, at least, and of 16 bytes of a tile; of a request's begin and end; of 1 MB at
-// the memory's rate; and what a launch takes before and after its tiles.
+// of cost, two CTAs on the SM, at least, and of 16 bytes of a tile; of 1 MB at the memory's rate; and what a launch takes before and after its tiles.
 constexpr int kAttnSms = 152;
-constexpr int64_t kAttnWideNs = 2100, kAttnNarrowNs = 900, kAttnNarrowPs = 470, kAttnPieceNs = 3000, kAttnMbNs = 160,
+constexpr int64_t kAttnWideNs = 2100, kAttnNarrowNs = 900, kAttnNarrowPs = 470, kAttnMbNs = 160,
                   kAttnStartNs = 10000;
 
 __device__ __forceinline__ AttnShare attn_share(const AttnParams &p, int64_t own, int64_t wide) {
   AttnShare s = {p.groups, p.wide_groups};
   if (p.wide_groups < 2 || own == 0 || wide == 0) return s;
   const int64_t bytes = (int64_t)kAttnKeyTile * p.head_dim * p.key_bytes * 2;  // of a narrow tile
-  const int64_t floor_ns = (own * p.kv_heads * bytes >> 20) * kAttnMbNs;
+  const int64_t tiles = max(own - (int64_t)p.n_reqs * p.unit_cost, (int64_t)0);
+  const int64_t floor_ns = (tiles * p.kv_heads * bytes >> 20) * kAttnMbNs;
   const int64_t unit_ns = max(kAttnNarrowNs, bytes / 16 * kAttnNarrowPs / 1000);
   auto narrow_ns = [&](int64_t groups) {
-    return kAttnStartNs + max(attn_up(own, groups) * unit_ns + attn_up(p.n_reqs, groups) * kAttnPieceNs, floor_ns);
+    return kAttnStartNs + max(attn_up(own, groups) * unit_ns, floor_ns);
   };
   auto wide_ns = [&](int64_t groups) { return kAttnStartNs + attn_up(wide, groups) * kAttnWideNs; };
   int64_t best = (wide_ns(p.wide_groups) + narrow_ns(p.groups)) * 9 / 10;  // a tenth sooner, or not at all
@@ -436,13 +441,15 @@ __device__ __forceinline__ void attn_pieces(const AttnParams &p, int g, int h, c
   int32_t none = 0;
   for (int s = l.seg; w < l.end; ++s) {
     const AttnSeg seg = p.planned ? p.segs[s] : attn_plain_seg(p, s, &none);
-    const int64_t tiles = attn_units(p, seg.rows) * seg.key_tiles;
-    // the seg's tiles that begin in this group's part: at .. last - 1
-    int64_t at = attn_up(max(w - tile0, (int64_t)0), seg.cost);
-    const int64_t last = min(tiles, attn_up(l.end - tile0, seg.cost));
-    while (at < last) {
-      const int unit = (int)attn_div(at, seg.key_tiles), kt = (int)(at - (int64_t)unit * seg.key_tiles);
-      const int take = (int)min((int64_t)(seg.key_tiles - kt), last - at);
+    const int64_t unit_length = attn_unit_length(p, seg), length = attn_units(p, seg.rows) * unit_length;
+    for (int64_t from = max(w - tile0, (int64_t)0), to = min(length, l.end - tile0); from < to;) {
+      // the unit's tiles that begin in this group's part: kt .. kt + take - 1
+      const int unit = (int)attn_div(from, unit_length);
+      const int64_t begin = unit * unit_length;
+      const int kt = (int)attn_up(from - begin, seg.cost);
+      const int take = (int)min((int64_t)seg.key_tiles, attn_up(to - begin, seg.cost)) - kt;
+      from = begin + unit_length;
+      if (take <= 0) continue;
       AttnPiece x;
       x.row0 = seg.row0 + unit * p.row_tile;
       x.rows = min(p.row_tile, seg.rows - unit * p.row_tile);
@@ -452,9 +459,8 @@ __device__ __forceinline__ void attn_pieces(const AttnParams &p, int g, int h, c
       x.table = s - 1;
       x.part = attn_part(p, s == 0, kt == 0, g, h, x.row0);
       f(x);
-      at += take;
     }
-    tile0 += tiles * seg.cost;
+    tile0 += length;
     w = max(w, tile0);
   }
 }
