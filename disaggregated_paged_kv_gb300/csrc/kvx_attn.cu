@@ -464,7 +464,8 @@ Sizes sizes(int64_t n_q, int64_t n_reqs, int64_t q_heads, int64_t kv_heads, int6
             bool wide) {
   Sizes z = {};
   const int64_t rows = n_q * (q_heads / kv_heads);
-  z.groups = (int32_t)std::max((int64_t)1, kAttnSms * 2 / kv_heads);
+  const int64_t per_sm = row_tile == kAttnGeneralRows && D <= 128 ? 3 : 2;
+  z.groups = (int32_t)std::max((int64_t)1, kAttnSms * per_sm / kv_heads);
   z.wide_groups = wide ? (int32_t)std::max((int64_t)1, kAttnSms / kv_heads) : 0;
   z.errors = z.groups * kv_heads + z.wide_groups * kv_heads;
   const int64_t parts = 2 * n_q * q_heads + z.groups * kv_heads * row_tile +

@@ -6,13 +6,18 @@
 // rows, a lane a key, four columns at a time, and takes the running maximum and sum of its rows with
 // shuffles; then every thread adds the tile's weighted values into its one or two columns of all 16
 // rows, held in registers, four keys at a time.  The next tile's elements are on their way meanwhile
-// where 16-byte loads are possible.
+// where 16-byte loads are possible.  Pieces of up to four rows (kFew) take one row a warp and leave the
+// other twelve out: 32 decode requests of 4 rows in 32 bits 219 -> 182 us.
 //
-// Bound: shared-memory reads (5 of 16 bytes for 64 multiply-adds) for many rows, the chain of look-up,
-// load and two passes for few keys.
+// Bound: shared-memory reads (5 of 16 bytes for 64 multiply-adds) and the barriers of a tile.  Up to 128
+// columns three CTAs share an SM (168 registers; two took 1208 us for 117 decode requests of 7 rows and
+// 4016 shared tokens in 32 bits, 8 kv heads; three 909 us; four, at 128 registers with spills, 1027 us).
+// With kFew 894 us: 15 TFLOP/s.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
+
+#include <type_traits>
 
 #include "kvx_attn.cuh"
 #include "kvx_launch.cuh"
@@ -21,7 +26,7 @@ namespace kvx {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kRows = kAttnGeneralRows;
+constexpr int kRows = kAttnGeneralRows, kFew = 4;
 constexpr int kKeys = 32;
 
 __device__ __forceinline__ float to_f(float x) { return x; }
@@ -42,7 +47,7 @@ __device__ __forceinline__ void unpack(const uint4 &v, float *o) {
 
 // NC: columns a thread.  VEC: 16-byte loads.
 template <typename KV, typename IO, int NC, bool VEC>
-__global__ void __launch_bounds__(kThreads) attn_general_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(kThreads, NC == 1 ? 3 : 2) attn_general_kernel(const __grid_constant__ AttnParams p) {
   extern __shared__ float4 smem4[];
   const int D = p.head_dim, P = pitch(D), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   float *sq = reinterpret_cast<float *>(smem4);  // [kRows][P]
@@ -90,6 +95,7 @@ __global__ void __launch_bounds__(kThreads) attn_general_kernel(const __grid_con
     __syncthreads();
     int most = 0, least = INT32_MAX;
     for (int r = 0; r < item.rows; ++r) most = max(most, slim[r]), least = min(least, slim[r]);
+    const bool few = item.rows <= kFew;  // the first row of each warp alone
     const int begin = max(item.key0, item.low), end = min(item.key1, most);
     // every warp looks all keys of a tile up, a lane a key: the offsets then go by shuffles
     auto look = [&](int k0) -> int64_t {
@@ -147,20 +153,25 @@ __global__ void __launch_bounds__(kThreads) attn_general_kernel(const __grid_con
       __syncthreads();
       float s[kRows / 4] = {};
       const float4 *kr = reinterpret_cast<const float4 *>(sk + lane * P);
-      const float4 *qr = reinterpret_cast<const float4 *>(sq + warp * (kRows / 4) * P);
+      const float4 *qr = reinterpret_cast<const float4 *>(sq + warp * P);  // row i of a warp: 4 i + warp
+      auto scores = [&](auto rows_) {
 #pragma unroll 4
-      for (int d = 0; d < (D + 3) / 4; ++d) {
-        const float4 k = kr[d];
+        for (int d = 0; d < (D + 3) / 4; ++d) {
+          const float4 k = kr[d];
 #pragma unroll
-        for (int i = 0; i < kRows / 4; ++i) {
-          const float4 q = qr[i * (P / 4) + d];
-          s[i] = fmaf(q.x, k.x, s[i]), s[i] = fmaf(q.y, k.y, s[i]);
-          s[i] = fmaf(q.z, k.z, s[i]), s[i] = fmaf(q.w, k.w, s[i]);
+          for (int i = 0; i < decltype(rows_)::value; ++i) {
+            const float4 q = qr[i * P + d];
+            s[i] = fmaf(q.x, k.x, s[i]), s[i] = fmaf(q.y, k.y, s[i]);
+            s[i] = fmaf(q.z, k.z, s[i]), s[i] = fmaf(q.w, k.w, s[i]);
+          }
         }
-      }
+      };
+      if (few) scores(std::integral_constant<int, kFew / 4>{});
+      else scores(std::integral_constant<int, kRows / 4>{});
 #pragma unroll
       for (int i = 0; i < kRows / 4; ++i) {
-        const int r = warp * (kRows / 4) + i;
+        const int r = i * 4 + warp;
+        if (few && i >= kFew / 4) continue;
         if (lane >= nk || k0 + lane >= slim[r]) s[i] = -INFINITY;
         float top = s[i];
 #pragma unroll
@@ -184,26 +195,31 @@ __global__ void __launch_bounds__(kThreads) attn_general_kernel(const __grid_con
       for (int c = 0; c < NC; ++c) {
         const int d = tid + c * kThreads;
         if (d < D) {
+          auto add = [&](auto rows_) {
+            constexpr int R = decltype(rows_)::value;
 #pragma unroll
-          for (int r = 0; r < kRows; ++r) acc[r][c] *= sc[r];
-          if (mixed) {
-            for (int j = 0; j < nk; ++j) {
-              const float v = sv[j * P + d];
+            for (int r = 0; r < R; ++r) acc[r][c] *= sc[r];
+            if (mixed) {
+              for (int j = 0; j < nk; ++j) {
+                const float v = sv[j * P + d];
 #pragma unroll
-              for (int r = 0; r < kRows; ++r)
-                if (k0 + j < slim[r]) acc[r][c] = fmaf(sp[r * kKeys + j], v, acc[r][c]);
-            }
-          } else {  // keys past nk are 0 and weigh 0
-            for (int j = 0; j < nk; j += 4) {
-              const float v0 = sv[j * P + d], v1 = sv[(j + 1) * P + d], v2 = sv[(j + 2) * P + d], v3 = sv[(j + 3) * P + d];
+                for (int r = 0; r < R; ++r)
+                  if (k0 + j < slim[r]) acc[r][c] = fmaf(sp[r * kKeys + j], v, acc[r][c]);
+              }
+            } else {  // keys past nk are 0 and weigh 0
+              for (int j = 0; j < nk; j += 4) {
+                const float v0 = sv[j * P + d], v1 = sv[(j + 1) * P + d], v2 = sv[(j + 2) * P + d], v3 = sv[(j + 3) * P + d];
 #pragma unroll
-              for (int r = 0; r < kRows; ++r) {
-                const float4 w = *reinterpret_cast<const float4 *>(sp + r * kKeys + j);
-                acc[r][c] = fmaf(w.x, v0, acc[r][c]), acc[r][c] = fmaf(w.y, v1, acc[r][c]);
-                acc[r][c] = fmaf(w.z, v2, acc[r][c]), acc[r][c] = fmaf(w.w, v3, acc[r][c]);
+                for (int r = 0; r < R; ++r) {
+                  const float4 w = *reinterpret_cast<const float4 *>(sp + r * kKeys + j);
+                  acc[r][c] = fmaf(w.x, v0, acc[r][c]), acc[r][c] = fmaf(w.y, v1, acc[r][c]);
+                  acc[r][c] = fmaf(w.z, v2, acc[r][c]), acc[r][c] = fmaf(w.w, v3, acc[r][c]);
+                }
               }
             }
-          }
+          };
+          if (few) add(std::integral_constant<int, kFew>{});
+          else add(std::integral_constant<int, kRows>{});
         }
       }
     }
@@ -218,7 +234,7 @@ __global__ void __launch_bounds__(kThreads) attn_general_kernel(const __grid_con
     if (lane == 0)
 #pragma unroll
       for (int i = 0; i < kRows / 4; ++i) {
-        const int r = warp * (kRows / 4) + i;
+        const int r = i * 4 + warp;
         if (r < item.rows) p.part_m[item.part + r] = m[i], p.part_l[item.part + r] = l[i];
       }
   });

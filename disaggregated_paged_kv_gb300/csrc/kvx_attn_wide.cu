@@ -10,7 +10,10 @@
 // issues the products.
 //
 // Bound: 4 D operations a score on the tensor cores (1024 cycles for 128 x 128 scores at D = 128)
-// against one exponential and about five instructions a score on four warps.
+// against one exponential and about five instructions a score on four warps.  Measured: eight prompts
+// behind a shared prefix, 842 GFLOP in all, 689 us with the plan and the join (1.22 PFLOP/s); the tensor
+// cores are busy 62-65 % of this kernel's time and wait for weights in the rest.  Two threads a row, each with
+// half of its keys, took longer (749 against 704 us then).
 //
 // A row's sums refer to a maximum that is renewed only when a score passes it by 2^8 (f16: 2^2): the factor
 // between the two cancels in the quotient, weights stay in range (see weight_shift), and the sums in
