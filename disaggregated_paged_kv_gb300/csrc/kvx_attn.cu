@@ -252,7 +252,9 @@ __device__ __forceinline__ RowPieces narrow_pieces(const AttnParams &p, const At
 }
 
 // A block joins the parts of `heads` query heads of one token, a warp a head at a time, prefix splits
-// first, in order.  DK: head_dim, 0: any.
+// first, in order.  DK: head_dim, 0: any.  Bound: reading the parts (4 D bytes a row and piece), or for few
+// rows the chain of a row's pieces.  Cold, 3100 tokens of 32 heads (prompts) 28 us, 64 tokens of 32 heads
+// 7 us, one token with 38 pieces a row 18 us.
 template <typename IO, int DK>
 __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid_constant__ AttnParams p, int heads) {
   attn_wait_prior();

@@ -11,7 +11,7 @@
 //
 // Bound: 4 D operations a score on the tensor cores (1024 cycles for 128 x 128 scores at D = 128)
 // against one exponential and about five instructions a score on four warps.  Measured: eight prompts
-// behind a shared prefix, 842 GFLOP in all, 689 us with the plan and the join (1.22 PFLOP/s); the tensor
+// behind a shared prefix, 842 GFLOP in all, 677-689 us with the plan and the join (1.22-1.24 PFLOP/s); the tensor
 // cores are busy 62-65 % of this kernel's time and wait for weights in the rest.  Two threads a row, each with
 // half of its keys, took longer (749 against 704 us then).
 //
