@@ -10,7 +10,8 @@
 // Up to kTabThreads requests with room for no more than kOneTokens tokens (decode steps, drafts,
 // short prompts) are one CTA's work in one launch, tables_one.
 // Bound: the writes (8 bytes a token, 4 a page) for prompts, launch latency for a decode step.  Kernel
-// times with cold caches: one request 5.4 us, 256 requests 8.2 us (a call 21 us; in two launches it took 36), 1024 prompts of 100-8000 tokens 7 and 25 us for 35 MB, the call itself 24 us.
+// times with cold caches: one request 5.4 us, 256 requests 8.2 us (a call 21 us; in two launches it took
+// 36), 1024 prompts of 100-8000 tokens 7 and 25 us for 35 MB, the call itself 24 us.
 #include <cstring>
 
 #include "kvx_internal.cuh"
