@@ -4,6 +4,8 @@
 // plan kernel adds up the key tiles of all units, and the kernels behind it walk that line with a
 // grid that does not depend on it.
 #include <algorithm>
+#include <atomic>
+#include <chrono>
 #include <cmath>
 #include <cstring>
 
@@ -270,6 +272,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid
     if (threadIdx.x == 0) {
       for (int i = 1; i < kJoinWarps; ++i) e = max(e, worst[i]);
       *p.status = e;
+      if (p.wide_groups > 0) *p.ready = 0;
     }
   }
   if (t >= p.n_q) return;
@@ -456,7 +459,7 @@ constexpr double kWideWork = 4.5e9, kWideBeside = 0.7e9, kWideBytes = 2e8;
 constexpr int32_t kNarrowUnitCost = 2;
 
 struct Sizes {
-  int64_t segs_off, units_off, start_off, base_off, prompt_off, limit_off, owner_off, tok_off, at_off;
+  int64_t ready_off, segs_off, units_off, start_off, base_off, prompt_off, limit_off, owner_off, tok_off, at_off;
   int64_t m_off, l_off, o_off, errors_off, errors, total;
   int32_t groups, wide_groups;
 };
@@ -480,6 +483,7 @@ Sizes sizes(int64_t n_q, int64_t n_reqs, int64_t q_heads, int64_t kv_heads, int6
     at = align_up(at + bytes, 256);
     return here;
   };
+  z.ready_off = take(8);
   z.segs_off = take((int64_t)sizeof(AttnSeg) * (n_reqs + 1));
   z.units_off = take((int64_t)sizeof(AttnUnit) * units);
   z.start_off = take(4 * (z.groups + z.wide_groups));
@@ -513,6 +517,16 @@ int row_tile(const kvx_layout *l) { return tensor_cores(l) ? kAttnNarrowRows : k
 // Whether a call may have work for the wide kernel: more rows than the narrow kernel has in a unit.
 bool takes_wide(const kvx_layout *l, int64_t n_q, int64_t q_heads) {
   return tensor_cores(l) && n_q * (q_heads / l->kv_heads) > kAttnNarrowRows;
+}
+
+// A number that no word of a workspace holds by chance: calls are counted from the process's first one's
+// time, and mixed (splitmix64; every step can be undone, so no two counts give the same).
+uint64_t next_call() {
+  static std::atomic<uint64_t> calls{(uint64_t)std::chrono::system_clock::now().time_since_epoch().count() << 20};
+  uint64_t x = calls.fetch_add(1, std::memory_order_relaxed) * 0x9e3779b97f4a7c15u;
+  x = (x ^ (x >> 30)) * 0xbf58476d1ce4e5b9u;
+  x = (x ^ (x >> 27)) * 0x94d049bb133111ebu;
+  return x ^ (x >> 31);
 }
 
 bool mult(const void *p, uintptr_t a) { return (uintptr_t)p % a == 0; }
@@ -631,6 +645,8 @@ extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_arg
   p.after_wide = wide;
   char *ws = static_cast<char *>(d_ws);
   p.head = reinterpret_cast<AttnHeader *>(ws);
+  p.ready = reinterpret_cast<uint64_t *>(ws + z.ready_off);
+  p.call = wide ? next_call() : 0;
   p.segs = reinterpret_cast<AttnSeg *>(ws + z.segs_off);
   p.units = reinterpret_cast<AttnUnit *>(ws + z.units_off);
   p.start = reinterpret_cast<int32_t *>(ws + z.start_off);

@@ -104,8 +104,10 @@ struct AttnParams {
   int32_t q_even;        // q's heads start on 4-byte boundaries
   int32_t q_vec;         // on 16-byte boundaries
   int32_t out_vec;       // out's heads do
+  uint64_t call;         // unlike any other call's (see attn_announce)
   // workspace
   AttnHeader *head;
+  uint64_t *ready;       // [1], calls with a wide kernel
   AttnSeg *segs;         // [1 + n_reqs]: the prefix, then the requests
   AttnUnit *units;
   int32_t *start;        // [groups + wide_groups]: the seg, or unit, that a group begins in
@@ -470,6 +472,21 @@ __device__ __forceinline__ void attn_wait_prior() {
 }
 __device__ __forceinline__ void attn_release_next() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// What was there before the wide kernel (the plan, the queries, the pool) is visible to a kernel beside
+// it, which does not wait for the wide kernel's end, by a release and an acquire: a thread of the wide
+// kernel that has waited for all before stores the call's number, and only then lets its successor in; a
+// thread of the narrow kernel that reads the number sees what the other saw.  One that reads anything else
+// waits for the wide kernel's end.  The join clears the word, so that a call captured into a graph, whose
+// number is the same in every replay, does not find its own of the time before.
+__device__ __forceinline__ void attn_announce(const AttnParams &p) {
+  asm volatile("st.release.gpu.global.b64 [%0], %1;" ::"l"(p.ready), "l"(p.call) : "memory");
+}
+__device__ __forceinline__ void attn_wait_announced(const AttnParams &p) {
+  uint64_t x;
+  asm volatile("ld.acquire.gpu.global.b64 %0, [%1];" : "=l"(x) : "l"(p.ready) : "memory");
+  if (x != p.call) attn_wait_prior();
 }
 
 // vec: heads are whole 16-byte pieces on 16-byte boundaries.

@@ -378,6 +378,7 @@ attn_narrow_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (!p.after_wide) attn_wait_prior();
+  else if (tid == 0) attn_wait_announced(p);  // for the others by the barrier below
   const int g = blockIdx.x / p.kv_heads, h = blockIdx.x - g * p.kv_heads;
   __syncthreads();
   const AttnLine line = attn_line<kThreads>(p, g, sm.scan);
@@ -393,6 +394,8 @@ attn_narrow_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     });
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    // (no kernel's end lies between the pool's writes and these copies)
+    if (p.after_wide) asm volatile("fence.proxy.async.global;" ::: "memory");
     constexpr int kRaw = FP8 ? D / 16 : D / 8;  // 16-byte chunks of a row
     constexpr int kPer = 32 / kRaw;             // rows of a copy of all lanes
     // lane pairs (K and V) of the warps take the boxes of a tile in turn

@@ -221,7 +221,11 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
   __syncthreads();
   fence_after();
   attn_wait_prior();
-  attn_release_next();  // the narrow kernel may take SMs that this one does not use; what it reads is there
+  if (blockIdx.x == 0) {
+    if (tid == 0) attn_announce(p);
+    __syncthreads();
+  }
+  attn_release_next();  // the narrow kernel may take SMs that this one does not use
   // this CTA's part of the line, and whether it has one
   const int g = blockIdx.x / p.kv_heads, h = blockIdx.x - g * p.kv_heads;
   int64_t w0, w1, quota;
