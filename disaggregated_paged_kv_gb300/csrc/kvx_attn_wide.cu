@@ -44,8 +44,11 @@ struct Smem {
   uint64_t q_full, full[kStages], empty[kStages], raw_full[kRawStages];
   uint64_t s_full[2], p_full[2][2], o_full[2], o_empty[2], drained;
   // of the piece, by its parity: the least position that a live row does not see, and whether
-  // infinities or NaN were taken out of the V tiles from there on
+  // infinities or NaN were taken out of the V tiles from there on.  Pieces of one or two tiles fit the ring
+  // together, so that the loads may be two pieces ahead: they write a pair anew when the 256 softmax threads
+  // have read it.
   int32_t least[2], odd[2];
+  uint64_t odd_read[2];
   int32_t warp_least[4];
   int32_t lost, error;
   int64_t scan[2 * (kThreads / 32)];
@@ -207,7 +210,7 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
     for (int i = 0; i < 2; ++i) {
       bar_init(&sm.s_full[i], 1), bar_init(&sm.p_full[i][0], 128), bar_init(&sm.p_full[i][1], 128);
       bar_init(&sm.o_full[i], 1), bar_init(&sm.o_empty[i], 128);
-      sm.odd[i] = 0;
+      bar_init(&sm.odd_read[i], 256);
     }
     bar_init(&sm.drained, 1);
     sm.lost = sm.error = 0;
@@ -388,6 +391,8 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
       if (!__all_sync(~0u, wait(&sm.o_full[t], o_phase))) return false;
       o_phase ^= 1;
       fence_after();
+      const int odd = *(volatile int32_t *)&sm.odd[parity], least = *(volatile int32_t *)&sm.least[parity];
+      bar_arrive(&sm.odd_read[parity]);
       if (active) {
         float l, l_odd;
         unpair(l2, l, l_odd);
@@ -397,7 +402,6 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
         const bool direct = x.whole && x.table >= 0;
         const float inv = l == 0.f ? 0.f : p.v_scale / l;
         IO *out = reinterpret_cast<IO *>(p.out + (int64_t)token * p.out_tok + (int64_t)qh * p.out_head);
-        const int odd = *(volatile int32_t *)&sm.odd[parity], least = *(volatile int32_t *)&sm.least[parity];
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
@@ -476,7 +480,7 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
     constexpr int kRaw = FP8 ? D / 16 : D / 8;         // 16-byte chunks of a row in the pool
     constexpr int kStep = 128 / kRaw, kPer = kKeys / kStep;
     const int c = i % kRaw, r0 = i / kRaw;
-    uint32_t stage = 0, phase = 1, parity = 0, raw_in = 0, raw_out = 0, raw_phase = 0;
+    uint32_t stage = 0, phase = 1, parity = 0, read_phase = 1, raw_in = 0, raw_out = 0, raw_phase = 0;
     uint64_t *pend[2] = {nullptr, nullptr};  // barriers of copies on their way, the older first
     auto arrive = [&](uint64_t *b) {
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -528,7 +532,10 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
       asm volatile("bar.sync 1, 128;" ::: "memory");
       least = min(min(sm.warp_least[0], sm.warp_least[1]), min(sm.warp_least[2], sm.warp_least[3]));
       if (least >= x.key1) least = INT32_MAX;
-      if (i == 0) sm.least[parity] = least, sm.odd[parity] = 0;
+      if (i == 0) {
+        wait(&sm.odd_read[parity], read_phase);
+        sm.least[parity] = least, sm.odd[parity] = 0;
+      }
       asm volatile("bar.sync 1, 128;" ::: "memory");  // odd is 0 before anyone sets it
 
       // a tile that tensor copies can bring: whole, the same for all live rows, and no box of it
@@ -671,6 +678,7 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
       }
       flush();
       asm volatile("bar.sync 1, 128;" ::: "memory");  // everyone has read warp_least
+      read_phase ^= parity;
       parity ^= 1;
       return true;
     });
