@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(kPlanCta) attn_plan_kernel(const AttnParams p)
     for (int t = tid; t < last; t += kPlanCta) {
       const int b = p.owner[t];
       if (p.prompt[b] != INT32_MIN) continue;
-      const int at = (t - p.q_start[b]) * p.group;
+      const int at = (t - req(b).t0) * p.group;  // (there may be no query starts)
       bool whole = true;
       for (int u = at / kAttnWideRows; u <= (at + p.group - 1) / kAttnWideRows; ++u) {
         const AttnUnit x = p.units[p.unit_base[1 + b] + u];
