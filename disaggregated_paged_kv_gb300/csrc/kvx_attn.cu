@@ -504,7 +504,8 @@ Sizes sizes(int64_t n_q, int64_t n_reqs, int64_t q_heads, int64_t kv_heads, int6
 bool shape_ok(const kvx_layout *l, int64_t n_q, int64_t n_reqs, int64_t q_heads, int64_t prefix) {
   return l && l->kv_planes == 2 && l->head_dim <= KVX_ATTN_MAX_HEAD_DIM && n_q >= 0 &&
          n_reqs >= 0 && n_reqs <= KVX_MAX_TABLE_REQUESTS && q_heads >= 1 &&
-         q_heads % l->kv_heads == 0 && prefix >= 0 && n_q * q_heads <= (int64_t)1 << 30;
+         q_heads % l->kv_heads == 0 && prefix >= 0 && prefix <= KVX_ATTN_MAX_POSITIONS &&
+         n_q * q_heads <= (int64_t)1 << 30;
 }
 
 // Whether the tensor-core kernels take a layout.

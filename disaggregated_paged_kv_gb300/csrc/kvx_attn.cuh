@@ -183,7 +183,8 @@ __device__ __forceinline__ AttnReq attn_request(const AttnParams &p, int b, int3
   if (r.len < 0) {
     *bad = max(*bad, (int32_t)KVX_ERR_INVALID_ARG);
     r.len = 0;
-  } else if (r.len > (int64_t)p.max_pages * p.page_size) {
+  } else if (r.len > (int64_t)p.max_pages * p.page_size || r.len > KVX_ATTN_MAX_POSITIONS) {
+    // (so that a tile's end, and what the lanes of a warp look up behind it, are 32-bit positions)
     *bad = max(*bad, (int32_t)KVX_ERR_OUT_OF_RANGE);
     r.len = 0;
   }

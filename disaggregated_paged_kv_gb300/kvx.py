@@ -181,6 +181,7 @@ class AttnArgs(ctypes.Structure):
 
 MAX_TABLE_REQUESTS = 65536
 ATTN_MAX_HEAD_DIM = 256
+ATTN_MAX_POSITIONS = 2 ** 31 - 65536
 
 RESHARD_MAX_LAYOUTS = 64
 RESHARD_MAX_PARTS = 128

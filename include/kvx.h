@@ -595,6 +595,8 @@ KVX_API kvx_status kvx_block_tables(kvx_layout_t pool, const kvx_tables_args *ar
 
 /* Largest head_dim of kvx_shared_attention. */
 #define KVX_ATTN_MAX_HEAD_DIM 256
+/* Most positions of a request, and of a prefix, in kvx_shared_attention (2^31 - 65536). */
+#define KVX_ATTN_MAX_POSITIONS 2147418112
 
 /* Arguments of kvx_shared_attention (read on the host at the call); pointers are device memory. */
 typedef struct kvx_attn_args {
@@ -607,7 +609,8 @@ typedef struct kvx_attn_args {
   int32_t n_reqs;            /* 0 .. KVX_MAX_TABLE_REQUESTS */
   int32_t page_size;         /* tokens per table entry (>= 1); the layout's with KVX_HND_PAGED */
   int32_t max_pages;         /* entries of a row of tables (>= 1) */
-  int32_t prefix_len;        /* leading positions that all requests share (>= 0) */
+  int32_t prefix_len;        /* leading positions that all requests share (0 ..
+                                KVX_ATTN_MAX_POSITIONS) */
   int64_t table_stride;      /* elements between rows of tables, >= max_pages */
   const int32_t *tables;     /* row b: request b's pages in order of position.  Entries of
                                 positions below prefix_len, and past the request's end, are not
@@ -649,9 +652,9 @@ typedef struct kvx_attn_args {
  * of 16-bit and FP8 pools with head_dim 64 or 128 and 16-byte aligned heads take the tensor
  * cores, all others a plain kernel.
  * d_status: *d_status = KVX_OK, KVX_ERR_INVALID_ARG (a length below 0, q_start not rising from
- * 0 to at most n_q) or KVX_ERR_OUT_OF_RANGE (a length beyond the table row, a page id outside
- * the pool), the larger if both: out and lse are then unspecified, and nothing outside the pool
- * was read.  (KVX_ERR_TIMEOUT: a wait within a kernel ran out after a second or so; never expected.)  Host errors: KVX_ERR_INVALID_ARG (also a kv_planes = 1 layout), KVX_ERR_ALIGNMENT
+ * 0 to at most n_q) or KVX_ERR_OUT_OF_RANGE (a length beyond the table row or above
+ * KVX_ATTN_MAX_POSITIONS, a page id outside the pool), the larger if both: out and lse are then
+ * unspecified, and nothing outside the pool was read.  (KVX_ERR_TIMEOUT: a wait within a kernel ran out after a second or so; never expected.)  Host errors: KVX_ERR_INVALID_ARG (also a kv_planes = 1 layout), KVX_ERR_ALIGNMENT
  * (q or out not element aligned, other arrays not 4-byte aligned), KVX_ERR_OVERLAP (out in the
  * pool), KVX_ERR_NO_WORKSPACE (d_ws 256-byte aligned, kvx_attention_workspace_size bytes, no
  * initialisation needed).  Calls that overlap on the GPU need workspaces of their own.
