@@ -131,7 +131,8 @@ struct Consumer {
     float o[D / 8][4] = {}, m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
     int odd = 0;
     for (int k0 = x.key0; k0 < x.key1; k0 += kTileKeys) {
-      bar_wait(&sm.full[stage], phase, &sm.lost, &sm.error);
+      bar_wait(&sm.full[stage], phase, &sm.lost, &sm.error);  // (given up: what follows is of no account)
+      __syncwarp();
       const uint32_t kb = smem_u32(sm.kv[stage][0]), vb = smem_u32(sm.kv[stage][1]);
       const bool mixed = k0 + kTileKeys > least;
 #pragma unroll
@@ -383,6 +384,8 @@ attn_narrow_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
   __syncthreads();
   const AttnLine line = attn_line<kThreads>(p, g, sm.scan);
   attn_release_next();  // the join takes its place as CTAs end, and waits for the last
+  int stage = 0;        // of the producers
+  uint32_t phase = 1;
 
   if (warp < 4) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
@@ -401,9 +404,9 @@ attn_narrow_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     // lane pairs (K and V) of the warps take the boxes of a tile in turn
     const int boxes = tma.rows > 0 ? kTileKeys / tma.rows : 1, kv = lane & 1, pw = warp - 4;
     const int box = (lane >> 1) * 4 + pw;
-    int stage = 0;
-    uint32_t phase = 1;
+    bool lost = false;  // a wait was given up: nothing more is sent on its way
     attn_pieces(p, g, h, line, [&](const AttnPiece &x) {
+      if (lost) return;
       const int tiles = (x.key1 - x.key0 + kTileKeys - 1) / kTileKeys;
       // a tile of keys that all count (its boxes each lie in a page: tiles begin at multiples of them)
       auto regular = [&](int j) {
@@ -423,7 +426,8 @@ attn_narrow_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
       for (int j = 0; j < tiles; ++j) {
         const int32_t id = next;
         next = look(j + 1);
-        bar_wait(&sm.empty[stage], phase, &sm.lost, &sm.error);
+        lost = !__all_sync(~0u, bar_wait(&sm.empty[stage], phase, &sm.lost, &sm.error));
+        if (lost) return;
         if (regular(j)) {
           // (a box may arrive before the tile's bytes are announced: the stage is not full before
           // thread 0 has arrived)
@@ -464,6 +468,10 @@ attn_narrow_kernel(const __grid_constant__ AttnParams p, const __grid_constant__
     cp_async_wait<0>();
   }
   __syncthreads();
+  if (sm.lost) {
+    if (warp >= 4) bar_drain<S::kStages>(sm.full, stage, phase);
+    __syncthreads();
+  }
   if (tid == 0) p.errors[blockIdx.x] = sm.error;
   if (p.after_wide) attn_wait_prior();  // the join's wait for this kernel covers the wide one as well
 }

@@ -61,18 +61,32 @@ __device__ __forceinline__ void tma_load(void *dst, const CUtensorMap *map, int 
   asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
                ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_u32(b)) : "memory");
 }
-// Waits for a phase.  False when the wait is given up: after kAttnPolls polls (a poll waits some
+// Waits for a phase.  False when the wait is given up: after so many polls (a poll waits some
 // microseconds itself), or because some other wait of the CTA was.
-__device__ __forceinline__ bool bar_wait(uint64_t *b, uint32_t parity, int32_t *lost, int32_t *error) {
+__device__ __forceinline__ bool bar_wait(uint64_t *b, uint32_t parity, int32_t *lost, int32_t *error,
+                                         uint32_t polls = kAttnPolls) {
   for (uint32_t n = 0; !bar_try(b, parity); ++n) {
     if (*(volatile int32_t *)lost) return false;
-    if (n == kAttnPolls) {
+    if (n == polls) {
       *(volatile int32_t *)lost = 1;
       *(volatile int32_t *)error = KVX_ERR_TIMEOUT;
       return false;
     }
   }
   return true;
+}
+
+// When a wait of the CTA was given up: waits until what a thread has sent on its way to a ring of Stages
+// stages is there (stage and phase: those of the `empty` barrier that it would wait for next), so that nothing
+// arrives in memory that the CTA has given back.  A stage that some threads did not fill any more is never
+// full; after kAttnDrainPolls polls its copies, which depend on nothing, are there.
+constexpr uint32_t kAttnDrainPolls = 1u << 11;
+template <int Stages>
+__device__ __forceinline__ void bar_drain(uint64_t *full, uint32_t stage, uint32_t phase) {
+  for (uint32_t i = 0; i < Stages; ++i) {
+    const uint32_t parity = i < stage ? phase ^ 1 : phase;
+    for (uint32_t n = 0; n < kAttnDrainPolls && !bar_try(&full[i], parity); ++n) {}
+  }
 }
 
 // The planes of a call as AttnTma says, for tiles of `keys` keys.  Boxes are whole groups of 8 tokens of a

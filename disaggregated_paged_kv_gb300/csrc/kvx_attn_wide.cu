@@ -256,6 +256,9 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
     return bar_wait(b, parity, &sm.lost, &sm.error);
   };
 
+  // where the loads are in the rings
+  uint32_t stage = 0, phase = 1, raw_in = 0, raw_in_phase = 1;
+
   if (warp < 8) {
     // ---- softmax of row tile t, a thread a row ----
     asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
@@ -480,7 +483,7 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
     constexpr int kRaw = FP8 ? D / 16 : D / 8;         // 16-byte chunks of a row in the pool
     constexpr int kStep = 128 / kRaw, kPer = kKeys / kStep;
     const int c = i % kRaw, r0 = i / kRaw;
-    uint32_t stage = 0, phase = 1, parity = 0, read_phase = 1, raw_in = 0, raw_out = 0, raw_phase = 0;
+    uint32_t parity = 0, read_phase = 1, raw_out = 0, raw_phase = 0;
     uint64_t *pend[2] = {nullptr, nullptr};  // barriers of copies on their way, the older first
     auto arrive = [&](uint64_t *b) {
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -506,7 +509,9 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
       pend[0] = pend[1], pend[1] = b;
     };
     // A wait that was given up is not waited for again (see bar_wait): these threads then run
-    // through what is left without waiting, since they meet at barriers of their own.
+    // through what is left without waiting, since they meet at barriers of their own, and send nothing more
+    // on its way.
+    bool lost = false;  // a warp's lanes agree
     wide_pieces(p, unit0, w0, w1, [&](const WidePiece &x) {
       const int boxes = tma.rows > 0 ? kKeys / tma.rows : 1, pw = warp - 8;
       // page look-ups: lane l of warp w has box 4 l + w of a regular tile
@@ -532,10 +537,8 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
       asm volatile("bar.sync 1, 128;" ::: "memory");
       least = min(min(sm.warp_least[0], sm.warp_least[1]), min(sm.warp_least[2], sm.warp_least[3]));
       if (least >= x.key1) least = INT32_MAX;
-      if (i == 0) {
-        wait(&sm.odd_read[parity], read_phase);
-        sm.least[parity] = least, sm.odd[parity] = 0;
-      }
+      lost |= !__all_sync(~0u, i != 0 || wait(&sm.odd_read[parity], read_phase));
+      if (i == 0) sm.least[parity] = least, sm.odd[parity] = 0;
       asm volatile("bar.sync 1, 128;" ::: "memory");  // odd is 0 before anyone sets it
 
       // a tile that tensor copies can bring: whole, the same for all live rows, and no box of it
@@ -580,10 +583,10 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
       int32_t ahead_page = page0, ahead_next = FP8 ? box_page(1) : 0;
       auto fetch = [&](int upto) {  // up to tile and half number `upto`
         for (; ahead < min(upto, 2 * x.tiles); ++ahead) {
-          if (regular(ahead >> 1)) {
+          if (regular(ahead >> 1) && !lost) {
             if (i == 0) bar_expect(&sm.raw_full[raw_in], kKeys * D);
             tensor(ahead >> 1, ahead & 1, ahead_page, sm.raw[raw_in], &sm.raw_full[raw_in]);
-            if (++raw_in == S::kRawStages) raw_in = 0;
+            if (++raw_in == S::kRawStages) raw_in = 0, raw_in_phase ^= 1;
           }
           if (ahead & 1) ahead_page = ahead_next, ahead_next = box_page((ahead + 3) >> 1);
         }
@@ -617,20 +620,25 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
               }
             }
           }
-          if (!bar_try(&sm.empty[stage], phase)) {
+          bool there = bar_try(&sm.empty[stage], phase);
+          if (!there) {
             flush();  // nothing that is there is held back meanwhile
-            wait(&sm.empty[stage], phase);
+            there = wait(&sm.empty[stage], phase);
           }
+          lost |= !__all_sync(~0u, there);
           char *dst = sm.kv[stage];
           if constexpr (FP8) {
             if (reg) {
-              wait(&sm.raw_full[raw_out], raw_phase);
+              lost |= !__all_sync(~0u, wait(&sm.raw_full[raw_out], raw_phase));
 #pragma unroll
               for (int k = 0; k < kPer; ++k)
                 raw[k] = *reinterpret_cast<const uint4 *>(sm.raw[raw_out] + place8<D>(r0 + k * kStep, c));
               asm volatile("bar.sync 1, 128;" ::: "memory");  // the raw stage may be filled again
               if (++raw_out == S::kRawStages) raw_out = 0, raw_phase ^= 1;
             }
+          }
+          if (lost) continue;
+          if constexpr (FP8) {
 #pragma unroll
             for (int k = 0; k < kPer; ++k) convert(raw[k], dst, r0 + k * kStep);
           } else if (reg) {
@@ -698,7 +706,8 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
       constexpr uint32_t kDescO = kBase | (uint32_t)(D >> 3) << 17 | 1u << 16;  // V read across its rows
       // (everything is a function of t by arithmetic and the loops over t are unrolled: one thread issues
       // a product every 64 cycles and has no time for tables in memory)
-      uint32_t stage = 0, phase = 0, q_phase = 0, p_phase = 0, oe_phase = 1;
+      uint32_t q_phase = 0, p_phase = 0, oe_phase = 1;
+      phase = 0;
       const uint64_t q0 = operand<D>(smem_u32(sm.q[0])), kv0 = operand<D>(smem_u32(sm.kv[0]));
       constexpr uint64_t kTileStep = 128 * D * 2 >> 4;
       auto scores = [&](int t, uint32_t kst) {
@@ -766,15 +775,21 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
         oe_phase ^= 1;
         return true;
       });
-      if (*(volatile int32_t *)&sm.lost) {  // products in flight end before their memory is given up
-        mma_commit(&sm.drained, lead);
-        for (int i = 0; i < 1 << 16 && !bar_try(&sm.drained, 0); ++i) {}
-      }
     }
   }
   fence_before();
   __syncthreads();
   fence_after();
+  if (sm.lost) {  // products and copies in flight end before their memory is given up
+    if (warp == 12) {
+      mma_commit(&sm.drained, elect_lane());  // (the lane that has issued them)
+      for (uint32_t n = 0; n < kAttnDrainPolls && !bar_try(&sm.drained, 0); ++n) {}
+    } else if (warp >= 8 && warp < 12) {
+      bar_drain<kStages>(sm.full, stage, phase);
+      if constexpr (FP8) bar_drain<S::kRawStages>(sm.raw_full, raw_in, raw_in_phase);
+    }
+    __syncthreads();
+  }
   if (tid == 0) p.errors[p.groups * p.kv_heads + blockIdx.x] = sm.error;
   if (warp == 12)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(sm.tmem) : "memory");
