@@ -292,6 +292,9 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
             }
           }
           f = half_scale(most, &scale);
+          // a row of zeros has the factor 2^-126: the product with a small scale must not be 0, by which
+          // masked scores of -infinity are multiplied (any number as small gives the same weights)
+          scale = fmaxf(scale, 1.17549435e-38f);
         }
         const char *src = p.q + token * p.q_tok + (int64_t)(h * p.group + member) * p.q_head;
 #pragma unroll 1
