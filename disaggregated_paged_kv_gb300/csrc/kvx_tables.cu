@@ -126,9 +126,16 @@ __device__ __forceinline__ Span checked_span(const TabParams &p, int b, bool pag
   return s;
 }
 
-// Cursor, totals, and every page id that the call is going to use, by thread at of step.
+// Whether request b is new and has tokens: its row begins with the shared prefix.
+__device__ __forceinline__ bool takes_prefix(const TabParams &p, int b) {
+  return !(p.a.old_lens && p.a.old_lens[b] != 0) && p.a.new_lens[b] != 0;
+}
+
+// Cursor, totals, and every page id that the call is going to use (prefix: those of the shared prefix as
+// well), by thread at of step.
 __device__ __forceinline__ void check_ids(const TabParams &p, int64_t cur, int64_t tokens,
-                                          int64_t pages, int64_t at, int64_t step, int32_t *bad) {
+                                          int64_t pages, bool prefix, int64_t at, int64_t step,
+                                          int32_t *bad) {
   if (cur < 0) {
     *bad = max(*bad, (int32_t)KVX_ERR_INVALID_ARG);
   } else if (cur + pages > p.a.n_free || tokens > p.a.max_tokens) {
@@ -136,7 +143,7 @@ __device__ __forceinline__ void check_ids(const TabParams &p, int64_t cur, int64
   } else {
     for (int64_t i = at; i < pages; i += step)
       if (!page_ok(p, p.a.free_pages[cur + i])) *bad = max(*bad, (int32_t)KVX_ERR_OUT_OF_RANGE);
-    for (int64_t i = at; i < p.a.n_prefix_pages; i += step)
+    for (int64_t i = at; prefix && i < p.a.n_prefix_pages; i += step)
       if (!page_ok(p, p.a.prefix_pages[i])) *bad = max(*bad, (int32_t)KVX_ERR_OUT_OF_RANGE);
   }
 }
@@ -147,10 +154,12 @@ __global__ void __launch_bounds__(kTabThreads) tables_plan_kernel(const TabParam
   const int n = p.a.n_reqs, tid = threadIdx.x;
   int32_t bad = 0;
   int64_t tokens = 0, pages = 0;
+  bool prefix = false;
   for (int b0 = 0; b0 < n; b0 += kTabThreads) {
     const int b = b0 + tid;
     int64_t cnt = 0, take = 0;
     if (b < n) {
+      prefix = prefix || takes_prefix(p, b);
       const Span s = checked_span(p, b, blockIdx.x == 0, &bad);
       cnt = s.end - s.start;
       take = s.need - s.have;
@@ -166,7 +175,7 @@ __global__ void __launch_bounds__(kTabThreads) tables_plan_kernel(const TabParam
     pages += tp;
   }
   const int64_t cur = p.a.cursor ? p.a.cursor[0] : 0;
-  check_ids(p, cur, tokens, pages, (int64_t)blockIdx.x * kTabThreads + tid,
+  check_ids(p, cur, tokens, pages, __syncthreads_or(prefix), (int64_t)blockIdx.x * kTabThreads + tid,
             (int64_t)p.ctas * kTabThreads, &bad);
   const int any_range = __syncthreads_or(bad == KVX_ERR_OUT_OF_RANGE);
   const int any_arg = __syncthreads_or(bad == KVX_ERR_INVALID_ARG);
@@ -255,7 +264,7 @@ __device__ __forceinline__ void fill(const TabParams &p, const int32_t *tok_base
   // the shared prefix at the head of every new request's row, a CTA per row
   if (p.a.n_prefix_pages > 0)
     for (int b = cta; b < n; b += ctas) {
-      if ((p.a.old_lens && p.a.old_lens[b] != 0) || p.a.new_lens[b] == 0) continue;
+      if (!takes_prefix(p, b)) continue;
       for (int j = tid; j < p.a.n_prefix_pages; j += Threads)
         p.a.tables[b * p.a.table_stride + j] = p.a.prefix_pages[j];
     }
@@ -288,7 +297,9 @@ __global__ void __launch_bounds__(kTabThreads) tables_one_kernel(const TabParams
   const int64_t cur = p.a.cursor ? p.a.cursor[0] : 0;
   int32_t bad = 0;
   int64_t cnt = 0, take = 0, tokens, pages;
+  bool prefix = false;
   if (b < n) {
+    prefix = takes_prefix(p, b);
     const Span s = checked_span(p, b, true, &bad);
     cnt = s.end - s.start;
     take = s.need - s.have;
@@ -296,7 +307,7 @@ __global__ void __launch_bounds__(kTabThreads) tables_one_kernel(const TabParams
   block_scan2(cnt, take, &tokens, &pages, sm);
   if (b < n) tok_base[b] = (int32_t)cnt, page_base[b] = (int32_t)take;
   if (b == n % kTabThreads) tok_base[n] = (int32_t)tokens, page_base[n] = (int32_t)pages;
-  check_ids(p, cur, tokens, pages, b, kTabThreads, &bad);
+  check_ids(p, cur, tokens, pages, __syncthreads_or(prefix), b, kTabThreads, &bad);
   const int any_range = __syncthreads_or(bad == KVX_ERR_OUT_OF_RANGE);
   const int any_arg = __syncthreads_or(bad == KVX_ERR_INVALID_ARG);
   if (b == 0) *p.status = any_range ? KVX_ERR_OUT_OF_RANGE : any_arg ? KVX_ERR_INVALID_ARG : KVX_OK;
