@@ -83,7 +83,8 @@ __global__ void __launch_bounds__(kPlanCta) attn_plan_kernel(const AttnParams p)
     if (b < n) {
       r = attn_request(p, b, &bad);
       most = max(most, r.len);
-      prompt = p.wide_groups > 0 && (int64_t)r.n * p.group > kAttnNarrowRows;
+      // (one token, of however many heads, shares the batch's pass over the prefix)
+      prompt = p.wide_groups > 0 && r.n > 1 && (int64_t)r.n * p.group > kAttnNarrowRows;
       mine = prompt ? 0 : r.n;
     }
     const int64_t at = plain + block_excl(mine, &total, sm);

@@ -5,8 +5,8 @@
 // h * G + r % G.  Three kinds of work, each a set of rows with the keys they all read:
 //   own      a request's rows and its positions behind the prefix;
 //   prefix   the rows of many requests and the prefix;
-//   prompt   a request with many rows of its own and all its positions, prefix included: its
-//            tiles of rows are full without the others', and one pass needs no join.
+//   prompt   a request with several tokens, more than 64 rows in all, and all its positions, prefix
+//            included: it takes tiles of rows of its own, and one pass needs no join.
 // The narrow kernel (and the plain one) takes units of up to row_tile rows: own work, and the
 // prefix where there are few rows in all.  The wide kernel takes units of up to 256 rows: the
 // prefix and prompts.  A unit's keys are cut into tiles, all units' key tiles stand in a line, each as

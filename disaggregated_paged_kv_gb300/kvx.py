@@ -744,7 +744,7 @@ def shared_attention(pool: Layout, layer: int, q, out, tables, seq_lens, page_si
     """kvx_shared_attention: causal attention of ``q`` ([n_q, q_heads, head_dim], a head's
     elements contiguous) over one layer of the pool, into ``out`` (and ``lse``, float32
     [n_q, q_heads]).  Request b's positions below ``prefix_len`` are those of ``prefix_pages``,
-    read once for the whole batch, the rest those of ``tables[b]``; its query tokens are
+    read once for the whole batch (long prompts may go over them each), the rest those of ``tables[b]``; its query tokens are
     ``q_start[b]`` up to ``q_start[b + 1]``, its last ``seq_lens[b]`` positions' end (None: one
     token each).  ``scale`` is head_dim ** -0.5 by default."""
     _i32_arrays((seq_lens, q_start, prefix_pages, status), tables)

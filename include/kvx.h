@@ -639,7 +639,8 @@ typedef struct kvx_attn_args {
  * drafted tokens a request, and for prompts.  Query token i of request b (of n) with length len
  * sees positions 0 .. len - n + i: those below prefix_len through prefix_pages, whose scores
  * with the queries of all requests are computed together so that the prefix is read once for
- * the batch, the others through row b.  With s_j = scale * k_scale * <q, K_j>:
+ * the batch, the others through row b.  (A request of several query tokens that are more than 64
+ * rows, n * q_heads / kv_heads, may go over the prefix by itself.)  With s_j = scale * k_scale * <q, K_j>:
  *   out = v_scale * sum_j exp(s_j) V_j / sum_j exp(s_j),   lse = log sum_j exp(s_j).
  * Sums are held in 32 bits; with 16- and 8-bit pools the weights exp(s_j - max) are rounded to the
  * pool's 16-bit type (F16 for an FP8 pool, its queries too) for the product with V.  Results do not

@@ -29,3 +29,14 @@ def test_single_tokens(dtype, n, starts):
 def test_single_tokens_among_prompts(G):
     run(ar.make("bf16", "planes", 16, 1, G, 64, lens=[700, 301, 0, 640, 333, 650], qlens=[1, 30, 1, 1, 33, 5],
                 prefix=300, room=100_000))
+
+
+def test_query_starts_change_nothing():
+    """Single tokens of 71 heads share the pass over the prefix whether or not their starts are given: the
+    same tiles, and so the same bits."""
+    lens = [128 + 1 + (5 * i) % 30 for i in range(2000)]
+    c = ar.make("bf16", "planes", 16, 1, 71, 64, lens=lens, prefix=128, layers=1, layer=0)
+    r = ar.Run(c)
+    out, lse = r.call(q_start=None).results()
+    with_starts = r.call(q_start=r.q_start).results()
+    assert out.equal(with_starts[0]) and lse.equal(with_starts[1])
