@@ -41,17 +41,6 @@ int elem_bytes_of(int32_t dtype) {
 
 bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
 
-bool ranges_overlap(uintptr_t a0, uintptr_t a1, uintptr_t b0, uintptr_t b1) {
-  return a0 < b1 && b0 < a1;
-}
-
-bool layout_overlaps_range(const kvx_layout *l, uintptr_t b0, uintptr_t b1) {
-  if (!ranges_overlap(l->lo, l->hi, b0, b1)) return false;
-  for (int p = 0; p < l->planes; ++p)
-    if (ranges_overlap(l->plane[p], l->plane[p] + l->extent, b0, b1)) return true;
-  return false;
-}
-
 bool layouts_overlap(const kvx_layout *a, const kvx_layout *b) {
   if (!ranges_overlap(a->lo, a->hi, b->lo, b->hi)) return false;
   for (int p = 0; p < a->planes; ++p)

@@ -580,8 +580,7 @@ extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_arg
     const uintptr_t b0 = (uintptr_t)a.out;
     const uintptr_t b1 = b0 + ((a.n_q - 1) * a.out_token_stride + (a.q_heads - 1) * a.out_head_stride +
                                pool->head_dim) * io;
-    for (int i = 2 * a.layer; i < 2 * a.layer + 2; ++i)
-      if (b0 < pool->plane[i] + pool->extent && pool->plane[i] < b1) return KVX_ERR_OVERLAP;
+    if (layout_overlaps_range(pool, b0, b1)) return KVX_ERR_OVERLAP;
   }
   // What the wide kernel may have: the prefix, and with several tokens a request prompts, whose keys
   // only the tables bound.  Below kWideWork operations its launch costs more than it saves.  It takes

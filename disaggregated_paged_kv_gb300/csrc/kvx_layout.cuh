@@ -19,3 +19,14 @@ struct kvx_layout {
   uintptr_t lo, hi;     // envelope of all planes
   uintptr_t plane[KVX_MAX_PLANES];
 };
+
+inline bool ranges_overlap(uintptr_t a0, uintptr_t a1, uintptr_t b0, uintptr_t b1) {
+  return a0 < b1 && b0 < a1;
+}
+
+inline bool layout_overlaps_range(const kvx_layout *l, uintptr_t b0, uintptr_t b1) {
+  if (!ranges_overlap(l->lo, l->hi, b0, b1)) return false;
+  for (int p = 0; p < l->planes; ++p)
+    if (ranges_overlap(l->plane[p], l->plane[p] + l->extent, b0, b1)) return true;
+  return false;
+}

@@ -655,10 +655,12 @@ typedef struct kvx_attn_args {
  * d_status: *d_status = KVX_OK, KVX_ERR_INVALID_ARG (a length below 0, q_start not rising from
  * 0 to at most n_q) or KVX_ERR_OUT_OF_RANGE (a length beyond the table row or above
  * KVX_ATTN_MAX_POSITIONS, a page id outside the pool), the larger if both: out and lse are then
- * unspecified, and nothing outside the pool was read.  (KVX_ERR_TIMEOUT: a wait within a kernel ran out after a second or so; never expected.)  Host errors: KVX_ERR_INVALID_ARG (also a kv_planes = 1 layout), KVX_ERR_ALIGNMENT
- * (q or out not element aligned, other arrays not 4-byte aligned), KVX_ERR_OVERLAP (out in the
- * pool), KVX_ERR_NO_WORKSPACE (d_ws 256-byte aligned, kvx_attention_workspace_size bytes, no
- * initialisation needed).  Calls that overlap on the GPU need workspaces of their own.
+ * unspecified, and nothing outside the pool was read.  (KVX_ERR_TIMEOUT: a wait within a kernel
+ * ran out after a second or so; never expected.)
+ * Host errors: KVX_ERR_INVALID_ARG (also a kv_planes = 1 layout), KVX_ERR_ALIGNMENT (q or out not
+ * element aligned, other arrays not 4-byte aligned), KVX_ERR_OVERLAP (out in a plane of the pool,
+ * of any layer), KVX_ERR_NO_WORKSPACE (d_ws 256-byte aligned, kvx_attention_workspace_size bytes,
+ * no initialisation needed).  Calls that overlap on the GPU need workspaces of their own.
  * kvx_attention_workspace_size returns 0 if the arguments are out of range; a size covers every
  * call with at most that many query tokens, requests, heads and prefix tokens on the layout. */
 KVX_API size_t kvx_attention_workspace_size(kvx_layout_t pool, int32_t n_q, int32_t n_reqs,
