@@ -571,6 +571,12 @@ extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_arg
   for (int64_t x : {a.q_token_stride, a.q_head_stride, a.out_token_stride, a.out_head_stride,
                     a.table_stride})
     if (x < 0 || x > most) return KVX_ERR_INVALID_ARG;
+  // the last element's byte, past any memory: offsets within q and out are 64-bit numbers
+  auto reach = [&](int64_t token, int64_t head) {
+    return ((double)token * std::max(0, a.n_q - 1) + (double)head * (a.q_heads - 1) + pool->head_dim) * io;
+  };
+  if (reach(a.q_token_stride, a.q_head_stride) > 0x1p60 || reach(a.out_token_stride, a.out_head_stride) > 0x1p60)
+    return KVX_ERR_INVALID_ARG;
   if (!mult(a.q, io) || !mult(a.out, io)) return KVX_ERR_ALIGNMENT;
   for (const void *q : {(const void *)a.tables, (const void *)a.prefix_pages,
                         (const void *)a.seq_lens, (const void *)a.q_start, (const void *)a.lse,

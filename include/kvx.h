@@ -624,7 +624,7 @@ typedef struct kvx_attn_args {
                                 q_start[b + 1] - 1, the last positions of the request, in order;
                                 q_start[n_reqs] <= n_q.  NULL: one token each (n_q == n_reqs) */
   const void *q;             /* [n_q][q_heads][head_dim], elements of a head contiguous */
-  int64_t q_token_stride, q_head_stride; /* elements */
+  int64_t q_token_stride, q_head_stride; /* elements, 0 .. 2^40, the last one below 2^60 bytes */
   void *out;                 /* as q */
   int64_t out_token_stride, out_head_stride;
   float *lse;                /* [n_q][q_heads] natural log of each row's sum of exponentials; or
