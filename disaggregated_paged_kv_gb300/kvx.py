@@ -284,18 +284,35 @@ def _nbytes(x) -> int:
     return int(x.numel() * x.element_size())
 
 
-_raw_stream = None  # torch's current stream as a number, without a Stream object around it
+_stream_number = None  # what _stream_function gave
+
+
+def _stream_function(torch):
+    """A function for torch.cuda.current_stream().cuda_stream: torch's own short way to the number, without a
+    Stream object around it, where it has both parts of that and they agree with the public way."""
+    def public():
+        return int(torch.cuda.current_stream().cuda_stream)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    device = getattr(torch._C, "_cuda_getDevice", None)
+    if raw is None or device is None:
+        return public
+
+    def short():
+        return raw(device())
+    try:
+        return short if short() == public() else public
+    except Exception:
+        return public
 
 
 def _current_stream() -> Optional[int]:
-    global _raw_stream
-    if _raw_stream is None:
+    global _stream_number
+    if _stream_number is None:
         import torch
-        if not torch.cuda.is_initialized() or not hasattr(torch._C, "_cuda_getCurrentRawStream"):
+        if not torch.cuda.is_initialized():
             return int(torch.cuda.current_stream().cuda_stream) or None
-        device, raw = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
-        _raw_stream = lambda: raw(device())  # noqa: E731
-    return _raw_stream() or None
+        _stream_number = _stream_function(torch)
+    return _stream_number() or None
 
 
 def _stream(stream) -> Optional[int]:
