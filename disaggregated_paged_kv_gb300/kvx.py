@@ -740,7 +740,7 @@ def block_tables(pool: Layout, page_size: int, new_lens, tables, free_pages, cur
         room = min(room, positions.numel())
     a = TablesArgs(n, page_size, _ptr(old_lens), new_lens.data_ptr(), _ptr(prefix_pages),
                    0 if prefix_pages is None else prefix_pages.numel(), width,
-                   tables.data_ptr(), tables.stride(0), free_pages.data_ptr(), free_pages.numel(),
+                   tables.data_ptr(), _row_stride(tables), free_pages.data_ptr(), free_pages.numel(),
                    0, _ptr(cursor), next_cursor.data_ptr(), q_start.data_ptr(), slots.data_ptr(),
                    _ptr(positions), room)
     _check(lib().kvx_block_tables(_h(pool), a, _ptr(ws), _nbytes(ws) if ws_bytes is None else ws_bytes,
@@ -780,7 +780,7 @@ def shared_attention(pool: Layout, layer: int, q, out, tables, seq_lens, page_si
                             or not lse.is_contiguous()):
         raise ValueError("lse is a contiguous float32 [n_q, q_heads]")
     a = AttnArgs(layer, _q_dtype(q), heads, n_q, n, page_size, width, prefix_len,
-                 tables.stride(0), tables.data_ptr(), _ptr(prefix_pages),
+                 _row_stride(tables), tables.data_ptr(), _ptr(prefix_pages),
                  0 if prefix_pages is None else prefix_pages.numel(), 0, seq_lens.data_ptr(),
                  _ptr(q_start), q.data_ptr(), q_tok, q_head, out.data_ptr(), o_tok, o_head,
                  _ptr(lse), dim ** -0.5 if scale is None else scale, k_scale, v_scale, 0)
@@ -797,6 +797,12 @@ def _q_dtype(q) -> int:
     if got is None:
         raise ValueError("q and out are float16, bfloat16 or float32")
     return got
+
+
+def _row_stride(tables) -> int:
+    """Elements between rows of tables; a single row has none, whatever its tensor's stride says."""
+    rows, width = tables.shape
+    return tables.stride(0) if rows > 1 else width
 
 
 def _i32_arrays(lists, tables) -> None:
