@@ -65,20 +65,11 @@ __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
   return r;
 }
 
-// Two E4M3 values as packed 16-bit ones (exact in either type).
-template <typename T>
-__device__ __forceinline__ uint32_t from_e4m3x2(uint16_t x);
-template <>
-__device__ __forceinline__ uint32_t from_e4m3x2<__half>(uint16_t x) {
+// Two E4M3 values as packed f16 ones (exact).
+__device__ __forceinline__ uint32_t from_e4m3x2(uint16_t x) {
   uint32_t r;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(x));
   return r;
-}
-template <>
-__device__ __forceinline__ uint32_t from_e4m3x2<__nv_bfloat16>(uint16_t x) {
-  const uint32_t h = from_e4m3x2<__half>(x);
-  const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-  return pack2<__nv_bfloat16>(f.x, f.y);
 }
 
 // Whether a packed pair of 16-bit values holds an infinity or NaN.

@@ -156,8 +156,8 @@ struct Consumer {
               for (int n = 0; n < 2; ++n)
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                  mma16816<T>(s[b][n], q[2 * k + e], from_e4m3x2<T>((uint16_t)f[2 * n + e]),
-                              from_e4m3x2<T>((uint16_t)(f[2 * n + e] >> 16)));
+                  mma16816<T>(s[b][n], q[2 * k + e], from_e4m3x2((uint16_t)f[2 * n + e]),
+                              from_e4m3x2((uint16_t)(f[2 * n + e] >> 16)));
             }
           } else {
 #pragma unroll
@@ -221,8 +221,8 @@ struct Consumer {
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 const uint32_t u = __byte_perm(f[e], 0, 0x3120);
-                v[2 * e] = from_e4m3x2<T>((uint16_t)u);
-                v[2 * e + 1] = from_e4m3x2<T>((uint16_t)(u >> 16));
+                v[2 * e] = from_e4m3x2((uint16_t)u);
+                v[2 * e + 1] = from_e4m3x2((uint16_t)(u >> 16));
               }
               if (mixed)
 #pragma unroll
@@ -320,7 +320,7 @@ struct Consumer {
           for (int i = 0; i < 2; ++i) {
             float e;
             if constexpr (FP8) {
-              const uint32_t u = from_e4m3x2<__half>(reinterpret_cast<const uint8_t *>(v)[column(n, i, c4)]);
+              const uint32_t u = from_e4m3x2(reinterpret_cast<const uint8_t *>(v)[column(n, i, c4)]);
               e = __half2float(*reinterpret_cast<const __half *>(&u));
             } else {
               e = (float)reinterpret_cast<const T *>(v)[column(n, i, c4)];

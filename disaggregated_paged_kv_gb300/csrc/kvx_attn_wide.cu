@@ -429,7 +429,7 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
               for (int k = 0; k < 32; ++k) {
                 float e;
                 if constexpr (FP8) {
-                  const uint32_t u = from_e4m3x2<__half>(reinterpret_cast<const uint8_t *>(v)[c * 32 + k]);
+                  const uint32_t u = from_e4m3x2(reinterpret_cast<const uint8_t *>(v)[c * 32 + k]);
                   e = __half2float(*reinterpret_cast<const __half *>(&u));
                 } else {
                   e = (float)reinterpret_cast<const T *>(v)[c * 32 + k];
@@ -574,8 +574,8 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
         uint32_t o[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          o[2 * e] = from_e4m3x2<T>((uint16_t)w[e]);
-          o[2 * e + 1] = from_e4m3x2<T>((uint16_t)(w[e] >> 16));
+          o[2 * e] = from_e4m3x2((uint16_t)w[e]);
+          o[2 * e + 1] = from_e4m3x2((uint16_t)(w[e] >> 16));
         }
         *reinterpret_cast<uint4 *>(dst + place<D>(r, 2 * c)) = make_uint4(o[0], o[1], o[2], o[3]);
         *reinterpret_cast<uint4 *>(dst + place<D>(r, 2 * c + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
