@@ -11,8 +11,8 @@
 //
 // Bound: 4 D operations a score on the tensor cores (1024 cycles for 128 x 128 scores at D = 128)
 // against one exponential and about five instructions a score on four warps.  Measured: eight prompts
-// behind a shared prefix, 842 GFLOP in all, 677-689 us with the plan and the join (1.22-1.24 PFLOP/s); the tensor
-// cores are busy 62-65 % of this kernel's time and wait for weights in the rest.  Two threads a row, each with
+// behind a shared prefix, 842 GFLOP in all, 682-708 us with the plan and the join (1.19-1.23 PFLOP/s); the tensor
+// cores are busy 61-64 % of this kernel's time and wait for weights in the rest.  Two threads a row, each with
 // half of its keys, took longer (749 against 704 us then).
 //
 // A row's sums refer to a maximum that is renewed only when a score passes it by 2^8 (f16: 2^2): the factor
