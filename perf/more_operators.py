@@ -7,9 +7,9 @@ is true, elementary torch operations otherwise) and ``exact`` the definition in 
 
 A 4-bit head vector of D elements is D / 2 bytes of codes (element 2 i in the low half of byte i) and, for
 every 32 elements, a pair of 16-bit floats, scale and low: an element is low + code * scale.  Of 32 values
-clamped to +-61440, all steps in 32 bits: low is the least, scale the 16-bit float nearest to (greatest - low) *
-(1 / 15), and a code (value - low) * (1 / scale), rounded to even and clamped to 0 .. 15 (0 where scale
-is 0).  An 8-bit element is the E4M3 value nearest to value * (1 / the plane's scale), within +-448.
+clamped to +-61440, all steps in 32 bits: low is the least, as a 16-bit float, scale the 16-bit float nearest to
+(greatest - low) * (1 / 15) and at least 0, and a code (value - low) * (1 / scale), rounded to even and
+clamped to 0 .. 15 (0 where scale is 0).  An 8-bit element is the E4M3 value nearest to value * (1 / the plane's scale), within +-448.
 """
 import math
 import random
@@ -152,7 +152,7 @@ def _encode(x):
     """The 4-bit vectors ([..., 5 D / 8] bytes) of 32-bit values [..., D]."""
     g = x.clamp(-_MOST, _MOST).unflatten(-1, (-1, _GROUP))
     low = g.amin(-1).half()
-    scale = ((g.amax(-1) - low.float()) * torch.tensor(1 / 15, dtype=torch.float32)).half()
+    scale = ((g.amax(-1) - low.float()) * torch.tensor(1 / 15, dtype=torch.float32)).clamp_(min=0).half()
     r = torch.where(scale > 0, 1 / scale.float(), 0.0)
     code = ((g - low.float().unsqueeze(-1)) * r.unsqueeze(-1)).round_().clamp_(0, 15).to(torch.uint8)
     code = code.flatten(-2).unflatten(-1, (-1, 2))
@@ -429,7 +429,7 @@ def _stored(x, dim):
         y = x[..., a:a + _GROUP].clamp(-_MOST, _MOST)
         low = y.min(-1, keepdim=True).values.half().double()
         reach = _single(_single(y.max(-1, keepdim=True).values - low) * _single(torch.tensor(1 / 15.0).double()))
-        scale = reach.float().half().double()
+        scale = reach.clamp(min=0).float().half().double()
         inverse = _single(1 / scale.masked_fill(scale == 0, 1.0))
         code = torch.round(_single(_single(y - low) * inverse)).clamp(0, 15)
         out[..., a:a + _GROUP] = low + code.masked_fill(scale == 0, 0.0) * scale
