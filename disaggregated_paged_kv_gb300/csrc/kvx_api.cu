@@ -7,6 +7,7 @@
 // and no half-written KV is left behind).
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
@@ -14,6 +15,7 @@
 
 #include "kvx_internal.cuh"
 #include "kvx_layout.cuh"
+#include "kvx_quant.cuh"
 #include "kvx_reshard.cuh"
 
 namespace {
@@ -33,6 +35,7 @@ int elem_bytes_of(int32_t dtype) {
     case KVX_F32:
       return 4;
     case KVX_FP8:
+    case KVX_Q4:  // bytes; a head vector's length is its own (see kvx_layout_create)
       return 1;
     default:
       return 0;
@@ -50,7 +53,8 @@ bool layouts_overlap(const kvx_layout *a, const kvx_layout *b) {
 
 bool same_rows(const kvx_layout *a, const kvx_layout *b) {
   return a->num_layers == b->num_layers && a->kv_planes == b->kv_planes &&
-         a->kv_heads == b->kv_heads && a->head_dim == b->head_dim && a->elem == b->elem;
+         a->kv_heads == b->kv_heads && a->head_dim == b->head_dim && a->elem == b->elem &&
+         a->seg_bytes == b->seg_bytes;
 }
 
 int32_t log2_exact(int64_t v) {
@@ -454,7 +458,9 @@ kvx_status kvx_layout_create(const kvx_layout_desc *d, kvx_layout_t *out) {
       d->head_dim < 1 || eb == 0 || d->num_slots < 1 || d->num_slots > INT32_MAX)
     return KVX_ERR_INVALID_ARG;
   if (d->kind != KVX_NHD && d->kind != KVX_HND_PAGED) return KVX_ERR_INVALID_ARG;
-  const int64_t seg = (int64_t)d->head_dim * eb;
+  const bool q4 = d->dtype == KVX_Q4;
+  if (q4 && d->head_dim % KVX_Q4_GROUP != 0) return KVX_ERR_INVALID_ARG;
+  const int64_t seg = q4 ? (int64_t)d->head_dim / 8 * 5 : (int64_t)d->head_dim * eb;
   const int64_t R = seg * d->kv_heads;
   if (R > (int64_t)1 << 30) return KVX_ERR_INVALID_ARG;
   kvx_layout *l = new (std::nothrow) kvx_layout;
@@ -471,6 +477,7 @@ kvx_status kvx_layout_create(const kvx_layout_desc *d, kvx_layout_t *out) {
   l->num_slots = d->num_slots;
   l->row_bytes = R;
   l->seg_bytes = seg;
+  const int64_t align = q4 ? 4 : eb;  // of planes: elements, or a head vector's scales, stay aligned
   kvx_status st = KVX_OK;
   // Rows move in the widest accesses that every row start, head vector and plane allows:
   // 16 bytes for the usual shapes, narrower for rows that are not 16-byte multiples.
@@ -487,6 +494,7 @@ kvx_status kvx_layout_create(const kvx_layout_desc *d, kvx_layout_t *out) {
     l->slot_stride = d->slot_stride == 0 ? R : d->slot_stride;
     if (l->slot_stride < R) st = KVX_ERR_INVALID_ARG;
     else if (l->slot_stride > ((int64_t)1 << 62) / d->num_slots) st = KVX_ERR_INVALID_ARG;
+    else if (q4 && l->slot_stride % align != 0) st = KVX_ERR_ALIGNMENT;
     l->vec = std::min(l->vec, pow2_align(l->slot_stride));
     l->extent = (d->num_slots - 1) * l->slot_stride + R;
   }
@@ -502,7 +510,7 @@ kvx_status kvx_layout_create(const kvx_layout_desc *d, kvx_layout_t *out) {
         a = (uintptr_t)d->base + (uintptr_t)(d->plane_stride * p);
       }
       if (a == 0) { st = KVX_ERR_INVALID_ARG; break; }
-      if (a % l->elem != 0) { st = KVX_ERR_ALIGNMENT; break; }  // elements stay aligned
+      if (a % align != 0) { st = KVX_ERR_ALIGNMENT; break; }
       l->vec = std::min(l->vec, pow2_align((int64_t)a));
       l->plane[p] = a;
       if (a < l->lo) l->lo = a;
@@ -1101,7 +1109,8 @@ kvx_status kvx_move_heads(int32_t op, kvx_layout_t src, const int32_t *d_src_slo
   c.shape = uses_src ? src : dst;
   if (c.src && c.dst) {
     if (src->num_layers != dst->num_layers || src->kv_planes != dst->kv_planes ||
-        src->head_dim != dst->head_dim || src->elem != dst->elem)
+        src->head_dim != dst->head_dim || src->elem != dst->elem ||
+        src->seg_bytes != dst->seg_bytes)
       return KVX_ERR_INVALID_ARG;
     if (layouts_overlap(src, dst)) return KVX_ERR_OVERLAP;
   }
@@ -1122,6 +1131,96 @@ kvx_status kvx_move_heads(int32_t op, kvx_layout_t src, const int32_t *d_src_slo
   kvx_status st = check_buffer(c, d_buf, buf_bytes);
   if (st != KVX_OK) return st;
   return run_call(c, d_src_slots, d_dst_slots, d_buf, d_ws, ws_bytes, d_status, stream);
+}
+
+// kvx_store_kv (store) and kvx_load_kv.
+static kvx_status run_cast(bool store, kvx_layout_t pool, const kvx_cast_args *args, void *d_ws,
+                           size_t ws_bytes, int32_t *d_status, uint32_t flags, kvx_stream_t stream) {
+  if (!pool || !args || !d_status || !aligned(d_status, 4)) return KVX_ERR_INVALID_ARG;
+  const kvx_cast_args &a = *args;
+  const bool q4 = pool->dtype == KVX_Q4;
+  if (a.reserved != 0 || (!q4 && pool->dtype != KVX_FP8) || pool->kv_planes != 2 || !valid_n(a.n) ||
+      a.layer < 0 || a.n_layers < 1 || a.n_layers > pool->num_layers - a.layer ||
+      (a.dtype != KVX_F16 && a.dtype != KVX_BF16 && a.dtype != KVX_F32))
+    return KVX_ERR_INVALID_ARG;
+  for (float x : {a.k_scale, a.v_scale})
+    if (!(x > 0.f) || !std::isfinite(x) || !std::isfinite(1.f / x)) return KVX_ERR_INVALID_ARG;
+  const int64_t e = elem_bytes_of(a.dtype), most = (int64_t)1 << 40;
+  for (int64_t x : {a.layer_stride, a.token_stride, a.head_stride})
+    if (x < 0 || x > most) return KVX_ERR_INVALID_ARG;
+  if (a.n > 0 && (!a.k || !a.v || !a.slots || (a.rows && a.n_rows < 1))) return KVX_ERR_INVALID_ARG;
+  const int64_t last_row = (a.rows ? a.n_rows : a.n) - 1;
+  // (in floating point: the products may pass 64 bits)
+  if (((double)(a.n_layers - 1) * a.layer_stride + (double)last_row * a.token_stride +
+       (double)(pool->kv_heads - 1) * a.head_stride + pool->head_dim) * e > 0x1p60)
+    return KVX_ERR_INVALID_ARG;
+  if (!aligned(a.k, e) || !aligned(a.v, e) || !aligned(a.slots, 4) || !aligned(a.rows, 4))
+    return KVX_ERR_ALIGNMENT;
+  Call c;
+  if (apply_flags(c, flags) != KVX_OK) return KVX_ERR_INVALID_ARG;
+  c.n_tokens = a.n;
+  c.shape = pool;
+  if (!store || a.rows) c.src = pool;  // (rows: a side of its own, set below)
+  if (store || a.rows) c.dst = pool;
+  c.op = a.rows ? KVX_OP_TRANSFER : store ? KVX_OP_SCATTER : KVX_OP_GATHER;
+  set_whole_rows(c);
+  const kvx::WsLayout L = slots_ws(c);
+  kvx_status st;
+  if (a.n > 0 && (st = check_ws(d_ws, ws_bytes, L)) != KVX_OK) return st;
+  if (a.n > 0) {
+    const int64_t bytes = ((a.n_layers - 1) * a.layer_stride + last_row * a.token_stride +
+                           (pool->kv_heads - 1) * a.head_stride + pool->head_dim) * e;
+    for (const void *x : {a.k, a.v})
+      if (layout_overlaps_range(pool, (uintptr_t)x, (uintptr_t)x + bytes)) return KVX_ERR_OVERLAP;
+  }
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  static thread_local kvx::QuantArgs q;  // ~2 KiB of plane pointers: keep it off the stack
+  std::memset(&q, 0, sizeof(q));
+  q.status = d_status;
+  // few tokens: one launch whose every CTA checks every index
+  q.check = a.n <= kvx::kSmallMaxTokens && !dup_check(c);
+  if (!q.check || a.n == 0) {
+    kvx::PlanArgs pa = plan_args(c, d_ws, d_status);
+    kvx::Side &rows = store ? pa.src : pa.dst;
+    if (a.rows) rows.num_slots = a.n_rows, rows.hnd = 0;
+    pa.src_idx = store ? a.rows : a.slots;
+    pa.dst_idx = store ? a.slots : a.rows;
+    pa.validate_only = 1;
+    st = enqueue_plan(c, pa, s);
+    if (st != KVX_OK || a.n == 0) return st;
+  }
+  q.pool = pool_side(pool);
+  q.slots = a.slots;
+  q.rows = a.rows;
+  q.n = a.n;
+  q.n_rows = a.rows ? a.n_rows : a.n;
+  q.planes = 2 * a.n_layers;
+  q.heads = pool->kv_heads;
+  q.head_dim = pool->head_dim;
+  q.k = static_cast<char *>(a.k);
+  q.v = static_cast<char *>(a.v);
+  q.layer_stride = a.layer_stride * e;
+  q.token_stride = a.token_stride * e;
+  q.head_stride = a.head_stride * e;
+  q.scale[0] = store ? 1.f / a.k_scale : a.k_scale;
+  q.scale[1] = store ? 1.f / a.v_scale : a.v_scale;
+  q.wide = ((uintptr_t)a.k | (uintptr_t)a.v | (uintptr_t)q.layer_stride | (uintptr_t)q.token_stride |
+            (uintptr_t)q.head_stride) % 16 == 0;
+  q.words = q4 || (pool->head_dim % 8 == 0 && side_vec(pool) >= 8);
+  for (int p = 0; p < q.planes; ++p)
+    q.base[p] = reinterpret_cast<char *>(pool->plane[2 * a.layer + p]);
+  const cudaError_t err = kvx::launch_quant(q, store, q4, a.dtype, s);
+  return err == cudaSuccess ? KVX_OK : cuda_fail(err);
+}
+
+kvx_status kvx_store_kv(kvx_layout_t pool, const kvx_cast_args *args, void *d_ws, size_t ws_bytes,
+                        int32_t *d_status, uint32_t flags, kvx_stream_t stream) {
+  return run_cast(true, pool, args, d_ws, ws_bytes, d_status, flags, stream);
+}
+
+kvx_status kvx_load_kv(kvx_layout_t pool, const kvx_cast_args *args, void *d_ws, size_t ws_bytes,
+                       int32_t *d_status, uint32_t flags, kvx_stream_t stream) {
+  return run_cast(false, pool, args, d_ws, ws_bytes, d_status, flags, stream);
 }
 
 kvx_status kvx_tp_plan(int32_t kv_heads, int32_t src_tp, int32_t dst_tp, kvx_head_part *parts,
@@ -1185,7 +1284,7 @@ static kvx_status prepare_reshard(const kvx_layout_t *srcs, int32_t n_srcs,
   for (int32_t k = 1; k < n_dsts; ++k)
     if (!dsts[k] || !same_pool(dsts[k], d0)) return KVX_ERR_INVALID_ARG;
   if (s0->num_layers != d0->num_layers || s0->kv_planes != d0->kv_planes ||
-      s0->head_dim != d0->head_dim || s0->elem != d0->elem)
+      s0->head_dim != d0->head_dim || s0->elem != d0->elem || s0->seg_bytes != d0->seg_bytes)
     return KVX_ERR_INVALID_ARG;
   const int32_t nh = parts[0].n_heads;
   for (int32_t k = 0; k < n_parts; ++k) {

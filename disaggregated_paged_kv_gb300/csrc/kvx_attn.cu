@@ -511,6 +511,7 @@ bool shape_ok(const kvx_layout *l, int64_t n_q, int64_t n_reqs, int64_t q_heads,
 
 // Whether the tensor-core kernels take a layout.
 bool tensor_cores(const kvx_layout *l) {
+  if (l->dtype == KVX_Q4) return false;
   return l->elem <= 2 && (l->head_dim == 64 || l->head_dim == 128) && l->vec == 16;
 }
 
@@ -555,7 +556,7 @@ extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_arg
       a.layer < 0 || a.layer >= pool->num_layers || a.page_size < 1 || a.max_pages < 1 ||
       a.table_stride < a.max_pages || a.n_prefix_pages < 0 || a.page_size > pool->num_slots)
     return KVX_ERR_INVALID_ARG;
-  if (pool->dtype == KVX_FP8 ? (a.q_dtype != KVX_F16 && a.q_dtype != KVX_BF16)
+  if (pool->dtype == KVX_FP8 || pool->dtype == KVX_Q4 ? (a.q_dtype != KVX_F16 && a.q_dtype != KVX_BF16)
                              : a.q_dtype != pool->dtype)
     return KVX_ERR_INVALID_ARG;
   if (pool->kind == KVX_HND_PAGED && pool->page_size != a.page_size) return KVX_ERR_INVALID_ARG;
@@ -640,7 +641,7 @@ extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_arg
   p.prefix_len = a.prefix_len;
   p.row_tile = row_tile(pool);
   p.unit_cost = tensor_cores(pool) ? kNarrowUnitCost : 0;
-  p.key_bytes = pool->elem;
+  p.head_bytes = (int32_t)pool->seg_bytes;
   const uintptr_t q_at = (uintptr_t)a.q | (uintptr_t)p.q_tok | (uintptr_t)p.q_head;
   p.q_even = q_at % 4 == 0;
   p.q_vec = q_at % 16 == 0;

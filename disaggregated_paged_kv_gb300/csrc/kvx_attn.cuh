@@ -93,7 +93,7 @@ struct AttnParams {
   float v_scale;
   int32_t n_q, n_reqs, q_heads, kv_heads, group, head_dim;
   int32_t page_size, max_pages, prefix_len;
-  int32_t key_bytes;     // of an element of the pool
+  int32_t head_bytes;    // of a head of one token in the pool
   int32_t row_tile;      // rows of a narrow unit
   int32_t unit_cost;     // what a unit's begin and end cost, in tiles of up to 16 rows
   int32_t groups;        // groups of kv_heads CTAs, narrow line
@@ -297,7 +297,7 @@ constexpr int64_t kAttnWideNs = 2100, kAttnNarrowNs = 900, kAttnNarrowPs = 470, 
 __device__ __forceinline__ AttnShare attn_share(const AttnParams &p, int64_t own, int64_t wide) {
   AttnShare s = {p.groups, p.wide_groups};
   if (p.wide_groups < 2 || own == 0 || wide == 0) return s;
-  const int64_t bytes = (int64_t)kAttnKeyTile * p.head_dim * p.key_bytes * 2;  // of a narrow tile
+  const int64_t bytes = (int64_t)kAttnKeyTile * p.head_bytes * 2;  // of a narrow tile
   const int64_t tiles = max(own - (int64_t)p.n_reqs * p.unit_cost, (int64_t)0);
   const int64_t floor_ns = (tiles * p.kv_heads * bytes >> 20) * kAttnMbNs;
   const int64_t unit_ns = max(kAttnNarrowNs, bytes / 16 * kAttnNarrowPs / 1000);

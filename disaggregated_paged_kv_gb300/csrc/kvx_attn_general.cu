@@ -34,6 +34,22 @@ __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_f(__nv_fp8_e4m3 x) { return (float)x; }
 
+// An element of a 4-bit pool is no object of its own: a byte holds two, and its group's scale and low stand
+// behind the codes.
+struct Q4 {};
+
+// Element d of the head vector at s.
+template <typename KV>
+__device__ __forceinline__ float element(const char *s, int d, int D) {
+  if constexpr (std::is_same<KV, Q4>::value) {
+    const uint32_t pair = reinterpret_cast<const uint32_t *>(s)[D / 8 + d / KVX_Q4_GROUP];
+    const float code = (float)(reinterpret_cast<const uint8_t *>(s)[d >> 1] >> (4 * (d & 1)) & 15);
+    return fmaf(code, __half2float(__ushort_as_half((uint16_t)pair)), __half2float(__ushort_as_half((uint16_t)(pair >> 16))));
+  } else {
+    return to_f(reinterpret_cast<const KV *>(s)[d]);
+  }
+}
+
 // Rows of D columns padded to pitch(D): a multiple of four, and 16-byte reads of eight rows of one
 // column lie in different banks.
 __host__ __device__ constexpr int pitch(int D) { return (D + 3) / 4 * 4 + 4; }
@@ -143,8 +159,8 @@ __global__ void __launch_bounds__(kThreads, NC == 1 ? 3 : 2) attn_general_kernel
           const int64_t o = soff[j];
           float x = 0.f, y = 0.f;
           if (j < nk) {
-            x = to_f(reinterpret_cast<const KV *>(p.pool.k + o)[d]);
-            y = to_f(reinterpret_cast<const KV *>(p.pool.v + o)[d]);
+            x = element<KV>(p.pool.k + o, d, D);
+            y = element<KV>(p.pool.v + o, d, D);
           }
           sk[j * P + d] = x;
           sv[j * P + d] = y;
@@ -245,8 +261,9 @@ __global__ void __launch_bounds__(kThreads, NC == 1 ? 3 : 2) attn_general_kernel
 template <typename KV, typename IO, int NC>
 cudaError_t launch_c(const AttnParams &p, bool vec, cudaStream_t s) {
   const size_t smem = sizeof(float) * ((size_t)pitch(p.head_dim) * (kRows + 2 * kKeys) + kRows * kKeys + kRows);
-  const void *fn = vec ? (const void *)attn_general_kernel<KV, IO, NC, true>
-                       : (const void *)attn_general_kernel<KV, IO, NC, false>;
+  const void *fn = (const void *)attn_general_kernel<KV, IO, NC, false>;
+  if constexpr (!std::is_same<KV, Q4>::value)
+    if (vec) fn = (const void *)attn_general_kernel<KV, IO, NC, true>;
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 100 * 1024);
   if (e != cudaSuccess) return e;
   void *args[] = {const_cast<AttnParams *>(&p)};
@@ -264,8 +281,10 @@ cudaError_t launch_attn_general(const AttnParams &p, int32_t dtype, int32_t io, 
   if (dtype == KVX_F32) return launch<float, float>(p, vec, s);
   if (dtype == KVX_F16) return launch<__half, __half>(p, vec, s);
   if (dtype == KVX_BF16) return launch<__nv_bfloat16, __nv_bfloat16>(p, vec, s);
-  if (io == KVX_F16) return launch<__nv_fp8_e4m3, __half>(p, vec, s);
-  return launch<__nv_fp8_e4m3, __nv_bfloat16>(p, vec, s);
+  if (dtype == KVX_FP8 && io == KVX_F16) return launch<__nv_fp8_e4m3, __half>(p, vec, s);
+  if (dtype == KVX_FP8) return launch<__nv_fp8_e4m3, __nv_bfloat16>(p, vec, s);
+  if (io == KVX_F16) return launch<Q4, __half>(p, false, s);
+  return launch<Q4, __nv_bfloat16>(p, false, s);
 }
 
 }  // namespace kvx

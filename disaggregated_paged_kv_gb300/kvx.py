@@ -32,7 +32,7 @@ ERR_NO_WORKSPACE = 7
 ERR_TIMEOUT = 8
 ERR_CANCELLED = 9
 
-F16, BF16, F32, FP8 = 1, 2, 3, 4
+F16, BF16, F32, FP8, Q4 = 1, 2, 3, 4, 5
 NHD, HND_PAGED = 0, 1
 OP_GATHER, OP_SCATTER, OP_TRANSFER, OP_BATCH = 0, 1, 2, 3
 
@@ -43,7 +43,13 @@ CHUNK_BYTES = 2048
 NOALLOC_MAX_TOKENS = 16384
 NOALLOC_MAX_DUP_TOKENS = 8192
 
-ELEM_BYTES = {F16: 2, BF16: 2, F32: 4, FP8: 1}
+ELEM_BYTES = {F16: 2, BF16: 2, F32: 4, FP8: 1}  # Q4: see head_bytes
+Q4_GROUP = 32
+
+
+def head_bytes(dtype: int, head_dim: int) -> int:
+    """Bytes of one head of one token in a pool of that type."""
+    return head_dim // 8 * 5 if dtype == Q4 else head_dim * ELEM_BYTES[dtype]
 
 
 class KvxError(RuntimeError):
@@ -147,6 +153,27 @@ class TablesArgs(ctypes.Structure):
     ]
 
 
+class CastArgs(ctypes.Structure):
+    """kvx_cast_args (kvx.h): what store_kv and load_kv are told about K and V rows outside the pool."""
+    _fields_ = [
+        ("layer", ctypes.c_int32),
+        ("n_layers", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("n", ctypes.c_int32),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("layer_stride", ctypes.c_int64),
+        ("token_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
+        ("slots", ctypes.c_void_p),
+        ("rows", ctypes.c_void_p),
+        ("n_rows", ctypes.c_int32),
+        ("k_scale", ctypes.c_float),
+        ("v_scale", ctypes.c_float),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
 class AttnArgs(ctypes.Structure):
     """kvx_attn_args (kvx.h): device addresses, strides and sizes of one shared_attention call."""
     _fields_ = [
@@ -230,6 +257,8 @@ _SIGS = {
                               _VP, _U32, _VP]),
     "kvx_execute": (_I32, [_I32, _VP, _VP, _VP, _I32, _I64, _VP, _SZ, _VP, _SZ, _VP, _U32, _VP]),
     "kvx_plan_export": (_I32, [_VP, _SZ, _I64, _VP, _I64, _VP, _VP]),
+    "kvx_store_kv": (_I32, [_VP, ctypes.POINTER(CastArgs), _VP, _SZ, _VP, _U32, _VP]),
+    "kvx_load_kv": (_I32, [_VP, ctypes.POINTER(CastArgs), _VP, _SZ, _VP, _U32, _VP]),
     "kvx_tables_workspace_size": (_SZ, [_I32]),
     "kvx_block_tables": (_I32, [_VP, ctypes.POINTER(TablesArgs), _VP, _SZ, _VP, _VP]),
     "kvx_attention_workspace_size": (_SZ, [_VP, _I32, _I32, _I32, _I32]),
@@ -713,6 +742,52 @@ def move_heads(op: int, src: Optional[Layout], src_slots, src_head0: int, dst: O
                               _nbytes(ws) if ws_bytes is None else ws_bytes, _ptr(status),
                               _flags(flags), _stream(stream))
     _check(rc, "kvx_move_heads")
+
+
+def _cast_args(pool: Layout, layer: int, k, v, slots, rows, k_scale, v_scale) -> CastArgs:
+    dtype = _Q_DTYPES.get(str(k.dtype))
+    if dtype is None or v.dtype is not k.dtype:
+        raise ValueError("k and v are float16, bfloat16 or float32 alike")
+    if k.dim() not in (3, 4) or v.shape != k.shape or v.stride() != k.stride():
+        raise ValueError("k and v are [tokens, kv_heads, head_dim] or [layers, tokens, kv_heads, head_dim], "
+                         "of one shape and of the same strides")
+    n_rows, heads, dim = k.shape[-3:]
+    if heads != pool.kv_heads or dim != pool.head_dim:
+        raise ValueError("k and v have the pool's kv_heads and head_dim")
+    if k.stride(-1) != 1 and dim > 1 and k.numel() > 0:
+        raise ValueError("a head's elements must be contiguous in k and v")
+    for x in (slots, rows):
+        if x is not None and (str(x.dtype) != "torch.int32" or not x.is_contiguous()):
+            raise ValueError("slots and rows are contiguous int32 tensors")
+    n = slots.numel()
+    if (n_rows != n) if rows is None else (rows.numel() != n):
+        raise ValueError("slots and " + ("k" if rows is None else "rows") + " differ in length")
+    layers = k.shape[0] if k.dim() == 4 else 1
+    # (an axis of one has no stride that counts)
+    token, head = (k.stride(-3) if n_rows > 1 else 0), (k.stride(-2) if heads > 1 else 0)
+    return CastArgs(layer, layers, dtype, n, k.data_ptr(), v.data_ptr(),
+                    k.stride(0) if layers > 1 else 0, token, head, slots.data_ptr(), _ptr(rows), n_rows,
+                    k_scale, v_scale, 0)
+
+
+def store_kv(pool: Layout, layer: int, k, v, slots, ws, status, rows=None, k_scale: float = 1.0,
+             v_scale: float = 1.0, flags=None, ws_bytes=None, stream=None) -> None:
+    """kvx_store_kv: quantises the K and V rows of ``slots.numel()`` tokens as they are written into a Q4
+    or FP8 pool.  ``k`` and ``v`` are [tokens, kv_heads, head_dim], or with a leading axis of layers
+    from ``layer`` on; with ``rows`` (int32) token i is row ``rows[i]`` of them.  The pool then holds values
+    divided by ``k_scale`` and ``v_scale``."""
+    a = _cast_args(pool, layer, k, v, slots, rows, k_scale, v_scale)
+    _check(lib().kvx_store_kv(_h(pool), a, _ptr(ws), _nbytes(ws) if ws_bytes is None else ws_bytes,
+                              _ptr(status), _flags(flags), _stream(stream)), "kvx_store_kv")
+
+
+def load_kv(pool: Layout, layer: int, k, v, slots, ws, status, rows=None, k_scale: float = 1.0,
+            v_scale: float = 1.0, flags=None, ws_bytes=None, stream=None) -> None:
+    """kvx_load_kv: the rows of ``slots`` in a Q4 or FP8 pool, times the scales, into ``k`` and ``v``
+    (shapes and ``rows`` as for store_kv)."""
+    a = _cast_args(pool, layer, k, v, slots, rows, k_scale, v_scale)
+    _check(lib().kvx_load_kv(_h(pool), a, _ptr(ws), _nbytes(ws) if ws_bytes is None else ws_bytes,
+                             _ptr(status), _flags(flags), _stream(stream)), "kvx_load_kv")
 
 
 def tables_workspace_size(n_reqs: int) -> int:

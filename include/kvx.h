@@ -91,8 +91,16 @@ typedef enum kvx_dtype {
   KVX_F16 = 1,  /* 2-byte elements */
   KVX_BF16 = 2, /* 2-byte elements */
   KVX_F32 = 3,  /* 4-byte elements */
-  KVX_FP8 = 4   /* 1-byte elements */
+  KVX_FP8 = 4,  /* 1-byte elements */
+  KVX_Q4 = 5    /* 4-bit codes with a scale for every KVX_Q4_GROUP elements (see kvx_store_kv) */
 } kvx_dtype;
+
+/* KVX_Q4: head_dim is a multiple of KVX_Q4_GROUP, and a head vector of head_dim elements is
+ * 5 * head_dim / 8 bytes: head_dim / 2 bytes of codes (element 2 i in the low half of byte i, 2 i + 1
+ * in the high half), then a pair of f16 numbers, scale and low, for every group of KVX_Q4_GROUP
+ * elements in order.  An element is low + code * scale.  Planes and the slot stride are multiples
+ * of 4 bytes.  The calls that move rows move such vectors as the bytes that they are. */
+#define KVX_Q4_GROUP 32
 
 typedef enum kvx_kind {
   /* Token rows: each plane is [num_slots][kv_heads][head_dim]; slot s starts at
@@ -157,7 +165,7 @@ typedef struct kvx_layout_desc {
   int32_t num_layers; /* L >= 1, kv_planes * L <= KVX_MAX_PLANES */
   int32_t kv_heads;   /* H >= 1 */
   int32_t head_dim;   /* D >= 1 (elements) */
-  int32_t dtype;      /* kvx_dtype; only its byte width is used */
+  int32_t dtype;      /* kvx_dtype; the calls that move rows use only its byte width */
   int32_t kind;       /* kvx_kind */
   int32_t page_size;  /* KVX_HND_PAGED: tokens per page (>= 1).  KVX_NHD: ignored. */
   int64_t num_slots;  /* token slots per plane; HND: a multiple of page_size */
@@ -537,6 +545,56 @@ KVX_API kvx_status kvx_stream_reshard(const kvx_layout_t *srcs, int32_t n_srcs,
                                       const kvx_stream_ctl *ctl, void *d_ws, size_t ws_bytes,
                                       int32_t *d_status, uint32_t flags, kvx_stream_t stream);
 
+/* ---- rows of quantised pools ------------------------------------------------------------ */
+
+/* Arguments of kvx_store_kv and kvx_load_kv (read on the host at the call).  Element d of head h of
+ * token i in layer `layer` + l is at k (K) and v (V) + l * layer_stride + r * token_stride +
+ * h * head_stride + d elements, where r is rows[i], or i without rows. */
+typedef struct kvx_cast_args {
+  int32_t layer;             /* first layer of the pool */
+  int32_t n_layers;          /* >= 1; layer + n_layers is at most the pool's */
+  int32_t dtype;             /* of k and v: KVX_F16, KVX_BF16 or KVX_F32 */
+  int32_t n;                 /* tokens (0 .. KVX_MAX_TOKENS) */
+  void *k, *v;               /* device, element aligned */
+  int64_t layer_stride, token_stride, head_stride; /* elements, 0 .. 2^40, and the last element's
+                                place below 2^60 bytes; of both */
+  const int32_t *slots;      /* device [n]: the pool slot of each token */
+  const int32_t *rows;       /* device [n]: its row in k and v, 0 .. n_rows - 1; NULL: i */
+  int32_t n_rows;            /* rows that k and v have (used with rows) */
+  float k_scale, v_scale;    /* > 0: what the pool's elements are multiplied by to be the values, as
+                                in kvx_attn_args */
+  int32_t reserved;          /* must be 0 */
+} kvx_cast_args;
+
+/* Quantises K and V rows as they are written into a pool of KVX_Q4 or KVX_FP8 elements with K and V
+ * planes: a projection's result (slices of a wider tensor are fine), a chunk of a prompt, or, with
+ * rows, tokens anywhere in planes of 16- or 32-bit rows -- a finished prefill's pool, whose
+ * token_stride is its slot stride -- for n_layers layers at once ([Mooncake] 7.4: what the decode
+ * side registers per layer).  Slots not named keep their bytes.
+ *  KVX_FP8: the E4M3 number nearest to x * (1 / scale), within +-448; NaN stays NaN.
+ *  KVX_Q4: with y = x * (1 / scale) clamped to +-61440, for each group of KVX_Q4_GROUP elements
+ *    low   = f16(least y),  scale = f16(max(0, (greatest y - low) * (1 / 15))),
+ *    code  = (y - low) * (1 / scale), rounded to the nearest whole number (ties to even), 0 .. 15
+ *  (0 where scale is 0), every step rounded to 32 bits.  What is read back differs from y by at most
+ *  (greatest y - least y) / 30 * (1 + 2^-9) + 2^-11 * (greatest |y|) + 2^-21 (scales below f16's normal
+ *  numbers are spaced 2^-24 apart).  A group with a NaN reads back as NaN; infinities become +-61440.
+ * d_ws, flags and the errors are those of kvx_scatter: kvx_workspace_size(n, 0) bytes; an index out
+ * of range is KVX_ERR_OUT_OF_RANGE in *d_status, a slot named twice with KVX_CHECK_DUP
+ * KVX_ERR_DUPLICATE_DST, with nothing written.  Without the check a repeated slot ends up with parts of
+ * its rows, which ones unspecified.  KVX_ERR_INVALID_ARG also for other pools, KVX_ERR_OVERLAP where
+ * k or v shares memory with the pool's planes. */
+KVX_API kvx_status kvx_store_kv(kvx_layout_t pool, const kvx_cast_args *args, void *d_ws,
+                                size_t ws_bytes, int32_t *d_status, uint32_t flags,
+                                kvx_stream_t stream);
+
+/* Reads rows of such a pool back into k and v: the pool's elements times k_scale or v_scale, in 32 bits
+ * and then rounded to dtype.  Arguments, workspace, status and errors as kvx_store_kv; slots
+ * may repeat, and with KVX_CHECK_DUP a row named twice in `rows` is KVX_ERR_DUPLICATE_DST.  Elements of k and v
+ * that belong to no token keep their values; the strides must not lay one element upon another. */
+KVX_API kvx_status kvx_load_kv(kvx_layout_t pool, const kvx_cast_args *args, void *d_ws,
+                               size_t ws_bytes, int32_t *d_status, uint32_t flags,
+                               kvx_stream_t stream);
+
 /* ---- block tables and slot maps -------------------------------------------------------- */
 
 /* Most requests of one kvx_block_tables or kvx_shared_attention call. */
@@ -602,7 +660,7 @@ KVX_API kvx_status kvx_block_tables(kvx_layout_t pool, const kvx_tables_args *ar
 typedef struct kvx_attn_args {
   int32_t layer;             /* K is plane 2 * layer, V plane 2 * layer + 1 */
   int32_t q_dtype;           /* type of q and out: the pool's (KVX_F16, KVX_BF16, KVX_F32); with
-                                a KVX_FP8 pool (E4M3 values) KVX_F16 or KVX_BF16 */
+                                a KVX_FP8 (E4M3 values) or KVX_Q4 pool KVX_F16 or KVX_BF16 */
   int32_t q_heads;           /* a multiple of the layout's kv_heads: query head h reads kv head
                                 h / (q_heads / kv_heads) */
   int32_t n_q;               /* query tokens of all requests (>= 0) */
