@@ -511,7 +511,9 @@ bool shape_ok(const kvx_layout *l, int64_t n_q, int64_t n_reqs, int64_t q_heads,
 
 // Whether the tensor-core kernels take a layout.
 bool tensor_cores(const kvx_layout *l) {
-  if (l->dtype == KVX_Q4) return false;
+  if (l->dtype == KVX_Q4)  // copies of a fifth of a head vector, at 32-bit distances within 16 keys
+    return (l->head_dim == 64 || l->head_dim == 128) && l->vec >= l->head_dim / 8 &&
+           l->slot_stride <= INT32_MAX / 32;
   return l->elem <= 2 && (l->head_dim == 64 || l->head_dim == 128) && l->vec == 16;
 }
 
@@ -519,7 +521,7 @@ int row_tile(const kvx_layout *l) { return tensor_cores(l) ? kAttnNarrowRows : k
 
 // Whether a call may have work for the wide kernel: more rows than the narrow kernel has in a unit.
 bool takes_wide(const kvx_layout *l, int64_t n_q, int64_t q_heads) {
-  return tensor_cores(l) && n_q * (q_heads / l->kv_heads) > kAttnNarrowRows;
+  return tensor_cores(l) && l->dtype != KVX_Q4 && n_q * (q_heads / l->kv_heads) > kAttnNarrowRows;
 }
 
 // A number that no word of a workspace holds by chance: calls are counted from the process's first one's
@@ -640,6 +642,9 @@ extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_arg
   p.max_pages = a.max_pages;
   p.prefix_len = a.prefix_len;
   p.row_tile = row_tile(pool);
+  const bool q4 = pool->dtype == KVX_Q4;
+  p.few_rows = q4 && tensor_cores(pool) ? 8 : 16;
+  p.paged_blocks = a.page_size % 16 == 0;
   p.unit_cost = tensor_cores(pool) ? kNarrowUnitCost : 0;
   p.head_bytes = (int32_t)pool->seg_bytes;
   const uintptr_t q_at = (uintptr_t)a.q | (uintptr_t)p.q_tok | (uintptr_t)p.q_head;
@@ -680,7 +685,8 @@ extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_arg
   if (a.n_q > 0) {
     if (e == cudaSuccess && wide) e = launch_attn_wide(p, pool->dtype, a.q_dtype, hnd, s);
     if (e == cudaSuccess)
-      e = tensor_cores(pool) ? launch_attn_narrow(p, pool->dtype, a.q_dtype, hnd, s)
+      e = tensor_cores(pool) && q4 ? launch_attn_q4(p, a.q_dtype, s)
+          : tensor_cores(pool) ? launch_attn_narrow(p, pool->dtype, a.q_dtype, hnd, s)
                              : launch_attn_general(p, pool->dtype, a.q_dtype, pool->vec == 16 && pool->seg_bytes % 16 == 0, s);
   }
   if (e == cudaSuccess) {

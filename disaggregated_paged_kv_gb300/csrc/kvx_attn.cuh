@@ -95,6 +95,8 @@ struct AttnParams {
   int32_t page_size, max_pages, prefix_len;
   int32_t head_bytes;    // of a head of one token in the pool
   int32_t row_tile;      // rows of a narrow unit
+  int32_t few_rows;      // a tile of up to so many rows costs 1 (see attn_cost)
+  int32_t paged_blocks;  // 4-bit pools: blocks of 16 positions lie in a page each
   int32_t unit_cost;     // what a unit's begin and end cost, in tiles of up to 16 rows
   int32_t groups;        // groups of kv_heads CTAs, narrow line
   int32_t wide_groups;   // of the wide line; 0: no wide kernel
@@ -205,10 +207,11 @@ __device__ __forceinline__ int64_t attn_up(int64_t a, int64_t b) { return attn_d
 
 // What a tile of a unit with that many rows costs: with up to 16 rows it is the bytes, with more the
 // products, which four warps share between 16-row groups.  (Tiles of 64 rows take 2 to 4 times the time of
-// tiles of 16 rows, depending on what else the SM has.)
-__host__ __device__ __forceinline__ int32_t attn_cost(int32_t rows, int32_t row_tile) {
+// tiles of 16 rows, depending on what else the SM has.)  few: 16; for the 4-bit kernel 8, whose warps have eight
+// rows each, so that rows beyond leave fewer warps for the keys.
+__host__ __device__ __forceinline__ int32_t attn_cost(int32_t rows, int32_t row_tile, int32_t few) {
   const int32_t r = rows < row_tile ? rows : row_tile;
-  return r <= 16 ? 1 : r <= 32 ? 2 : 4;
+  return r <= few ? 1 : r <= 2 * few ? 2 : r <= 4 * few ? 4 : 8;
 }
 
 __device__ __forceinline__ int64_t attn_units(const AttnParams &p, int32_t rows) {
@@ -225,7 +228,7 @@ __device__ __forceinline__ int64_t attn_length(const AttnParams &p, const AttnSe
 }
 
 __device__ __forceinline__ void attn_tile_seg(const AttnParams &p, AttnSeg *g) {
-  g->cost = attn_cost(g->rows, p.row_tile);
+  g->cost = attn_cost(g->rows, p.row_tile, p.few_rows);
   g->key0 = g->low / kAttnKeyTile * kAttnKeyTile;
   if (g->rows > 0 && g->key1 > g->low)
     g->key_tiles = (int32_t)attn_up((int64_t)g->key1 - g->key0, kAttnKeyTile);
@@ -494,6 +497,8 @@ __device__ __forceinline__ void attn_wait_announced(const AttnParams &p) {
 cudaError_t launch_attn_general(const AttnParams &p, int32_t dtype, int32_t io, bool vec, cudaStream_t s);
 // head_dim 64 or 128, 16-bit or 8-bit pool with 16-byte aligned heads.
 cudaError_t launch_attn_narrow(const AttnParams &p, int32_t dtype, int32_t io, bool hnd, cudaStream_t s);
+// head_dim 64 or 128, 4-bit pool with head vectors on 8- or 16-byte boundaries.
+cudaError_t launch_attn_q4(const AttnParams &p, int32_t io, cudaStream_t s);
 cudaError_t launch_attn_wide(const AttnParams &p, int32_t dtype, int32_t io, bool hnd, cudaStream_t s);
 
 }  // namespace kvx
