@@ -521,7 +521,7 @@ int row_tile(const kvx_layout *l) { return tensor_cores(l) ? kAttnNarrowRows : k
 
 // Whether a call may have work for the wide kernel: more rows than the narrow kernel has in a unit.
 bool takes_wide(const kvx_layout *l, int64_t n_q, int64_t q_heads) {
-  return tensor_cores(l) && l->dtype != KVX_Q4 && n_q * (q_heads / l->kv_heads) > kAttnNarrowRows;
+  return tensor_cores(l) && n_q * (q_heads / l->kv_heads) > kAttnNarrowRows;
 }
 
 // A number that no word of a workspace holds by chance: calls are counted from the process's first one's

@@ -481,7 +481,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_q4_kernel(const __grid_const
   if (tid == 0) sm.error = 0;
   // (what lies between the head vectors of a stage is read with them, and has to be finite)
   for (int i = tid; i < (int)sizeof(sm.ring) / 16; i += kThreads) reinterpret_cast<uint4 *>(sm.ring)[i] = make_uint4(0, 0, 0, 0);
-  attn_wait_prior();
+  if (!p.after_wide) attn_wait_prior();
+  else if (tid == 0) attn_wait_announced(p);  // for the others by the barrier below
   const int g = blockIdx.x / p.kv_heads, h = blockIdx.x - g * p.kv_heads;
   __syncthreads();
   const AttnLine line = attn_line<kThreads>(p, g, sm.scan);
@@ -509,6 +510,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_q4_kernel(const __grid_const
   }
   cp_async_wait<0>();
   if (tid == 0) p.errors[blockIdx.x] = sm.error;
+  if (p.after_wide) attn_wait_prior();  // the join's wait for this kernel covers the wide one as well
 }
 
 template <typename IO, int D>

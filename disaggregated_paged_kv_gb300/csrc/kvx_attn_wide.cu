@@ -33,13 +33,17 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kKeys = kAttnWideKeys;
 
-template <bool FP8, int D>
+// What a pool's elements are: 16-bit, 8-bit or 4-bit.
+enum Elements : int { k16 = 0, k8 = 1, k4 = 2 };
+
+template <int E, int D>
 struct Smem {
-  static constexpr int kStages = FP8 ? 3 : 5;  // of one K or V tile each, as 16-bit values
-  static constexpr int kRawStages = FP8 ? 3 : 1;
+  static constexpr int kStages = E == k16 ? 5 : E == k8 ? 3 : 4;  // of one K or V tile each, as 16-bit values
+  static constexpr int kRawStages = E == k16 ? 1 : 3;
+  static constexpr int kRawPitch = D == 128 ? 80 : 48;  // of a head vector of 4-bit elements
   alignas(1024) char q[2][128 * D * 2];
   alignas(1024) char kv[kStages][kKeys * D * 2];
-  alignas(1024) char raw[kRawStages][FP8 ? kKeys * D : 128];  // 8-bit tiles as they come
+  alignas(1024) char raw[kRawStages][E == k8 ? kKeys * D : E == k4 ? kKeys * kRawPitch : 128];  // tiles as they come
   int64_t off[kKeys];
   uint64_t q_full, full[kStages], empty[kStages], raw_full[kRawStages];
   uint64_t s_full[2], p_full[2][2], o_full[2], o_empty[2], drained;
@@ -191,13 +195,19 @@ __device__ __forceinline__ int row_token(const AttnParams &p, const WidePiece &x
   return x.table < 0 && p.planned ? p.prefix_tok[t] : t;
 }
 
-template <typename IO, bool FP8, int D>
+// Element columns of a 4-bit pool's products stand as codes come out of a word: of eight, 0, 4, 1, 5, 2, 6, 3, 7.
+__host__ __device__ __forceinline__ constexpr int column_of(bool q4, int e) {
+  return q4 ? (e & ~7) | ((e & 3) << 1) | (e >> 2 & 1) : e;
+}
+
+template <typename IO, int E, int D>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnTma tma,
                  const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
   extern __shared__ char raw_smem[];
-  using S = Smem<FP8, D>;
-  using T = typename std::conditional<FP8, __half, IO>::type;  // of the products
+  using S = Smem<E, D>;
+  constexpr bool FP8 = E == k8, Q4 = E == k4;
+  using T = typename std::conditional<E != k16, __half, IO>::type;  // of the products
   // (f16: little room above the maximum, so that the weights keep their range below it)
   constexpr float kRenew = std::is_same<T, __half>::value ? 2.f : 8.f, kShift = weight_shift<T>(kRenew);
   constexpr int kStages = S::kStages;
@@ -276,7 +286,7 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
       float scale = p.scale_log2;
       if (active) {  // this row's queries; the products of the piece before are done with the last
         float f = 1.f;
-        if constexpr (FP8 && std::is_same<IO, __nv_bfloat16>::value) {  // see attn_narrow_kernel
+        if constexpr (E != k16 && std::is_same<IO, __nv_bfloat16>::value) {  // see attn_narrow_kernel
           const uint16_t *u = reinterpret_cast<const uint16_t *>(p.q + token * p.q_tok + (int64_t)(h * p.group + member) * p.q_head);
           uint32_t most = 0;
           if (live) {
@@ -315,13 +325,16 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
           }
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
-            if constexpr (FP8 && std::is_same<IO, __nv_bfloat16>::value) {
+            if constexpr (E != k16 && std::is_same<IO, __nv_bfloat16>::value) {
               uint32_t v[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
 #pragma unroll
               for (int e = 0; e < 4; ++e)
                 v[e] = pack2<__half>(__uint_as_float(v[e] << 16) * f, __uint_as_float(v[e] & 0xffff0000u) * f);
               w[c] = make_uint4(v[0], v[1], v[2], v[3]);
             }
+            if constexpr (Q4)
+              w[c] = make_uint4(__byte_perm(w[c].x, w[c].z, 0x5410), __byte_perm(w[c].x, w[c].z, 0x7632),
+                                __byte_perm(w[c].y, w[c].w, 0x5410), __byte_perm(w[c].y, w[c].w, 0x7632));
             *reinterpret_cast<uint4 *>(sm.q[t] + place<D>(r, c0 + c)) = w[c];
           }
         }
@@ -428,15 +441,27 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
 #pragma unroll
               for (int k = 0; k < 32; ++k) {
                 float e;
-                if constexpr (FP8) {
+                if constexpr (Q4) {
+                  const uint32_t pair = reinterpret_cast<const uint32_t *>(v)[D / 8 + c];
+                  const uint32_t code = reinterpret_cast<const uint8_t *>(v)[c * 16 + (k >> 1)] >> (4 * (k & 1)) & 15u;
+                  e = fmaf((float)code, __half2float(__ushort_as_half((uint16_t)pair)), __half2float(__ushort_as_half((uint16_t)(pair >> 16))));
+                } else if constexpr (FP8) {
                   const uint32_t u = from_e4m3x2(reinterpret_cast<const uint8_t *>(v)[c * 32 + k]);
                   e = __half2float(*reinterpret_cast<const __half *>(&u));
                 } else {
                   e = (float)reinterpret_cast<const T *>(v)[c * 32 + k];
                 }
-                if (!isfinite(e)) o[k] = __float_as_uint(__uint_as_float(o[k]) + e);
+                const int col = column_of(Q4, k);
+                if (!isfinite(e)) o[col] = __float_as_uint(__uint_as_float(o[col]) + e);
               }
             }
+          }
+          if constexpr (Q4) {  // elements in their own order
+            uint32_t x[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) x[k] = o[column_of(true, k)];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = x[k];
           }
           if (direct) {
             uint32_t w[16];
@@ -544,6 +569,100 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
       if (i == 0) sm.least[parity] = least, sm.odd[parity] = 0;
       asm volatile("bar.sync 1, 128;" ::: "memory");  // odd is 0 before anyone sets it
 
+      if constexpr (Q4) {
+        // A thread brings its key's head vectors in by itself, K and V in turn, and makes 16-bit tiles of them: no
+        // thread of the four warps waits for another.  Codes are exact as 16-bit numbers (1024 + code and
+        // 1024 + 16 * code are, by their bits), and low + code * scale is rounded once.
+        constexpr int kChunk = D / 8;  // bytes of a copy; a head vector is five
+        const int halves = 2 * x.tiles;
+        int sent = 0;
+        int64_t from = -1;
+        auto entry = [&](int j) -> int32_t {  // as it stands in the table
+          const int pos = x.key0 + j * kKeys + i;
+          if (j >= x.tiles || pos >= x.key1) return 0;
+          int pg, off;
+          attn_split(p, pos, &pg, &off);
+          return attn_entry(p, pos < p.prefix_len ? -1 : x.table, pg);
+        };
+        int32_t id = entry(0);
+        auto send = [&]() {
+          if (sent < halves && !lost) {
+            if ((sent & 1) == 0) {
+              const int pos = x.key0 + (sent >> 1) * kKeys + i;
+              from = -1;
+              if (pos < x.key1) {
+                int pg, off;
+                attn_split(p, pos, &pg, &off);
+                from = attn_checked(p, id, &sm.error) * p.pool.page_stride + off * p.pool.tok_stride + h * p.pool.head_stride;
+              }
+              id = entry((sent >> 1) + 1);
+            }
+            const char *src = (sent & 1 ? p.pool.v : p.pool.k) + (from < 0 ? 0 : from);
+            const uint32_t to = smem_u32(sm.raw[raw_in]) + i * S::kRawPitch;
+            const int n = from < 0 ? 0 : kChunk;  // nothing: zeros
+#pragma unroll
+            for (int k = 0; k < 5; ++k) {
+              if constexpr (D == 128) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + k * kChunk), "l"(src + k * kChunk), "r"(n) : "memory");
+              else asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to + k * kChunk), "l"(src + k * kChunk), "r"(n) : "memory");
+            }
+            if (++raw_in == S::kRawStages) raw_in = 0;
+            ++sent;
+          }
+          cp_async_commit();
+        };
+        raw_out = raw_in;
+#pragma unroll
+        for (int k = 0; k < S::kRawStages - 1; ++k) send();
+#pragma unroll 1
+        for (int half = 0; half < halves; ++half) {
+          cp_async_wait<S::kRawStages - 2>();  // (a thread's own copies: no one else's matter to it)
+          const char *raw = sm.raw[raw_out] + i * S::kRawPitch;
+          if (++raw_out == S::kRawStages) raw_out = 0;
+          uint32_t w[D / 8], pair[D / 32];
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k) {
+            const uint4 v = reinterpret_cast<const uint4 *>(raw)[k];
+            w[4 * k] = v.x, w[4 * k + 1] = v.y, w[4 * k + 2] = v.z, w[4 * k + 3] = v.w;
+          }
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k) pair[k] = reinterpret_cast<const uint32_t *>(raw + D / 2)[k];
+          send();
+          lost |= !__all_sync(~0u, wait(&sm.empty[stage], phase));
+          if (!lost) {
+            if ((half & 1) && x.key0 + (half >> 1) * kKeys + kKeys > least) {  // see attn_narrow_kernel
+              bool any = false;
+#pragma unroll
+              for (int k = 0; k < D / 32; ++k)
+                if (odd2<__half>(pair[k])) pair[k] = 0, any = true;
+              if (any) *(volatile int32_t *)&sm.odd[parity] = 1;
+            }
+            char *dst = sm.kv[stage];
+            const __half2 less = __half2half2(__ushort_as_half(0xe400)), small = __half2half2(__ushort_as_half(0x2c00)),
+                          less4 = __half2half2(__ushort_as_half(0xd400));  // -1024, 1 / 16, -64
+#pragma unroll
+            for (int k = 0; k < D / 8; ++k) {
+              const uint32_t s2 = __byte_perm(pair[k / 4], 0, 0x1010), l2 = __byte_perm(pair[k / 4], 0, 0x3232);
+              const __half2 s = *reinterpret_cast<const __half2 *>(&s2), l = *reinterpret_cast<const __half2 *>(&l2);
+              uint32_t o[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t b = (e & 2 ? w[k] >> 8 : w[k]) & (e & 1 ? 0x00f000f0u : 0x000f000fu) | 0x64006400u;
+                const __half2 c = *reinterpret_cast<const __half2 *>(&b);
+                const __half2 y = __hfma2(e & 1 ? __hfma2(c, small, less4) : __hadd2(c, less), s, l);
+                o[e] = *reinterpret_cast<const uint32_t *>(&y);
+              }
+              *reinterpret_cast<uint4 *>(dst + place<D>(i, k)) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+            arrive(&sm.full[stage]);
+          }
+          if (++stage == kStages) stage = 0, phase ^= 1;
+        }
+        cp_async_wait<0>();
+        asm volatile("bar.sync 1, 128;" ::: "memory");  // everyone has read warp_least
+        read_phase ^= parity;
+        parity ^= 1;
+        return true;
+      } else {
       // a tile that tensor copies can bring: whole, the same for all live rows, and no box of it
       // partly in the prefix
       auto regular = [&](int j) {
@@ -692,6 +811,7 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
       read_phase ^= parity;
       parity ^= 1;
       return true;
+      }
     });
   } else {
     // ---- products ----
@@ -798,32 +918,32 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(sm.tmem) : "memory");
 }
 
-template <typename IO, bool FP8, int D>
+template <typename IO, int E, int D>
 cudaError_t launch(const AttnParams &p, bool hnd, cudaStream_t s) {
-  const void *fn = (const void *)attn_wide_kernel<IO, FP8, D>;
-  constexpr int kSmem = (int)sizeof(Smem<FP8, D>) + 1024;
+  const void *fn = (const void *)attn_wide_kernel<IO, E, D>;
+  constexpr int kSmem = (int)sizeof(Smem<E, D>) + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory of one SM");
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  AttnTma tma;
-  CUtensorMap km, vm;
-  attn_make_tma(p, kKeys, FP8, hnd, &tma, &km, &vm);
+  AttnTma tma = {};
+  CUtensorMap km = {}, vm = {};
+  if (E != k4) attn_make_tma(p, kKeys, E == k8, hnd, &tma, &km, &vm);
   void *args[] = {const_cast<AttnParams *>(&p), &tma, &km, &vm};
   return launch_pdl(fn, dim3(p.wide_groups * p.kv_heads), dim3(kThreads), args, s, kSmem);
 }
 
-template <typename IO, bool FP8>
+template <typename IO, int E>
 cudaError_t launch_d(const AttnParams &p, bool hnd, cudaStream_t s) {
-  return p.head_dim == 64 ? launch<IO, FP8, 64>(p, hnd, s) : launch<IO, FP8, 128>(p, hnd, s);
+  return p.head_dim == 64 ? launch<IO, E, 64>(p, hnd, s) : launch<IO, E, 128>(p, hnd, s);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_wide(const AttnParams &p, int32_t dtype, int32_t io, bool hnd, cudaStream_t s) {
-  if (dtype == KVX_F16) return launch_d<__half, false>(p, hnd, s);
-  if (dtype == KVX_BF16) return launch_d<__nv_bfloat16, false>(p, hnd, s);
-  if (io == KVX_F16) return launch_d<__half, true>(p, hnd, s);
-  return launch_d<__nv_bfloat16, true>(p, hnd, s);
+  if (dtype == KVX_F16) return launch_d<__half, k16>(p, hnd, s);
+  if (dtype == KVX_BF16) return launch_d<__nv_bfloat16, k16>(p, hnd, s);
+  if (dtype == KVX_FP8) return io == KVX_F16 ? launch_d<__half, k8>(p, hnd, s) : launch_d<__nv_bfloat16, k8>(p, hnd, s);
+  return io == KVX_F16 ? launch_d<__half, k4>(p, hnd, s) : launch_d<__nv_bfloat16, k4>(p, hnd, s);
 }
 
 }  // namespace kvx

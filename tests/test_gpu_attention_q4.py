@@ -12,9 +12,9 @@ pytestmark = pytest.mark.gpu
 KINDS = ["planes", "slots", "hnd"]
 
 
-def run(c, **more):
+def run(c, wide=False, **more):
     r = q4.Run(c)
-    q4.check(c, r.call(**more).results())
+    q4.check(c, r.call(**more).results(), wide)
     return r
 
 
@@ -92,7 +92,7 @@ ROOM = 300_000
 @pytest.mark.parametrize("D", [64, 128])
 def test_wide_prefix_by_page_size(kind, page, prefix, D):
     lens = [prefix + 1 + 29 * (i % 5) for i in range(40)]
-    run(q4.make("bf16", kind, page, 2, G=4, D=D, lens=lens, prefix=prefix, seed=page, room=ROOM, starts=True))
+    run(q4.make("bf16", kind, page, 2, G=4, D=D, lens=lens, prefix=prefix, seed=page, room=ROOM, starts=True), wide=True)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
@@ -101,26 +101,52 @@ def test_wide_prefix_by_page_size(kind, page, prefix, D):
 def test_prompts(dtype, kind, page, prefix, D):
     q = [200, 1, 77, 150]
     run(q4.make(dtype, kind, page, 2, G=4, D=D, lens=[prefix + 200, prefix + 50, prefix + 377, prefix + 150],
-                qlens=q, prefix=prefix, seed=page, room=ROOM))
+                qlens=q, prefix=prefix, seed=page, room=ROOM), wide=True)
 
 
 def test_prompts_among_padding_and_single_tokens():
     run(q4.make("f16", "planes", 16, 2, G=8, D=64, lens=[0, 700, 301, 0, 640, 333, 299],
-                qlens=[1, 300, 1, 40, 5, 33, 60], prefix=300, room=ROOM))
+                qlens=[1, 300, 1, 40, 5, 33, 60], prefix=300, room=ROOM), wide=True)
 
 
-@pytest.mark.parametrize("D", [64, 128])
-@pytest.mark.parametrize("starts", [False, True])
-def test_values_far_from_zero_and_of_every_size(D, starts):
-    """Lows far greater than the scales; groups whose scales lie far apart; large and tiny values."""
+def _spread_scales(D):
+    """Values' groups multiplied by powers of two that lie far apart."""
     def edit(b):
         pair = b[..., D // 2:].view(np.float16)
         g = np.random.default_rng(b.size)
         f = g.choice([2.0 ** -8, 1, 1, 2.0 ** 6], size=pair.shape[-1] // 2)
         pair[:, 1, :, 0::2] = pair[:, 1, :, 0::2] * f
         pair[:, 1, :, 1::2] = pair[:, 1, :, 1::2] * f
-    run(q4.make("bf16", "planes", 16, 2, G=4, D=D, lens=[500, 300, 411], prefix=100, shift=5.0, edit_bytes=edit,
-                starts=starts, room=ROOM if starts else 0))
+    return edit
+
+
+@pytest.mark.parametrize("D", [64, 96, 128])
+def test_values_far_from_zero_and_of_every_size(D):
+    """Lows far greater than the scales; groups whose scales lie far apart; large and tiny values."""
+    run(q4.make("bf16", "planes", 16, 2, G=4, D=D, lens=[500, 300, 411], prefix=100, shift=5.0,
+                edit_bytes=_spread_scales(D)))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_the_same_with_many_rows(D):
+    run(q4.make("bf16", "planes", 16, 2, G=4, D=D, lens=[500, 300, 411], qlens=[70, 40, 90], prefix=100, shift=5.0,
+                edit_bytes=_spread_scales(D), room=ROOM), wide=True)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("what", [0x7C00, 0xFC00, 0x7E00])
+def test_prompts_mask_infinities_and_nan(D, what):
+    """The last tokens of a prompt of many rows, as below; with lows of infinity alone too."""
+    c = q4.make("bf16", "planes", 16, 1, G=2, D=D, lens=[270], qlens=[200], prefix=0, layers=1, layer=0, room=2 * ROOM)
+    pool = c.pool.view(2, c.slots, D // 8 * 5)
+    for j in (266, 267, 269):
+        slot = int(c.tables[0, j // 16]) * 16 + j % 16
+        pool[:, slot, D // 2:] = torch.tensor([what & 255, what >> 8] * (D // 16), dtype=torch.uint8)
+    out, lse = q4.Run(c).call().results()
+    want, wlse, tol, tol_l = q4.reference(c, True)
+    q4.ar._near(out[:196], want[:196], tol[:196], "out")
+    q4.ar._near(lse[:196], wlse[:196], tol_l[:196], "lse")
+    assert not bool(torch.isfinite(out[196:]).any())
 
 
 @pytest.mark.parametrize("D", [64, 128])
