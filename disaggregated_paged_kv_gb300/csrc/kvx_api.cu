@@ -1206,7 +1206,7 @@ static kvx_status run_cast(bool store, kvx_layout_t pool, const kvx_cast_args *a
   q.scale[1] = store ? 1.f / a.v_scale : a.v_scale;
   q.wide = ((uintptr_t)a.k | (uintptr_t)a.v | (uintptr_t)q.layer_stride | (uintptr_t)q.token_stride |
             (uintptr_t)q.head_stride) % 16 == 0;
-  q.words = q4 || (pool->head_dim % 8 == 0 && side_vec(pool) >= 8);
+  q.words = side_vec(pool) >= 8;
   for (int p = 0; p < q.planes; ++p)
     q.base[p] = reinterpret_cast<char *>(pool->plane[2 * a.layer + p]);
   const cudaError_t err = kvx::launch_quant(q, store, q4, a.dtype, s);

@@ -1,13 +1,16 @@
 // kvx_quant.cu -- rows quantised as they are written into a pool, and read back.
 //
-// A thread has eight neighbouring elements of a head (16 bytes of 16-bit values), so a 4-bit group of 32
-// is four lanes': its least and greatest value take two shuffles each, its codes are four words side by
-// side, and one lane writes scale and low.  The four such pieces of a thread are loaded before anything is
-// waited for; as in the row copy kernel, the planner's verdict (or, for few tokens, the CTA's own check of
-// every index) is looked at between the loads and the first store, so that a call writes all or nothing.
+// A thread has 16 neighbouring elements of a head (8-bit pools: eight), so a 4-bit group of 32 is two lanes'.
+// Which head and which elements depends on the thread alone; it takes a few tokens in turn, whose slots
+// give the rows, so that an element costs a handful of instructions beside its bytes.  All rows of a turn are
+// loaded before anything is waited for; as in the row copy kernel, the planner's verdict (or, for few
+// tokens, the CTA's own check of every index) is looked at between the first loads and the first store: a
+// call writes all or nothing.
 //
 // Bound: bytes, 2 + 5/8 of them an element of a 16-bit tensor and a 4-bit pool.
 #include <cuda_bf16.h>
+
+#include <type_traits>
 
 #include "kvx_launch.cuh"
 #include "kvx_quant.cuh"
@@ -16,7 +19,6 @@ namespace kvx {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPieces = 4;  // of a thread, on their way together
 
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
@@ -51,81 +53,119 @@ __device__ __forceinline__ uint32_t from_e4m3x2(uint16_t x) {
 
 constexpr float kMost = 61440.f;  // what low + 15 * scale can reach without passing f16's end
 
-// The codes of this lane's eight elements, element i in bits 4 i .., and the group's (scale, low), which all
-// four lanes of the group get.  Steps are rounded one by one (no fused multiply-add), as kvx.h says.
-__device__ __forceinline__ uint32_t encode(float (&x)[8], uint32_t *pair) {
-  float lo = x[0], hi = x[0];
+// Least and greatest of a thread's elements, by pairs where they come as 16-bit numbers; NaN if any is.
+template <typename IO, int N>
+__device__ __forceinline__ void ends(const IO (&e)[N], float *lo, float *hi) {
+  if constexpr (sizeof(IO) == 4) {
+    float a = e[0], b = e[0];
 #pragma unroll
-  for (int i = 1; i < 8; ++i) lo = min_nan(lo, x[i]), hi = max_nan(hi, x[i]);
+    for (int i = 1; i < N; ++i) a = min_nan(a, e[i]), b = max_nan(b, e[i]);
+    *lo = a, *hi = b;
+  } else {
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(e);
+    uint32_t a = w[0], b = w[0];
 #pragma unroll
-  for (int o = 1; o < 4; o <<= 1) {
-    lo = min_nan(lo, __shfl_xor_sync(~0u, lo, o));
-    hi = max_nan(hi, __shfl_xor_sync(~0u, hi, o));
+    for (int i = 1; i < N / 2; ++i) {
+      if constexpr (std::is_same<IO, __half>::value) {
+        asm("min.NaN.f16x2 %0, %0, %1;" : "+r"(a) : "r"(w[i]));
+        asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(b) : "r"(w[i]));
+      } else {
+        asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(w[i]));
+        asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(b) : "r"(w[i]));
+      }
+    }
+    IO x[2], y[2];
+    *reinterpret_cast<uint32_t *>(x) = a, *reinterpret_cast<uint32_t *>(y) = b;
+    *lo = min_nan(to_f(x[0]), to_f(x[1])), *hi = max_nan(to_f(y[0]), to_f(y[1]));
   }
-  if (isnan(lo)) {
-    *pair = 0x7fff0000u;
-    return 0;
-  }
-  // (clamping the ends is clamping the values: codes past them are clamped below)
-  const __half low = __float2half_rn(fminf(fmaxf(lo, -kMost), kMost));
+}
+
+// The codes of this lane's 16 elements times mul, element i in bits 4 i .., and the group's (scale, low), which both
+// lanes of the group get.  Steps are rounded one by one (no fused multiply-add), as kvx.h says.
+template <typename IO>
+__device__ __forceinline__ uint64_t encode(const IO (&e)[16], float mul, uint32_t *pair) {
+  float lo, hi;
+  ends(e, &lo, &hi);
+  lo = min_nan(lo, __shfl_xor_sync(~0u, lo, 1));
+  hi = max_nan(hi, __shfl_xor_sync(~0u, hi, 1));
+  lo = __fmul_rn(lo, mul), hi = __fmul_rn(hi, mul);  // (mul > 0: the ends of the products)
+  const bool nan = isnan(lo);
+  const float least = fminf(fmaxf(lo, -kMost), kMost), most = fminf(fmaxf(hi, -kMost), kMost);
+  const __half low = __float2half_rn(least);
   const float base = __half2float(low);
-  const float reach = __fsub_rn(fminf(fmaxf(hi, -kMost), kMost), base);
-  const __half scale = __float2half_rn(fmaxf(__fmul_rn(reach, 1.f / 15.f), 0.f));
-  *pair = (uint32_t)__half_as_ushort(scale) | (uint32_t)__half_as_ushort(low) << 16;
+  const __half scale = __float2half_rn(fmaxf(__fmul_rn(__fsub_rn(most, base), 1.f / 15.f), 0.f));
+  *pair = nan ? 0x7fff0000u : (uint32_t)__half_as_ushort(scale) | (uint32_t)__half_as_ushort(low) << 16;
   const float s = __half2float(scale), r = s > 0.f ? __frcp_rn(s) : 0.f;
-  uint32_t codes = 0;
+  // (clamping the ends is clamping the values: codes past them are clamped here.)  No code can be below 0 where no
+  // value is below the low, none above 15 where the scale is a normal number, within 2^-11 of a 15th of the reach.
+  const bool plain = !nan && base <= lo && hi <= kMost && s >= 0x1p-14f;
+  const bool fast = __all_sync(~0u, plain);
+  uint32_t w[2] = {0, 0};
 #pragma unroll
-  for (int i = 7; i >= 0; --i) {
-    const float y = fminf(fmaxf(x[i], -kMost), kMost);
-    const float c = fminf(fmaxf(__fmul_rn(__fsub_rn(y, base), r), 0.f), 15.f);
-    // the nearest whole number, ties to even, in the low bits of c + 1.5 * 2^23
-    codes = codes << 4 | (__float_as_uint(__fadd_rn(c, 12582912.f)) & 15u);
+  for (int k = 0; k < 2; ++k) {
+#pragma unroll
+    for (int i = 7; i >= 0; --i) {
+      float c = to_f(e[8 * k + i]);
+      if (mul != 1.f) c = __fmul_rn(c, mul);
+      c = __fmul_rn(__fsub_rn(c, base), r);
+      if (!fast) c = fminf(fmaxf(c, 0.f), 15.f);
+      // the nearest whole number, ties to even, in the low bits of c + 1.5 * 2^23, whose others cancel below
+      w[k] = w[k] * 16u + __float_as_uint(__fadd_rn(c, 12582912.f));
+    }
+    w[k] -= 0x4b400000u * 0x11111111u;
   }
-  return codes;
+  return nan ? 0 : (uint64_t)w[1] << 32 | w[0];
 }
 
-// An element of a group.
-__device__ __forceinline__ float decode(uint32_t code, float scale, float low) {
-  // 2^23 + code, less 2^23
-  return __fmaf_rn(__uint_as_float(0x4b000000u | code) - 8388608.f, scale, low);
-}
+// Which elements of a row a thread has, wherever the row is.
+template <int N>
+struct Place {
+  int32_t first, step;   // its first token's place among the CTA's, and how far apart its tokens are
+  int32_t d;             // first element in the head
+  int64_t pool, data;    // bytes from a row's (HND: a page's, plus the token's) to the head vector; to the elements
+  bool any;
+  __device__ __forceinline__ Place(const QuantArgs &q, int32_t part, int e) {
+    const int32_t per_head = q.head_dim / N, per_row = per_head * q.heads;
+    int32_t c = threadIdx.x;
+    first = 0, step = 1;
+    if (per_row < kThreads) {
+      step = kThreads / per_row;
+      first = c / per_row;
+      c -= first * per_row;
+      any = first < step;
+    } else {
+      c += part * kThreads;
+      any = c < per_row;
+    }
+    const int32_t h = c / per_head;
+    d = (c - h * per_head) * N;
+    pool = h * (int64_t)q.pool.seg_bytes * (q.pool.hnd ? q.pool.page_size : 1);
+    data = h * q.head_stride + (int64_t)d * e;
+  }
+};
 
-// Where a piece is: N elements of one head of one token.
-struct Piece {
-  char *pool;       // the head vector; nullptr: nothing to be done
-  char *data;       // the elements in k or v
-  int32_t d;        // first element in the head
+// A token's head vector in the pool and its elements outside; nullptr: no token, or an index out of range.
+struct Row {
+  char *pool, *data;
 };
 
 template <int N>
-__device__ __forceinline__ Piece piece_at(const QuantArgs &q, int p, int64_t at, int64_t most, int e) {
-  Piece x = {nullptr, nullptr, 0};
-  if (at >= most) return x;
-  const int32_t per_head = q.head_dim / N, per_row = per_head * q.heads;
-  int64_t i;
-  int32_t c;
-  if (most <= INT32_MAX) {
-    i = (uint32_t)at / (uint32_t)per_row;
-    c = (int32_t)((uint32_t)at - (uint32_t)i * (uint32_t)per_row);
-  } else {
-    i = at / per_row;
-    c = (int32_t)(at - i * per_row);
-  }
-  const int32_t h = c / per_head;
-  x.d = (c - h * per_head) * N;
+__device__ __forceinline__ Row row_at(const QuantArgs &q, int p, const Place<N> &x, int64_t i) {
+  Row r = {nullptr, nullptr};
+  if (!x.any || i >= q.n) return r;
   const int32_t slot = q.slots[i];
   const int64_t row = q.rows ? (int64_t)q.rows[i] : i;
-  if (slot < 0 || slot >= q.pool.num_slots || row < 0 || row >= q.n_rows) return x;
-  int64_t off;
+  if (slot < 0 || slot >= q.pool.num_slots || row < 0 || row >= q.n_rows) return r;
+  int64_t off = x.pool;
   if (q.pool.hnd) {
-    const int32_t page = slot / q.pool.page_size, in = slot - page * q.pool.page_size;
-    off = page * q.pool.page_bytes + ((int64_t)h * q.pool.page_size + in) * q.pool.seg_bytes;
+    const int32_t page = q.pool.ps_shift >= 0 ? slot >> q.pool.ps_shift : slot / q.pool.page_size;
+    off += page * q.pool.page_bytes + (int64_t)(slot - page * q.pool.page_size) * q.pool.seg_bytes;
   } else {
-    off = slot * q.pool.slot_stride + (int64_t)h * q.pool.seg_bytes;
+    off += slot * q.pool.slot_stride;
   }
-  x.pool = q.base[p] + off;
-  x.data = (p & 1 ? q.v : q.k) + (p >> 1) * q.layer_stride + row * q.token_stride + h * q.head_stride + (int64_t)x.d * e;
-  return x;
+  r.pool = q.base[p] + off;
+  r.data = (p & 1 ? q.v : q.k) + (p >> 1) * q.layer_stride + row * q.token_stride + x.data;
+  return r;
 }
 
 // False: some index is out of range, and nothing may be written.
@@ -166,106 +206,123 @@ struct Raw {
   }
 };
 
-// N: elements of a piece, eight, or one where an 8-bit pool's head vectors are no multiple of that.
+// Rows of a turn, on their way together.
+template <typename IO>
+constexpr int kTurn = sizeof(IO) == 4 ? 2 : 4;
+
+// The first look at the verdict: whether anything may be written.
+__device__ __forceinline__ bool may_write(const QuantArgs &q) {
+  if (q.check) return all_in_range(q);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  return *(volatile int32_t *)q.status == KVX_OK;
+}
+
+// Calls f(first token of a turn) for this CTA's tokens; blockIdx.x counts them, its parts of long rows within.
+template <int N, int T, typename F>
+__device__ __forceinline__ void turns(const QuantArgs &q, int32_t step, F f) {
+  const int64_t block = blockIdx.x / q.parts;
+  for (int32_t k = 0; k < q.turns; ++k) {
+    const int64_t i = (block * q.turns + k) * (T * step);
+    if (i >= q.n && k > 0) return;
+    if (!f(i, k == 0)) return;
+  }
+}
+
+// N: elements of a thread: 16 (4-bit pools), 8, or 1 where an 8-bit pool's head vectors are no multiple of that.
 template <typename IO, bool Q4, int N>
-__global__ void __launch_bounds__(kThreads) store_kernel(const __grid_constant__ QuantArgs q) {
+__global__ void __launch_bounds__(kThreads, 3) store_kernel(const __grid_constant__ QuantArgs q) {
+  constexpr int T = kTurn<IO>;
   const int p = blockIdx.y;
-  const int64_t most = q.n * (q.head_dim / N * q.heads), step = (int64_t)gridDim.x * (kPieces * kThreads);
-  bool first = true, ok = true;
+  const Place<N> x(q, (int32_t)(blockIdx.x % q.parts), sizeof(IO));
+  const float scale = q.scale[p & 1];
   // behind the planner the rows are complete (it has waited for whoever wrote them)
   if (q.check) asm volatile("griddepcontrol.wait;" ::: "memory");
-  for (int64_t at = (int64_t)blockIdx.x * (kPieces * kThreads) + threadIdx.x; first || at - threadIdx.x < most; at += step) {
-    Piece x[kPieces];
-    Raw<IO, N> raw[kPieces];
+  turns<N, T>(q, x.step, [&](int64_t i0, bool first) {
+    Row r[T];
+    Raw<IO, N> raw[T];
 #pragma unroll
-    for (int u = 0; u < kPieces; ++u) {
-      x[u] = piece_at<N>(q, p, at + u * kThreads, most, sizeof(IO));
-      if (x[u].pool) raw[u].load(x[u].data, q.wide);
+    for (int u = 0; u < T; ++u) {
+      r[u] = row_at<N>(q, p, x, i0 + x.first + u * x.step);
+      if (r[u].pool) raw[u].load(r[u].data, q.wide);
     }
-    if (first) {
-      if (q.check) {
-        ok = all_in_range(q);
-      } else {
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-        ok = *(volatile int32_t *)q.status == KVX_OK;
-      }
-      first = false;
-    }
-    if (!ok) return;
-    const float scale = q.scale[p & 1];
+    if (first && !may_write(q)) return false;
 #pragma unroll
-    for (int u = 0; u < kPieces; ++u) {
+    for (int u = 0; u < T; ++u) {
       if constexpr (Q4) {
-        float y[8];
+        if (!r[u].pool)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = x[u].pool ? __fmul_rn(to_f(raw[u].e[i]), scale) : 0.f;
+          for (int i = 0; i < N; ++i) from_f(&raw[u].e[i], 0.f);
         uint32_t pair;
-        const uint32_t codes = encode(y, &pair);
-        if (x[u].pool) {
-          uint32_t *o = reinterpret_cast<uint32_t *>(x[u].pool);
-          o[x[u].d / 8] = codes;
-          if (x[u].d % KVX_Q4_GROUP == 0) o[q.head_dim / 8 + x[u].d / KVX_Q4_GROUP] = pair;
+        const uint64_t codes = encode(raw[u].e, scale, &pair);
+        if (r[u].pool) {
+          uint32_t *o = reinterpret_cast<uint32_t *>(r[u].pool) + x.d / 8;
+          if (q.words) *reinterpret_cast<uint64_t *>(o) = codes;
+          else o[0] = (uint32_t)codes, o[1] = (uint32_t)(codes >> 32);
+          if (x.d % KVX_Q4_GROUP == 0) reinterpret_cast<uint32_t *>(r[u].pool)[q.head_dim / 8 + x.d / KVX_Q4_GROUP] = pair;
         }
-      } else if (x[u].pool) {
+      } else if (r[u].pool) {
         if constexpr (N == 8) {
           uint32_t w[2];
 #pragma unroll
           for (int i = 0; i < 2; ++i)
             w[i] = (uint32_t)to_e4m3x2(__fmul_rn(to_f(raw[u].e[4 * i]), scale), __fmul_rn(to_f(raw[u].e[4 * i + 1]), scale)) |
                    (uint32_t)to_e4m3x2(__fmul_rn(to_f(raw[u].e[4 * i + 2]), scale), __fmul_rn(to_f(raw[u].e[4 * i + 3]), scale)) << 16;
-          *reinterpret_cast<uint2 *>(x[u].pool + x[u].d) = make_uint2(w[0], w[1]);
+          *reinterpret_cast<uint2 *>(r[u].pool + x.d) = make_uint2(w[0], w[1]);
         } else {
-          x[u].pool[x[u].d] = (char)to_e4m3x2(__fmul_rn(to_f(raw[u].e[0]), scale), 0.f);
+          r[u].pool[x.d] = (char)to_e4m3x2(__fmul_rn(to_f(raw[u].e[0]), scale), 0.f);
         }
       }
     }
-  }
+    return true;
+  });
 }
 
 template <typename IO, bool Q4, int N>
 __global__ void __launch_bounds__(kThreads) load_kernel(const __grid_constant__ QuantArgs q) {
+  constexpr int T = 4;
   const int p = blockIdx.y;
-  const int64_t most = q.n * (q.head_dim / N * q.heads), step = (int64_t)gridDim.x * (kPieces * kThreads);
-  bool first = true, ok = true;
+  const Place<N> x(q, (int32_t)(blockIdx.x % q.parts), sizeof(IO));
+  const float scale = q.scale[p & 1];
   if (q.check) asm volatile("griddepcontrol.wait;" ::: "memory");
-  for (int64_t at = (int64_t)blockIdx.x * (kPieces * kThreads) + threadIdx.x; first || at - threadIdx.x < most; at += step) {
-    Piece x[kPieces];
-    uint32_t w[kPieces][2];  // codes and (scale, low), or eight E4M3 numbers
+  turns<N, T>(q, x.step, [&](int64_t i0, bool first) {
+    Row r[T];
+    uint32_t w[T][3];  // codes and (scale, low), or eight E4M3 numbers
 #pragma unroll
-    for (int u = 0; u < kPieces; ++u) {
-      x[u] = piece_at<N>(q, p, at + u * kThreads, most, sizeof(IO));
-      w[u][0] = w[u][1] = 0;
-      if (!x[u].pool) continue;
+    for (int u = 0; u < T; ++u) {
+      r[u] = row_at<N>(q, p, x, i0 + x.first + u * x.step);
+      if (!r[u].pool) continue;
       if constexpr (Q4) {
-        const uint32_t *o = reinterpret_cast<const uint32_t *>(x[u].pool);
-        w[u][0] = o[x[u].d / 8], w[u][1] = o[q.head_dim / 8 + x[u].d / KVX_Q4_GROUP];
+        const uint32_t *o = reinterpret_cast<const uint32_t *>(r[u].pool);
+        if (q.words) {
+          const uint2 v = *reinterpret_cast<const uint2 *>(o + x.d / 8);
+          w[u][0] = v.x, w[u][1] = v.y;
+        } else {
+          w[u][0] = o[x.d / 8], w[u][1] = o[x.d / 8 + 1];
+        }
+        w[u][2] = o[q.head_dim / 8 + x.d / KVX_Q4_GROUP];
       } else if constexpr (N == 8) {
-        const uint2 v = *reinterpret_cast<const uint2 *>(x[u].pool + x[u].d);
+        const uint2 v = *reinterpret_cast<const uint2 *>(r[u].pool + x.d);
         w[u][0] = v.x, w[u][1] = v.y;
       } else {
-        w[u][0] = (uint8_t)x[u].pool[x[u].d];
+        w[u][0] = (uint8_t)r[u].pool[x.d];
       }
     }
-    if (first) {
-      if (q.check) {
-        ok = all_in_range(q);
-      } else {
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-        ok = *(volatile int32_t *)q.status == KVX_OK;
-      }
-      first = false;
-    }
-    if (!ok) return;
-    const float scale = q.scale[p & 1];
+    if (first && !may_write(q)) return false;
 #pragma unroll
-    for (int u = 0; u < kPieces; ++u) {
-      if (!x[u].pool) continue;
+    for (int u = 0; u < T; ++u) {
+      if (!r[u].pool) continue;
       Raw<IO, N> out;
       if constexpr (Q4) {
-        const float s = __half2float(__ushort_as_half((uint16_t)w[u][1]));
-        const float low = __half2float(__ushort_as_half((uint16_t)(w[u][1] >> 16)));
+        const float s = __half2float(__ushort_as_half((uint16_t)w[u][2]));
+        const float low = __half2float(__ushort_as_half((uint16_t)(w[u][2] >> 16)));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) from_f(&out.e[i], __fmul_rn(decode(w[u][0] >> (4 * i) & 15u, s, low), scale));
+        for (int i = 0; i < N; ++i) {
+          // 2^23 + code, less 2^23
+          const float code = __uint_as_float(0x4b000000u | (w[u][i >> 3] >> (4 * (i & 7)) & 15u)) - 8388608.f;
+          float y = __fmaf_rn(code, s, low);
+          if (scale != 1.f) y = __fmul_rn(y, scale);
+          from_f(&out.e[i], y);
+        }
       } else {
 #pragma unroll
         for (int i = 0; i < N; i += 2) {
@@ -275,29 +332,38 @@ __global__ void __launch_bounds__(kThreads) load_kernel(const __grid_constant__ 
             from_f(&out.e[i + 1], __fmul_rn(__half2float(__ushort_as_half((uint16_t)(v >> 16))), scale));
         }
       }
-      out.store(x[u].data, q.wide);
+      out.store(r[u].data, q.wide);
     }
-  }
+    return true;
+  });
 }
 
+constexpr int kSms = 152;
+
 template <typename IO, bool Q4, int N>
-cudaError_t launch(const QuantArgs &q, bool store, cudaStream_t s) {
+cudaError_t launch(QuantArgs &q, bool store, cudaStream_t s) {
   const void *fn = store ? (const void *)store_kernel<IO, Q4, N> : (const void *)load_kernel<IO, Q4, N>;
-  const int64_t pieces = q.n * (q.head_dim / N * q.heads), per = kPieces * kThreads;
-  const int64_t grid = (pieces + per - 1) / per, most = 1 << 30;
-  void *args[] = {const_cast<QuantArgs *>(&q)};
-  return launch_pdl(fn, dim3((unsigned)(grid < most ? grid : most), (unsigned)q.planes), dim3(kThreads), args, s);
+  const int64_t per_row = (int64_t)(q.head_dim / N) * q.heads, turn = store ? kTurn<IO> : 4;
+  const int64_t step = per_row < kThreads ? kThreads / per_row : 1;  // tokens of a pass
+  q.parts = (int32_t)((per_row + kThreads - 1) / kThreads);
+  const int64_t all = (q.n + turn * step - 1) / (turn * step);
+  // some turns a CTA where that still leaves each SM many CTAs
+  const int64_t many = all * q.parts * q.planes / (kSms * 16);
+  q.turns = (int32_t)(many < 1 ? 1 : many > 8 ? 8 : many);
+  int64_t grid = (all + q.turns - 1) / q.turns * q.parts;
+  void *args[] = {&q};
+  return launch_pdl(fn, dim3((unsigned)grid, (unsigned)q.planes), dim3(kThreads), args, s);
 }
 
 template <typename IO>
-cudaError_t launch_io(const QuantArgs &q, bool store, bool q4, cudaStream_t s) {
-  if (q4) return launch<IO, true, 8>(q, store, s);
+cudaError_t launch_io(QuantArgs &q, bool store, bool q4, cudaStream_t s) {
+  if (q4) return launch<IO, true, 16>(q, store, s);
   return q.words ? launch<IO, false, 8>(q, store, s) : launch<IO, false, 1>(q, store, s);
 }
 
 }  // namespace
 
-cudaError_t launch_quant(const QuantArgs &q, bool store, bool q4, int32_t dtype, cudaStream_t s) {
+cudaError_t launch_quant(QuantArgs &q, bool store, bool q4, int32_t dtype, cudaStream_t s) {
   if (dtype == KVX_F16) return launch_io<__half>(q, store, q4, s);
   if (dtype == KVX_BF16) return launch_io<__nv_bfloat16>(q, store, q4, s);
   return launch_io<float>(q, store, q4, s);
