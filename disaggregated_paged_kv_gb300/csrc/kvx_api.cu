@@ -1204,8 +1204,9 @@ static kvx_status run_cast(bool store, kvx_layout_t pool, const kvx_cast_args *a
   q.head_stride = a.head_stride * e;
   q.scale[0] = store ? 1.f / a.k_scale : a.k_scale;
   q.scale[1] = store ? 1.f / a.v_scale : a.v_scale;
-  q.wide = ((uintptr_t)a.k | (uintptr_t)a.v | (uintptr_t)q.layer_stride | (uintptr_t)q.token_stride |
-            (uintptr_t)q.head_stride) % 16 == 0;
+  const uintptr_t at = (uintptr_t)a.k | (uintptr_t)a.v | (uintptr_t)q.layer_stride | (uintptr_t)q.token_stride |
+                       (uintptr_t)q.head_stride;
+  q.wide = at % 16 == 0;
   q.words = side_vec(pool) >= 8;
   for (int p = 0; p < q.planes; ++p)
     q.base[p] = reinterpret_cast<char *>(pool->plane[2 * a.layer + p]);

@@ -51,6 +51,31 @@ __device__ __forceinline__ uint32_t from_e4m3x2(uint16_t x) {
   return r;
 }
 
+// Two 32-bit floats at a time.
+__device__ __forceinline__ uint64_t pair2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair2(uint64_t x, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 constexpr float kMost = 61440.f;  // what low + 15 * scale can reach without passing f16's end
 
 // Least and greatest of a thread's elements, by pairs where they come as 16-bit numbers; NaN if any is.
@@ -81,14 +106,15 @@ __device__ __forceinline__ void ends(const IO (&e)[N], float *lo, float *hi) {
 }
 
 // The codes of this lane's 16 elements times mul, element i in bits 4 i .., and the group's (scale, low), which both
-// lanes of the group get.  Steps are rounded one by one (no fused multiply-add), as kvx.h says.
-template <typename IO>
-__device__ __forceinline__ uint64_t encode(const IO (&e)[16], float mul, uint32_t *pair) {
+// lanes of the group get.  Steps are rounded one by one (no fused multiply-add), as kvx.h says.  live: the elements
+// are some token's (a group's lanes agree).
+template <bool SCALED, typename IO>
+__device__ __forceinline__ uint64_t encode(const IO (&e)[16], bool live, float mul, uint32_t *pair) {
   float lo, hi;
   ends(e, &lo, &hi);
   lo = min_nan(lo, __shfl_xor_sync(~0u, lo, 1));
   hi = max_nan(hi, __shfl_xor_sync(~0u, hi, 1));
-  lo = __fmul_rn(lo, mul), hi = __fmul_rn(hi, mul);  // (mul > 0: the ends of the products)
+  if (SCALED) lo = __fmul_rn(lo, mul), hi = __fmul_rn(hi, mul);  // (mul > 0: the ends of the products)
   const bool nan = isnan(lo);
   const float least = fminf(fmaxf(lo, -kMost), kMost), most = fminf(fmaxf(hi, -kMost), kMost);
   const __half low = __float2half_rn(least);
@@ -96,25 +122,56 @@ __device__ __forceinline__ uint64_t encode(const IO (&e)[16], float mul, uint32_
   const __half scale = __float2half_rn(fmaxf(__fmul_rn(__fsub_rn(most, base), 1.f / 15.f), 0.f));
   *pair = nan ? 0x7fff0000u : (uint32_t)__half_as_ushort(scale) | (uint32_t)__half_as_ushort(low) << 16;
   const float s = __half2float(scale), r = s > 0.f ? __frcp_rn(s) : 0.f;
-  // (clamping the ends is clamping the values: codes past them are clamped here.)  No code can be below 0 where no
-  // value is below the low, none above 15 where the scale is a normal number, within 2^-11 of a 15th of the reach.
+  float y[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) y[i] = to_f(e[i]);
+  if (SCALED)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) y[i] = __fmul_rn(y[i], mul);
+  // A code is the nearest whole number, ties to even: the low bits of c + 1.5 * 2^23.  (Clamping the ends is clamping the
+  // values: codes past them are clamped here.)  No code can be below 0 where no value is below the low, none
+  // above 15 where the scale is a normal number, within 2^-11 of a 15th of the reach.
   const bool plain = !nan && base <= lo && hi <= kMost && s >= 0x1p-14f;
-  const bool fast = __all_sync(~0u, plain);
+  if (__all_sync(~0u, plain || !live)) {
+    const uint64_t base2 = pair2(-base, -base), r2 = pair2(r, r);
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+      unpair2(mul2(add2(pair2(y[i], y[i + 1]), base2), r2), y[i], y[i + 1]);
+      // (as pairs, product and sum would become one operation with one rounding)
+      y[i] = __fadd_rn(y[i], 12582912.f), y[i + 1] = __fadd_rn(y[i + 1], 12582912.f);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      y[i] = __fadd_rn(fminf(fmaxf(__fmul_rn(__fsub_rn(y[i], base), r), 0.f), 15.f), 12582912.f);
+  }
   uint32_t w[2] = {0, 0};
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
 #pragma unroll
-    for (int i = 7; i >= 0; --i) {
-      float c = to_f(e[8 * k + i]);
-      if (mul != 1.f) c = __fmul_rn(c, mul);
-      c = __fmul_rn(__fsub_rn(c, base), r);
-      if (!fast) c = fminf(fmaxf(c, 0.f), 15.f);
-      // the nearest whole number, ties to even, in the low bits of c + 1.5 * 2^23, whose others cancel below
-      w[k] = w[k] * 16u + __float_as_uint(__fadd_rn(c, 12582912.f));
-    }
-    w[k] -= 0x4b400000u * 0x11111111u;
+    for (int i = 7; i >= 0; --i) w[k] = w[k] * 16u + __float_as_uint(y[8 * k + i]);
+    w[k] -= 0x4b400000u * 0x11111111u;  // what 1.5 * 2^23 has left of its bits
   }
   return nan ? 0 : (uint64_t)w[1] << 32 | w[0];
+}
+
+// Eight elements from their codes, SCALED: times scale.
+template <bool SCALED>
+__device__ __forceinline__ void decode(uint32_t codes, float step, float low, float scale, float (&o)[8]) {
+  // 2^23 + 16^i code, less 2^23, times step / 16^i: all exact, and rounded once with the low
+  const uint64_t less = pair2(-8388608.f, -8388608.f), low2 = pair2(low, low), scale2 = pair2(scale, scale);
+  const uint64_t step01 = pair2(step, step * 0x1p-4f), step23 = pair2(step * 0x1p-8f, step * 0x1p-12f);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t w = k ? codes >> 16 : codes;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint64_t c = pair2(__uint_as_float((w & (0xfu << (8 * i))) | 0x4b000000u), __uint_as_float((w & (0xf0u << (8 * i))) | 0x4b000000u));
+      uint64_t y = fma2(add2(c, less), i ? step23 : step01, low2);
+      if (SCALED) y = mul2(y, scale2);
+      unpair2(y, o[4 * k + 2 * i], o[4 * k + 2 * i + 1]);
+    }
+  }
 }
 
 // Which elements of a row a thread has, wherever the row is.
@@ -122,9 +179,9 @@ template <int N>
 struct Place {
   int32_t first, step;   // its first token's place among the CTA's, and how far apart its tokens are
   int32_t d;             // first element in the head
-  int64_t pool, data;    // bytes from a row's (HND: a page's, plus the token's) to the head vector; to the elements
+  char *pool, *data;     // the head vector and the elements in row 0 (HND: token 0 of page 0)
   bool any;
-  __device__ __forceinline__ Place(const QuantArgs &q, int32_t part, int e) {
+  __device__ __forceinline__ Place(const QuantArgs &q, int p, int32_t part, int e) {
     const int32_t per_head = q.head_dim / N, per_row = per_head * q.heads;
     int32_t c = threadIdx.x;
     first = 0, step = 1;
@@ -139,10 +196,15 @@ struct Place {
     }
     const int32_t h = c / per_head;
     d = (c - h * per_head) * N;
-    pool = h * (int64_t)q.pool.seg_bytes * (q.pool.hnd ? q.pool.page_size : 1);
-    data = h * q.head_stride + (int64_t)d * e;
+    pool = q.base[p] + h * (int64_t)q.pool.seg_bytes * (q.pool.hnd ? q.pool.page_size : 1);
+    data = (p & 1 ? q.v : q.k) + (p >> 1) * q.layer_stride + h * q.head_stride + (int64_t)d * e;
   }
 };
+
+// a * b, in one instruction where b has 31 bits.
+__device__ __forceinline__ int64_t times(int32_t a, int64_t b) {
+  return (b >> 31) == 0 ? (int64_t)((uint64_t)(uint32_t)a * (uint32_t)b) : a * b;
+}
 
 // A token's head vector in the pool and its elements outside; nullptr: no token, or an index out of range.
 struct Row {
@@ -150,21 +212,18 @@ struct Row {
 };
 
 template <int N>
-__device__ __forceinline__ Row row_at(const QuantArgs &q, int p, const Place<N> &x, int64_t i) {
+__device__ __forceinline__ Row row_at(const QuantArgs &q, const Place<N> &x, int64_t i) {
   Row r = {nullptr, nullptr};
   if (!x.any || i >= q.n) return r;
-  const int32_t slot = q.slots[i];
-  const int64_t row = q.rows ? (int64_t)q.rows[i] : i;
-  if (slot < 0 || slot >= q.pool.num_slots || row < 0 || row >= q.n_rows) return r;
-  int64_t off = x.pool;
+  const int32_t slot = q.slots[i], row = q.rows ? q.rows[i] : (int32_t)i;
+  if ((uint32_t)slot >= (uint32_t)q.pool.num_slots || (uint32_t)row >= (uint32_t)q.n_rows) return r;
   if (q.pool.hnd) {
     const int32_t page = q.pool.ps_shift >= 0 ? slot >> q.pool.ps_shift : slot / q.pool.page_size;
-    off += page * q.pool.page_bytes + (int64_t)(slot - page * q.pool.page_size) * q.pool.seg_bytes;
+    r.pool = x.pool + times(page, q.pool.page_bytes) + times(slot - page * q.pool.page_size, q.pool.seg_bytes);
   } else {
-    off += slot * q.pool.slot_stride;
+    r.pool = x.pool + times(slot, q.pool.slot_stride);
   }
-  r.pool = q.base[p] + off;
-  r.data = (p & 1 ? q.v : q.k) + (p >> 1) * q.layer_stride + row * q.token_stride + x.data;
+  r.data = x.data + times(row, q.token_stride);
   return r;
 }
 
@@ -206,9 +265,12 @@ struct Raw {
   }
 };
 
-// Rows of a turn, on their way together.
+// Rows of a turn, on their way together.  (Loads of two turns more warps into what an SM holds: 20000 tokens of 28
+// layers 133 us, of four 153, of one 159.  Stores of two, four and eight: 2048 tokens of 36 layers, written
+// and read, 163, 159 and 205 us.)
 template <typename IO>
-constexpr int kTurn = sizeof(IO) == 4 ? 2 : 4;
+constexpr int kStoreTurn = sizeof(IO) == 4 ? 2 : 4;
+constexpr int kLoadTurn = 2;
 
 // The first look at the verdict: whether anything may be written.
 __device__ __forceinline__ bool may_write(const QuantArgs &q) {
@@ -229,11 +291,11 @@ __device__ __forceinline__ void turns(const QuantArgs &q, int32_t step, F f) {
 }
 
 // N: elements of a thread: 16 (4-bit pools), 8, or 1 where an 8-bit pool's head vectors are no multiple of that.
-template <typename IO, bool Q4, int N>
+template <typename IO, bool Q4, int N, bool SCALED>
 __global__ void __launch_bounds__(kThreads, 3) store_kernel(const __grid_constant__ QuantArgs q) {
-  constexpr int T = kTurn<IO>;
+  constexpr int T = kStoreTurn<IO>;
   const int p = blockIdx.y;
-  const Place<N> x(q, (int32_t)(blockIdx.x % q.parts), sizeof(IO));
+  const Place<N> x(q, p, (int32_t)(blockIdx.x % q.parts), sizeof(IO));
   const float scale = q.scale[p & 1];
   // behind the planner the rows are complete (it has waited for whoever wrote them)
   if (q.check) asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -242,18 +304,15 @@ __global__ void __launch_bounds__(kThreads, 3) store_kernel(const __grid_constan
     Raw<IO, N> raw[T];
 #pragma unroll
     for (int u = 0; u < T; ++u) {
-      r[u] = row_at<N>(q, p, x, i0 + x.first + u * x.step);
+      r[u] = row_at<N>(q, x, i0 + x.first + u * x.step);
       if (r[u].pool) raw[u].load(r[u].data, q.wide);
     }
     if (first && !may_write(q)) return false;
 #pragma unroll
     for (int u = 0; u < T; ++u) {
       if constexpr (Q4) {
-        if (!r[u].pool)
-#pragma unroll
-          for (int i = 0; i < N; ++i) from_f(&raw[u].e[i], 0.f);
         uint32_t pair;
-        const uint64_t codes = encode(raw[u].e, scale, &pair);
+        const uint64_t codes = encode<SCALED>(raw[u].e, r[u].pool != nullptr, scale, &pair);
         if (r[u].pool) {
           uint32_t *o = reinterpret_cast<uint32_t *>(r[u].pool) + x.d / 8;
           if (q.words) *reinterpret_cast<uint64_t *>(o) = codes;
@@ -277,11 +336,11 @@ __global__ void __launch_bounds__(kThreads, 3) store_kernel(const __grid_constan
   });
 }
 
-template <typename IO, bool Q4, int N>
+template <typename IO, bool Q4, int N, bool SCALED>
 __global__ void __launch_bounds__(kThreads) load_kernel(const __grid_constant__ QuantArgs q) {
-  constexpr int T = 4;
+  constexpr int T = kLoadTurn;
   const int p = blockIdx.y;
-  const Place<N> x(q, (int32_t)(blockIdx.x % q.parts), sizeof(IO));
+  const Place<N> x(q, p, (int32_t)(blockIdx.x % q.parts), sizeof(IO));
   const float scale = q.scale[p & 1];
   if (q.check) asm volatile("griddepcontrol.wait;" ::: "memory");
   turns<N, T>(q, x.step, [&](int64_t i0, bool first) {
@@ -289,7 +348,7 @@ __global__ void __launch_bounds__(kThreads) load_kernel(const __grid_constant__ 
     uint32_t w[T][3];  // codes and (scale, low), or eight E4M3 numbers
 #pragma unroll
     for (int u = 0; u < T; ++u) {
-      r[u] = row_at<N>(q, p, x, i0 + x.first + u * x.step);
+      r[u] = row_at<N>(q, x, i0 + x.first + u * x.step);
       if (!r[u].pool) continue;
       if constexpr (Q4) {
         const uint32_t *o = reinterpret_cast<const uint32_t *>(r[u].pool);
@@ -316,12 +375,11 @@ __global__ void __launch_bounds__(kThreads) load_kernel(const __grid_constant__ 
         const float s = __half2float(__ushort_as_half((uint16_t)w[u][2]));
         const float low = __half2float(__ushort_as_half((uint16_t)(w[u][2] >> 16)));
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          // 2^23 + code, less 2^23
-          const float code = __uint_as_float(0x4b000000u | (w[u][i >> 3] >> (4 * (i & 7)) & 15u)) - 8388608.f;
-          float y = __fmaf_rn(code, s, low);
-          if (scale != 1.f) y = __fmul_rn(y, scale);
-          from_f(&out.e[i], y);
+        for (int k = 0; k < N / 8; ++k) {
+          float y[8];
+          decode<SCALED>(w[u][k], s, low, scale, y);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) from_f(&out.e[8 * k + i], y[i]);
         }
       } else {
 #pragma unroll
@@ -342,8 +400,12 @@ constexpr int kSms = 152;
 
 template <typename IO, bool Q4, int N>
 cudaError_t launch(QuantArgs &q, bool store, cudaStream_t s) {
-  const void *fn = store ? (const void *)store_kernel<IO, Q4, N> : (const void *)load_kernel<IO, Q4, N>;
-  const int64_t per_row = (int64_t)(q.head_dim / N) * q.heads, turn = store ? kTurn<IO> : 4;
+  // (an 8-bit pool's elements are multiplied in any case)
+  const bool scaled = !Q4 || q.scale[0] != 1.f || q.scale[1] != 1.f;
+  const void *fn = store ? (const void *)store_kernel<IO, Q4, N, true> : (const void *)load_kernel<IO, Q4, N, true>;
+  if constexpr (Q4)
+    if (!scaled) fn = store ? (const void *)store_kernel<IO, Q4, N, false> : (const void *)load_kernel<IO, Q4, N, false>;
+  const int64_t per_row = (int64_t)(q.head_dim / N) * q.heads, turn = store ? kStoreTurn<IO> : kLoadTurn;
   const int64_t step = per_row < kThreads ? kThreads / per_row : 1;  // tokens of a pass
   q.parts = (int32_t)((per_row + kThreads - 1) / kThreads);
   const int64_t all = (q.n + turn * step - 1) / (turn * step);

@@ -744,30 +744,46 @@ def move_heads(op: int, src: Optional[Layout], src_slots, src_head0: int, dst: O
     _check(rc, "kvx_move_heads")
 
 
+_row_dtypes = {}  # torch dtype -> kvx dtype of k and v, as they come up
+
+
+def _row_dtype(dtype) -> int:
+    got = _row_dtypes.get(dtype)
+    if got is None:
+        got = _Q_DTYPES.get(str(dtype))
+        if got is None:
+            raise ValueError("k and v are float16, bfloat16 or float32 alike")
+        _row_dtypes[dtype] = got
+    return got
+
+
+def _index_list(x) -> int:
+    """The length of a list of slots or rows."""
+    if str(x.dtype) != "torch.int32" or not x.is_contiguous():
+        raise ValueError("slots and rows are contiguous int32 tensors")
+    return x.numel()
+
+
 def _cast_args(pool: Layout, layer: int, k, v, slots, rows, k_scale, v_scale) -> CastArgs:
-    dtype = _Q_DTYPES.get(str(k.dtype))
-    if dtype is None or v.dtype is not k.dtype:
-        raise ValueError("k and v are float16, bfloat16 or float32 alike")
-    if k.dim() not in (3, 4) or v.shape != k.shape or v.stride() != k.stride():
+    # (a decode step makes these calls layer by layer: each attribute of a tensor is asked for once)
+    shape, strides = k.shape, k.stride()
+    if v.shape != shape or v.stride() != strides or v.dtype is not k.dtype or not 3 <= len(shape) <= 4:
         raise ValueError("k and v are [tokens, kv_heads, head_dim] or [layers, tokens, kv_heads, head_dim], "
-                         "of one shape and of the same strides")
-    n_rows, heads, dim = k.shape[-3:]
+                         "of one type and shape and of the same strides")
+    n_rows, heads, dim = shape[-3:]
+    token, head, element = strides[-3:]
     if heads != pool.kv_heads or dim != pool.head_dim:
         raise ValueError("k and v have the pool's kv_heads and head_dim")
-    if k.stride(-1) != 1 and dim > 1 and k.numel() > 0:
+    if element != 1 and dim > 1 and k.numel() > 0:
         raise ValueError("a head's elements must be contiguous in k and v")
-    for x in (slots, rows):
-        if x is not None and (str(x.dtype) != "torch.int32" or not x.is_contiguous()):
-            raise ValueError("slots and rows are contiguous int32 tensors")
-    n = slots.numel()
-    if (n_rows != n) if rows is None else (rows.numel() != n):
+    n = _index_list(slots)
+    if n_rows != n if rows is None else _index_list(rows) != n:
         raise ValueError("slots and " + ("k" if rows is None else "rows") + " differ in length")
-    layers = k.shape[0] if k.dim() == 4 else 1
+    layers = shape[0] if len(shape) == 4 else 1
     # (an axis of one has no stride that counts)
-    token, head = (k.stride(-3) if n_rows > 1 else 0), (k.stride(-2) if heads > 1 else 0)
-    return CastArgs(layer, layers, dtype, n, k.data_ptr(), v.data_ptr(),
-                    k.stride(0) if layers > 1 else 0, token, head, slots.data_ptr(), _ptr(rows), n_rows,
-                    k_scale, v_scale, 0)
+    return CastArgs(layer, layers, _row_dtype(k.dtype), n, k.data_ptr(), v.data_ptr(),
+                    strides[0] if layers > 1 else 0, token if n_rows > 1 else 0, head if heads > 1 else 0,
+                    slots.data_ptr(), None if rows is None else rows.data_ptr(), n_rows, k_scale, v_scale, 0)
 
 
 def store_kv(pool: Layout, layer: int, k, v, slots, ws, status, rows=None, k_scale: float = 1.0,
