@@ -465,13 +465,44 @@ struct Sizes {
   int32_t groups, wide_groups;
 };
 
-// How many groups of kv_heads CTAs: as many as are resident at once.
-Sizes sizes(int64_t n_q, int64_t n_reqs, int64_t q_heads, int64_t kv_heads, int64_t D, int row_tile,
-            bool wide) {
+// Whether the tensor-core kernels take a layout.
+bool tensor_cores(const kvx_layout *l) {
+  if (l->dtype == KVX_Q4)  // copies of a fifth of a head vector, head vectors counted in 32 bits
+    return (l->head_dim == 64 || l->head_dim == 128) && l->vec >= l->head_dim / 8 && l->slot_stride <= INT32_MAX &&
+           (l->kind == KVX_NHD || l->num_slots * l->kv_heads < (int64_t)1 << 32);
+  return l->elem <= 2 && (l->head_dim == 64 || l->head_dim == 128) && l->vec == 16;
+}
+
+// kv heads of a CTA of the 4-bit kernel: up to eight, an even number where that makes whole 16-byte pieces.
+int q4_chunk(const kvx_layout *l) {
+  const int chunks = (l->kv_heads + kAttnQ4Warps - 1) / kAttnQ4Warps;
+  const int c = (l->kv_heads + chunks - 1) / chunks;
+  return l->head_dim == 64 && c % 2 != 0 && c > 1 ? c + 1 : c;
+}
+int q4_slot_shift(const kvx_layout *l) {
+  int s = 0;
+  while (1 << s < q4_chunk(l)) ++s;
+  return s;
+}
+
+bool q4_kernel(const kvx_layout *l) { return l->dtype == KVX_Q4 && tensor_cores(l); }
+
+int row_tile_of(const kvx_layout *l) {
+  if (q4_kernel(l)) return 8 * (kAttnQ4Warps >> q4_slot_shift(l));
+  return tensor_cores(l) ? kAttnNarrowRows : kAttnGeneralRows;
+}
+
+int group_ctas(const kvx_layout *l) {
+  return q4_kernel(l) ? (l->kv_heads + q4_chunk(l) - 1) / q4_chunk(l) : l->kv_heads;
+}
+
+// How many groups of CTAs: as many as are resident at once.
+Sizes sizes(const kvx_layout *l, int64_t n_q, int64_t n_reqs, int64_t q_heads, bool wide) {
   Sizes z = {};
+  const int64_t kv_heads = l->kv_heads, D = l->head_dim, row_tile = row_tile_of(l);
   const int64_t rows = n_q * (q_heads / kv_heads);
-  const int64_t per_sm = row_tile == kAttnGeneralRows && D <= 128 ? 3 : 2;
-  z.groups = (int32_t)std::max((int64_t)1, kAttnSms * per_sm / kv_heads);
+  const int64_t per_sm = !tensor_cores(l) && D <= 128 ? 3 : 2;
+  z.groups = (int32_t)std::max((int64_t)1, kAttnSms * per_sm / group_ctas(l));
   z.wide_groups = wide ? (int32_t)std::max((int64_t)1, kAttnSms / kv_heads) : 0;
   z.errors = z.groups * kv_heads + z.wide_groups * kv_heads;
   const int64_t parts = 2 * n_q * q_heads + z.groups * kv_heads * row_tile +
@@ -509,16 +540,6 @@ bool shape_ok(const kvx_layout *l, int64_t n_q, int64_t n_reqs, int64_t q_heads,
          n_q * q_heads <= (int64_t)1 << 30;
 }
 
-// Whether the tensor-core kernels take a layout.
-bool tensor_cores(const kvx_layout *l) {
-  if (l->dtype == KVX_Q4)  // copies of a fifth of a head vector, at 32-bit distances within 16 keys
-    return (l->head_dim == 64 || l->head_dim == 128) && l->vec >= l->head_dim / 8 &&
-           l->slot_stride <= INT32_MAX / 32;
-  return l->elem <= 2 && (l->head_dim == 64 || l->head_dim == 128) && l->vec == 16;
-}
-
-int row_tile(const kvx_layout *l) { return tensor_cores(l) ? kAttnNarrowRows : kAttnGeneralRows; }
-
 // Whether a call may have work for the wide kernel: more rows than the narrow kernel has in a unit.
 bool takes_wide(const kvx_layout *l, int64_t n_q, int64_t q_heads) {
   return tensor_cores(l) && n_q * (q_heads / l->kv_heads) > kAttnNarrowRows;
@@ -544,8 +565,7 @@ static_assert(sizeof(kvx_attn_args) == 152, "the binding mirrors this structure"
 extern "C" size_t kvx_attention_workspace_size(kvx_layout_t pool, int32_t n_q, int32_t n_reqs,
                                                int32_t q_heads, int32_t prefix_len) {
   if (!kvx::shape_ok(pool, n_q, n_reqs, q_heads, prefix_len)) return 0;
-  return (size_t)kvx::sizes(n_q, n_reqs, q_heads, pool->kv_heads, pool->head_dim,
-                            kvx::row_tile(pool), kvx::takes_wide(pool, n_q, q_heads)).total;
+  return (size_t)kvx::sizes(pool, n_q, n_reqs, q_heads, kvx::takes_wide(pool, n_q, q_heads)).total;
 }
 
 extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_args *args,
@@ -600,8 +620,7 @@ extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_arg
   const bool wide = takes_wide(pool, a.n_q, a.q_heads) &&
                     4.0 * pool->head_dim * a.q_heads * a.n_q * wide_keys >= (beside ? kWideBeside : kWideWork) &&
                     a.scale * a.k_scale > 0.f;
-  const Sizes z = sizes(a.n_q, a.n_reqs, a.q_heads, pool->kv_heads, pool->head_dim, row_tile(pool),
-                        wide);
+  const Sizes z = sizes(pool, a.n_q, a.n_reqs, a.q_heads, wide);
   if (!d_ws || !mult(d_ws, 256) || (int64_t)ws_bytes < z.total) return KVX_ERR_NO_WORKSPACE;
 
   AttnParams p;
@@ -641,10 +660,30 @@ extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_arg
   p.page_size = a.page_size;
   p.max_pages = a.max_pages;
   p.prefix_len = a.prefix_len;
-  p.row_tile = row_tile(pool);
-  const bool q4 = pool->dtype == KVX_Q4;
-  p.few_rows = q4 && tensor_cores(pool) ? 8 : 16;
-  p.paged_blocks = a.page_size % 16 == 0;
+  p.row_tile = row_tile_of(pool);
+  const bool q4 = q4_kernel(pool);
+  p.few_rows = q4 ? 8 : 16;
+  p.key_shift = q4 ? 5 : 6;
+  static_assert(1 << 5 == kAttnQ4KeyTile && 1 << 6 == kAttnKeyTile, "tiles of these kernels");
+  p.group_ctas = group_ctas(pool);
+  p.chunk = q4 ? q4_chunk(pool) : 1;
+  p.tile_ns = (int32_t)std::max(kAttnNarrowNs, ((pool->seg_bytes * p.chunk) << p.key_shift) * 2 / 16 * kAttnNarrowPs / 1000);
+  if (q4) {
+    p.slot_shift = q4_slot_shift(pool);
+    p.page_vectors = (uint32_t)(hnd ? (int64_t)a.page_size * pool->kv_heads : a.page_size);
+    // 16 tokens of a head lie side by side in head-major pages, or where there is one head
+    const bool even = ((uintptr_t)p.pool.k | (uintptr_t)p.pool.v) % 16 == 0;
+    const bool dense = hnd || (pool->kv_heads == 1 && pool->slot_stride == seg);
+    const int32_t keys = 16 * (kAttnQ4Warps >> p.slot_shift);  // of a stage
+    p.q4_copies = dense && even && a.page_size % 16 == 0                    ? kAttnQ4Runs
+                  : !hnd && pool->vec == 16 && p.chunk * seg % 16 == 0      ? kAttnQ4Tokens
+                                                                            : kAttnQ4Parts;
+    p.q4_key_pitch = (int32_t)seg, p.q4_head_pitch = (int32_t)seg * keys;
+    if (p.q4_copies == kAttnQ4Tokens) {
+      // an odd number of 16-byte pieces a key: eight keys' lie in different banks
+      p.q4_key_pitch = (int32_t)(p.chunk * seg) | 16, p.q4_head_pitch = (int32_t)seg;
+    }
+  }
   p.unit_cost = tensor_cores(pool) ? kNarrowUnitCost : 0;
   p.head_bytes = (int32_t)pool->seg_bytes;
   const uintptr_t q_at = (uintptr_t)a.q | (uintptr_t)p.q_tok | (uintptr_t)p.q_head;
@@ -685,7 +724,7 @@ extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_arg
   if (a.n_q > 0) {
     if (e == cudaSuccess && wide) e = launch_attn_wide(p, pool->dtype, a.q_dtype, hnd, s);
     if (e == cudaSuccess)
-      e = tensor_cores(pool) && q4 ? launch_attn_q4(p, a.q_dtype, s)
+      e = q4                   ? launch_attn_q4(p, a.q_dtype, s)
           : tensor_cores(pool) ? launch_attn_narrow(p, pool->dtype, a.q_dtype, hnd, s)
                              : launch_attn_general(p, pool->dtype, a.q_dtype, pool->vec == 16 && pool->seg_bytes % 16 == 0, s);
   }

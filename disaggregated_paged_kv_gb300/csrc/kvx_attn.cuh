@@ -32,12 +32,17 @@
 namespace kvx {
 
 constexpr int kAttnKeyTile = 64;       // of the narrow and the plain kernel
+constexpr int kAttnQ4KeyTile = 32;     // of the 4-bit kernel, whose CTAs have several heads
+constexpr int kAttnQ4Warps = 8;        // and so many warps that compute
 constexpr int kAttnGeneralRows = 16;   // rows of a unit, plain kernel
 constexpr int kAttnNarrowRows = 64;    // narrow kernel
 constexpr int kAttnWideKeys = 128;     // key tile of the wide kernel
 constexpr int kAttnWideRows = 256;     // rows of its units
 
 constexpr int kAttnWritten = -2;
+
+// How the 4-bit kernel's head vectors come: 16 tokens of a head at a time, a token's heads, or fifths of a head vector.
+enum AttnQ4Copies : int32_t { kAttnQ4Runs = 0, kAttnQ4Tokens = 1, kAttnQ4Parts = 2 };
 
 // Where a layer's rows are: element row (page id, offset in page, kv head) starts at
 // plane + id * page_stride + offset * tok_stride + head * head_stride (bytes), in either kind of
@@ -96,9 +101,14 @@ struct AttnParams {
   int32_t head_bytes;    // of a head of one token in the pool
   int32_t row_tile;      // rows of a narrow unit
   int32_t few_rows;      // a tile of up to so many rows costs 1 (see attn_cost)
-  int32_t paged_blocks;  // 4-bit pools: blocks of 16 positions lie in a page each
+  int32_t key_shift;     // log2 of a narrow tile's keys
+  int32_t tile_ns;       // what a narrow tile of cost 1 takes a CTA (see attn_share)
+  int32_t group_ctas;    // of a narrow group: one a kv head, or one a chunk of them
+  // the 4-bit kernel: kv heads of a CTA, log2 of the places for them, how they come, and where a stage has them
+  int32_t chunk, slot_shift, q4_copies, q4_key_pitch, q4_head_pitch;
+  uint32_t page_vectors; // head vectors of a page, in strides of a token (fewer than 2^32 in all)
   int32_t unit_cost;     // what a unit's begin and end cost, in tiles of up to 16 rows
-  int32_t groups;        // groups of kv_heads CTAs, narrow line
+  int32_t groups;        // groups of group_ctas CTAs, narrow line
   int32_t wide_groups;   // of the wide line; 0: no wide kernel
   int32_t planned;       // 1: the plan kernel has laid the work out.  0: one query token a request,
                          // and every kernel works its part out from the lengths
@@ -229,9 +239,9 @@ __device__ __forceinline__ int64_t attn_length(const AttnParams &p, const AttnSe
 
 __device__ __forceinline__ void attn_tile_seg(const AttnParams &p, AttnSeg *g) {
   g->cost = attn_cost(g->rows, p.row_tile, p.few_rows);
-  g->key0 = g->low / kAttnKeyTile * kAttnKeyTile;
+  g->key0 = g->low >> p.key_shift << p.key_shift;
   if (g->rows > 0 && g->key1 > g->low)
-    g->key_tiles = (int32_t)attn_up((int64_t)g->key1 - g->key0, kAttnKeyTile);
+    g->key_tiles = (int32_t)(((int64_t)g->key1 - g->key0 + (1 << p.key_shift) - 1) >> p.key_shift);
 }
 
 // Seg s of a call without a plan (its tile0 aside).
@@ -279,7 +289,7 @@ __device__ __forceinline__ int attn_find(const E *e, int n, int64_t w) {
 
 // A piece: keys [key0, key1), those below low left out, for rows [row0, row0 + rows).
 struct AttnPiece {
-  int64_t part;
+  int64_t part, head_step;  // its first row's place, and how far the next kv head's is
   int32_t row0, rows, low, key0, key1, table;
 };
 
@@ -292,7 +302,7 @@ struct AttnShare {
 };
 
 // The GPU's SMs, and measured times in ns: of a CTA's tile of 128 keys and 256 rows; of a narrow CTA's unit
-// of cost, two CTAs on the SM, at least, and of 16 bytes of a tile; of 1 MB at the memory's rate; and what a launch takes before and after its tiles.
+// of cost, two CTAs on the SM, at least, and of 16 bytes of a tile (the host makes tile_ns of them); of 1 MB at the memory's rate; and what a launch takes before and after its tiles.
 constexpr int kAttnSms = 152;
 constexpr int64_t kAttnWideNs = 2100, kAttnNarrowNs = 900, kAttnNarrowPs = 470, kAttnMbNs = 160,
                   kAttnStartNs = 10000;
@@ -300,18 +310,17 @@ constexpr int64_t kAttnWideNs = 2100, kAttnNarrowNs = 900, kAttnNarrowPs = 470, 
 __device__ __forceinline__ AttnShare attn_share(const AttnParams &p, int64_t own, int64_t wide) {
   AttnShare s = {p.groups, p.wide_groups};
   if (p.wide_groups < 2 || own == 0 || wide == 0) return s;
-  const int64_t bytes = (int64_t)kAttnKeyTile * p.head_bytes * 2;  // of a narrow tile
+  const int64_t bytes = ((int64_t)p.head_bytes << p.key_shift) * 2;  // of a narrow tile and head
   const int64_t tiles = max(own - (int64_t)p.n_reqs * p.unit_cost, (int64_t)0);
   const int64_t floor_ns = (tiles * p.kv_heads * bytes >> 20) * kAttnMbNs;
-  const int64_t unit_ns = max(kAttnNarrowNs, bytes / 16 * kAttnNarrowPs / 1000);
   auto narrow_ns = [&](int64_t groups) {
-    return kAttnStartNs + max(attn_up(own, groups) * unit_ns, floor_ns);
+    return kAttnStartNs + max(attn_up(own, groups) * p.tile_ns, floor_ns);
   };
   auto wide_ns = [&](int64_t groups) { return kAttnStartNs + attn_up(wide, groups) * kAttnWideNs; };
   int64_t best = (wide_ns(p.wide_groups) + narrow_ns(p.groups)) * 9 / 10;  // a tenth sooner, or not at all
   int at = p.wide_groups;
   for (int g = 1 + (threadIdx.x & 31); g < p.wide_groups; g += 32) {
-    const int left = (kAttnSms - g * p.kv_heads) * 2 / p.kv_heads;
+    const int left = (kAttnSms - g * p.kv_heads) * 2 / p.group_ctas;
     if (left < 1) continue;
     const int64_t a = wide_ns(g), b = narrow_ns(left), both = a > b ? a : b;
     if (both < best) best = both, at = g;
@@ -322,7 +331,7 @@ __device__ __forceinline__ AttnShare attn_share(const AttnParams &p, int64_t own
     const int g = __shfl_xor_sync(~0u, at, o);
     if (b < best || (b == best && g < at)) best = b, at = g;
   }
-  if (at < p.wide_groups) s.wide_groups = at, s.groups = min(p.groups, (kAttnSms - at * p.kv_heads) * 2 / p.kv_heads);
+  if (at < p.wide_groups) s.wide_groups = at, s.groups = min(p.groups, (kAttnSms - at * p.kv_heads) * 2 / p.group_ctas);
   return s;
 }
 
@@ -460,10 +469,11 @@ __device__ __forceinline__ void attn_pieces(const AttnParams &p, int g, int h, c
       x.row0 = seg.row0 + unit * p.row_tile;
       x.rows = min(p.row_tile, seg.rows - unit * p.row_tile);
       x.low = seg.low;
-      x.key0 = seg.key0 + kt * kAttnKeyTile;
-      x.key1 = (int32_t)min((int64_t)seg.key1, (int64_t)x.key0 + (int64_t)take * kAttnKeyTile);
+      x.key0 = seg.key0 + (kt << p.key_shift);
+      x.key1 = (int32_t)min((int64_t)seg.key1, (int64_t)x.key0 + ((int64_t)take << p.key_shift));
       x.table = s - 1;
       x.part = attn_part(p, s == 0, kt == 0, g, h, x.row0);
+      x.head_step = kt == 0 ? (int64_t)p.n_q * p.group : p.row_tile;
       f(x);
     }
     tile0 += length;

@@ -11,46 +11,47 @@
 // queries (as two f16 numbers, so exact to 2^-22) and against the weights.
 //
 // Keys are the rows of both products (m16n8k16, M = 16 keys, N = 8 query rows; then M = 16 columns, K = 16
-// keys): the eight columns suit a group of up to eight query heads.  A warp walks blocks of 16 keys that it
-// brings in itself, 80 (or 40) bytes of K and V a key, into a ring of its own: no barrier within a piece.  The
-// warps of a CTA share a piece's blocks, and where it has more than eight rows its rows; their sums are joined in
-// shared memory at its end.
+// keys): the eight columns suit a group of up to eight query heads.
+//
+// A head vector is 80 (or 40) bytes, so a CTA has up to eight neighbouring heads (a chunk): a token's are one
+// stretch of memory and one bulk copy, or 16 tokens' of a head in head-major pages.  A producer warp fills a ring
+// of stages of 16 to 128 keys; eight warps share the heads, the rows where there are more than eight, and blocks
+// of 16 keys.  Copies of 16 bytes by the computing warps themselves, a head a CTA, took 16 cycles a key and head of
+// an SM's time, 9 of them for the copies alone (each fetches whole sectors of 32 bytes); the memory's rate is 6.8.
 #include <type_traits>
 
 #include "kvx_attn.cuh"
 #include "kvx_attn_mma.cuh"
+#include "kvx_attn_tma.cuh"
 #include "kvx_launch.cuh"
 #include "kvx_quant.cuh"
 
 namespace kvx {
 namespace {
 
-constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int kWarps = kAttnQ4Warps, kThreads = kWarps * 32 + 32;
 constexpr int kBlock = 16;    // keys at a time
 constexpr int kRows = 8;      // of a warp
 constexpr int kPieces = 32;   // listed at a time
+constexpr int kStages = 3;
 constexpr float kTop = 13.f;  // the greatest weight is about 2^kTop (see weight_shift), less for scales above 1
 constexpr float kRenew = 2.f; // by so many powers of two may a score pass what weights refer to
 
 template <int D>
 struct Smem {
-  static constexpr int kPitch = D == 128 ? 80 : 48;  // eight rows' 16-byte chunks lie in different banks
-  static constexpr int kStages = 3;
-  static constexpr int kStage = 2 * kBlock * kPitch;  // keys, then values
-  static constexpr int kSum = D + 4;                  // floats of a row on its way to be joined
-  alignas(128) char ring[kWarps][kStages][kStage];
+  // keys' head vectors, then values'; of at most 128 (key, head) pairs, rows padded by up to 16 bytes a key
+  static constexpr int kHalf = 128 * q4_bytes(D) + (D == 128 ? 1024 : 512);
+  static constexpr int kSum = D + 4;  // floats of a row on its way to be joined
+  alignas(128) char ring[kStages][2][kHalf];
   alignas(16) float sum[kWarps][kRows][kSum];
   float base[kWarps][kRows], l[kWarps][kRows];
+  uint32_t vector[128];  // where a stage's keys are, for copies of a part of a head
   AttnPiece pieces[kPieces];
-  int64_t scan[2 * kWarps + 4];
-  int32_t n_pieces, more, error;
+  int64_t scan[2 * (kThreads / 32) + 4];
+  uint64_t full[kStages], empty[kStages];
+  int32_t n_pieces, lost, error;
 };
 
-template <int B>
-__device__ __forceinline__ void cp_async(uint32_t dst, const char *src) {
-  if constexpr (B == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-  else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
 // ... or zeros.
 template <int B>
 __device__ __forceinline__ void cp_async_if(uint32_t dst, const char *src, bool ok) {
@@ -58,11 +59,26 @@ __device__ __forceinline__ void cp_async_if(uint32_t dst, const char *src, bool 
   if constexpr (B == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
   else asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const char *src, int bytes, uint64_t *bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
+}
 __device__ __forceinline__ void ldmatrix2(uint32_t (&r)[2], uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(a) : "memory");
 }
 __device__ __forceinline__ void ldmatrix2t(uint32_t (&r)[2], uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void load_shared(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void load_shared(uint32_t (&r)[2], uint32_t a) {
+  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ uint32_t load_shared(uint32_t a) {
+  uint32_t r;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(a) : "memory");
+  return r;
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t r;
@@ -77,90 +93,142 @@ __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ float low_half(uint32_t x) { return __half2float(__ushort_as_half((uint16_t)x)); }
 __device__ __forceinline__ bool odd_word(uint32_t x) { return odd2<__half>(x); }
 
-// How a piece's rows and keys are shared by the warps: 2^split sets of eight rows, the others take other blocks.
-__device__ __forceinline__ int split_of(int rows) { return rows <= 8 ? 0 : rows <= 16 ? 1 : rows <= 32 ? 2 : 3; }
+// Two 32-bit floats at a time.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 
-// A piece's blocks of 16 keys, from the one that its first key is in.
-struct Blocks {
-  int32_t start, count;
-  __device__ __forceinline__ Blocks(const AttnPiece &x) {
-    start = max(x.key0, x.low) / kBlock * kBlock;
-    count = x.key1 > max(x.key0, x.low) ? (x.key1 - start + kBlock - 1) / kBlock : 0;
+// What a CTA's warps have of a piece: slots of a chunk's heads (a power of two), and by each head's warps 2^split sets of
+// eight rows and the blocks of 16 keys that are left to share.
+struct Share {
+  int32_t warps;      // a head's
+  int32_t sets, keys; // sets * keys = warps
+  int32_t start, stages;
+  __device__ __forceinline__ Share(const AttnParams &p, const AttnPiece &x) {
+    warps = kWarps >> p.slot_shift;
+    sets = x.rows <= 8 ? 1 : x.rows <= 16 ? 2 : x.rows <= 32 ? 4 : 8;
+    keys = warps / sets;
+    const int32_t first = max(x.key0, x.low), stage = kBlock * warps;
+    start = first / kBlock * kBlock;
+    stages = x.key1 > first ? (x.key1 - start + stage - 1) / stage : 0;
   }
 };
 
-// Brings a warp's blocks in, in the order in which they are worked.
+// Brings the stages of all pieces in, in order, by one warp.
 template <int D>
-struct Loader {
+struct Producer {
   using S = Smem<D>;
-  static constexpr int kChunk = D / 8;  // bytes of a copy: a head vector is five of them
+  static constexpr int kBytes = q4_bytes(D), kChunk = D / 8;  // of a head vector, and of a fifth of it
   const AttnParams &p;
   S &sm;
-  const int h, lane, warp;
-  int piece = -1, block = 0, count = 0, step = 1, stage = 0;
-  int32_t start = 0, low = 0, key1 = 0, table = 0;
-  int32_t id = 0;            // the page of the block to be sent next (whole blocks in a page)
-  int32_t off[5], dst[5];    // this lane's copies of a block in a page: from its first key's head vector, in a stage
+  const int h0, heads, lane;
+  uint32_t stage = 0, phase = 1;
+  bool lost = false;  // a wait was given up: nothing more is sent on its way
 
-  __device__ __forceinline__ Loader(const AttnParams &p, S &sm, int h, int lane, int warp)
-      : p(p), sm(sm), h(h), lane(lane), warp(warp) {
+  // The page of position pos of a piece (a request's table, or the prefix's), as it stands there.
+  __device__ __forceinline__ int32_t page_of(const AttnPiece &x, int32_t pos) const {
+    if (pos < x.low || pos >= x.key1) return 0;
+    int32_t pg, o;
+    attn_split(p, pos, &pg, &o);
+    return attn_entry(p, x.table, pg);
+  }
+  __device__ __forceinline__ void piece(const AttnPiece &x) {
+    if (lost) return;
+    const Share w(p, x);
+    const int32_t keys = kBlock * w.warps;
+    // look-ups, a stage ahead of their use: of runs of 16 tokens, the lane pair's (lanes of K and V); of tokens, lane's,
+    // lane + 32's and so on (16 keys: lanes of K and V)
+    const int run_head = (lane >> 1) & ((1 << p.slot_shift) - 1), run_block = lane >> (1 + p.slot_shift);
+    const bool runs = p.q4_copies == kAttnQ4Runs, pairs = keys == 16 && !runs;
+    int32_t id[4] = {};
+    auto look = [&](int j) {
+      if (j >= w.stages) return;
+      const int32_t pos = w.start + j * keys;
+      if (runs) {
+        if (run_block < w.warps) id[0] = page_of(x, max(pos + run_block * kBlock, x.low));
+      } else {
 #pragma unroll
-    for (int r = 0; r < 5; ++r) {
-      const int j = r * 32 + lane, row = j / 5, c = j - row * 5;
-      off[r] = (row & 15) * (int32_t)p.pool.tok_stride + c * kChunk;
-      dst[r] = row * S::kPitch + c * kChunk;
-    }
-  }
-  // The next block that is this warp's.
-  __device__ __forceinline__ void next() {
-    block += step;
-    while (block >= count) {
-      if (++piece >= sm.n_pieces) return;
-      const AttnPiece &x = sm.pieces[piece];
-      const Blocks b(x);
-      const int split = split_of(x.rows);
-      start = b.start, count = b.count, low = x.low, key1 = x.key1, table = x.table;
-      block = warp >> split, step = kWarps >> split;
-    }
-    if (p.paged_blocks) {
-      int32_t pg, o;
-      attn_split(p, start + block * kBlock, &pg, &o);
-      id = attn_entry(p, table, pg);
-    }
-  }
-  __device__ __forceinline__ void begin() {
-    piece = -1, block = count = 0, step = 1;
-    next();
-  }
-  __device__ __forceinline__ void send() {
-    if (piece < sm.n_pieces) {
-      const uint32_t to = smem_u32(sm.ring[warp][stage]);
-      const int32_t pos = start + block * kBlock;
-      if (p.paged_blocks && pos >= low && pos + kBlock <= key1) {
-        int32_t pg, o;
-        attn_split(p, pos, &pg, &o);
-        const int64_t at = attn_checked(p, id, &sm.error) * p.pool.page_stride + o * p.pool.tok_stride + h * p.pool.head_stride;
-        const char *k = p.pool.k + at, *v = p.pool.v + at;
+        for (int i = 0; i < 4; ++i)
+          if (i == 0 || i * 32 < keys) id[i] = page_of(x, pos + (pairs ? lane & 15 : i * 32 + lane));
+      }
+    };
+    look(0);
+    for (int j = 0; j < w.stages; ++j) {
+      const int32_t pos = w.start + j * keys;
+      int32_t now[4];
 #pragma unroll
-        for (int r = 0; r < 5; ++r) {
-          const bool val = r == 2 ? lane >= 16 : r > 2;  // copies 80 on are of the values
-          cp_async<kChunk>(to + dst[r], (val ? v : k) + off[r]);
+      for (int i = 0; i < 4; ++i) now[i] = id[i];
+      look(j + 1);
+      lost = !__all_sync(~0u, bar_wait(&sm.empty[stage], phase, &sm.lost, &sm.error));
+      if (lost) return;
+      const uint32_t to = smem_u32(sm.ring[stage][0]);
+      if (runs) {
+        // 16 tokens of a head, whole: what lies beside the piece's keys is masked
+        const int32_t at = pos + run_block * kBlock;
+        const bool mine = run_block < w.warps && at < x.key1, take = mine && run_head < heads;
+        if (lane == 0) bar_expect(&sm.full[stage], 2 * heads * min(w.warps, (x.key1 - pos + kBlock - 1) / kBlock) * kBlock * kBytes);
+        if (take) {
+          int32_t pg, o;
+          attn_split(p, at, &pg, &o);
+          const char *src = (lane & 1 ? p.pool.v : p.pool.k) + attn_checked(p, now[0], &sm.error) * p.pool.page_stride +
+                            (h0 + run_head) * p.pool.head_stride + o * p.pool.tok_stride;
+          bulk_copy(to + (lane & 1) * S::kHalf + run_head * p.q4_head_pitch + run_block * kBlock * kBytes, src, kBlock * kBytes, &sm.full[stage]);
+        }
+      } else if (p.q4_copies == kAttnQ4Tokens) {
+        const int32_t first = max(pos, x.low), last = min(pos + keys, x.key1);
+        if (lane == 0) bar_expect(&sm.full[stage], 2 * (last - first) * heads * kBytes);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int32_t key = pairs ? lane & 15 : i * 32 + lane, at = pos + key;
+          if ((i > 0 && i * 32 >= keys) || at < first || at >= last) continue;
+          int32_t pg, o;
+          attn_split(p, at, &pg, &o);
+          const int64_t off = attn_checked(p, now[i], &sm.error) * p.pool.page_stride + o * p.pool.tok_stride + h0 * p.pool.head_stride;
+          const uint32_t dst = to + key * p.q4_key_pitch;
+          if (!pairs || lane < 16) bulk_copy(dst, p.pool.k + off, heads * kBytes, &sm.full[stage]);
+          if (!pairs || lane >= 16) bulk_copy(dst + S::kHalf, p.pool.v + off, heads * kBytes, &sm.full[stage]);
         }
       } else {
-        const int32_t mine = pos + (lane & 15);
-        int64_t at = -1;
-        if (mine >= low && mine < key1) at = attn_key_offset(p, table, mine, &sm.error) + h * p.pool.head_stride;
+        // a fifth of a head vector at a time; head vectors by their number in the plane (see AttnParams::page_vectors)
 #pragma unroll
-        for (int r = 0; r < 5; ++r) {
-          const int j = r * 32 + lane, row = j / 5, c = j - row * 5;
-          const int64_t from = __shfl_sync(~0u, at, row & 15);
-          cp_async_if<kChunk>(to + dst[r], (row >= 16 ? p.pool.v : p.pool.k) + (from < 0 ? 0 : from + c * kChunk), from >= 0);
+        for (int i = 0; i < 4; ++i) {
+          const int32_t key = i * 32 + lane, at = pos + key;
+          if (key >= keys) continue;
+          uint32_t n = ~0u;
+          if (at >= x.low && at < x.key1) {
+            int32_t pg, o;
+            attn_split(p, at, &pg, &o);
+            n = (uint32_t)attn_checked(p, now[i], &sm.error) * p.page_vectors + (uint32_t)o;
+          }
+          sm.vector[key] = n;
         }
+        __syncwarp();
+        const int chunks = heads * 5;
+        for (int i = lane; i < keys * chunks; i += 32) {
+          const int key = i / chunks, c = i - key * chunks, head = c / 5;
+          const uint32_t n = sm.vector[key];
+          const bool ok = n != ~0u;
+          const int64_t off = (ok ? (int64_t)((uint64_t)n * (uint32_t)p.pool.tok_stride) : 0) + (h0 + head) * p.pool.head_stride + (c - head * 5) * kChunk;
+          const uint32_t dst = to + key * p.q4_key_pitch + head * p.q4_head_pitch + (c - head * 5) * kChunk;
+          cp_async_if<kChunk>(dst, p.pool.k + off, ok);
+          cp_async_if<kChunk>(dst + S::kHalf, p.pool.v + off, ok);
+        }
+        // this lane's arrival when its copies are there
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(&sm.full[stage])) : "memory");
+        __syncwarp();  // (before the places are written anew)
       }
-      next();
+      if (++stage == kStages) stage = 0, phase ^= 1;
     }
-    cp_async_commit();
-    if (++stage == S::kStages) stage = 0;
   }
 };
 
@@ -170,9 +238,8 @@ struct Worker {
   static constexpr int G = D / KVX_Q4_GROUP;
   const AttnParams &p;
   S &sm;
-  Loader<D> &load;
-  const int h, lane, warp;
-  int stage = 0;
+  const int h, slot, sub, lane, warp;  // a query head's kv head, its place in the chunk, and the warp's place among its
+  uint32_t stage = 0, phase = 0;
 
   // Eight elements of a query row from d on, as 32-bit numbers.
   __device__ __forceinline__ void eight(const char *row, int d, float (&o)[8]) const {
@@ -197,12 +264,15 @@ struct Worker {
   }
 
   __device__ __forceinline__ void piece(const AttnPiece &x) {
-    const int split = split_of(x.rows), set = warp & ((1 << split) - 1), c4 = lane & 3, r8 = lane >> 2;
-    const Blocks blocks(x);
+    const Share share(p, x);
+    const int set = sub & (share.sets - 1), first_block = sub / share.sets, c4 = lane & 3, r8 = lane >> 2;
     // ---- queries: of row set * 8 + r8, elements 8 c4 .. 8 c4 + 7 of every group, so that a word of codes
     // (eight elements of a key) meets them: pairs (0, 4), (1, 5), (2, 6), (3, 7), the odd ones divided by 16,
     // by which their codes are greater
-    uint32_t q[G][2][2], qs[2];
+    // (kept in shared memory, a group's four words of a lane together, where the warp's sums go in the end)
+    if (share.warps > 1) head_sync(share);  // the sums of the piece before have been read
+    const uint32_t q_at = smem_u32(&sm.sum[warp][0][0]) + lane * 16;
+    uint32_t qs[2];
     float factor = 1.f;
     {
       const int r = set * kRows + r8;
@@ -232,11 +302,9 @@ struct Worker {
         sum += __shfl_xor_sync(~0u, sum, 1);
         sum += __shfl_xor_sync(~0u, sum, 2);
         if (c4 == g) mine = sum;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          q[g][k][0] = pack2<__half>(e[g][2 * k], e[g][2 * k + 4]);
-          q[g][k][1] = pack2<__half>(e[g][2 * k + 1] * 0.0625f, e[g][2 * k + 5] * 0.0625f);
-        }
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(q_at + g * 512), "r"(pack2<__half>(e[g][0], e[g][4])),
+                     "r"(pack2<__half>(e[g][1] * 0.0625f, e[g][5] * 0.0625f)), "r"(pack2<__half>(e[g][2], e[g][6])),
+                     "r"(pack2<__half>(e[g][3] * 0.0625f, e[g][7] * 0.0625f)) : "memory");
       }
       mine *= 0.03125f;  // of at most 32 numbers up to 2^15: back into f16's range
       const __half hi = __float2half_rn(mine);
@@ -244,7 +312,8 @@ struct Worker {
       qs[1] = (uint32_t)__half_as_ushort(__float2half_rn(mine - __half2float(hi))) << 16;
     }
     // ---- of this lane's rows, set * 8 + 2 c4 and the one behind
-    float sc[2], base[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    // (a base below any score: nothing seen yet)
+    float sc[2], base[2] = {-3.40282347e38f, -3.40282347e38f}, l[2] = {0.f, 0.f};
     int lim[2];
     const int first = max(x.key0, x.low);
     int least = INT32_MAX;
@@ -260,62 +329,68 @@ struct Worker {
     float o[G][2][4] = {}, z[4] = {};  // z: of the unit of (scale, low) words that is r8's
     float top = kTop;
     int odd = 0;
-    const float limit0 = r8 & 1 ? INFINITY : 1.f;  // of values' scales: at first 1
-    float limit = limit0;
+    // the values' scales may be up to this (units of lows: anything)
+    __half2 limit = __half2half2(__ushort_as_half(r8 & 1 ? 0x7c00 : 0x3c00));
+    const uint32_t kp = p.q4_key_pitch, mine = slot * p.q4_head_pitch;
+    const uint32_t row16 = mine + (lane & 15) * kp, row8 = mine + r8 * kp, col4 = mine + 2 * c4 * kp;
 
 #pragma unroll 1
-    for (int b = warp >> split; b < blocks.count; b += kWarps >> split) {
-      cp_async_wait<S::kStages - 2>();
+    for (int j = 0; j < share.stages; ++j) {
+      bar_wait(&sm.full[stage], phase, &sm.lost, &sm.error);  // (given up: what follows is of no account)
       __syncwarp();
-      load.send();
-      const uint32_t kt = smem_u32(sm.ring[warp][stage]), vt = kt + kBlock * S::kPitch;
-      if (++stage == S::kStages) stage = 0;
-      const int pos = blocks.start + b * kBlock;
+      const uint32_t ring = smem_u32(sm.ring[stage][0]);
+#pragma unroll 1
+      for (int b = first_block; b < share.warps; b += share.keys) {
+      const int pos = share.start + (j * share.warps + b) * kBlock;
+      if (pos >= x.key1) break;
+      const uint32_t kt = ring + b * kBlock * kp, vt = kt + S::kHalf;
       const bool mixed = pos + kBlock > least || pos < x.low || pos + kBlock > x.key1;
-      const uint32_t row16 = (uint32_t)((lane & 15) * S::kPitch);  // (addresses of ldmatrix: 16 keys, two chunks)
       // ---- scores of keys r8 and r8 + 8
-      float s[4] = {};
+      float s[4];
+      uint32_t ks[2][G];  // (scale, low) of the two keys
+#pragma unroll
+      for (int i = 0; i < 2; ++i) load_shared(ks[i], kt + row8 + 8 * i * kp + D / 2);
       {
         float a[4] = {};
         uint32_t w[2];
-        ldmatrix2(w, kt + row16 + D / 2);
+        if constexpr (G == 4) {
+          ldmatrix2(w, kt + row16 + D / 2);
+        } else {
+          w[0] = c4 == 0 ? ks[0][0] : c4 == 1 ? ks[0][1] : 0, w[1] = c4 == 0 ? ks[1][0] : c4 == 1 ? ks[1][1] : 0;
+        }
         const uint32_t f[4] = {w[0], w[1], w[0], w[1]};
         mma16816<__half>(a, f, qs[0], qs[1]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[i] = a[i] * 0x1p-19f;
-      }
-      uint32_t ks[2][G];  // (scale, low) of the two keys
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const char *at = sm.ring[warp][0] + (kt - smem_u32(sm.ring[warp][0])) + (r8 + 8 * i) * S::kPitch + D / 2;
-        if constexpr (G == 4) {
-          const uint4 v = *reinterpret_cast<const uint4 *>(at);
-          ks[i][0] = v.x, ks[i][1] = v.y, ks[i][2] = v.z, ks[i][3] = v.w;
-        } else {
-          const uint2 v = *reinterpret_cast<const uint2 *>(at);
-          ks[i][0] = v.x, ks[i][1] = v.y;
-        }
+        unpair(mul2(pair(a[0], a[1]), pair(0x1p-19f, 0x1p-19f)), s[0], s[1]);
+        unpair(mul2(pair(a[2], a[3]), pair(0x1p-19f, 0x1p-19f)), s[2], s[3]);
       }
 #pragma unroll
       for (int g = 0; g < G; g += 2) {
         uint32_t w[4];
-        ldmatrix4(w, kt + row16 + (g + (lane >> 4)) * 16);
+        if constexpr (G == 4) {
+          ldmatrix4(w, kt + row16 + (g + (lane >> 4)) * 16);
+        } else {  // (head vectors of 40 bytes: an odd one is off 16 bytes)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = load_shared(kt + row8 + 8 * (i & 1) * kp + (i >> 1) * 16 + c4 * 4);
+        }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const uint32_t u = w[2 * e], v = w[2 * e + 1];
           float a[4] = {};
+          uint32_t q[4];
+          load_shared(q, q_at + (g + e) * 512);
           const uint32_t f0[4] = {u & 0x000f000fu, v & 0x000f000fu, u & 0x00f000f0u, v & 0x00f000f0u};
-          mma16816<__half>(a, f0, q[g + e][0][0], q[g + e][0][1]);
+          mma16816<__half>(a, f0, q[0], q[1]);
           const uint32_t u8 = u >> 8, v8 = v >> 8;
           const uint32_t f1[4] = {u8 & 0x000f000fu, v8 & 0x000f000fu, u8 & 0x00f000f0u, v8 & 0x00f000f0u};
-          mma16816<__half>(a, f1, q[g + e][1][0], q[g + e][1][1]);
+          mma16816<__half>(a, f1, q[2], q[3]);
           const float s0 = low_half(ks[0][g + e]), s1 = low_half(ks[1][g + e]);
           s[0] = fmaf(a[0], s0, s[0]), s[1] = fmaf(a[1], s0, s[1]);
           s[2] = fmaf(a[2], s1, s[2]), s[3] = fmaf(a[3], s1, s[3]);
         }
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[i] = s[i] * 0x1p24f * sc[i & 1];
+      const uint64_t up24 = pair(0x1p24f, 0x1p24f), sc2 = pair(sc[0], sc[1]);
+      unpair(mul2(mul2(pair(s[0], s[1]), up24), sc2), s[0], s[1]);
+      unpair(mul2(mul2(pair(s[2], s[3]), up24), sc2), s[2], s[3]);
       if (mixed) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -323,9 +398,14 @@ struct Worker {
           if (key < x.low || key >= lim[i & 1]) s[i] = -INFINITY;
         }
       }
-      // ---- the values' (scale, low) words, a unit a lane's row; what weights refer to
+      // ---- the values' (scale, low) words, a unit a lane's row
       uint32_t zw[2];
-      ldmatrix2t(zw, vt + row16 + D / 2);
+      if constexpr (G == 4) {
+        ldmatrix2t(zw, vt + row16 + D / 2);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) zw[i] = transpose8(c4 < 2 ? load_shared(vt + row8 + 8 * i * kp + D / 2 + c4 * 4) : 0);
+      }
       if (mixed) {
         // (infinities and NaN of keys that some row does not see are taken out and put back at the end)
 #pragma unroll
@@ -334,43 +414,39 @@ struct Worker {
           if (odd_word(zw[i] & 0xffff0000u)) zw[i] &= 0xffffu, odd = 1;
         }
       }
-      {
-        const float t0 = fmaxf(s[0], s[2]), t1 = fmaxf(s[1], s[3]);
-        const __half2 zm = __hmax2(*reinterpret_cast<const __half2 *>(&zw[0]), *reinterpret_cast<const __half2 *>(&zw[1]));
-        const float big = fmaxf(__low2float(zm), __high2float(zm));
-        const float edge = top + kRenew;
-        // (a row that has seen nothing yet has a base of -infinity, and any score passes it)
-        if (__any_sync(~0u, t0 - base[0] > edge || t1 - base[1] > edge || big > limit)) {
-          float n0 = t0, n1 = t1, up = limit0 < INFINITY ? big : 0.f;
+      // ---- weights; what they refer to is renewed where a score passes it by far, or a scale the limit
+      float e[4] = {s[0] - base[0], s[1] - base[1], s[2] - base[0], s[3] - base[1]};
+      const __half2 zm = __hmax2(*reinterpret_cast<const __half2 *>(&zw[0]), *reinterpret_cast<const __half2 *>(&zw[1]));
+      if (__any_sync(~0u, fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3])) > top + kRenew || !__hble2(zm, limit))) {
+        float n0 = fmaxf(s[0], s[2]), n1 = fmaxf(s[1], s[3]), up = r8 & 1 ? 0.f : fmaxf(__low2float(zm), __high2float(zm));
 #pragma unroll
-          for (int d = 4; d < 32; d <<= 1) {
-            n0 = fmaxf(n0, __shfl_xor_sync(~0u, n0, d));
-            n1 = fmaxf(n1, __shfl_xor_sync(~0u, n1, d));
-          }
-#pragma unroll
-          for (int d = 1; d < 32; d <<= 1) up = fmaxf(up, __shfl_xor_sync(~0u, up, d));
-          float now = top;
-          if (up > 1.f) now = fminf(top, kTop - (float)(ilogbf(fminf(up, 65504.f)) + 1));
-          limit = limit0 < INFINITY ? exp2f(kTop - now) : INFINITY;
-          // the greatest score so far, or what stood for it
-          const float m0 = fmaxf(base[0] + top, n0), m1 = fmaxf(base[1] + top, n1);
-          const float b0 = m0 - now, b1 = m1 - now;
-          const float f0 = base[0] == -INFINITY ? 0.f : ex2(base[0] - b0), f1 = base[1] == -INFINITY ? 0.f : ex2(base[1] - b1);
-          l[0] *= f0, l[1] *= f1;
-#pragma unroll
-          for (int g = 0; g < G; ++g)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) o[g][k][0] *= f0, o[g][k][1] *= f1, o[g][k][2] *= f0, o[g][k][3] *= f1;
-          z[0] *= f0, z[1] *= f1;
-          base[0] = b0, base[1] = b1, top = now;
+        for (int d = 4; d < 32; d <<= 1) {
+          n0 = fmaxf(n0, __shfl_xor_sync(~0u, n0, d));
+          n1 = fmaxf(n1, __shfl_xor_sync(~0u, n1, d));
         }
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) up = fmaxf(up, __shfl_xor_sync(~0u, up, d));
+        float now = top;
+        if (up > 1.f) now = fminf(top, kTop - (float)(ilogbf(fminf(up, 65504.f)) + 1));
+        if (!(r8 & 1)) limit = __half2half2(__float2half_rn(fminf(exp2f(kTop - now), 65504.f)));
+        // the greatest score so far, or what stood for it
+        const float b0 = fmaxf(base[0] + top, n0) - now, b1 = fmaxf(base[1] + top, n1) - now;
+        const float f0 = ex2(base[0] - b0), f1 = ex2(base[1] - b1);
+        l[0] *= f0, l[1] *= f1;
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) o[g][k][0] *= f0, o[g][k][1] *= f1, o[g][k][2] *= f0, o[g][k][3] *= f1;
+        z[0] *= f0, z[1] *= f1;
+        base[0] = b0, base[1] = b1, top = now;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e[i] = s[i] - base[i & 1];
       }
-      // ---- weights, their rows and keys exchanged: row r8, keys 2 c4, 2 c4 + 1 and 8 behind
-      const float from0 = base[0] == -INFINITY ? 0.f : base[0], from1 = base[1] == -INFINITY ? 0.f : base[1];
-      s[0] = ex2(s[0] - from0), s[1] = ex2(s[1] - from1), s[2] = ex2(s[2] - from0), s[3] = ex2(s[3] - from1);
-      l[0] += s[0] + s[2], l[1] += s[1] + s[3];
-      // rounded to f16 for the products; their sum is not
-      const uint32_t p0 = transpose8(pack2<__half>(s[0], s[1])), p1 = transpose8(pack2<__half>(s[2], s[3]));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) e[i] = ex2(e[i]);
+      l[0] += e[0] + e[2], l[1] += e[1] + e[3];
+      // rounded to f16 for the products (their sum is not), rows and keys exchanged: row r8, keys 2 c4, 2 c4 + 1 and 8 behind
+      const uint32_t p0 = transpose8(pack2<__half>(e[0], e[1])), p1 = transpose8(pack2<__half>(e[2], e[3]));
       {
         const uint32_t f[4] = {zw[0], 0, zw[1], 0};
         mma16816<__half>(z, f, p0, p1);
@@ -378,14 +454,7 @@ struct Worker {
       uint32_t vs[4][G];  // (scale, low) of keys 2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const char *at = sm.ring[warp][0] + (vt - smem_u32(sm.ring[warp][0])) + (2 * c4 + (i & 1) + 8 * (i >> 1)) * S::kPitch + D / 2;
-        if constexpr (G == 4) {
-          const uint4 v = *reinterpret_cast<const uint4 *>(at);
-          vs[i][0] = v.x, vs[i][1] = v.y, vs[i][2] = v.z, vs[i][3] = v.w;
-        } else {
-          const uint2 v = *reinterpret_cast<const uint2 *>(at);
-          vs[i][0] = v.x, vs[i][1] = v.y;
-        }
+        load_shared(vs[i], vt + col4 + ((i & 1) + 8 * (i >> 1)) * kp + D / 2);
         if (mixed)
 #pragma unroll
           for (int g = 0; g < G; ++g)
@@ -394,18 +463,27 @@ struct Worker {
 #pragma unroll
       for (int g = 0; g < G; g += 2) {
         uint32_t w[4];
-        ldmatrix4t(w, vt + row16 + (g + (lane >> 4)) * 16);
+        if constexpr (G == 4) {
+          ldmatrix4t(w, vt + row16 + (g + (lane >> 4)) * 16);
+        } else {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint32_t b0 = mul_half2(p0, __byte_perm(vs[0][g + e], vs[1][g + e], 0x5410));
-          const uint32_t b1 = mul_half2(p1, __byte_perm(vs[2][g + e], vs[3][g + e], 0x5410));
-          const uint32_t u = w[2 * e], v = w[2 * e + 1], u8 = u >> 8, v8 = v >> 8;
+          for (int i = 0; i < 4; ++i) w[i] = transpose8(load_shared(vt + row8 + 8 * (i & 1) * kp + (i >> 1) * 16 + c4 * 4));
+        }
+#pragma unroll
+        for (int e2 = 0; e2 < 2; ++e2) {
+          const uint32_t b0 = mul_half2(p0, __byte_perm(vs[0][g + e2], vs[1][g + e2], 0x5410));
+          const uint32_t b1 = mul_half2(p1, __byte_perm(vs[2][g + e2], vs[3][g + e2], 0x5410));
+          const uint32_t u = w[2 * e2], v = w[2 * e2 + 1], u8 = u >> 8, v8 = v >> 8;
           const uint32_t f0[4] = {u & 0x000f000fu, u8 & 0x000f000fu, v & 0x000f000fu, v8 & 0x000f000fu};
-          mma16816<__half>(o[g + e][0], f0, b0, b1);
+          mma16816<__half>(o[g + e2][0], f0, b0, b1);
           const uint32_t f1[4] = {u & 0x00f000f0u, u8 & 0x00f000f0u, v & 0x00f000f0u, v8 & 0x00f000f0u};
-          mma16816<__half>(o[g + e][1], f1, b0, b1);
+          mma16816<__half>(o[g + e2][1], f1, b0, b1);
         }
       }
+      }
+      __syncwarp();
+      if (lane == 0) bar_arrive(&sm.empty[stage]);
+      if (++stage == kStages) stage = 0, phase ^= 1;
     }
     // ---- the warp's sums: columns 32 g + 4 r8 .. + 3 of its two rows
 #pragma unroll
@@ -414,11 +492,11 @@ struct Worker {
       l[1] += __shfl_xor_sync(~0u, l[1], d);
     }
     odd = __any_sync(~0u, odd);
-    __syncthreads();  // the sums of the piece before have been read
+    const int64_t part = x.part + h * x.head_step;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const bool none = lim[i] <= first || l[i] == 0.f;  // (a row that sees nothing of the piece has worked on all)
-      const int r = 2 * c4 + i;
+      const int in = 2 * c4 + i, r = set * kRows + in;
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         const float low = __shfl_sync(~0u, z[i], (2 * g + 1) * 4 + c4);
@@ -426,21 +504,32 @@ struct Worker {
                       fmaf(o[g][0][2 + i], 0x1p24f, low), fmaf(o[g][1][2 + i], 0x1p20f, low)};
 #pragma unroll
         for (int k = 0; k < 4; ++k) v[k] = none ? 0.f : v[k];
-        if (odd && !none) put_back(x, g, lim[i], least, v);
-        *reinterpret_cast<float4 *>(&sm.sum[warp][r][g * KVX_Q4_GROUP + 4 * r8]) = make_float4(v[0], v[1], v[2], v[3]);
+        const float4 out = make_float4(v[0], v[1], v[2], v[3]);
+        const int d = g * KVX_Q4_GROUP + 4 * r8;
+        if (share.keys > 1) *reinterpret_cast<float4 *>(&sm.sum[warp][in][d]) = out;
+        else if (r < x.rows) *reinterpret_cast<float4 *>(p.part_o + (part + r) * D + d) = out;
       }
-      if (r8 == 0) sm.base[warp][r] = none ? -INFINITY : base[i], sm.l[warp][r] = none ? 0.f : l[i];
+      const float m = none ? -INFINITY : base[i], sum = none ? 0.f : l[i];
+      if (r8 == 0) {
+        if (share.keys > 1) sm.base[warp][in] = m, sm.l[warp][in] = sum;
+        else if (r < x.rows) p.part_m[part + r] = m, p.part_l[part + r] = sum;
+      }
     }
-    __syncthreads();
-    // ---- all warps join the sums of those that shared rows, a float4 of a row at a time
-    const int sets = 1 << split;
-    for (int i = threadIdx.x; i < x.rows * (D / 4); i += kThreads) {
-      const int r = i / (D / 4), c = i % (D / 4), w0 = r >> 3, in = r & 7;
+    if (odd) {
+      __syncwarp();
+      put_back(x, share, part, set, least, lim[0] <= first || l[0] == 0.f ? 0 : lim[0], lim[1] <= first || l[1] == 0.f ? 0 : lim[1]);
+    }
+    if (share.keys == 1) return;
+    head_sync(share);
+    // ---- the head's warps join the sums of those that shared rows, a float4 of a row at a time
+    const int w00 = slot * share.warps;
+    for (int i = sub * 32 + lane; i < x.rows * (D / 4); i += share.warps * 32) {
+      const int r = i / (D / 4), c = i % (D / 4), w0 = w00 + (r >> 3), in = r & 7;
       float m = -INFINITY;
-      for (int w = w0; w < kWarps; w += sets) m = fmaxf(m, sm.base[w][in]);
+      for (int w = w0; w < w00 + share.warps; w += share.sets) m = fmaxf(m, sm.base[w][in]);
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
       float sum = 0.f;
-      for (int w = w0; w < kWarps; w += sets) {
+      for (int w = w0; w < w00 + share.warps; w += share.sets) {
         const float bw = sm.base[w][in];
         if (bw == -INFINITY) continue;
         const float f = ex2(bw - m);
@@ -448,26 +537,40 @@ struct Worker {
         a.x = fmaf(f, v.x, a.x), a.y = fmaf(f, v.y, a.y), a.z = fmaf(f, v.z, a.z), a.w = fmaf(f, v.w, a.w);
         sum = fmaf(f, sm.l[w][in], sum);
       }
-      const int64_t at = x.part + r;
+      const int64_t at = part + r;
       *reinterpret_cast<float4 *>(p.part_o + at * D + c * 4) = a;
       if (c == 0) p.part_m[at] = m, p.part_l[at] = sum;
     }
   }
 
-  // Adds the elements that are not finite of keys that a row sees, from the first block that was looked through.
-  __device__ __noinline__ void put_back(const AttnPiece &x, int g, int lim, int least, float (&v)[4]) const {
-    const int first = max(x.key0, x.low), c0 = g * KVX_Q4_GROUP + 4 * (lane >> 2);
-    const int split = split_of(x.rows), start = first / kBlock * kBlock;
-    for (int key = first; key < lim; ++key) {
-      const int b = (key - start) / kBlock, pos = start + b * kBlock;
-      if (b % (kWarps >> split) != warp >> split) continue;  // another warp's
-      if (!(pos + kBlock > least || pos < x.low || pos + kBlock > x.key1)) continue;
-      const char *at = p.pool.v + attn_key_offset(p, x.table, key, &sm.error) + h * p.pool.head_stride;
-      const uint32_t pair = reinterpret_cast<const uint32_t *>(at)[D / 8 + g];
-      if (!odd_word(pair)) continue;
-      const uint32_t codes = reinterpret_cast<const uint16_t *>(at)[c0 / 4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] += fmaf((float)(codes >> (4 * k) & 15u), low_half(pair), low_half(pair >> 16));
+  // The warps of a head.
+  __device__ __forceinline__ void head_sync(const Share &share) const {
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + slot), "r"(share.warps * 32) : "memory");
+  }
+
+  // Adds the elements that are not finite of keys that a row sees, of the blocks that were looked through, to the sums
+  // as they have been written.
+  __device__ __forceinline__ void put_back(const AttnPiece &x, const Share &share, int64_t part, int set, int least, int lim0, int lim1) const {
+    const int first = max(x.key0, x.low), c4 = lane & 3, r8 = lane >> 2;
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+      const int in = 2 * c4 + i, lim = i ? lim1 : lim0;
+#pragma unroll 1
+      for (int key = first; key < lim; ++key) {
+        const int b = (key - share.start) / kBlock, pos = share.start + b * kBlock;
+        if (b % share.warps % share.keys != sub / share.sets) continue;  // another warp's
+        if (!(pos + kBlock > least || pos < x.low || pos + kBlock > x.key1)) continue;
+        const char *at = p.pool.v + attn_key_offset(p, x.table, key, &sm.error) + h * p.pool.head_stride;
+#pragma unroll 1
+        for (int g = 0; g < G; ++g) {
+          const uint32_t pair = reinterpret_cast<const uint32_t *>(at)[D / 8 + g];
+          if (!odd_word(pair)) continue;
+          const int d = g * KVX_Q4_GROUP + 4 * r8;
+          const uint32_t codes = reinterpret_cast<const uint16_t *>(at)[d / 4];
+          float *o = share.keys > 1 ? &sm.sum[warp][in][d] : p.part_o + (part + set * kRows + in) * D + d;
+          for (int k = 0; k < 4; ++k) o[k] += fmaf((float)(codes >> (4 * k) & 15u), low_half(pair), low_half(pair >> 16));
+        }
+      }
     }
   }
 };
@@ -478,38 +581,62 @@ __global__ void __launch_bounds__(kThreads, 2) attn_q4_kernel(const __grid_const
   using S = Smem<D>;
   S &sm = *reinterpret_cast<S *>(raw_smem + (-smem_u32(raw_smem) & 127));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) sm.error = 0;
-  // (what lies between the head vectors of a stage is read with them, and has to be finite)
+  const int g = blockIdx.x / p.group_ctas, h0 = (blockIdx.x - g * p.group_ctas) * p.chunk;
+  const int heads = min(p.chunk, p.kv_heads - h0), warps = kWarps >> p.slot_shift;
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i)
+      bar_init(&sm.full[i], p.q4_copies == kAttnQ4Parts ? 32 : 1), bar_init(&sm.empty[i], heads * warps);
+    sm.lost = sm.error = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  // (what no copy has written is read with the rest, and masked by finite numbers)
   for (int i = tid; i < (int)sizeof(sm.ring) / 16; i += kThreads) reinterpret_cast<uint4 *>(sm.ring)[i] = make_uint4(0, 0, 0, 0);
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   if (!p.after_wide) attn_wait_prior();
   else if (tid == 0) attn_wait_announced(p);  // for the others by the barrier below
-  const int g = blockIdx.x / p.kv_heads, h = blockIdx.x - g * p.kv_heads;
   __syncthreads();
   const AttnLine line = attn_line<kThreads>(p, g, sm.scan);
   attn_release_next();  // the join takes its place as CTAs end, and waits for the last
-  Loader<D> load(p, sm, h, lane, warp);
-  Worker<IO, D> work{p, sm, load, h, lane, warp};
-  for (int done = 0;; done += kPieces) {
-    int n = 0;
-    attn_pieces(p, g, h, line, [&](const AttnPiece &x) {
-      if (tid == 0 && n >= done && n < done + kPieces) sm.pieces[n - done] = x;
-      ++n;
+  // Calls f(piece) for the CTA's pieces, listed some at a time; all threads come along.
+  auto all_pieces = [&](auto f) {
+    for (int done = 0;; done += kPieces) {
+      int n = 0;
+      attn_pieces(p, g, 0, line, [&](const AttnPiece &x) {
+        if (tid == 0 && n >= done && n < done + kPieces) sm.pieces[n - done] = x;
+        ++n;
+      });
+      if (tid == 0) sm.n_pieces = max(0, min(n - done, kPieces));
+      __syncthreads();
+      const int count = sm.n_pieces;
+#pragma unroll 1
+      for (int i = 0; i < count; ++i) f(sm.pieces[i]);
+      __syncthreads();
+      if (n <= done + kPieces) break;
+    }
+  };
+  Producer<D> producer{p, sm, h0, heads, lane};
+  if (warp < kWarps) {
+    const int slot = warp / warps;
+    Worker<IO, D> work{p, sm, h0 + slot, slot, warp - slot * warps, lane, warp};
+    all_pieces([&](const AttnPiece &x) {
+      if (slot < heads) work.piece(x);
     });
-    if (tid == 0) sm.n_pieces = min(n - done, kPieces);
-    __syncthreads();
-    load.begin();
-#pragma unroll 1
-    for (int i = 0; i < S::kStages - 1; ++i) load.send();
-#pragma unroll 1
-    for (int i = 0; i < sm.n_pieces; ++i) work.piece(sm.pieces[i]);
-    __syncthreads();
-    if (n <= done + kPieces) break;
-    // what was sent for no block is nothing: the ring begins anew
-    cp_async_wait<0>();
-    load.stage = work.stage = 0;
+  } else {
+    // (no kernel's end lies between the pool's writes and these copies)
+    if (p.after_wide) asm volatile("fence.proxy.async.global;" ::: "memory");
+    all_pieces([&](const AttnPiece &x) {
+      producer.piece(x);
+    });
   }
-  cp_async_wait<0>();
-  if (tid == 0) p.errors[blockIdx.x] = sm.error;
+  if (sm.lost) {
+    if (warp == kWarps) {
+      cp_async_commit();
+      cp_async_wait<0>();
+      bar_drain<kStages>(sm.full, producer.stage, producer.phase);
+    }
+    __syncthreads();
+  }
+  if (tid < heads) p.errors[g * p.kv_heads + h0 + tid] = sm.error;
   if (p.after_wide) attn_wait_prior();  // the join's wait for this kernel covers the wide one as well
 }
 
@@ -521,7 +648,7 @@ cudaError_t launch(const AttnParams &p, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   void *args[] = {const_cast<AttnParams *>(&p)};
-  return launch_pdl(fn, dim3(p.groups * p.kv_heads), dim3(kThreads), args, s, kSmem);
+  return launch_pdl(fn, dim3(p.groups * p.group_ctas), dim3(kThreads), args, s, kSmem);
 }
 
 }  // namespace
