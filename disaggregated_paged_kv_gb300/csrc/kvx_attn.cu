@@ -258,20 +258,23 @@ __device__ __forceinline__ RowPieces narrow_pieces(const AttnParams &p, const At
 // first, in order.  DK: head_dim, 0: any.  Bound: reading the parts (4 D bytes a row and piece), or for few
 // rows the chain of a row's pieces.  Cold, 3100 tokens of 32 heads (prompts) 28 us, 64 tokens of 32 heads
 // 7 us, one token with 38 pieces a row 18 us.
-template <typename IO, int DK>
-__global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid_constant__ AttnParams p, int heads) {
+// W: the warps of a row, each with a stretch of its pieces, whose sums are added up in order; 1 but for few rows of
+// 4-bit pools, whose narrow line has many more groups (one token of 304 pieces a row: KJOIN).
+template <typename IO, int DK, int W>
+__global__ void __launch_bounds__((W > 1 ? W : kJoinWarps) * 32) attn_join_kernel(const __grid_constant__ AttnParams p, int heads) {
+  constexpr int kWarps = W > 1 ? W : kJoinWarps;
   attn_wait_prior();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = blockIdx.x;
   const AttnHeader head = *p.head;
   if (blockIdx.x == 0 && blockIdx.y == 0) {  // the call's verdict
     int32_t e = head.refused;
-    for (int i = threadIdx.x; i < p.n_errors; i += kJoinWarps * 32) e = max(e, p.errors[i]);
+    for (int i = threadIdx.x; i < p.n_errors; i += kWarps * 32) e = max(e, p.errors[i]);
     for (int o = 16; o; o >>= 1) e = max(e, __shfl_xor_sync(~0u, e, o));
-    __shared__ int32_t worst[kJoinWarps];
+    __shared__ int32_t worst[kWarps];
     if (lane == 0) worst[warp] = e;
     __syncthreads();
     if (threadIdx.x == 0) {
-      for (int i = 1; i < kJoinWarps; ++i) e = max(e, worst[i]);
+      for (int i = 1; i < kWarps; ++i) e = max(e, worst[i]);
       *p.status = e;
       if (p.wide_groups > 0) *p.ready = 0;
     }
@@ -293,7 +296,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid
     else wide_row = p.prefix_at[t] * p.group;
   }
   const int qh1 = min(p.q_heads, (int)(blockIdx.y + 1) * heads);
-  for (int qh = blockIdx.y * heads + warp; qh < qh1; qh += kJoinWarps) {
+  for (int qh = blockIdx.y * heads + (W > 1 ? 0 : warp); qh < qh1; qh += W > 1 ? 1 : kJoinWarps) {
     const int h = qh / p.group, member = qh - h * p.group, r = t * p.group + member;
     // the pieces of the row: those of the prefix (or of the prompt), then the request's own
     RowPieces pre = {}, own = {};
@@ -328,8 +331,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid
     float top = -INFINITY, l = 0.f;
     constexpr int kCols = DK ? DK / 32 : KVX_ATTN_MAX_HEAD_DIM / 32;
     float acc[kCols] = {};
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      const int left = min(32, n - i0);
+    const int per = W > 1 ? (n + W - 1) / W : n, begin = W > 1 ? min(warp * per, n) : 0, end = W > 1 ? min(begin + per, n) : n;
+    for (int i0 = begin; i0 < end; i0 += 32) {
+      const int left = min(32, end - i0);
       int64_t at = 0;
       float m = -INFINITY, pl = 0.f;
       if (lane < left) {
@@ -342,7 +346,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid
       for (int o = 16; o; o >>= 1) now = fmaxf(now, __shfl_xor_sync(~0u, now, o));
       now = fmaxf(now, top);
       const float base = now == -INFINITY ? 0.f : now;
-      if (i0 > 0) {  // more than 32 parts: what the first ones gave refers to the greatest so far
+      if (i0 > begin) {  // more than 32 parts: what the first ones gave refers to the greatest so far
         const float f = top == -INFINITY ? 0.f : exp2f(top - base);
         l *= f;
 #pragma unroll
@@ -371,6 +375,28 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
+    if constexpr (W > 1) {
+      __shared__ float s_acc[W][kCols * 32], s_top[W], s_l[W];
+      __syncthreads();  // (the head before has been added up)
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) s_acc[warp][c * 32 + lane] = acc[c];
+      if (lane == 0) s_top[warp] = top, s_l[warp] = l;
+      __syncthreads();
+      if (warp != 0) continue;
+      top = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) top = fmaxf(top, s_top[w]);
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) acc[c] = 0.f;
+      const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const float f = exp2f(s_top[w] - base);
+        l = fmaf(f, s_l[w], l);
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) acc[c] = fmaf(f, s_acc[w][c * 32 + lane], acc[c]);
+      }
+    }
     const float inv = l == 0.f ? 0.f : p.v_scale / l;
     IO *out = reinterpret_cast<IO *>(p.out + t * p.out_tok + qh * p.out_head);
 #pragma unroll
@@ -384,11 +410,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const __grid
   }
 }
 
+constexpr int kDeepWarps = 16;
+
 template <typename IO>
-const void *join_kernel(int D) {
-  return D == 64    ? (const void *)attn_join_kernel<IO, 64>
-         : D == 128 ? (const void *)attn_join_kernel<IO, 128>
-                    : (const void *)attn_join_kernel<IO, 0>;
+const void *join_kernel(int D, bool deep) {
+  if (deep) return D == 64 ? (const void *)attn_join_kernel<IO, 64, kDeepWarps> : (const void *)attn_join_kernel<IO, 128, kDeepWarps>;
+  return D == 64    ? (const void *)attn_join_kernel<IO, 64, 1>
+         : D == 128 ? (const void *)attn_join_kernel<IO, 128, 1>
+                    : (const void *)attn_join_kernel<IO, 0, 1>;
 }
 
 using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
@@ -441,6 +470,29 @@ void attn_make_tma(const AttnParams &p, int keys, bool fp8, bool hnd, AttnTma *t
   t->head_y = hnd ? p.page_size : 0;
 }
 
+bool attn_q4_maps(const AttnParams &p, CUtensorMap *km, CUtensorMap *vm) {
+  const cuuint64_t S = p.head_bytes, ps = p.page_size, pages = p.pool.num_pages, H = p.kv_heads;
+  if (!encoder()) return false;
+  cuuint64_t dims[3], strides[2];
+  cuuint32_t box[3];
+  const cuuint32_t one[3] = {1, 1, 1};
+  if (p.q4_runs) {
+    dims[0] = ps * S / 8, dims[1] = pages * H, dims[2] = 1;
+    strides[0] = ps * S, strides[1] = ps * S * pages * H;
+    box[0] = (cuuint32_t)(16 * S / 8), box[1] = p.chunk, box[2] = 1;
+  } else {
+    dims[0] = (S << p.q4_pair) / 8, dims[1] = pages * ps, dims[2] = H >> p.q4_pair;
+    strides[0] = p.pool.tok_stride, strides[1] = S << p.q4_pair;
+    box[0] = (cuuint32_t)dims[0], box[1] = 16, box[2] = p.chunk >> p.q4_pair;
+  }
+  for (int kv = 0; kv < 2; ++kv)
+    if (encoder()(kv ? vm : km, CU_TENSOR_MAP_DATA_TYPE_UINT64, 3, const_cast<char *>(kv ? p.pool.v : p.pool.k), dims, strides,
+                  box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return false;
+  return true;
+}
+
 namespace {
 
 // Calls with one query token a request do without the plan kernel up to this many requests.
@@ -473,36 +525,41 @@ bool tensor_cores(const kvx_layout *l) {
   return l->elem <= 2 && (l->head_dim == 64 || l->head_dim == 128) && l->vec == 16;
 }
 
-// kv heads of a CTA of the 4-bit kernel: up to eight, an even number where that makes whole 16-byte pieces.
-int q4_chunk(const kvx_layout *l) {
-  const int chunks = (l->kv_heads + kAttnQ4Warps - 1) / kAttnQ4Warps;
-  const int c = (l->kv_heads + chunks - 1) / chunks;
-  return l->head_dim == 64 && c % 2 != 0 && c > 1 ? c + 1 : c;
-}
-int q4_slot_shift(const kvx_layout *l) {
-  int s = 0;
-  while (1 << s < q4_chunk(l)) ++s;
-  return s;
-}
-
 bool q4_kernel(const kvx_layout *l) { return l->dtype == KVX_Q4 && tensor_cores(l); }
 
-int row_tile_of(const kvx_layout *l) {
-  if (q4_kernel(l)) return 8 * (kAttnQ4Warps >> q4_slot_shift(l));
+// kv heads of a CTA: 1, but up to `most` (of eight) in the 4-bit kernel, as evenly as it goes, and pairs where a head
+// vector is no whole number of 16-byte pieces.
+int chunk_of(const kvx_layout *l, int most) {
+  if (!q4_kernel(l)) return 1;
+  const int chunks = (l->kv_heads + most - 1) / most, c = (l->kv_heads + chunks - 1) / chunks;
+  return l->head_dim == 64 && c % 2 != 0 && l->kv_heads > 1 ? c + 1 : c;
+}
+int slot_shift_of(int chunk) {
+  int s = 0;
+  while (1 << s < chunk) ++s;
+  return s;
+}
+int row_tile_of(const kvx_layout *l, int chunk) {
+  if (q4_kernel(l)) return 8 * (kAttnQ4Warps >> slot_shift_of(chunk));
   return tensor_cores(l) ? kAttnNarrowRows : kAttnGeneralRows;
 }
+int group_ctas_of(const kvx_layout *l, int chunk) { return (l->kv_heads + chunk - 1) / chunk; }
 
-int group_ctas(const kvx_layout *l) {
-  return q4_kernel(l) ? (l->kv_heads + q4_chunk(l) - 1) / q4_chunk(l) : l->kv_heads;
+// How many heads of a CTA suit calls of n_q tokens of n_reqs requests: eight warps have eight rows each, and a unit of
+// more rows than they have for its heads reads the keys again.
+int q4_most_heads(int64_t n_q, int64_t n_reqs, int64_t group) {
+  int most = kAttnQ4Warps;
+  while (most > 1 && n_q * group > 8 * (kAttnQ4Warps / most) * n_reqs) most /= 2;
+  return most;
 }
 
 // How many groups of CTAs: as many as are resident at once.
-Sizes sizes(const kvx_layout *l, int64_t n_q, int64_t n_reqs, int64_t q_heads, bool wide) {
+Sizes sizes(const kvx_layout *l, int64_t n_q, int64_t n_reqs, int64_t q_heads, bool wide, int chunk) {
   Sizes z = {};
-  const int64_t kv_heads = l->kv_heads, D = l->head_dim, row_tile = row_tile_of(l);
+  const int64_t kv_heads = l->kv_heads, D = l->head_dim, row_tile = row_tile_of(l, chunk);
   const int64_t rows = n_q * (q_heads / kv_heads);
   const int64_t per_sm = !tensor_cores(l) && D <= 128 ? 3 : 2;
-  z.groups = (int32_t)std::max((int64_t)1, kAttnSms * per_sm / group_ctas(l));
+  z.groups = (int32_t)std::max((int64_t)1, kAttnSms * per_sm / group_ctas_of(l, chunk));
   z.wide_groups = wide ? (int32_t)std::max((int64_t)1, kAttnSms / kv_heads) : 0;
   z.errors = z.groups * kv_heads + z.wide_groups * kv_heads;
   const int64_t parts = 2 * n_q * q_heads + z.groups * kv_heads * row_tile +
@@ -565,7 +622,11 @@ static_assert(sizeof(kvx_attn_args) == 152, "the binding mirrors this structure"
 extern "C" size_t kvx_attention_workspace_size(kvx_layout_t pool, int32_t n_q, int32_t n_reqs,
                                                int32_t q_heads, int32_t prefix_len) {
   if (!kvx::shape_ok(pool, n_q, n_reqs, q_heads, prefix_len)) return 0;
-  return (size_t)kvx::sizes(pool, n_q, n_reqs, q_heads, kvx::takes_wide(pool, n_q, q_heads)).total;
+  // (whatever number of heads a CTA has: fewer tokens or requests may take another)
+  int64_t most = 0;
+  for (int heads = kvx::kAttnQ4Warps; heads >= 1; heads /= 2)
+    most = std::max(most, kvx::sizes(pool, n_q, n_reqs, q_heads, kvx::takes_wide(pool, n_q, q_heads), kvx::chunk_of(pool, heads)).total);
+  return (size_t)most;
 }
 
 extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_args *args,
@@ -620,7 +681,8 @@ extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_arg
   const bool wide = takes_wide(pool, a.n_q, a.q_heads) &&
                     4.0 * pool->head_dim * a.q_heads * a.n_q * wide_keys >= (beside ? kWideBeside : kWideWork) &&
                     a.scale * a.k_scale > 0.f;
-  const Sizes z = sizes(pool, a.n_q, a.n_reqs, a.q_heads, wide);
+  const int chunk = chunk_of(pool, q4_most_heads(a.n_q, a.n_reqs, a.q_heads / pool->kv_heads));
+  const Sizes z = sizes(pool, a.n_q, a.n_reqs, a.q_heads, wide, chunk);
   if (!d_ws || !mult(d_ws, 256) || (int64_t)ws_bytes < z.total) return KVX_ERR_NO_WORKSPACE;
 
   AttnParams p;
@@ -660,28 +722,39 @@ extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_arg
   p.page_size = a.page_size;
   p.max_pages = a.max_pages;
   p.prefix_len = a.prefix_len;
-  p.row_tile = row_tile_of(pool);
+  p.row_tile = row_tile_of(pool, chunk);
   const bool q4 = q4_kernel(pool);
   p.few_rows = q4 ? 8 : 16;
   p.key_shift = q4 ? 5 : 6;
   static_assert(1 << 5 == kAttnQ4KeyTile && 1 << 6 == kAttnKeyTile, "tiles of these kernels");
-  p.group_ctas = group_ctas(pool);
-  p.chunk = q4 ? q4_chunk(pool) : 1;
+  p.group_ctas = group_ctas_of(pool, chunk);
+  p.chunk = chunk;
   p.tile_ns = (int32_t)std::max(kAttnNarrowNs, ((pool->seg_bytes * p.chunk) << p.key_shift) * 2 / 16 * kAttnNarrowPs / 1000);
   if (q4) {
-    p.slot_shift = q4_slot_shift(pool);
+    p.slot_shift = slot_shift_of(chunk);
     p.page_vectors = (uint32_t)(hnd ? (int64_t)a.page_size * pool->kv_heads : a.page_size);
-    // 16 tokens of a head lie side by side in head-major pages, or where there is one head
-    const bool even = ((uintptr_t)p.pool.k | (uintptr_t)p.pool.v) % 16 == 0;
-    const bool dense = hnd || (pool->kv_heads == 1 && pool->slot_stride == seg);
-    const int32_t keys = 16 * (kAttnQ4Warps >> p.slot_shift);  // of a stage
-    p.q4_copies = dense && even && a.page_size % 16 == 0                    ? kAttnQ4Runs
-                  : !hnd && pool->vec == 16 && p.chunk * seg % 16 == 0      ? kAttnQ4Tokens
-                                                                            : kAttnQ4Parts;
-    p.q4_key_pitch = (int32_t)seg, p.q4_head_pitch = (int32_t)seg * keys;
-    if (p.q4_copies == kAttnQ4Tokens) {
-      // an odd number of 16-byte pieces a key: eight keys' lie in different banks
-      p.q4_key_pitch = (int32_t)(p.chunk * seg) | 16, p.q4_head_pitch = (int32_t)seg;
+    const int32_t keys = 16 * (kAttnQ4Warps >> p.slot_shift), S = (int32_t)seg;  // of a stage; of a head vector
+    const bool even = ((uintptr_t)p.pool.k | (uintptr_t)p.pool.v) % 16 == 0 && a.page_size % 16 == 0;
+    p.q4_runs = hnd || (pool->kv_heads == 1 && pool->slot_stride == S);
+    p.q4_pair = !p.q4_runs && S % 16 != 0;  // (40 bytes are no whole pieces of 16, two heads' are)
+    const bool boxes = even && (p.q4_runs ? p.pool.num_pages * pool->kv_heads <= INT32_MAX
+                                          : pool->slot_stride % 16 == 0 && (!p.q4_pair || (pool->kv_heads | p.chunk) % 2 == 0));
+    const bool tokens = !hnd && pool->vec == 16 && p.chunk * S % 16 == 0;
+    p.q4_copies = boxes ? kAttnQ4Boxes : tokens ? kAttnQ4Tokens : kAttnQ4Parts;
+    if (boxes) {
+      p.q4_key_pitch = S << p.q4_pair, p.q4_head_pitch = 16 * S << p.q4_pair;
+      p.q4_block_pitch = 16 * S * p.chunk, p.q4_v_off = 16 * S * kAttnQ4Warps;
+    } else if (tokens) {
+      // an odd number of 16-byte pieces a token: eight tokens' lie in different banks
+      const bool together = p.group_ctas == 1 && p.pool.v - p.pool.k == pool->row_bytes;
+      p.q4_pair = 0;
+      p.q4_head_pitch = S;
+      p.q4_key_pitch = (p.chunk * S * (together ? 2 : 1)) | 16;
+      p.q4_v_off = together ? p.chunk * S : keys * p.q4_key_pitch;
+      p.q4_block_pitch = 16 * p.q4_key_pitch;
+    } else {
+      p.q4_pair = 0;
+      p.q4_key_pitch = S, p.q4_head_pitch = S * keys, p.q4_block_pitch = 16 * S, p.q4_v_off = 128 * S;
     }
   }
   p.unit_cost = tensor_cores(pool) ? kNarrowUnitCost : 0;
@@ -729,16 +802,19 @@ extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_arg
                              : launch_attn_general(p, pool->dtype, a.q_dtype, pool->vec == 16 && pool->seg_bytes % 16 == 0, s);
   }
   if (e == cudaSuccess) {
-    const void *join = a.q_dtype == KVX_F32   ? join_kernel<float>(pool->head_dim)
-                       : a.q_dtype == KVX_F16 ? join_kernel<__half>(pool->head_dim)
-                                              : join_kernel<__nv_bfloat16>(pool->head_dim);
+    // all warps that an SM has for a row, while there is a row or two an SM
+    const bool deep = q4 && (int64_t)a.n_q * a.q_heads <= 2 * kAttnSms;
+    const void *join = a.q_dtype == KVX_F32   ? join_kernel<float>(pool->head_dim, false)
+                       : a.q_dtype == KVX_F16 ? join_kernel<__half>(pool->head_dim, deep)
+                                              : join_kernel<__nv_bfloat16>(pool->head_dim, deep);
     // a warp a row while that fills the GPU; then a block a token, which reads what is the token's once
     int heads = kJoinWarps;
     if ((int64_t)a.n_q * a.q_heads > (int64_t)kJoinWarps * kAttnSms * 16 || a.q_heads > kJoinWarps * 65535)
       heads = a.q_heads;
+    if (deep) heads = 1;
     void *jargs[] = {&p, &heads};
     e = launch_pdl(join, dim3((unsigned)std::max(1, a.n_q), (unsigned)((a.q_heads + heads - 1) / heads)),
-                   dim3(kJoinWarps * 32), jargs, s);
+                   dim3((deep ? kDeepWarps : kJoinWarps) * 32), jargs, s);
   }
   if (e != cudaSuccess) {
     record_cuda_error(e);

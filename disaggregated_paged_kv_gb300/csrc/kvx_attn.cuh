@@ -41,8 +41,9 @@ constexpr int kAttnWideRows = 256;     // rows of its units
 
 constexpr int kAttnWritten = -2;
 
-// How the 4-bit kernel's head vectors come: 16 tokens of a head at a time, a token's heads, or fifths of a head vector.
-enum AttnQ4Copies : int32_t { kAttnQ4Runs = 0, kAttnQ4Tokens = 1, kAttnQ4Parts = 2 };
+// How the 4-bit kernel's head vectors come: 16 tokens of a chunk's heads at a time by tensor copies, a token's heads, or
+// fifths of a head vector.
+enum AttnQ4Copies : int32_t { kAttnQ4Boxes = 0, kAttnQ4Tokens = 1, kAttnQ4Parts = 2 };
 
 // Where a layer's rows are: element row (page id, offset in page, kv head) starts at
 // plane + id * page_stride + offset * tok_stride + head * head_stride (bytes), in either kind of
@@ -104,8 +105,11 @@ struct AttnParams {
   int32_t key_shift;     // log2 of a narrow tile's keys
   int32_t tile_ns;       // what a narrow tile of cost 1 takes a CTA (see attn_share)
   int32_t group_ctas;    // of a narrow group: one a kv head, or one a chunk of them
-  // the 4-bit kernel: kv heads of a CTA, log2 of the places for them, how they come, and where a stage has them
-  int32_t chunk, slot_shift, q4_copies, q4_key_pitch, q4_head_pitch;
+  // the 4-bit kernel: kv heads of a CTA, log2 of the places for them, how they come, and where a stage has them:
+  // key (of 16) k of place s (q4_pair 1: two neighbours lie together) in block b at b * block_pitch +
+  // (s >> pair) * head_pitch + (s & pair) * bytes + k * key_pitch, values at v_off behind.
+  int32_t chunk, slot_shift, q4_copies, q4_key_pitch, q4_head_pitch, q4_block_pitch, q4_v_off, q4_pair;
+  int32_t q4_runs;       // boxes of a head-major pool, whose tokens of a page and head lie side by side
   uint32_t page_vectors; // head vectors of a page, in strides of a token (fewer than 2^32 in all)
   int32_t unit_cost;     // what a unit's begin and end cost, in tiles of up to 16 rows
   int32_t groups;        // groups of group_ctas CTAs, narrow line

@@ -13,11 +13,12 @@
 // Keys are the rows of both products (m16n8k16, M = 16 keys, N = 8 query rows; then M = 16 columns, K = 16
 // keys): the eight columns suit a group of up to eight query heads.
 //
-// A head vector is 80 (or 40) bytes, so a CTA has up to eight neighbouring heads (a chunk): a token's are one
-// stretch of memory and one bulk copy, or 16 tokens' of a head in head-major pages.  A producer warp fills a ring
-// of stages of 16 to 128 keys; eight warps share the heads, the rows where there are more than eight, and blocks
-// of 16 keys.  Copies of 16 bytes by the computing warps themselves, a head a CTA, took 16 cycles a key and head of
-// an SM's time, 9 of them for the copies alone (each fetches whole sectors of 32 bytes); the memory's rate is 6.8.
+// A head vector is 80 (or 40) bytes, so a CTA has up to eight neighbouring heads (a chunk).  A producer warp fills a ring
+// of stages of 16 to 128 keys, by a tensor copy of 16 tokens of all heads where pages are multiples of that, else by
+// a bulk copy a token; eight warps share the heads, the rows where there are more than eight, and blocks of 16 keys.
+// Cycles of an SM a key and head (the memory's rate is 6.8): copies of 16 bytes by the computing warps themselves, a
+// head a CTA, took 16, 9 of them for the copies alone (each fetches whole sectors of 32 bytes).  A bulk copy takes the
+// copy engine some 45 cycles whatever its size: two a token of eight heads are 11.
 #include <type_traits>
 
 #include "kvx_attn.cuh"
@@ -39,10 +40,10 @@ constexpr float kRenew = 2.f; // by so many powers of two may a score pass what 
 
 template <int D>
 struct Smem {
-  // keys' head vectors, then values'; of at most 128 (key, head) pairs, rows padded by up to 16 bytes a key
+  // head vectors of keys and of values, of at most 128 (key, head) pairs, tokens padded by up to 16 bytes
   static constexpr int kHalf = 128 * q4_bytes(D) + (D == 128 ? 1024 : 512);
   static constexpr int kSum = D + 4;  // floats of a row on its way to be joined
-  alignas(128) char ring[kStages][2][kHalf];
+  alignas(128) char ring[kStages][2 * kHalf];
   alignas(16) float sum[kWarps][kRows][kSum];
   float base[kWarps][kRows], l[kWarps][kRows];
   uint32_t vector[128];  // where a stage's keys are, for copies of a part of a head
@@ -58,6 +59,10 @@ __device__ __forceinline__ void cp_async_if(uint32_t dst, const char *src, bool 
   const int n = ok ? B : 0;
   if constexpr (B == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
   else asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint64_t *b) {
+  asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+               ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(b)) : "memory");
 }
 __device__ __forceinline__ void bulk_copy(uint32_t dst, const char *src, int bytes, uint64_t *bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
@@ -131,6 +136,7 @@ struct Producer {
   static constexpr int kBytes = q4_bytes(D), kChunk = D / 8;  // of a head vector, and of a fifth of it
   const AttnParams &p;
   S &sm;
+  const CUtensorMap *k_map, *v_map;
   const int h0, heads, lane;
   uint32_t stage = 0, phase = 1;
   bool lost = false;  // a wait was given up: nothing more is sent on its way
@@ -146,16 +152,15 @@ struct Producer {
     if (lost) return;
     const Share w(p, x);
     const int32_t keys = kBlock * w.warps;
-    // look-ups, a stage ahead of their use: of runs of 16 tokens, the lane pair's (lanes of K and V); of tokens, lane's,
+    // look-ups, a stage ahead of their use: of blocks of 16 tokens, the lane pair's (lanes of K and V); of tokens, lane's,
     // lane + 32's and so on (16 keys: lanes of K and V)
-    const int run_head = (lane >> 1) & ((1 << p.slot_shift) - 1), run_block = lane >> (1 + p.slot_shift);
-    const bool runs = p.q4_copies == kAttnQ4Runs, pairs = keys == 16 && !runs;
+    const bool boxes = p.q4_copies == kAttnQ4Boxes, pairs = keys == 16 && !boxes;
     int32_t id[4] = {};
     auto look = [&](int j) {
       if (j >= w.stages) return;
       const int32_t pos = w.start + j * keys;
-      if (runs) {
-        if (run_block < w.warps) id[0] = page_of(x, max(pos + run_block * kBlock, x.low));
+      if (boxes) {
+        if (lane >> 1 < w.warps) id[0] = page_of(x, max(pos + (lane >> 1) * kBlock, x.low));
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -171,22 +176,23 @@ struct Producer {
       look(j + 1);
       lost = !__all_sync(~0u, bar_wait(&sm.empty[stage], phase, &sm.lost, &sm.error));
       if (lost) return;
-      const uint32_t to = smem_u32(sm.ring[stage][0]);
-      if (runs) {
-        // 16 tokens of a head, whole: what lies beside the piece's keys is masked
-        const int32_t at = pos + run_block * kBlock;
-        const bool mine = run_block < w.warps && at < x.key1, take = mine && run_head < heads;
-        if (lane == 0) bar_expect(&sm.full[stage], 2 * heads * min(w.warps, (x.key1 - pos + kBlock - 1) / kBlock) * kBlock * kBytes);
-        if (take) {
+      const uint32_t to = smem_u32(sm.ring[stage]);
+      if (boxes) {
+        // 16 tokens of all heads, whole: what lies beside the piece's keys, or the chunk's heads, is masked or not looked at
+        const int32_t at = pos + (lane >> 1) * kBlock;
+        if (lane == 0) bar_expect(&sm.full[stage], 2 * min(w.warps, (x.key1 - pos + kBlock - 1) / kBlock) * p.q4_block_pitch);
+        if (lane >> 1 < w.warps && at < x.key1) {
           int32_t pg, o;
           attn_split(p, at, &pg, &o);
-          const char *src = (lane & 1 ? p.pool.v : p.pool.k) + attn_checked(p, now[0], &sm.error) * p.pool.page_stride +
-                            (h0 + run_head) * p.pool.head_stride + o * p.pool.tok_stride;
-          bulk_copy(to + (lane & 1) * S::kHalf + run_head * p.q4_head_pitch + run_block * kBlock * kBytes, src, kBlock * kBytes, &sm.full[stage]);
+          const int32_t page = attn_checked(p, now[0], &sm.error);
+          // (see attn_q4_maps)
+          const int32_t cx = p.q4_runs ? o * (kBytes / 8) : 0, cy = p.q4_runs ? page * p.kv_heads + h0 : page * p.page_size + o;
+          tma_load3(to + (lane >> 1) * p.q4_block_pitch + (lane & 1) * p.q4_v_off, lane & 1 ? v_map : k_map, cx, cy,
+                    p.q4_runs ? 0 : h0 >> p.q4_pair, &sm.full[stage]);
         }
       } else if (p.q4_copies == kAttnQ4Tokens) {
-        const int32_t first = max(pos, x.low), last = min(pos + keys, x.key1);
-        if (lane == 0) bar_expect(&sm.full[stage], 2 * (last - first) * heads * kBytes);
+        const int32_t first = max(pos, x.low), last = min(pos + keys, x.key1), bytes = heads * kBytes;
+        if (lane == 0) bar_expect(&sm.full[stage], 2 * (last - first) * bytes);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int32_t key = pairs ? lane & 15 : i * 32 + lane, at = pos + key;
@@ -195,8 +201,12 @@ struct Producer {
           attn_split(p, at, &pg, &o);
           const int64_t off = attn_checked(p, now[i], &sm.error) * p.pool.page_stride + o * p.pool.tok_stride + h0 * p.pool.head_stride;
           const uint32_t dst = to + key * p.q4_key_pitch;
-          if (!pairs || lane < 16) bulk_copy(dst, p.pool.k + off, heads * kBytes, &sm.full[stage]);
-          if (!pairs || lane >= 16) bulk_copy(dst + S::kHalf, p.pool.v + off, heads * kBytes, &sm.full[stage]);
+          if (p.q4_v_off == bytes) {  // a token's values are behind its keys, here and there
+            if (!pairs || lane < 16) bulk_copy(dst, p.pool.k + off, 2 * bytes, &sm.full[stage]);
+          } else {
+            if (!pairs || lane < 16) bulk_copy(dst, p.pool.k + off, bytes, &sm.full[stage]);
+            if (!pairs || lane >= 16) bulk_copy(dst + p.q4_v_off, p.pool.v + off, bytes, &sm.full[stage]);
+          }
         }
       } else {
         // a fifth of a head vector at a time; head vectors by their number in the plane (see AttnParams::page_vectors)
@@ -221,7 +231,7 @@ struct Producer {
           const int64_t off = (ok ? (int64_t)((uint64_t)n * (uint32_t)p.pool.tok_stride) : 0) + (h0 + head) * p.pool.head_stride + (c - head * 5) * kChunk;
           const uint32_t dst = to + key * p.q4_key_pitch + head * p.q4_head_pitch + (c - head * 5) * kChunk;
           cp_async_if<kChunk>(dst, p.pool.k + off, ok);
-          cp_async_if<kChunk>(dst + S::kHalf, p.pool.v + off, ok);
+          cp_async_if<kChunk>(dst + p.q4_v_off, p.pool.v + off, ok);
         }
         // this lane's arrival when its copies are there
         asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(&sm.full[stage])) : "memory");
@@ -331,19 +341,19 @@ struct Worker {
     int odd = 0;
     // the values' scales may be up to this (units of lows: anything)
     __half2 limit = __half2half2(__ushort_as_half(r8 & 1 ? 0x7c00 : 0x3c00));
-    const uint32_t kp = p.q4_key_pitch, mine = slot * p.q4_head_pitch;
+    const uint32_t kp = p.q4_key_pitch, mine = (slot >> p.q4_pair) * p.q4_head_pitch + (slot & p.q4_pair) * q4_bytes(D);
     const uint32_t row16 = mine + (lane & 15) * kp, row8 = mine + r8 * kp, col4 = mine + 2 * c4 * kp;
 
 #pragma unroll 1
     for (int j = 0; j < share.stages; ++j) {
       bar_wait(&sm.full[stage], phase, &sm.lost, &sm.error);  // (given up: what follows is of no account)
       __syncwarp();
-      const uint32_t ring = smem_u32(sm.ring[stage][0]);
+      const uint32_t ring = smem_u32(sm.ring[stage]);
 #pragma unroll 1
       for (int b = first_block; b < share.warps; b += share.keys) {
       const int pos = share.start + (j * share.warps + b) * kBlock;
       if (pos >= x.key1) break;
-      const uint32_t kt = ring + b * kBlock * kp, vt = kt + S::kHalf;
+      const uint32_t kt = ring + b * p.q4_block_pitch, vt = kt + p.q4_v_off;
       const bool mixed = pos + kBlock > least || pos < x.low || pos + kBlock > x.key1;
       // ---- scores of keys r8 and r8 + 8
       float s[4];
@@ -576,7 +586,7 @@ struct Worker {
 };
 
 template <typename IO, int D>
-__global__ void __launch_bounds__(kThreads, 2) attn_q4_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(kThreads, 2) attn_q4_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
   extern __shared__ char raw_smem[];
   using S = Smem<D>;
   S &sm = *reinterpret_cast<S *>(raw_smem + (-smem_u32(raw_smem) & 127));
@@ -614,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_q4_kernel(const __grid_const
       if (n <= done + kPieces) break;
     }
   };
-  Producer<D> producer{p, sm, h0, heads, lane};
+  Producer<D> producer{p, sm, &k_map, &v_map, h0, heads, lane};
   if (warp < kWarps) {
     const int slot = warp / warps;
     Worker<IO, D> work{p, sm, h0 + slot, slot, warp - slot * warps, lane, warp};
@@ -647,7 +657,9 @@ cudaError_t launch(const AttnParams &p, cudaStream_t s) {
   static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs an SM");
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  void *args[] = {const_cast<AttnParams *>(&p)};
+  CUtensorMap km = {}, vm = {};
+  if (p.q4_copies == kAttnQ4Boxes && !attn_q4_maps(p, &km, &vm)) return cudaErrorInvalidValue;
+  void *args[] = {const_cast<AttnParams *>(&p), &km, &vm};
   return launch_pdl(fn, dim3(p.groups * p.group_ctas), dim3(kThreads), args, s, kSmem);
 }
 

@@ -94,4 +94,9 @@ __device__ __forceinline__ void bar_drain(uint64_t *full, uint32_t stage, uint32
 void attn_make_tma(const AttnParams &p, int keys, bool fp8, bool hnd, AttnTma *t, CUtensorMap *km,
                    CUtensorMap *vm);
 
+
+// The planes of a 4-bit pool for boxes of 16 tokens and a chunk's heads, in words of 8 bytes.  Token rows: [head, or pair of
+// heads of 64][token][its bytes]; head-major pages: [page and head][the bytes of its tokens].  False: no such map.
+bool attn_q4_maps(const AttnParams &p, CUtensorMap *km, CUtensorMap *vm);
+
 }  // namespace kvx
