@@ -342,7 +342,7 @@ struct Worker {
     // the values' scales may be up to this (units of lows: anything)
     __half2 limit = __half2half2(__ushort_as_half(r8 & 1 ? 0x7c00 : 0x3c00));
     const uint32_t kp = p.q4_key_pitch, mine = (slot >> p.q4_pair) * p.q4_head_pitch + (slot & p.q4_pair) * q4_bytes(D);
-    const uint32_t row16 = mine + (lane & 15) * kp, row8 = mine + r8 * kp, col4 = mine + 2 * c4 * kp;
+    const uint32_t row16 = mine + (lane & 15) * kp, row8 = mine + r8 * kp;
 
 #pragma unroll 1
     for (int j = 0; j < share.stages; ++j) {
@@ -461,15 +461,6 @@ struct Worker {
         const uint32_t f[4] = {zw[0], 0, zw[1], 0};
         mma16816<__half>(z, f, p0, p1);
       }
-      uint32_t vs[4][G];  // (scale, low) of keys 2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        load_shared(vs[i], vt + col4 + ((i & 1) + 8 * (i >> 1)) * kp + D / 2);
-        if (mixed)
-#pragma unroll
-          for (int g = 0; g < G; ++g)
-            if (odd_word(vs[i][g] & 0xffffu)) vs[i][g] = 0, odd = 1;
-      }
 #pragma unroll
       for (int g = 0; g < G; g += 2) {
         uint32_t w[4];
@@ -481,8 +472,9 @@ struct Worker {
         }
 #pragma unroll
         for (int e2 = 0; e2 < 2; ++e2) {
-          const uint32_t b0 = mul_half2(p0, __byte_perm(vs[0][g + e2], vs[1][g + e2], 0x5410));
-          const uint32_t b1 = mul_half2(p1, __byte_perm(vs[2][g + e2], vs[3][g + e2], 0x5410));
+          // the group's scales of keys 2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9, from the lanes whose row is their unit
+          const int from = (g + e2) * 8 + c4;
+          const uint32_t b0 = mul_half2(p0, __shfl_sync(~0u, zw[0], from)), b1 = mul_half2(p1, __shfl_sync(~0u, zw[1], from));
           const uint32_t u = w[2 * e2], v = w[2 * e2 + 1], u8 = u >> 8, v8 = v >> 8;
           const uint32_t f0[4] = {u & 0x000f000fu, u8 & 0x000f000fu, v & 0x000f000fu, v8 & 0x000f000fu};
           mma16816<__half>(o[g + e2][0], f0, b0, b1);
