@@ -228,8 +228,12 @@ __host__ __device__ __forceinline__ int32_t attn_cost(int32_t rows, int32_t row_
   return r <= few ? 1 : r <= 2 * few ? 2 : r <= 4 * few ? 4 : 8;
 }
 
+// The same by a power of two.
+__device__ __forceinline__ int64_t attn_up2(int64_t a, int32_t b) { return (a + b - 1) >> (__ffs(b) - 1); }
+
+// (a unit's rows, and what a tile costs, are powers of two)
 __device__ __forceinline__ int64_t attn_units(const AttnParams &p, int32_t rows) {
-  return rows <= p.row_tile ? rows > 0 : attn_up(rows, p.row_tile);
+  return rows <= p.row_tile ? rows > 0 : attn_up2(rows, p.row_tile);
 }
 
 // The length of a unit and of a seg in the line.  A unit's begin and end (its queries, joining its warps,
@@ -463,10 +467,10 @@ __device__ __forceinline__ void attn_pieces(const AttnParams &p, int g, int h, c
     const int64_t unit_length = attn_unit_length(p, seg), length = attn_units(p, seg.rows) * unit_length;
     for (int64_t from = max(w - tile0, (int64_t)0), to = min(length, l.end - tile0); from < to;) {
       // the unit's tiles that begin in this group's part: kt .. kt + take - 1
-      const int unit = (int)attn_div(from, unit_length);
+      const int unit = from < unit_length ? 0 : (int)attn_div(from, unit_length);
       const int64_t begin = unit * unit_length;
-      const int kt = (int)attn_up(from - begin, seg.cost);
-      const int take = (int)min((int64_t)seg.key_tiles, attn_up(to - begin, seg.cost)) - kt;
+      const int kt = (int)attn_up2(from - begin, seg.cost);
+      const int take = (int)min((int64_t)seg.key_tiles, attn_up2(to - begin, seg.cost)) - kt;
       from = begin + unit_length;
       if (take <= 0) continue;
       AttnPiece x;
