@@ -803,7 +803,7 @@ extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_arg
   }
   if (e == cudaSuccess) {
     // all warps that an SM has for a row, while there is a row or two an SM
-    const bool deep = q4 && (int64_t)a.n_q * a.q_heads <= 2 * kAttnSms;
+    const bool deep = q4 && a.n_q > 0 && (int64_t)a.n_q * a.q_heads <= 2 * kAttnSms;
     const void *join = a.q_dtype == KVX_F32   ? join_kernel<float>(pool->head_dim, false)
                        : a.q_dtype == KVX_F16 ? join_kernel<__half>(pool->head_dim, deep)
                                               : join_kernel<__nv_bfloat16>(pool->head_dim, deep);

@@ -34,34 +34,46 @@ __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_f(__nv_fp8_e4m3 x) { return (float)x; }
 
-// An element of a 4-bit pool is no object of its own: a byte holds two, and its group's scale and low stand
+// An element of a 4-bit pool is no object of its own: eight are a word of codes, and their group's scale and low stand
 // behind the codes.
 struct Q4 {};
-
-// Element d of the head vector at s.
-template <typename KV>
-__device__ __forceinline__ float element(const char *s, int d, int D) {
-  if constexpr (std::is_same<KV, Q4>::value) {
-    const uint32_t pair = reinterpret_cast<const uint32_t *>(s)[D / 8 + d / KVX_Q4_GROUP];
-    const float code = (float)(reinterpret_cast<const uint8_t *>(s)[d >> 1] >> (4 * (d & 1)) & 15);
-    return fmaf(code, __half2float(__ushort_as_half((uint16_t)pair)), __half2float(__ushort_as_half((uint16_t)(pair >> 16))));
-  } else {
-    return to_f(reinterpret_cast<const KV *>(s)[d]);
-  }
-}
 
 // Rows of D columns padded to pitch(D): a multiple of four, and 16-byte reads of eight rows of one
 // column lie in different banks.
 __host__ __device__ constexpr int pitch(int D) { return (D + 3) / 4 * 4 + 4; }
 
+// A load of some neighbouring elements of a head vector, and what they are.
 template <typename KV>
-__device__ __forceinline__ void unpack(const uint4 &v, float *o) {
-  const KV *e = reinterpret_cast<const KV *>(&v);
+struct Load {
+  static constexpr int kElems = 16 / sizeof(KV);
+  uint4 v;
+  // Load c of the head vector at s + o (of D elements).
+  __device__ __forceinline__ void from(const char *s, int64_t o, int c, int) {
+    o += c * 16;
+    v = *reinterpret_cast<const uint4 *>(s + o);
+  }
+  __device__ __forceinline__ void unpack(float *o) const {
+    const KV *e = reinterpret_cast<const KV *>(&v);
 #pragma unroll
-  for (int i = 0; i < (int)(16 / sizeof(KV)); ++i) o[i] = to_f(e[i]);
-}
+    for (int i = 0; i < kElems; ++i) o[i] = to_f(e[i]);
+  }
+};
+template <>
+struct Load<Q4> {
+  static constexpr int kElems = 8;
+  uint32_t codes, pair;
+  __device__ __forceinline__ void from(const char *s, int64_t o, int c, int D) {
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(s + o);
+    codes = w[c], pair = w[D / 8 + c / 4];
+  }
+  __device__ __forceinline__ void unpack(float *o) const {
+    const float scale = __half2float(__ushort_as_half((uint16_t)pair)), low = __half2float(__ushort_as_half((uint16_t)(pair >> 16)));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = fmaf((float)(codes >> (4 * i) & 15u), scale, low);
+  }
+};
 
-// NC: columns a thread.  VEC: 16-byte loads.
+// NC: columns a thread.  VEC: 16-byte loads (4-bit pools: a word and its group's).
 template <typename KV, typename IO, int NC, bool VEC>
 __global__ void __launch_bounds__(kThreads, NC == 1 ? 3 : 2) attn_general_kernel(const __grid_constant__ AttnParams p) {
   extern __shared__ float4 smem4[];
@@ -75,7 +87,7 @@ __global__ void __launch_bounds__(kThreads, NC == 1 ? 3 : 2) attn_general_kernel
   __shared__ int64_t scan[2 * (kThreads / 32) + 4];
   __shared__ int64_t soff[kKeys];
   __shared__ int32_t error;
-  constexpr int kElems = 16 / sizeof(KV);             // of a 16-byte load
+  constexpr int kElems = Load<KV>::kElems;
   constexpr int kMost = VEC ? kKeys * NC * 128 / kElems / kThreads : 1;  // loads a thread and tile, K or V
   attn_wait_prior();
   if (tid == 0) error = 0;
@@ -118,15 +130,15 @@ __global__ void __launch_bounds__(kThreads, NC == 1 ? 3 : 2) attn_general_kernel
       return k0 + lane < end ? attn_key_offset(p, item.table, k0 + lane, &error) + head * p.pool.head_stride : 0;
     };
     const int chunks = D / kElems;  // VEC: D is a multiple of kElems
-    uint4 rk[kMost], rv[kMost];
+    Load<KV> rk[kMost], rv[kMost];
     auto fetch = [&](int64_t off) {
 #pragma unroll
       for (int i = 0; i < kMost; ++i) {
         const int e = i * kThreads + tid, j = e / chunks, c = e - j * chunks;
-        const int64_t o = __shfl_sync(~0u, off, j & 31) + c * 16;  // a row has whole warps' loads or its lanes agree
+        const int64_t o = __shfl_sync(~0u, off, j & 31);  // a row has whole warps' loads or its lanes agree
         if (j < kKeys) {
-          rk[i] = *reinterpret_cast<const uint4 *>(p.pool.k + o);
-          rv[i] = *reinterpret_cast<const uint4 *>(p.pool.v + o);
+          rk[i].from(p.pool.k, o, c, D);
+          rv[i].from(p.pool.v, o, c, D);
         }
       }
     };
@@ -140,8 +152,8 @@ __global__ void __launch_bounds__(kThreads, NC == 1 ? 3 : 2) attn_general_kernel
           const int e = i * kThreads + tid, j = e / chunks, c = e - j * chunks;
           if (j >= kKeys) continue;
           float x[kElems], y[kElems];
-          unpack<KV>(rk[i], x);
-          unpack<KV>(rv[i], y);
+          rk[i].unpack(x);
+          rv[i].unpack(y);
 #pragma unroll
           for (int w = 0; w < kElems; w += 4) {
             float4 a = make_float4(x[w], x[w + 1], x[w + 2], x[w + 3]), b = make_float4(y[w], y[w + 1], y[w + 2], y[w + 3]);
@@ -159,8 +171,10 @@ __global__ void __launch_bounds__(kThreads, NC == 1 ? 3 : 2) attn_general_kernel
           const int64_t o = soff[j];
           float x = 0.f, y = 0.f;
           if (j < nk) {
-            x = element<KV>(p.pool.k + o, d, D);
-            y = element<KV>(p.pool.v + o, d, D);
+            if constexpr (!std::is_same<KV, Q4>::value) {
+              x = to_f(reinterpret_cast<const KV *>(p.pool.k + o)[d]);
+              y = to_f(reinterpret_cast<const KV *>(p.pool.v + o)[d]);
+            }
           }
           sk[j * P + d] = x;
           sv[j * P + d] = y;
@@ -261,9 +275,9 @@ __global__ void __launch_bounds__(kThreads, NC == 1 ? 3 : 2) attn_general_kernel
 template <typename KV, typename IO, int NC>
 cudaError_t launch_c(const AttnParams &p, bool vec, cudaStream_t s) {
   const size_t smem = sizeof(float) * ((size_t)pitch(p.head_dim) * (kRows + 2 * kKeys) + kRows * kKeys + kRows);
-  const void *fn = (const void *)attn_general_kernel<KV, IO, NC, false>;
+  const void *fn = (const void *)attn_general_kernel<KV, IO, NC, true>;
   if constexpr (!std::is_same<KV, Q4>::value)
-    if (vec) fn = (const void *)attn_general_kernel<KV, IO, NC, true>;
+    if (!vec) fn = (const void *)attn_general_kernel<KV, IO, NC, false>;
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 100 * 1024);
   if (e != cudaSuccess) return e;
   void *args[] = {const_cast<AttnParams *>(&p)};
@@ -283,8 +297,8 @@ cudaError_t launch_attn_general(const AttnParams &p, int32_t dtype, int32_t io, 
   if (dtype == KVX_BF16) return launch<__nv_bfloat16, __nv_bfloat16>(p, vec, s);
   if (dtype == KVX_FP8 && io == KVX_F16) return launch<__nv_fp8_e4m3, __half>(p, vec, s);
   if (dtype == KVX_FP8) return launch<__nv_fp8_e4m3, __nv_bfloat16>(p, vec, s);
-  if (io == KVX_F16) return launch<Q4, __half>(p, false, s);
-  return launch<Q4, __nv_bfloat16>(p, false, s);
+  if (io == KVX_F16) return launch<Q4, __half>(p, true, s);
+  return launch<Q4, __nv_bfloat16>(p, true, s);
 }
 
 }  // namespace kvx

@@ -44,6 +44,31 @@ def test_head_counts(G, H, D):
     run(q4.make("bf16", "planes", 16, H, G=G, D=D, lens=[90, 70, 65], prefix=60, seed=G))
 
 
+@pytest.mark.parametrize("H", [3, 5, 6, 9, 10, 16, 33])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("kind,page", [("planes", 16), ("slots", 1), ("hnd", 32), ("planes", 3), ("hnd", 8)])
+def test_heads_that_share_a_cta(H, D, kind, page):
+    """Chunks of heads that do not fill their places, or the last of which is smaller; every way of copying."""
+    run(q4.make("bf16", kind, page, H, G=2, D=D, lens=[150, 33, 70], prefix=17, seed=H, layers=1, layer=0))
+
+
+@pytest.mark.parametrize("H", [1, 2, 4, 8])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("kind,page", [("planes", 16), ("slots", 1), ("hnd", 64), ("planes", 1), ("slots", 24)])
+@pytest.mark.parametrize("qlens", [None, (3, 9, 1, 33)])
+def test_splits_of_rows_and_keys(H, D, kind, page, qlens):
+    """Long enough for several stages of a CTA and pieces that go on; rows that take one to eight warps."""
+    run(q4.make("f16", kind, page, H, G=3, D=D, lens=[2100, 333, 40, 1200], qlens=qlens, prefix=35, seed=H, layers=1,
+                layer=0))
+
+
+@pytest.mark.parametrize("n", [2500, 4100])
+def test_many_tiny_requests(n):
+    """More pieces a CTA than it lists at a time."""
+    lens = [(i * 7) % 4 for i in range(n)]
+    run(q4.make("bf16", "hnd", 16, 40, G=1, D=64, lens=lens, prefix=0, layers=1, layer=0))
+
+
 @pytest.mark.parametrize("n", [1, 2, 15, 16, 17, 31, 32, 63, 64, 65, 127, 128, 129, 255, 256, 257, 700, 5000])
 @pytest.mark.parametrize("prefix", [0, 1])
 def test_lengths(n, prefix):
@@ -219,11 +244,13 @@ def test_large_queries():
     run(q4.make("bf16", "planes", 16, 2, G=4, D=64, lens=[200, 61], prefix=30, spread=1e-6, scale=1e5))
 
 
-def test_a_bad_page_is_reported():
-    c = q4.make("bf16", "planes", 16, 2, G=4, D=128, lens=[200, 61], prefix=30)
+@pytest.mark.parametrize("kind,page,D", [("planes", 16, 128), ("slots", 1, 128), ("planes", 3, 128), ("hnd", 16, 64),
+                                         ("hnd", 3, 128), ("planes", 16, 96)])
+def test_a_bad_page_is_reported(kind, page, D):
+    c = q4.make("bf16", kind, page, 2, G=4, D=D, lens=[200, 61], prefix=30)
     for bad in (c.pages, -1, 2 ** 31 - 1):
         r = q4.Run(c)
-        r.tables[0, 5] = bad
+        r.tables[0, 150 // page] = bad
         r.call()
         torch.cuda.synchronize()
         assert int(r.status.item()) == r.kvx.ERR_OUT_OF_RANGE
@@ -248,3 +275,47 @@ def test_captured_and_replayed():
         r.prefix_pages.copy_(d.prefix_pages)
         graph.replay()
         q4.check(d, r.results())
+
+
+def test_tokens_of_no_request():
+    """Query tokens behind the last request's get 0 and -infinity."""
+    c = q4.make("bf16", "planes", 16, 2, G=4, D=128, lens=[60, 61], qlens=[2, 3], prefix=20)
+    r = q4.Run(c, extra_tokens=3)
+    out, lse = r.call().results()
+    q4.check(c, (out, lse))
+    assert bool((out[c.T:] == 0).all() and (lse[c.T:] == -math.inf).all())
+
+
+@pytest.mark.parametrize("kind,page", [("planes", 16), ("planes", 1), ("hnd", 16)])
+def test_planes_past_4_gib(kind, page):
+    """Pages whose bytes begin beyond 2^32 of a plane."""
+    from disaggregated_paged_kv_gb300 import kvx
+    H, D, S = 8, 128, 80
+    slots = 16 * 450_000
+    pool = torch.full((2 * slots * H * S,), 255, dtype=torch.uint8, device="cuda")
+    more = dict(kind=kvx.HND_PAGED, page_size=page) if kind == "hnd" else {}
+    layout = kvx.Layout(1, H, D, kvx.Q4, slots, base=pool, plane_stride=slots * H * S, **more)
+    c = q4.make("bf16", kind, page, H, G=4, D=D, lens=[100], prefix=0, layers=1, layer=0)
+    n = -(-100 // page)
+    far = torch.arange(n, dtype=torch.int32) + slots // page - n - 3
+    small, big = c.pool.view(2, -1, page * H * S), pool.view(2, -1, page * H * S)
+    for j in range(n):
+        big[:, int(far[j])] = small[:, int(c.tables[0, j])].cuda()
+    r = q4.Run(c)
+    r.layout = layout
+    r.tables[0, :n] = far.cuda()
+    q4.check(c, r.call().results())
+
+
+def test_two_calls_at_once():
+    """Two streams, workspaces of their own."""
+    runs = [q4.Run(q4.make("bf16", "planes", 16, 8, G=4, D=128, lens=[900 + i, 61, 300], prefix=30, seed=i, layers=1, layer=0))
+            for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in runs]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for r, s in zip(runs, streams):
+            r.call(stream=s)
+    torch.cuda.synchronize()
+    for r in runs:
+        q4.check(r.c, r.results())
