@@ -265,11 +265,11 @@ struct Raw {
   }
 };
 
-// Rows of a turn, on their way together.  (Loads of two turns more warps into what an SM holds: 20000 tokens of 28
-// layers 133 us, of four 153, of one 159.  Stores of two, four and eight: 2048 tokens of 36 layers, written
-// and read, 163, 159 and 205 us.)
+// Rows of a turn, on their way together: two, which leaves registers for five CTAs an SM.  (20000 tokens of 28 layers read:
+// turns of one, two and four rows 159, 133 and 153 us.  2048 tokens of 36 layers, written and read: stores of one, two,
+// four and eight rows 155, 152, 156 and 185 us, with as many CTAs as they leave room for.)
 template <typename IO>
-constexpr int kStoreTurn = sizeof(IO) == 4 ? 2 : 4;
+constexpr int kStoreTurn = sizeof(IO) == 4 ? 1 : 2;
 constexpr int kLoadTurn = 2;
 
 // The first look at the verdict: whether anything may be written.
@@ -292,7 +292,7 @@ __device__ __forceinline__ void turns(const QuantArgs &q, int32_t step, F f) {
 
 // N: elements of a thread: 16 (4-bit pools), 8, or 1 where an 8-bit pool's head vectors are no multiple of that.
 template <typename IO, bool Q4, int N, bool SCALED>
-__global__ void __launch_bounds__(kThreads, 3) store_kernel(const __grid_constant__ QuantArgs q) {
+__global__ void __launch_bounds__(kThreads, 5) store_kernel(const __grid_constant__ QuantArgs q) {
   constexpr int T = kStoreTurn<IO>;
   const int p = blockIdx.y;
   const Place<N> x(q, p, (int32_t)(blockIdx.x % q.parts), sizeof(IO));
