@@ -39,12 +39,19 @@ enum Elements : int { k16 = 0, k8 = 1, k4 = 2 };
 template <int E, int D>
 struct Smem {
   static constexpr int kStages = E == k16 ? 5 : E == k8 ? 3 : 4;  // of one K or V tile each, as 16-bit values
-  static constexpr int kRawStages = E == k16 ? 1 : 3;
+  static constexpr int kRawStages = E == k16 ? 1 : E == k8 ? 3 : 2;
   static constexpr int kRawPitch = D == 128 ? 80 : 48;  // of a head vector of 4-bit elements
   alignas(1024) char q[2][128 * D * 2];
   alignas(1024) char kv[kStages][kKeys * D * 2];
   alignas(1024) char raw[kRawStages][E == k8 ? kKeys * D : E == k4 ? kKeys * kRawPitch : 128];  // tiles as they come
-  int64_t off[kKeys];
+  // 4-bit pools: eight more columns, the keys' lows against the sums of the queries' groups (of either
+  // row tile), and the zeros that fill them up to the 16 of a product
+  static constexpr int kX = E == k4 ? 128 * 16 : 16;
+  struct X {
+    char q[2][kX], k[kX], zeros[kX];
+  };
+  alignas(128) X x;
+  int64_t off[E == k4 ? 1 : kKeys];
   uint64_t q_full, full[kStages], empty[kStages], raw_full[kRawStages];
   uint64_t s_full[2], p_full[2][2], o_full[2], o_empty[2], drained;
   // of the piece, by its parity: the least position that a live row does not see, and whether
@@ -164,6 +171,12 @@ __device__ __forceinline__ uint64_t operand(uint32_t addr) {
          1ull << 46 | 2ull << 61;
 }
 
+// A matrix operand of 16 columns whose two blocks of eight, rows of 16 bytes one behind another, are at addr and `next`
+// bytes behind.
+__device__ __forceinline__ uint64_t operand8(uint32_t addr, uint32_t next) {
+  return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(next >> 4) << 16 | (uint64_t)(128 >> 4) << 32 | 1ull << 46;
+}
+
 struct WidePiece {
   int32_t row0, rows, key0, tiles, key1, table;
   bool first, whole;
@@ -226,6 +239,10 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
     sm.lost = sm.error = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (Q4) {
+    if (tid < 128) *reinterpret_cast<uint4 *>(sm.x.zeros + tid * 16) = make_uint4(0, 0, 0, 0);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
   if (warp == 12) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sm.tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -284,9 +301,68 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
       const int lim = live ? min(attn_limit(p, token), x.key1) : 0;
       const int member = (x.row0 + i) % p.group;
       float scale = p.scale_log2;
-      if (active) {  // this row's queries; the products of the piece before are done with the last
+      if (Q4 && active) {  // this row's queries; the products of the piece before are done with the last
+        const char *src = p.q + token * p.q_tok + (int64_t)(h * p.group + member) * p.q_head;
+        uint4 w[D / 8];
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          w[c] = make_uint4(0, 0, 0, 0);
+          if (live && p.q_vec) w[c] = reinterpret_cast<const uint4 *>(src)[c];
+        }
+        if (live && !p.q_vec) {
+          const uint16_t *u = reinterpret_cast<const uint16_t *>(src);
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) {
+            w[c].x = u[8 * c] | (uint32_t)u[8 * c + 1] << 16, w[c].y = u[8 * c + 2] | (uint32_t)u[8 * c + 3] << 16;
+            w[c].z = u[8 * c + 4] | (uint32_t)u[8 * c + 5] << 16, w[c].w = u[8 * c + 6] | (uint32_t)u[8 * c + 7] << 16;
+          }
+        }
+        // rows are scaled as in attn_q4_kernel, to 2^8 .. 2^9, so that sums of 32 elements are in f16's range too
+        auto widen = [](uint32_t v, float &a, float &b) {
+          if constexpr (std::is_same<IO, __half>::value) {
+            const float2 t = __half22float2(*reinterpret_cast<const __half2 *>(&v));
+            a = t.x, b = t.y;
+          } else {
+            a = __uint_as_float(v << 16), b = __uint_as_float(v & 0xffff0000u);
+          }
+        };
+        uint32_t most = 0;  // greatest magnitude, by its bits in either type
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c)
+          most = max(most, max(max(max(w[c].x & 0x7fffu, w[c].x >> 16 & 0x7fffu), max(w[c].y & 0x7fffu, w[c].y >> 16 & 0x7fffu)),
+                               max(max(w[c].z & 0x7fffu, w[c].z >> 16 & 0x7fffu), max(w[c].w & 0x7fffu, w[c].w >> 16 & 0x7fffu))));
+        if constexpr (std::is_same<IO, __half>::value) most = __float_as_uint(__half2float(__ushort_as_half((uint16_t)most))) >> 16;
+        const float f = half_scale(most, &scale) * 0x1p-6f;
+        scale = fmaxf(scale * 0x1p6f, 1.17549435e-38f);  // (see below)
+        float sums[D / 32] = {};
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          uint32_t v[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float a, b;
+            widen(v[e], a, b);
+            a *= f, b *= f;
+            sums[c / 4] += a + b;
+            v[e] = pack2<__half>(a, b);
+          }
+          *reinterpret_cast<uint4 *>(sm.q[t] + place<D>(r, c)) =  // in the order of column_of
+              make_uint4(__byte_perm(v[0], v[2], 0x5410), __byte_perm(v[0], v[2], 0x7632),
+                         __byte_perm(v[1], v[3], 0x5410), __byte_perm(v[1], v[3], 0x7632));
+        }
+        // the sums as two f16 numbers each, exact to 2^-22: groups' first numbers, then their second ones
+        uint32_t x4[4] = {};
+#pragma unroll
+        for (int g = 0; g < D / 32; g += 2) {
+          x4[g / 2] = pack2<__half>(sums[g], sums[g + 1]);
+          const float2 hi = __half22float2(*reinterpret_cast<const __half2 *>(&x4[g / 2]));
+          x4[2 + g / 2] = pack2<__half>(sums[g] - hi.x, sums[g + 1] - hi.y);
+        }
+        *reinterpret_cast<uint4 *>(sm.x.q[t] + r * 16) = make_uint4(x4[0], x4[1], x4[2], x4[3]);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      } else if (active) {
         float f = 1.f;
-        if constexpr (E != k16 && std::is_same<IO, __nv_bfloat16>::value) {  // see attn_narrow_kernel
+        if constexpr (FP8 && std::is_same<IO, __nv_bfloat16>::value) {  // see attn_narrow_kernel
           const uint16_t *u = reinterpret_cast<const uint16_t *>(p.q + token * p.q_tok + (int64_t)(h * p.group + member) * p.q_head);
           uint32_t most = 0;
           if (live) {
@@ -325,16 +401,13 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
           }
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
-            if constexpr (E != k16 && std::is_same<IO, __nv_bfloat16>::value) {
+            if constexpr (FP8 && std::is_same<IO, __nv_bfloat16>::value) {
               uint32_t v[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
 #pragma unroll
               for (int e = 0; e < 4; ++e)
                 v[e] = pack2<__half>(__uint_as_float(v[e] << 16) * f, __uint_as_float(v[e] & 0xffff0000u) * f);
               w[c] = make_uint4(v[0], v[1], v[2], v[3]);
             }
-            if constexpr (Q4)
-              w[c] = make_uint4(__byte_perm(w[c].x, w[c].z, 0x5410), __byte_perm(w[c].x, w[c].z, 0x7632),
-                                __byte_perm(w[c].y, w[c].w, 0x5410), __byte_perm(w[c].y, w[c].w, 0x7632));
             *reinterpret_cast<uint4 *>(sm.q[t] + place<D>(r, c0 + c)) = w[c];
           }
         }
@@ -572,7 +645,14 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
       if constexpr (Q4) {
         // A thread brings its key's head vectors in by itself, K and V in turn, and makes 16-bit tiles of them: no
         // thread of the four warps waits for another.  Codes are exact as 16-bit numbers (1024 + code and
-        // 1024 + 16 * code are, by their bits), and low + code * scale is rounded once.
+        // 1024 + 16 * code are, by their bits).  Keys become two tiles, the code times the scale's first seven bits and the code
+        // times the other four, both exact; their lows are eight columns of their own (Smem::x).  As one tile of
+        // low + code * scale, rounded once, keys took the prompts of eight 767 us instead of 1,142, but scores were off by
+        // 2^-12 of their terms' sizes, which showed in the sums of exponentials (1e-3 of a row with few keys).  A
+        // value is low + code * scale, rounded once to the type of its product with the weights.
+        // (What bounds it: the two tiles' stores next to the products' reads of shared memory, 4 of them a score.  Slower: the
+        // tiles one after the other, as their stages come free, 1,200 us; all of a tile computed before its stage is waited for,
+        // 1,660 us with 104 registers a thread; with the stores left out it took 764 us.)
         constexpr int kChunk = D / 8;  // bytes of a copy; a head vector is five
         const int halves = 2 * x.tiles;
         int sent = 0;
@@ -627,35 +707,71 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
 #pragma unroll
           for (int k = 0; k < D / 32; ++k) pair[k] = reinterpret_cast<const uint32_t *>(raw + D / 2)[k];
           send();
-          lost |= !__all_sync(~0u, wait(&sm.empty[stage], phase));
-          if (!lost) {
-            if ((half & 1) && x.key0 + (half >> 1) * kKeys + kKeys > least) {  // see attn_narrow_kernel
+          const __half2 less = __half2half2(__ushort_as_half(0xe400)), small = __half2half2(__ushort_as_half(0x2c00)),
+                        less4 = __half2half2(__ushort_as_half(0xd400));  // -1024, 1 / 16, -64
+          // codes e * 2, e * 2 + 1 (in the order of column_of) of word x
+          auto codes = [&](uint32_t x, int e) {
+            const uint32_t b = ((e & 2 ? x >> 8 : x) & (e & 1 ? 0x00f000f0u : 0x000f000fu)) | 0x64006400u;
+            const __half2 c = *reinterpret_cast<const __half2 *>(&b);
+            return e & 1 ? __hfma2(c, small, less4) : __hadd2(c, less);
+          };
+          auto twice = [](uint32_t x, uint32_t pick) {
+            const uint32_t y = __byte_perm(x, 0, pick);
+            return *reinterpret_cast<const __half2 *>(&y);
+          };
+          auto bits = [](__half2 x) { return *reinterpret_cast<const uint32_t *>(&x); };
+          static_assert(kStages == 4, "a tile takes three stages, so that the second of its keys is the first of those before");
+          const uint32_t st0 = stage, ph0 = phase;
+          if (++stage == kStages) stage = 0, phase ^= 1;
+          const uint32_t st1 = stage, ph1 = phase;  // of the second tile of keys
+          bool there = wait(&sm.empty[st0], ph0);
+          if (!(half & 1)) {
+            there = wait(&sm.empty[st1], ph1) && there;
+            if (++stage == kStages) stage = 0, phase ^= 1;
+          }
+          lost |= !__all_sync(~0u, there);
+          if (lost) continue;
+          if (!(half & 1)) {
+            char *hi = sm.kv[st0], *lo = sm.kv[st1];
+#pragma unroll
+            for (int k = 0; k < D / 8; ++k) {
+              const uint32_t s2 = __byte_perm(pair[k / 4], 0, 0x1010), first = s2 & 0xfff0fff0u;
+              const __half2 sh = *reinterpret_cast<const __half2 *>(&first), sl = __hsub2(*reinterpret_cast<const __half2 *>(&s2), sh);
+              uint32_t o[4], q[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const __half2 c = codes(w[k], e);
+                o[e] = bits(__hmul2(c, sh)), q[e] = bits(__hmul2(c, sl));
+              }
+              *reinterpret_cast<uint4 *>(hi + place<D>(i, k)) = make_uint4(o[0], o[1], o[2], o[3]);
+              *reinterpret_cast<uint4 *>(lo + place<D>(i, k)) = make_uint4(q[0], q[1], q[2], q[3]);
+            }
+            // (the second stage was that of the tile before's first one, given back when its lows' products were done)
+            uint32_t l[2] = {};
+#pragma unroll
+            for (int k = 0; k < D / 64; ++k) l[k] = __byte_perm(pair[2 * k], pair[2 * k + 1], 0x7632);
+            *reinterpret_cast<uint4 *>(sm.x.k + i * 16) = make_uint4(l[0], l[1], l[0], l[1]);
+            arrive(&sm.full[st0]);
+            bar_arrive(&sm.full[st1]);
+          } else {
+            if (x.key0 + (half >> 1) * kKeys + kKeys > least) {  // see attn_narrow_kernel
               bool any = false;
 #pragma unroll
               for (int k = 0; k < D / 32; ++k)
                 if (odd2<__half>(pair[k])) pair[k] = 0, any = true;
               if (any) *(volatile int32_t *)&sm.odd[parity] = 1;
             }
-            char *dst = sm.kv[stage];
-            const __half2 less = __half2half2(__ushort_as_half(0xe400)), small = __half2half2(__ushort_as_half(0x2c00)),
-                          less4 = __half2half2(__ushort_as_half(0xd400));  // -1024, 1 / 16, -64
+            char *dst = sm.kv[st0];
 #pragma unroll
             for (int k = 0; k < D / 8; ++k) {
-              const uint32_t s2 = __byte_perm(pair[k / 4], 0, 0x1010), l2 = __byte_perm(pair[k / 4], 0, 0x3232);
-              const __half2 s = *reinterpret_cast<const __half2 *>(&s2), l = *reinterpret_cast<const __half2 *>(&l2);
+              const __half2 s = twice(pair[k / 4], 0x1010), l = twice(pair[k / 4], 0x3232);
               uint32_t o[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t b = (e & 2 ? w[k] >> 8 : w[k]) & (e & 1 ? 0x00f000f0u : 0x000f000fu) | 0x64006400u;
-                const __half2 c = *reinterpret_cast<const __half2 *>(&b);
-                const __half2 y = __hfma2(e & 1 ? __hfma2(c, small, less4) : __hadd2(c, less), s, l);
-                o[e] = *reinterpret_cast<const uint32_t *>(&y);
-              }
+              for (int e = 0; e < 4; ++e) o[e] = bits(__hfma2(codes(w[k], e), s, l));
               *reinterpret_cast<uint4 *>(dst + place<D>(i, k)) = make_uint4(o[0], o[1], o[2], o[3]);
             }
-            arrive(&sm.full[stage]);
+            arrive(&sm.full[st0]);
           }
-          if (++stage == kStages) stage = 0, phase ^= 1;
         }
         cp_async_wait<0>();
         asm volatile("bar.sync 1, 128;" ::: "memory");  // everyone has read warp_least
@@ -833,12 +949,24 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
       phase = 0;
       const uint64_t q0 = operand<D>(smem_u32(sm.q[0])), kv0 = operand<D>(smem_u32(sm.kv[0]));
       constexpr uint64_t kTileStep = 128 * D * 2 >> 4;
-      auto scores = [&](int t, uint32_t kst) {
+      // (4-bit pools: keys are two tiles and their lows' columns)
+      const uint32_t zeros = smem_u32(sm.x.zeros), xq = smem_u32(sm.x.q[0]), xk = smem_u32(sm.x.k);
+      const uint64_t xq0 = operand8(xq, zeros - xq), xq1 = operand8(xq + S::kX, zeros - xq - S::kX), xk0 = operand8(xk, zeros - xk);
+      auto scores = [&](int t, uint32_t kst, uint32_t kst2) {
         const uint64_t qd = q0 + t * kTileStep, kd = kv0 + kst * kTileStep;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint64_t step = (uint64_t)((k >> 2) * (1024 >> 4) + (k & 3) * 2);
           mma_ss(tm + t * 128, qd + step, kd + step, kDescS, k > 0, lead);
+        }
+        if constexpr (Q4) {
+          const uint64_t k2 = kv0 + kst2 * kTileStep;
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint64_t step = (uint64_t)((k >> 2) * (1024 >> 4) + (k & 3) * 2);
+            mma_ss(tm + t * 128, qd + step, k2 + step, kDescS, 1, lead);
+          }
+          mma_ss(tm + t * 128, t ? xq1 : xq0, xk0, kDescS, 1, lead);
         }
       };
       // About five products wait in the tensor cores' queue, 350 cycles: no two waits stand together, and
@@ -849,14 +977,20 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
         wait_all(&sm.q_full, q_phase);
         wait_all(&sm.full[stage], phase);
         q_phase ^= 1;
+        const uint32_t first = stage;
+        if constexpr (Q4) {
+          if (++stage == kStages) stage = 0, phase ^= 1;
+          wait_all(&sm.full[stage], phase);
+        }
         fence_after();
 #pragma unroll
         for (int t = 0; t < 2; ++t)
           if (t == 0 || two) {
-            scores(t, stage);
+            scores(t, first, stage);
             mma_commit(&sm.s_full[t], lead);
           }
-        mma_commit(&sm.empty[stage], lead);
+        mma_commit(&sm.empty[first], lead);
+        if constexpr (Q4) mma_commit(&sm.empty[stage], lead);
         if (++stage == kStages) stage = 0, phase ^= 1;
         wait_all(&sm.full[stage], phase);
         for (int j = 0; j < tiles; ++j) {
@@ -864,6 +998,11 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
           if (++stage == kStages) stage = 0, phase ^= 1;
           const uint32_t kst = stage, k_phase = phase;  // of the next tile's keys
           const bool more = j + 1 < tiles;
+          uint32_t kst2 = stage, k2_phase = phase;  // 4-bit pools: of its second tile of keys
+          if constexpr (Q4) {
+            if (more && ++stage == kStages) stage = 0, phase ^= 1;
+            kst2 = stage, k2_phase = phase;
+          }
           if (more && ++stage == kStages) stage = 0, phase ^= 1;  // now its values
           const uint64_t vd = kv0 + vst * kTileStep;
 #pragma unroll
@@ -882,10 +1021,11 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
             }
             if (t == 1) mma_commit(&sm.empty[vst], lead);
             if (more) {
-              if (t == 0) wait_all(&sm.full[kst], k_phase);
+              // (the second tile of keys comes after the first)
+              if (t == 0) wait_all(&sm.full[Q4 ? kst2 : kst], Q4 ? k2_phase : k_phase);
               else wait_all(&sm.full[stage], phase);
               if (t == 0 || two) {
-                scores(t, kst);
+                scores(t, kst, kst2);
                 mma_commit(&sm.s_full[t], lead);
               }
             } else {
@@ -894,6 +1034,7 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
           }
           p_phase ^= two ? 3 : 1;
           if (more) mma_commit(&sm.empty[kst], lead);
+          if (Q4 && more) mma_commit(&sm.empty[kst2], lead);
         }
         oe_phase ^= 1;
         return true;

@@ -12,9 +12,9 @@ pytestmark = pytest.mark.gpu
 KINDS = ["planes", "slots", "hnd"]
 
 
-def run(c, wide=False, **more):
+def run(c, **more):
     r = q4.Run(c)
-    q4.check(c, r.call(**more).results(), wide)
+    q4.check(c, r.call(**more).results())
     return r
 
 
@@ -117,7 +117,7 @@ ROOM = 300_000
 @pytest.mark.parametrize("D", [64, 128])
 def test_wide_prefix_by_page_size(kind, page, prefix, D):
     lens = [prefix + 1 + 29 * (i % 5) for i in range(40)]
-    run(q4.make("bf16", kind, page, 2, G=4, D=D, lens=lens, prefix=prefix, seed=page, room=ROOM, starts=True), wide=True)
+    run(q4.make("bf16", kind, page, 2, G=4, D=D, lens=lens, prefix=prefix, seed=page, room=ROOM, starts=True))
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
@@ -126,12 +126,12 @@ def test_wide_prefix_by_page_size(kind, page, prefix, D):
 def test_prompts(dtype, kind, page, prefix, D):
     q = [200, 1, 77, 150]
     run(q4.make(dtype, kind, page, 2, G=4, D=D, lens=[prefix + 200, prefix + 50, prefix + 377, prefix + 150],
-                qlens=q, prefix=prefix, seed=page, room=ROOM), wide=True)
+                qlens=q, prefix=prefix, seed=page, room=ROOM))
 
 
 def test_prompts_among_padding_and_single_tokens():
     run(q4.make("f16", "planes", 16, 2, G=8, D=64, lens=[0, 700, 301, 0, 640, 333, 299],
-                qlens=[1, 300, 1, 40, 5, 33, 60], prefix=300, room=ROOM), wide=True)
+                qlens=[1, 300, 1, 40, 5, 33, 60], prefix=300, room=ROOM))
 
 
 def _spread_scales(D):
@@ -155,7 +155,7 @@ def test_values_far_from_zero_and_of_every_size(D):
 @pytest.mark.parametrize("D", [64, 128])
 def test_the_same_with_many_rows(D):
     run(q4.make("bf16", "planes", 16, 2, G=4, D=D, lens=[500, 300, 411], qlens=[70, 40, 90], prefix=100, shift=5.0,
-                edit_bytes=_spread_scales(D), room=ROOM), wide=True)
+                edit_bytes=_spread_scales(D), room=ROOM))
 
 
 @pytest.mark.parametrize("D", [64, 128])
@@ -168,7 +168,7 @@ def test_prompts_mask_infinities_and_nan(D, what):
         slot = int(c.tables[0, j // 16]) * 16 + j % 16
         pool[:, slot, D // 2:] = torch.tensor([what & 255, what >> 8] * (D // 16), dtype=torch.uint8)
     out, lse = q4.Run(c).call().results()
-    want, wlse, tol, tol_l = q4.reference(c, True)
+    want, wlse, tol, tol_l = q4.reference(c)
     q4.ar._near(out[:196], want[:196], tol[:196], "out")
     q4.ar._near(lse[:196], wlse[:196], tol_l[:196], "lse")
     assert not bool(torch.isfinite(out[196:]).any())
