@@ -259,7 +259,7 @@ __device__ __forceinline__ RowPieces narrow_pieces(const AttnParams &p, const At
 // rows the chain of a row's pieces.  Cold, 3100 tokens of 32 heads (prompts) 28 us, 64 tokens of 32 heads
 // 7 us, one token with 38 pieces a row 18 us.
 // W: the warps of a row, each with a stretch of its pieces, whose sums are added up in order; 1 but for few rows of
-// 4-bit pools, whose narrow line has many more groups (one token of 304 pieces a row: KJOIN).
+// 4-bit pools, whose narrow line has many more groups (one token of 304 pieces a row, cold: 15.5 us).
 template <typename IO, int DK, int W>
 __global__ void __launch_bounds__((W > 1 ? W : kJoinWarps) * 32) attn_join_kernel(const __grid_constant__ AttnParams p, int heads) {
   constexpr int kWarps = W > 1 ? W : kJoinWarps;
@@ -737,7 +737,7 @@ extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_arg
     const bool even = ((uintptr_t)p.pool.k | (uintptr_t)p.pool.v) % 16 == 0 && a.page_size % 16 == 0;
     p.q4_runs = hnd || (pool->kv_heads == 1 && pool->slot_stride == S);
     p.q4_pair = !p.q4_runs && S % 16 != 0;  // (40 bytes are no whole pieces of 16, two heads' are)
-    const bool boxes = even && (p.q4_runs ? p.pool.num_pages * pool->kv_heads <= INT32_MAX
+    const bool boxes = even && (p.q4_runs ? p.pool.num_pages * pool->kv_heads <= INT32_MAX && (int64_t)a.page_size * S / 8 <= INT32_MAX
                                           : pool->slot_stride % 16 == 0 && (!p.q4_pair || (pool->kv_heads | p.chunk) % 2 == 0));
     const bool tokens = !hnd && pool->vec == 16 && p.chunk * S % 16 == 0;
     p.q4_copies = boxes ? kAttnQ4Boxes : tokens ? kAttnQ4Tokens : kAttnQ4Parts;

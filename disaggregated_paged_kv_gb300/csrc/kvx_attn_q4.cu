@@ -53,7 +53,7 @@ struct Smem {
   int32_t n_pieces, lost, error;
 };
 
-// ... or zeros.
+// Copies 16 or 8 bytes, or zeros.
 template <int B>
 __device__ __forceinline__ void cp_async_if(uint32_t dst, const char *src, bool ok) {
   const int n = ok ? B : 0;
@@ -426,7 +426,7 @@ struct Worker {
       }
       // ---- weights; what they refer to is renewed where a score passes it by far, or a scale the limit
       float e[4] = {s[0] - base[0], s[1] - base[1], s[2] - base[0], s[3] - base[1]};
-      const __half2 zm = __hmax2(*reinterpret_cast<const __half2 *>(&zw[0]), *reinterpret_cast<const __half2 *>(&zw[1]));
+      const __half2 zm = __hmax2(__habs2(*reinterpret_cast<const __half2 *>(&zw[0])), __habs2(*reinterpret_cast<const __half2 *>(&zw[1])));
       if (__any_sync(~0u, fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3])) > top + kRenew || !__hble2(zm, limit))) {
         float n0 = fmaxf(s[0], s[2]), n1 = fmaxf(s[1], s[3]), up = r8 & 1 ? 0.f : fmaxf(__low2float(zm), __high2float(zm));
 #pragma unroll

@@ -333,7 +333,7 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
                                max(max(w[c].z & 0x7fffu, w[c].z >> 16 & 0x7fffu), max(w[c].w & 0x7fffu, w[c].w >> 16 & 0x7fffu))));
         if constexpr (std::is_same<IO, __half>::value) most = __float_as_uint(__half2float(__ushort_as_half((uint16_t)most))) >> 16;
         const float f = half_scale(most, &scale) * 0x1p-6f;
-        scale = fmaxf(scale * 0x1p6f, 1.17549435e-38f);  // (see below)
+        scale = fmaxf(scale * 0x1p7f, 1.17549435e-38f);  // (keys are halved; see below)
         float sums[D / 32] = {};
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) {
@@ -354,6 +354,7 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
         uint32_t x4[4] = {};
 #pragma unroll
         for (int g = 0; g < D / 32; g += 2) {
+          sums[g] *= 0.5f, sums[g + 1] *= 0.5f;  // (the lows are not)
           x4[g / 2] = pack2<__half>(sums[g], sums[g + 1]);
           const float2 hi = __half22float2(*reinterpret_cast<const __half2 *>(&x4[g / 2]));
           x4[2 + g / 2] = pack2<__half>(sums[g] - hi.x, sums[g + 1] - hi.y);
@@ -647,9 +648,12 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
         // thread of the four warps waits for another.  Codes are exact as 16-bit numbers (1024 + code and
         // 1024 + 16 * code are, by their bits).  Keys become two tiles, the code times the scale's first seven bits and the code
         // times the other four, both exact; their lows are eight columns of their own (Smem::x).  As one tile of
-        // low + code * scale, rounded once, keys took the prompts of eight 767 us instead of 1,142, but scores were off by
-        // 2^-12 of their terms' sizes, which showed in the sums of exponentials (1e-3 of a row with few keys).  A
-        // value is low + code * scale, rounded once to the type of its product with the weights.
+        // low + code * scale, rounded once, keys took the prompts of eight 767 us instead of 1,170, but scores were off by
+        // 2^-12 of their terms' sizes, which showed in the sums of exponentials (1e-3 of a row with few keys).  All
+        // of a key is halved, as 15 times a scale can pass f16's end (a group from -61440 to 61440); that is exact but for
+        // scales below 2^-13, where a product may be off by 2^-24.  (A look at every scale instead, for those above
+        // 2^12, took prompts 4 % longer.)  A value is low + code * scale, rounded once to the type of its product with the
+        // weights.
         // (What bounds it: the two tiles' stores next to the products' reads of shared memory, 4 of them a score.  Slower: the
         // tiles one after the other, as their stages come free, 1,200 us; all of a tile computed before its stage is waited for,
         // 1,660 us with 104 registers a thread; with the stores left out it took 764 us.)
@@ -707,12 +711,14 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
 #pragma unroll
           for (int k = 0; k < D / 32; ++k) pair[k] = reinterpret_cast<const uint32_t *>(raw + D / 2)[k];
           send();
-          const __half2 less = __half2half2(__ushort_as_half(0xe400)), small = __half2half2(__ushort_as_half(0x2c00)),
-                        less4 = __half2half2(__ushort_as_half(0xd400));  // -1024, 1 / 16, -64
-          // codes e * 2, e * 2 + 1 (in the order of column_of) of word x
+          // codes e * 2, e * 2 + 1 (in the order of column_of) of word x, K: halved
           auto codes = [&](uint32_t x, int e) {
-            const uint32_t b = ((e & 2 ? x >> 8 : x) & (e & 1 ? 0x00f000f0u : 0x000f000fu)) | 0x64006400u;
+            const bool key = !(half & 1);
+            const uint32_t b = ((e & 2 ? x >> 8 : x) & (e & 1 ? 0x00f000f0u : 0x000f000fu)) | (key ? 0x60006000u : 0x64006400u);
             const __half2 c = *reinterpret_cast<const __half2 *>(&b);
+            const __half2 less = __half2half2(__ushort_as_half(key ? 0xe000 : 0xe400));   // -512 or -1024
+            const __half2 less4 = __half2half2(__ushort_as_half(key ? 0xd000 : 0xd400));  // -32 or -64
+            const __half2 small = __half2half2(__ushort_as_half(0x2c00));                 // 1 / 16
             return e & 1 ? __hfma2(c, small, less4) : __hadd2(c, less);
           };
           auto twice = [](uint32_t x, uint32_t pick) {

@@ -410,9 +410,9 @@ cudaError_t launch(QuantArgs &q, bool store, cudaStream_t s) {
   q.parts = (int32_t)((per_row + kThreads - 1) / kThreads);
   const int64_t all = (q.n + turn * step - 1) / (turn * step);
   // some turns a CTA where that still leaves each SM many CTAs
-  const int64_t many = all * q.parts * q.planes / (kSms * 16);
-  q.turns = (int32_t)(many < 1 ? 1 : many > 8 ? 8 : many);
-  int64_t grid = (all + q.turns - 1) / q.turns * q.parts;
+  const int64_t many = all * q.parts * q.planes / (kSms * 16), least = all * q.parts / INT32_MAX + 1;  // (a grid has 31 bits)
+  q.turns = (int32_t)(many < 1 ? 1 : many > 8 ? (least > 8 ? 2 * least : 8) : many);
+  const int64_t grid = (all + q.turns - 1) / q.turns * q.parts;
   void *args[] = {&q};
   return launch_pdl(fn, dim3((unsigned)grid, (unsigned)q.planes), dim3(kThreads), args, s);
 }

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 from tests import attention_q4_ref as q4
+from tests import quant_ref as qr
 
 pytestmark = pytest.mark.gpu
 
@@ -158,6 +159,46 @@ def test_the_same_with_many_rows(D):
                 edit_bytes=_spread_scales(D), room=ROOM))
 
 
+def _pairs(b, D):
+    """(scales, lows) of tokens' bytes [tokens, 2, H, bytes], to be changed in place."""
+    pair = b[..., D // 2:].view(np.float16)
+    return pair[..., 0::2], pair[..., 1::2]
+
+
+def _falling(D):
+    """Scales below 0, as a quantiser of another convention may have them: elements fall as codes rise."""
+    def edit(b):
+        scale, low = _pairs(b, D)
+        top = (low.astype(np.float32) + 15 * scale.astype(np.float32)).astype(np.float16)
+        scale[:], low[:] = -scale * np.float16(32), top * np.float16(32)
+    return edit
+
+
+@pytest.mark.parametrize("D,qlens", [(64, None), (96, None), (128, None), (64, [70, 40]), (128, [70, 40])])
+def test_scales_below_0(D, qlens):
+    """32 times the usual values, so that weights as they are would not fit next to such a scale."""
+    run(q4.make("bf16", "planes", 16, 2, G=4, D=D, lens=[500, 300], qlens=qlens, prefix=100, scale=1e-3,
+                edit_bytes=_falling(D), room=ROOM))
+
+
+def _far_keys(D):
+    """Keys from -61440 to 61440, groups whose codes times their scale pass f16's end among them."""
+    def edit(b):
+        scale, low = (x[:, 0] for x in _pairs(b, D))
+        lows = np.clip(low.astype(np.float32) * 2.0 ** 13.4, -61440, 0).astype(np.float16)
+        most = (61440 - lows.astype(np.float32)) / 15
+        scale[:] = np.minimum(scale.astype(np.float32) * 2.0 ** 13.4, most * (1 - 2.0 ** -10)).astype(np.float16)
+        low[:] = lows
+        assert (scale > 4400).any() and (scale < 3900).any()
+    return edit
+
+
+@pytest.mark.parametrize("D,qlens", [(64, None), (128, None), (64, [70, 40]), (128, [70, 40])])
+def test_keys_at_the_ends_of_the_range(D, qlens):
+    run(q4.make("bf16", "planes", 16, 2, G=4, D=D, lens=[500, 300], qlens=qlens, prefix=100, scale=2.0 ** -18,
+                edit_bytes=_far_keys(D), room=ROOM))
+
+
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("what", [0x7C00, 0xFC00, 0x7E00])
 def test_prompts_mask_infinities_and_nan(D, what):
@@ -305,6 +346,39 @@ def test_planes_past_4_gib(kind, page):
     r.layout = layout
     r.tables[0, :n] = far.cuda()
     q4.check(c, r.call().results())
+
+
+def test_one_page_beyond_31_bits_of_words():
+    """A head-major pool that is a single page of more than 2^31 8-byte words a head: all its keys are zeros but the
+    last 40 (scores 0, values 0), so that the sums are known."""
+    from disaggregated_paged_kv_gb300 import kvx
+    D, S, G, last = 128, 80, 4, 40
+    slots = (2 ** 31 // 10 + 1000) // 16 * 16
+    pool = torch.zeros(2, slots, S, dtype=torch.uint8, device="cuda")
+    layout = kvx.Layout(1, 1, D, kvx.Q4, slots, base=pool, plane_stride=slots * S, kind=kvx.HND_PAGED, page_size=slots)
+    g = np.random.default_rng(0)
+    held = qr.encode_q4(g.standard_normal((last, 2, 1, D)).astype(np.float32) * 8, 1.0)
+    pool[:, -last:] = torch.from_numpy(held)[:, :, 0].transpose(0, 1).cuda()
+    code, step, low = qr.parts_q4(held, D)
+    k, v = torch.from_numpy(code * step + low).double()[:, :, 0].unbind(1)
+    q = (torch.from_numpy(g.standard_normal((1, G, D))) * 2).half().cuda()
+    out, lse = torch.full_like(q, math.nan), torch.full((1, G), math.nan, device="cuda")
+    ws = torch.empty(kvx.attention_workspace_size(layout, 1, 1, G, 0), dtype=torch.uint8, device="cuda")
+    status = torch.full((1,), -1, dtype=torch.int32, device="cuda")
+    kvx.shared_attention(layout, 0, q, out, torch.zeros(1, 1, dtype=torch.int32, device="cuda"),
+                         torch.tensor([slots], dtype=torch.int32, device="cuda"), slots, ws, status, lse=lse)
+    torch.cuda.synchronize()
+    assert status.item() == kvx.OK
+    s = q.cpu().double()[0] @ k.T * D ** -0.5
+    most = s.max(1).values.clamp(min=0)
+    l = (slots - last) * (-most).exp() + (s - most[:, None]).exp().sum(1)
+    want = ((s - most[:, None]).exp() @ v) / l[:, None]
+    # beside the rounding of a weight, of its product with a scale and of the result (2^-11 each; v is up to 2^5, the
+    # lows' part up to as much again): the sum of 2^28 equal weights, split 2432 ways or more and over 8 rows of keys, takes
+    # no more than 2^13 additions in a row, each off by 2^-24
+    weight = ((s - most[:, None]).exp() @ v.abs()) / l[:, None]
+    assert bool(((out.cpu().double()[0] - want).abs() <= 2 ** -11 * want.abs() + (2 ** -8 + 2 ** -11) * weight + 2 ** -24).all())
+    assert bool((lse.cpu().double()[0] - (l.log() + most)).abs().max() <= 2 ** -11 + 2 ** -16)
 
 
 def test_two_calls_at_once():
