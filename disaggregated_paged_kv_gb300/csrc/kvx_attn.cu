@@ -505,6 +505,11 @@ constexpr int kPlanReqs = 2048;
 // us with the narrow kernel alone, 93 us side by side.
 constexpr double kWideWork = 4.5e9, kWideBeside = 0.7e9, kWideBytes = 2e8;
 
+// The same of 4-bit pools, whose wide kernel takes some 20 us to begin and whose other one reads short tiles at about 100
+// TFLOP/s.  64 requests of 1000-2000 tokens behind 2048 shared ones (2.1e9): 57 us without the wide kernel, 64 to 78 with
+// it; 100-1000 tokens behind 4096 (4.3e9): 55 and 42.
+constexpr double kQ4WideWork = 2.5e9;
+
 // A narrow unit's begin and end take about as long as some tiles of 16 rows.  Counted as 0, 2, 3 and 4 of
 // them: 95 requests of up to 25 own tokens behind 1360 shared ones 121, 66, 57 and 53 us; 96 FP8 decode
 // requests 60, 52, 59 and 60 us; 256 decode requests of 4096 own tokens 350, 344, 342 and 366 us.  The plain
@@ -676,10 +681,11 @@ extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_arg
   // only the tables bound.  Below kWideWork operations its launch costs more than it saves.  It takes
   // the greatest score from the greatest product, so the factor between them has to be above 0.
   const double room = (double)a.max_pages * a.page_size;
+  const bool q4 = q4_kernel(pool);
   const bool beside = (room - a.prefix_len) * a.n_reqs * pool->row_bytes * 2 >= kWideBytes;
   const double wide_keys = a.q_start ? (double)a.max_pages * a.page_size : (double)a.prefix_len;
   const bool wide = takes_wide(pool, a.n_q, a.q_heads) &&
-                    4.0 * pool->head_dim * a.q_heads * a.n_q * wide_keys >= (beside ? kWideBeside : kWideWork) &&
+                    4.0 * pool->head_dim * a.q_heads * a.n_q * wide_keys >= (q4 ? kQ4WideWork : beside ? kWideBeside : kWideWork) &&
                     a.scale * a.k_scale > 0.f;
   const int chunk = chunk_of(pool, q4_most_heads(a.n_q, a.n_reqs, a.q_heads / pool->kv_heads));
   const Sizes z = sizes(pool, a.n_q, a.n_reqs, a.q_heads, wide, chunk);
@@ -723,13 +729,14 @@ extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_arg
   p.max_pages = a.max_pages;
   p.prefix_len = a.prefix_len;
   p.row_tile = row_tile_of(pool, chunk);
-  const bool q4 = q4_kernel(pool);
   p.few_rows = q4 ? 8 : 16;
   p.key_shift = q4 ? 5 : 6;
   static_assert(1 << 5 == kAttnQ4KeyTile && 1 << 6 == kAttnKeyTile, "tiles of these kernels");
   p.group_ctas = group_ctas_of(pool, chunk);
   p.chunk = chunk;
-  p.tile_ns = (int32_t)std::max(kAttnNarrowNs, ((pool->seg_bytes * p.chunk) << p.key_shift) * 2 / 16 * kAttnNarrowPs / 1000);
+  p.tile_ns = (int32_t)(q4 ? kAttnQ4TileNs << slot_shift_of(chunk) : std::max(kAttnNarrowNs, (pool->seg_bytes << p.key_shift) * 2 / 16 * kAttnNarrowPs / 1000));
+  p.wide_ns = (int32_t)(q4 ? kAttnQ4WideNs : kAttnWideNs);
+  p.wide_start_ns = (int32_t)(q4 ? kAttnQ4WideStartNs : kAttnStartNs);
   if (q4) {
     p.slot_shift = slot_shift_of(chunk);
     p.page_vectors = (uint32_t)(hnd ? (int64_t)a.page_size * pool->kv_heads : a.page_size);

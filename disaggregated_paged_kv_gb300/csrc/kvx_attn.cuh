@@ -7,11 +7,11 @@
 //   prefix   the rows of many requests and the prefix;
 //   prompt   a request with several tokens, more than 64 rows in all, and all its positions, prefix
 //            included: it takes tiles of rows of its own, and one pass needs no join.
-// The narrow kernel (and the plain one) takes units of up to row_tile rows: own work, and the
+// The narrow kernel (or the 4-bit one, or the plain one) takes units of up to row_tile rows: own work, and the
 // prefix where there are few rows in all.  The wide kernel takes units of up to 256 rows: the
 // prefix and prompts.  A unit's keys are cut into tiles, all units' key tiles stand in a line, each as
-// long as its cost, and the line is dealt out evenly: group g of kv_heads CTAs, one CTA a head, takes
-// the tiles that begin in [g * quota, (g + 1) * quota).  So every CTA has about the same work whatever
+// long as its cost, and the line is dealt out evenly: group g of CTAs, one a kv head (4-bit kernel: one a chunk of
+// up to eight neighbouring heads), takes the tiles that begin in [g * quota, (g + 1) * quota).  So every CTA has about the same work whatever
 // the lengths, and the CTAs of a group read the heads of the same rows at the same time.
 //
 // A piece is what a CTA has of one unit.  It is worked through with a running maximum and sum and
@@ -103,7 +103,8 @@ struct AttnParams {
   int32_t row_tile;      // rows of a narrow unit
   int32_t few_rows;      // a tile of up to so many rows costs 1 (see attn_cost)
   int32_t key_shift;     // log2 of a narrow tile's keys
-  int32_t tile_ns;       // what a narrow tile of cost 1 takes a CTA (see attn_share)
+  int32_t tile_ns;       // what a narrow tile of cost 1 takes a CTA, and
+  int32_t wide_ns, wide_start_ns;  // a wide one, and what comes before and after them (see attn_share)
   int32_t group_ctas;    // of a narrow group: one a kv head, or one a chunk of them
   // the 4-bit kernel: kv heads of a CTA, log2 of the places for them, how they come, and where a stage has them:
   // key (of 16) k of place s (q4_pair 1: two neighbours lie together) in block b at b * block_pitch +
@@ -310,10 +311,15 @@ struct AttnShare {
 };
 
 // The GPU's SMs, and measured times in ns: of a CTA's tile of 128 keys and 256 rows; of a narrow CTA's unit
-// of cost, two CTAs on the SM, at least, and of 16 bytes of a tile (the host makes tile_ns of them); of 1 MB at the memory's rate; and what a launch takes before and after its tiles.
+// of cost, two CTAs on the SM, at least, and of 16 bytes of a tile; of 1 MB at the memory's rate; and what a launch takes
+// before and after its tiles.  Of 4-bit pools: a wide tile; a narrow one, for each place that a CTA has for a head (a warp
+// works through its own keys, whatever the bytes); and what the wide kernel takes before and after its tiles.  (With
+// the 16-bit pools' figures 29 calls of 16 to 200 decode requests or drafts behind 512 to 16384 shared tokens took 60.1
+// us in the geometric mean, with these 52.3; 96 of 1-900 tokens 55 to 72, and 47.  A narrow tile of 200, 250 and 400:
+// 54.0, 53.6 and 54.9; beginnings of 15000 and 25000: 56.0 and 52.9.)
 constexpr int kAttnSms = 152;
-constexpr int64_t kAttnWideNs = 2100, kAttnNarrowNs = 900, kAttnNarrowPs = 470, kAttnMbNs = 160,
-                  kAttnStartNs = 10000;
+constexpr int64_t kAttnWideNs = 2100, kAttnNarrowNs = 900, kAttnNarrowPs = 470, kAttnMbNs = 160, kAttnStartNs = 10000;
+constexpr int64_t kAttnQ4WideNs = 3000, kAttnQ4TileNs = 300, kAttnQ4WideStartNs = 20000;
 
 __device__ __forceinline__ AttnShare attn_share(const AttnParams &p, int64_t own, int64_t wide) {
   AttnShare s = {p.groups, p.wide_groups};
@@ -324,7 +330,7 @@ __device__ __forceinline__ AttnShare attn_share(const AttnParams &p, int64_t own
   auto narrow_ns = [&](int64_t groups) {
     return kAttnStartNs + max(attn_up(own, groups) * p.tile_ns, floor_ns);
   };
-  auto wide_ns = [&](int64_t groups) { return kAttnStartNs + attn_up(wide, groups) * kAttnWideNs; };
+  auto wide_ns = [&](int64_t groups) { return p.wide_start_ns + attn_up(wide, groups) * p.wide_ns; };
   int64_t best = (wide_ns(p.wide_groups) + narrow_ns(p.groups)) * 9 / 10;  // a tenth sooner, or not at all
   int at = p.wide_groups;
   for (int g = 1 + (threadIdx.x & 31); g < p.wide_groups; g += 32) {

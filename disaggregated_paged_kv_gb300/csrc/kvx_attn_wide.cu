@@ -13,7 +13,8 @@
 // against one exponential and about five instructions a score on four warps.  Measured: eight prompts
 // behind a shared prefix, 842 GFLOP in all, 682-708 us with the plan and the join (1.19-1.23 PFLOP/s); the tensor
 // cores are busy 61-64 % of this kernel's time and wait for weights in the rest.  Two threads a row, each with
-// half of its keys, took longer (749 against 704 us then).
+// half of its keys, took longer (749 against 704 us then).  The same prompts over a 4-bit pool take 1,150 to 1,180 us: its tiles
+// are made from codes by warps 8-11, keys as two tiles (see there), so that the products are half as many again.
 //
 // A row's sums refer to a maximum that is renewed only when a score passes it by 2^8 (f16: 2^2): the factor
 // between the two cancels in the quotient, weights stay in range (see weight_shift), and the sums in
@@ -652,8 +653,8 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
         // 2^-12 of their terms' sizes, which showed in the sums of exponentials (1e-3 of a row with few keys).  All
         // of a key is halved, as 15 times a scale can pass f16's end (a group from -61440 to 61440); that is exact but for
         // scales below 2^-13, where a product may be off by 2^-24.  (A look at every scale instead, for those above
-        // 2^12, took prompts 4 % longer.)  A value is low + code * scale, rounded once to the type of its product with the
-        // weights.
+        // 2^12, took prompts 4 % longer.)  A value is low + code * scale, rounded once to f16
+        // for its product with the weights.
         // (What bounds it: the two tiles' stores next to the products' reads of shared memory, 4 of them a score.  Slower: the
         // tiles one after the other, as their stages come free, 1,200 us; all of a tile computed before its stage is waited for,
         // 1,660 us with 104 registers a thread; with the stores left out it took 764 us.)

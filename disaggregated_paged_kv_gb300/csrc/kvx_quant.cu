@@ -7,7 +7,10 @@
 // tokens, the CTA's own check of every index) is looked at between the first loads and the first store: a
 // call writes all or nothing.
 //
-// Bound: bytes, 2 + 5/8 of them an element of a 16-bit tensor and a 4-bit pool.
+// Bound: bytes, 2 + 5/8 of them an element of a 16-bit tensor and a 4-bit pool, and instructions close behind: an element
+// costs about five to encode and four to decode.  2048 tokens of 36 layers of 8 heads of 128, written from bf16 and read
+// back, 152 us (the bytes take 103); 20000 tokens of 28 layers of 4 heads read back 136 us (111), 5.5 TB/s.  Stores alone keep
+// 69 % of the issue slots busy.  A call of few tokens is 2.3 us on the GPU, less than its host side.
 #include <cuda_bf16.h>
 
 #include <type_traits>
@@ -227,7 +230,8 @@ __device__ __forceinline__ Row row_at(const QuantArgs &q, const Place<N> &x, int
   return r;
 }
 
-// False: some index is out of range, and nothing may be written.
+// False: some index is out of range, and nothing may be written.  (For up to kSmallMaxTokens tokens: a longer
+// list read by every CTA costs more than the planner's launch.)
 __device__ __forceinline__ bool all_in_range(const QuantArgs &q) {
   int bad = 0;
   for (int64_t i = threadIdx.x; i < q.n; i += kThreads) {

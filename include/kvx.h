@@ -701,15 +701,20 @@ typedef struct kvx_attn_args {
  * rows, n * q_heads / kv_heads, may go over the prefix by itself.)  With s_j = scale * k_scale * <q, K_j>:
  *   out = v_scale * sum_j exp(s_j) V_j / sum_j exp(s_j),   lse = log sum_j exp(s_j).
  * Sums are held in 32 bits; with 16- and 8-bit pools the weights exp(s_j - max) are rounded to the
- * pool's 16-bit type (F16 for an FP8 pool, its queries too) for the product with V.  Results do not
- * depend on scheduling: the same call gives the same bits.
+ * pool's 16-bit type (F16 for an FP8 or KVX_Q4 pool, its queries too) for the product with V.  With a
+ * KVX_Q4 pool the weights' products with the scales of V are rounded to F16 too, or, where many rows
+ * meet the same keys, V's elements; K's elements are exact (to 2^-24 where a scale is below 2^-13).
+ * Elements are expected within +-65504, as kvx_store_kv leaves them.  Results do not depend on
+ * scheduling: the same call gives the same bits.
  * A row that sees nothing (a length of 0, or fewer positions than query tokens), or whose every
  * score is -inf, is 0 with lse -inf.  What masked positions and other slots hold, NaN and
  * infinities included, does not reach a result.  Tokens of no request (at or past
  * q_start[n_reqs]) get 0 and -inf.
  * Any head_dim up to KVX_ATTN_MAX_HEAD_DIM, page size, stride and element-aligned address; rows
  * of 16-bit and FP8 pools with head_dim 64 or 128 and 16-byte aligned heads take the tensor
- * cores, all others a plain kernel.
+ * cores, and so do those of KVX_Q4 pools with head_dim 128 and 16-byte aligned heads or head_dim
+ * 64 and 8-byte aligned ones (slot strides below 2^31, HND pools of fewer than 2^32 heads of slots a plane);
+ * all others a plain kernel.
  * d_status: *d_status = KVX_OK, KVX_ERR_INVALID_ARG (a length below 0, q_start not rising from
  * 0 to at most n_q) or KVX_ERR_OUT_OF_RANGE (a length beyond the table row or above
  * KVX_ATTN_MAX_POSITIONS, a page id outside the pool), the larger if both: out and lse are then
