@@ -516,6 +516,11 @@ constexpr double kQ4WideWork = 2.5e9;
 // kernel's tiles take so long that they do not tell.
 constexpr int32_t kNarrowUnitCost = 2;
 
+// The same of 4-bit pools where a CTA has one head; the more places for heads it has, the longer its tiles take.  Counted as 2, 8,
+// 12, 16 and 24: 95 requests of 4-81 own tokens of 1 x 4 heads of 64 behind 6859 shared ones 58, 37, 33, 32 and 29 us; 91 of
+// 1-1208 of 2 x 8 heads behind 16944 65, and 56 from 8 on; 125 of 31-358 of 1 x 6 heads 18.8, 18.2, 18.6, 20.5 and 21.1.
+constexpr int32_t kQ4UnitCost = 12;
+
 struct Sizes {
   int64_t ready_off, segs_off, units_off, start_off, base_off, prompt_off, limit_off, owner_off, tok_off, at_off;
   int64_t m_off, l_off, o_off, errors_off, errors, total;
@@ -764,7 +769,7 @@ extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_arg
       p.q4_key_pitch = S, p.q4_head_pitch = S * keys, p.q4_block_pitch = 16 * S, p.q4_v_off = 128 * S;
     }
   }
-  p.unit_cost = tensor_cores(pool) ? kNarrowUnitCost : 0;
+  p.unit_cost = q4 ? std::max(kNarrowUnitCost, kQ4UnitCost >> p.slot_shift) : tensor_cores(pool) ? kNarrowUnitCost : 0;
   p.head_bytes = (int32_t)pool->seg_bytes;
   const uintptr_t q_at = (uintptr_t)a.q | (uintptr_t)p.q_tok | (uintptr_t)p.q_head;
   p.q_even = q_at % 4 == 0;
