@@ -22,7 +22,7 @@
 //
 // Bound: the memory for long requests, and begins and ends of units for short ones.  In a graph, plan and join included: one
 // request of 2^20 tokens, 8 x 4 heads of 128, 5.85 TB/s (86 % of a copy's rate); one of 131072 tokens 61 us (its bytes 25); 256
-// requests of 1000 to 2000 tokens 126 us (75); 64 of them behind 2048 shared tokens 57 us (19), beside the wide kernel.
+// requests of 1000 to 2000 tokens 126 us (75); 64 of them behind 2048 shared tokens 57 us (19).
 #include <type_traits>
 
 #include "kvx_attn.cuh"
