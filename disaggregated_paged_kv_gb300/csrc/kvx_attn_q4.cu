@@ -330,16 +330,19 @@ struct Worker {
     float sc[2], base[2] = {-3.40282347e38f, -3.40282347e38f}, l[2] = {0.f, 0.f};
     int lim[2];
     const int first = max(x.key0, x.low);
-    int least = INT32_MAX;
+    int least = INT32_MAX, most = 0;  // of the warp's rows that see some of the piece
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       sc[i] = p.scale_log2 * __shfl_sync(~0u, factor, (2 * c4 + i) * 4);
       const int r = set * kRows + 2 * c4 + i;
       lim[i] = r < x.rows ? min(attn_limit(p, (x.row0 + r) / p.group), x.key1) : 0;
-      if (lim[i] > first) least = min(least, lim[i]);
+      if (lim[i] > first) least = min(least, lim[i]), most = max(most, lim[i]);
     }
-    least = min(least, __shfl_xor_sync(~0u, least, 1));
-    least = min(least, __shfl_xor_sync(~0u, least, 2));
+#pragma unroll
+    for (int d = 1; d < 4; d <<= 1) {
+      least = min(least, __shfl_xor_sync(~0u, least, d));
+      most = max(most, __shfl_xor_sync(~0u, most, d));
+    }
     float o[G][2][4] = {}, z[4] = {};  // z: of the unit of (scale, low) words that is r8's
     float top = kTop;
     int odd = 0;
@@ -358,7 +361,7 @@ struct Worker {
       const int pos = share.start + (j * share.warps + b) * kBlock;
       if (pos >= x.key1) break;
       const uint32_t kt = ring + b * p.q4_block_pitch, vt = kt + p.q4_v_off;
-      const bool mixed = pos + kBlock > least || pos < x.low || pos + kBlock > x.key1;
+      const bool mixed = pos + kBlock > least || pos < x.low;  // (no row sees further than key1)
       // ---- scores of keys r8 and r8 + 8
       float s[4];
       uint32_t ks[2][G];  // (scale, low) of the two keys
@@ -421,9 +424,13 @@ struct Worker {
         for (int i = 0; i < 2; ++i) zw[i] = transpose8(c4 < 2 ? load_shared(vt + row8 + 8 * i * kp + D / 2 + c4 * 4) : 0);
       }
       if (mixed) {
-        // (infinities and NaN of keys that some row does not see are taken out and put back at the end)
+        // Nothing of keys that no row sees; infinities and NaN of keys that some row does not see are taken out and put
+        // back at the end.
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
+          const int key = pos + 2 * c4 + 8 * i;
+          if (key < x.low || key >= most) zw[i] &= 0xffff0000u;
+          if (key + 1 < x.low || key + 1 >= most) zw[i] &= 0xffffu;
           if (odd_word(zw[i] & 0xffffu)) zw[i] &= 0xffff0000u, odd = 1;
           if (odd_word(zw[i] & 0xffff0000u)) zw[i] &= 0xffffu, odd = 1;
         }
@@ -565,7 +572,7 @@ struct Worker {
       for (int key = first; key < lim; ++key) {
         const int b = (key - share.start) / kBlock, pos = share.start + b * kBlock;
         if (b % share.warps % share.keys != sub / share.sets) continue;  // another warp's
-        if (!(pos + kBlock > least || pos < x.low || pos + kBlock > x.key1)) continue;
+        if (!(pos + kBlock > least || pos < x.low)) continue;
         const char *at = p.pool.v + attn_key_offset(p, x.table, key, &sm.error) + h * p.pool.head_stride;
 #pragma unroll 1
         for (int g = 0; g < G; ++g) {
