@@ -209,6 +209,11 @@ __device__ __forceinline__ int row_token(const AttnParams &p, const WidePiece &x
   return x.table < 0 && p.planned ? p.prefix_tok[t] : t;
 }
 
+// Two f16 numbers with 0 for an infinity or NaN.
+__device__ __forceinline__ uint32_t finite2(uint32_t x) {
+  return (odd2<__half>(x & 0xffffu) ? 0 : x & 0xffffu) | (odd2<__half>(x & 0xffff0000u) ? 0 : x & 0xffff0000u);
+}
+
 // Element columns of a 4-bit pool's products stand as codes come out of a word: of eight, 0, 4, 1, 5, 2, 6, 3, 7.
 __host__ __device__ __forceinline__ constexpr int column_of(bool q4, int e) {
   return q4 ? (e & ~7) | ((e & 3) << 1) | (e >> 2 & 1) : e;
@@ -519,7 +524,8 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
                 if constexpr (Q4) {
                   const uint32_t pair = reinterpret_cast<const uint32_t *>(v)[D / 8 + c];
                   const uint32_t code = reinterpret_cast<const uint8_t *>(v)[c * 16 + (k >> 1)] >> (4 * (k & 1)) & 15u;
-                  e = fmaf((float)code, __half2float(__ushort_as_half((uint16_t)pair)), __half2float(__ushort_as_half((uint16_t)(pair >> 16))));
+                  // (rounded as in the tile)
+                  e = __half2float(__hfma(__uint2half_rn(code), __ushort_as_half((uint16_t)pair), __ushort_as_half((uint16_t)(pair >> 16))));
                 } else if constexpr (FP8) {
                   const uint32_t u = from_e4m3x2(reinterpret_cast<const uint8_t *>(v)[c * 32 + k]);
                   e = __half2float(*reinterpret_cast<const __half *>(&u));
@@ -727,6 +733,7 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
             return *reinterpret_cast<const __half2 *>(&y);
           };
           auto bits = [](__half2 x) { return *reinterpret_cast<const uint32_t *>(&x); };
+          static_assert(S::kRawStages == 2, "the stage of raw tiles before this one's next is this one's");
           static_assert(kStages == 4, "a tile takes three stages, so that the second of its keys is the first of those before");
           const uint32_t st0 = stage, ph0 = phase;
           if (++stage == kStages) stage = 0, phase ^= 1;
@@ -761,13 +768,6 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
             arrive(&sm.full[st0]);
             bar_arrive(&sm.full[st1]);
           } else {
-            if (x.key0 + (half >> 1) * kKeys + kKeys > least) {  // see attn_narrow_kernel
-              bool any = false;
-#pragma unroll
-              for (int k = 0; k < D / 32; ++k)
-                if (odd2<__half>(pair[k])) pair[k] = 0, any = true;
-              if (any) *(volatile int32_t *)&sm.odd[parity] = 1;
-            }
             char *dst = sm.kv[st0];
 #pragma unroll
             for (int k = 0; k < D / 8; ++k) {
@@ -776,6 +776,26 @@ attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ A
 #pragma unroll
               for (int e = 0; e < 4; ++e) o[e] = bits(__hfma2(codes(w[k], e), s, l));
               *reinterpret_cast<uint4 *>(dst + place<D>(i, k)) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+            // (see attn_narrow_kernel.  Elements that are not finite: 15 * scale may pass f16's end where the scale does not.  A
+            // group has some if its first or last code is one; its words still stand where they came)
+            if (x.key0 + (half >> 1) * kKeys + kKeys > least) {
+              const uint32_t *words = reinterpret_cast<const uint32_t *>(sm.raw[raw_out ^ 1] + i * S::kRawPitch + D / 2);
+              bool any = false;
+#pragma unroll
+              for (int k = 0; k < D / 32; ++k) {
+                const __half l = __ushort_as_half((uint16_t)(words[k] >> 16));
+                any |= odd2<__half>(bits(__halves2half2(l, __hfma(__ushort_as_half(0x4b80), __ushort_as_half((uint16_t)words[k]), l))));
+              }
+              if (any) {
+#pragma unroll 1
+                for (int k = 0; k < D / 8; ++k) {
+                  uint4 *at = reinterpret_cast<uint4 *>(dst + place<D>(i, k));
+                  const uint4 v = *at;
+                  *at = make_uint4(finite2(v.x), finite2(v.y), finite2(v.z), finite2(v.w));
+                }
+                *(volatile int32_t *)&sm.odd[parity] = 1;
+              }
             }
             arrive(&sm.full[st0]);
           }
