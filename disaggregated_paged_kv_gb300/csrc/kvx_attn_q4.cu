@@ -39,8 +39,9 @@ constexpr int kBlock = 16;    // keys at a time
 constexpr int kRows = 8;      // of a warp
 constexpr int kPieces = 32;   // listed at a time
 constexpr int kStages = 3;
-constexpr float kTop = 13.f;  // the greatest weight is about 2^kTop (see weight_shift), less for scales above 1
+constexpr float kTop = 13.f;  // the greatest weight is about 2^kTop (see weight_shift)
 constexpr float kRenew = 2.f; // by so many powers of two may a score pass what weights refer to
+constexpr float kLeast = 0x1p-10f;  // scales this far below the greatest, or further, are multiplied in 32 bits
 
 template <int D>
 struct Smem {
@@ -101,6 +102,16 @@ __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
 }
 __device__ __forceinline__ float low_half(uint32_t x) { return __half2float(__ushort_as_half((uint16_t)x)); }
 __device__ __forceinline__ bool odd_word(uint32_t x) { return odd2<__half>(x); }
+
+__device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2 *>(&x); }
+__device__ __forceinline__ uint32_t as_word(__half2 x) { return *reinterpret_cast<const uint32_t *>(&x); }
+// Magnitudes of two f16 numbers, 0 for an infinity or NaN.
+__device__ __forceinline__ __half2 finite_abs2(uint32_t x) {
+  return as_half2((odd_word(x & 0xffffu) ? 0 : x & 0x7fffu) | (odd_word(x & 0xffff0000u) ? 0 : x & 0x7fff0000u));
+}
+// Of a positive normal number; and 2^e, e from -126 to 127.
+__device__ __forceinline__ int exponent(float x) { return (int)(__float_as_uint(x) >> 23) - 127; }
+__device__ __forceinline__ float power_of_2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
 // Two 32-bit floats at a time.
 __device__ __forceinline__ uint64_t pair(float a, float b) {
@@ -344,10 +355,13 @@ struct Worker {
       most = max(most, __shfl_xor_sync(~0u, most, d));
     }
     float o[G][2][4] = {}, z[4] = {};  // z: of the unit of (scale, low) words that is r8's
-    float top = kTop;
     int odd = 0;
-    // the values' scales may be up to this (units of lows: anything)
-    __half2 limit = __half2half2(__ushort_as_half(r8 & 1 ? 0x7c00 : 0x3c00));
+    // Weights' products with the values' scales are f16 numbers times `factor`, a power of two.  While all scales of the
+    // piece so far, and it is the same for all rows, are 0 or within kLeast .. 1 once multiplied by it, that is exact, and the products of
+    // the greatest weights are far above f16's least numbers; from the first that is not, products are of 32 bits, rounded
+    // once, and the factor is the block's and row r8's own.
+    float up_by = 0x1p15f;
+    bool apart = false;
     const uint32_t kp = p.q4_key_pitch, mine = (slot >> p.q4_pair) * p.q4_head_pitch + (slot & p.q4_pair) * q4_bytes(D);
     const uint32_t row16 = mine + (lane & 15) * kp, row8 = mine + r8 * kp;
 
@@ -435,31 +449,44 @@ struct Worker {
           if (odd_word(zw[i] & 0xffff0000u)) zw[i] &= 0xffffu, odd = 1;
         }
       }
-      // ---- weights; what they refer to is renewed where a score passes it by far, or a scale the limit
+      // ---- weights; what they refer to is renewed where a score passes it by far, the scales' factor where one asks for it
       float e[4] = {s[0] - base[0], s[1] - base[1], s[2] - base[0], s[3] - base[1]};
-      const __half2 zm = __hmax2(__habs2(*reinterpret_cast<const __half2 *>(&zw[0])), __habs2(*reinterpret_cast<const __half2 *>(&zw[1])));
-      if (__any_sync(~0u, fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3])) > top + kRenew || !__hble2(zm, limit))) {
-        float n0 = fmaxf(s[0], s[2]), n1 = fmaxf(s[1], s[3]), up = r8 & 1 ? 0.f : fmaxf(__low2float(zm), __high2float(zm));
+      uint32_t zs[2];  // the scales times the factor
+      auto scales_fit = [&]() {
+        // (units of scales; lows are of no account)
+        const __half2 none = as_half2(0), by = __float2half2_rn(up_by), s0 = as_half2(r8 & 1 ? 0 : zw[0]), s1 = as_half2(r8 & 1 ? 0 : zw[1]);
+        const __half2 a = __hmul2(s0, by), b = __hmul2(s1, by);
+        zs[0] = as_word(a), zs[1] = as_word(b);
+        // (0 counts as 1)
+        const __half2 a1 = __hadd2(__habs2(a), __heq2(s0, none)), b1 = __hadd2(__habs2(b), __heq2(s1, none));
+        return __hbge2(__hmin2(a1, b1), __float2half2_rn(kLeast)) && __hble2(__hmax2(a1, b1), as_half2(0x3c003c00u));
+      };
+      const bool fit = scales_fit() || apart;
+      if (__any_sync(~0u, fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3])) > kTop + kRenew || !fit)) {
+        float n0 = fmaxf(s[0], s[2]), n1 = fmaxf(s[1], s[3]), change = 1.f;
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) {
           n0 = fmaxf(n0, __shfl_xor_sync(~0u, n0, d));
           n1 = fmaxf(n1, __shfl_xor_sync(~0u, n1, d));
         }
+        if (!apart) {
+          const __half2 most2 = r8 & 1 ? as_half2(0) : __hmax2(finite_abs2(zw[0]), finite_abs2(zw[1]));
+          float up = fmaxf(__low2float(most2), __high2float(most2));
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) up = fmaxf(up, __shfl_xor_sync(~0u, up, d));
-        float now = top;
-        if (up > 1.f) now = fminf(top, kTop - (float)(ilogbf(fminf(up, 65504.f)) + 1));
-        if (!(r8 & 1)) limit = __half2half2(__float2half_rn(fminf(exp2f(kTop - now), 65504.f)));
+          for (int d = 1; d < 32; d <<= 1) up = fmaxf(up, __shfl_xor_sync(~0u, up, d));
+          if (up * up_by > 1.f) {
+            const float now = power_of_2(-1 - exponent(up));
+            change = now * __frcp_rn(up_by), up_by = now;
+          }
+          apart = !__all_sync(~0u, scales_fit());
+        }
         // the greatest score so far, or what stood for it
-        const float b0 = fmaxf(base[0] + top, n0) - now, b1 = fmaxf(base[1] + top, n1) - now;
+        const float b0 = fmaxf(base[0] + kTop, n0) - kTop, b1 = fmaxf(base[1] + kTop, n1) - kTop;
         const float f0 = ex2(base[0] - b0), f1 = ex2(base[1] - b1);
         l[0] *= f0, l[1] *= f1;
-#pragma unroll
-        for (int g = 0; g < G; ++g)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) o[g][k][0] *= f0, o[g][k][1] *= f1, o[g][k][2] *= f0, o[g][k][3] *= f1;
+        scale_sums(o, f0 * change, f1 * change);
         z[0] *= f0, z[1] *= f1;
-        base[0] = b0, base[1] = b1, top = now;
+        base[0] = b0, base[1] = b1;
 #pragma unroll
         for (int i = 0; i < 4; ++i) e[i] = s[i] - base[i & 1];
       }
@@ -472,27 +499,57 @@ struct Worker {
         const uint32_t f[4] = {zw[0], 0, zw[1], 0};
         mma16816<__half>(z, f, p0, p1);
       }
+      if (apart) {  // the factor by the row's greatest product in the block
+        __half2 h[2];
 #pragma unroll
-      for (int g = 0; g < G; g += 2) {
-        uint32_t w[4];
-        if constexpr (G == 4) {
-          ldmatrix4t(w, vt + row16 + (g + (lane >> 4)) * 16);
-        } else {
+        for (int i = 0; i < 2; ++i) {
+          h[i] = r8 & 1 ? as_half2(0) : finite_abs2(zw[i]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) w[i] = transpose8(load_shared(vt + row8 + 8 * (i & 1) * kp + (i >> 1) * 16 + c4 * 4));
+          for (int d = 4; d < 32; d <<= 1) h[i] = __hmax2(h[i], as_half2(__shfl_xor_sync(~0u, as_word(h[i]), d)));
         }
-#pragma unroll
-        for (int e2 = 0; e2 < 2; ++e2) {
-          // the group's scales of keys 2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9, from the lanes whose row is their unit
-          const int from = (g + e2) * 8 + c4;
-          const uint32_t b0 = mul_half2(p0, __shfl_sync(~0u, zw[0], from)), b1 = mul_half2(p1, __shfl_sync(~0u, zw[1], from));
-          const uint32_t u = w[2 * e2], v = w[2 * e2 + 1], u8 = u >> 8, v8 = v >> 8;
-          const uint32_t f0[4] = {u & 0x000f000fu, u8 & 0x000f000fu, v & 0x000f000fu, v8 & 0x000f000fu};
-          mma16816<__half>(o[g + e2][0], f0, b0, b1);
-          const uint32_t f1[4] = {u & 0x00f000f0u, u8 & 0x00f000f0u, v & 0x00f000f0u, v8 & 0x00f000f0u};
-          mma16816<__half>(o[g + e2][1], f1, b0, b1);
+        float m = fmaxf(fmaxf(low_half(p0) * __low2float(h[0]), low_half(p0 >> 16) * __high2float(h[0])),
+                        fmaxf(low_half(p1) * __low2float(h[1]), low_half(p1 >> 16) * __high2float(h[1])));
+        m = fmaxf(m, __shfl_xor_sync(~0u, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(~0u, m, 2));
+        float change = 1.f;
+        if (m > 0.f && !(m * up_by >= 1.f && m * up_by <= 0x1p14f)) {
+          const float now = power_of_2(13 - exponent(m));
+          change = now * __frcp_rn(up_by), up_by = now;
         }
+        if (__any_sync(~0u, change != 1.f)) scale_sums(o, __shfl_sync(~0u, change, c4 * 8), __shfl_sync(~0u, change, c4 * 8 + 4));
       }
+      auto values = [&](auto exact) {
+#pragma unroll
+        for (int g = 0; g < G; g += 2) {
+          uint32_t w[4];
+          if constexpr (G == 4) {
+            ldmatrix4t(w, vt + row16 + (g + (lane >> 4)) * 16);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = transpose8(load_shared(vt + row8 + 8 * (i & 1) * kp + (i >> 1) * 16 + c4 * 4));
+          }
+#pragma unroll
+          for (int e2 = 0; e2 < 2; ++e2) {
+            // the group's scales of keys 2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9, from the lanes whose row is their unit
+            const int from = (g + e2) * 8 + c4;
+            uint32_t b0, b1;
+            if constexpr (decltype(exact)::value) {
+              b0 = __shfl_sync(~0u, zw[0], from), b1 = __shfl_sync(~0u, zw[1], from);
+              b0 = pack2<__half>(low_half(p0) * up_by * low_half(b0), low_half(p0 >> 16) * up_by * low_half(b0 >> 16));
+              b1 = pack2<__half>(low_half(p1) * up_by * low_half(b1), low_half(p1 >> 16) * up_by * low_half(b1 >> 16));
+            } else {
+              b0 = mul_half2(p0, __shfl_sync(~0u, zs[0], from)), b1 = mul_half2(p1, __shfl_sync(~0u, zs[1], from));
+            }
+            const uint32_t u = w[2 * e2], v = w[2 * e2 + 1], u8 = u >> 8, v8 = v >> 8;
+            const uint32_t f0[4] = {u & 0x000f000fu, u8 & 0x000f000fu, v & 0x000f000fu, v8 & 0x000f000fu};
+            mma16816<__half>(o[g + e2][0], f0, b0, b1);
+            const uint32_t f1[4] = {u & 0x00f000f0u, u8 & 0x00f000f0u, v & 0x00f000f0u, v8 & 0x00f000f0u};
+            mma16816<__half>(o[g + e2][1], f1, b0, b1);
+          }
+        }
+      };
+      if (apart) values(std::true_type());
+      else values(std::false_type());
       }
       __syncwarp();
       if (lane == 0) bar_arrive(&sm.empty[stage]);
@@ -508,13 +565,14 @@ struct Worker {
     const int64_t part = x.part + h * x.head_step;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+      const float down = __frcp_rn(__shfl_sync(~0u, up_by, (2 * c4 + i) * 4));
       const bool none = lim[i] <= first || l[i] == 0.f;  // (a row that sees nothing of the piece has worked on all)
       const int in = 2 * c4 + i, r = set * kRows + in;
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         const float low = __shfl_sync(~0u, z[i], (2 * g + 1) * 4 + c4);
-        float v[4] = {fmaf(o[g][0][i], 0x1p24f, low), fmaf(o[g][1][i], 0x1p20f, low),
-                      fmaf(o[g][0][2 + i], 0x1p24f, low), fmaf(o[g][1][2 + i], 0x1p20f, low)};
+        float v[4] = {fmaf(o[g][0][i], 0x1p24f * down, low), fmaf(o[g][1][i], 0x1p20f * down, low),
+                      fmaf(o[g][0][2 + i], 0x1p24f * down, low), fmaf(o[g][1][2 + i], 0x1p20f * down, low)};
 #pragma unroll
         for (int k = 0; k < 4; ++k) v[k] = none ? 0.f : v[k];
         const float4 out = make_float4(v[0], v[1], v[2], v[3]);
@@ -554,6 +612,14 @@ struct Worker {
       *reinterpret_cast<float4 *>(p.part_o + at * D + c * 4) = a;
       if (c == 0) p.part_m[at] = m, p.part_l[at] = sum;
     }
+  }
+
+  // The sums of a lane's two rows, times a factor each.
+  __device__ __forceinline__ static void scale_sums(float (&o)[G][2][4], float f0, float f1) {
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) o[g][k][0] *= f0, o[g][k][1] *= f1, o[g][k][2] *= f0, o[g][k][3] *= f1;
   }
 
   // The warps of a head.
