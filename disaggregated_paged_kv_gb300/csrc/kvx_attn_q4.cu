@@ -358,8 +358,8 @@ struct Worker {
     int odd = 0;
     // Weights' products with the values' scales are f16 numbers times `factor`, a power of two.  While all scales of the
     // piece so far, and it is the same for all rows, are 0 or within kLeast .. 1 once multiplied by it, that is exact, and the products of
-    // the greatest weights are far above f16's least numbers; from the first that is not, products are of 32 bits, rounded
-    // once, and the factor is the block's and row r8's own.
+    // the greatest weights are far above f16's least numbers; from the first that is not, or
+    // from where on rows differ in what they see, products are of 32 bits, rounded once, and the factor is the block's and row r8's own.
     float up_by = 0x1p15f;
     bool apart = false;
     const uint32_t kp = p.q4_key_pitch, mine = (slot >> p.q4_pair) * p.q4_head_pitch + (slot & p.q4_pair) * q4_bytes(D);
@@ -461,6 +461,7 @@ struct Worker {
         const __half2 a1 = __hadd2(__habs2(a), __heq2(s0, none)), b1 = __hadd2(__habs2(b), __heq2(s1, none));
         return __hbge2(__hmin2(a1, b1), __float2half2_rn(kLeast)) && __hble2(__hmax2(a1, b1), as_half2(0x3c003c00u));
       };
+      if (least < most && pos + kBlock > least) apart = true;  // rows differ in what they see, from here to the end
       const bool fit = scales_fit() || apart;
       if (__any_sync(~0u, fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3])) > kTop + kRenew || !fit)) {
         float n0 = fmaxf(s[0], s[2]), n1 = fmaxf(s[1], s[3]), change = 1.f;
@@ -480,8 +481,8 @@ struct Worker {
           }
           apart = !__all_sync(~0u, scales_fit());
         }
-        // the greatest score so far, or what stood for it
-        const float b0 = fmaxf(base[0] + kTop, n0) - kTop, b1 = fmaxf(base[1] + kTop, n1) - kTop;
+        // each row by its own scores: what others see is nothing to it
+        const float b0 = n0 > base[0] + (kTop + kRenew) ? n0 - kTop : base[0], b1 = n1 > base[1] + (kTop + kRenew) ? n1 - kTop : base[1];
         const float f0 = ex2(base[0] - b0), f1 = ex2(base[1] - b1);
         l[0] *= f0, l[1] *= f1;
         scale_sums(o, f0 * change, f1 * change);
