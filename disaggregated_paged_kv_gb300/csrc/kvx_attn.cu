@@ -742,6 +742,8 @@ extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_arg
   p.tile_ns = (int32_t)(q4 ? kAttnQ4TileNs << slot_shift_of(chunk) : std::max(kAttnNarrowNs, (pool->seg_bytes << p.key_shift) * 2 / 16 * kAttnNarrowPs / 1000));
   p.wide_ns = (int32_t)(q4 ? kAttnQ4WideNs : kAttnWideNs);
   p.wide_start_ns = (int32_t)(q4 ? kAttnQ4WideStartNs : kAttnStartNs);
+  p.head_bytes = (int32_t)pool->seg_bytes;
+  CUtensorMap k_map = {}, v_map = {};  // of the 4-bit kernel's boxes
   if (q4) {
     p.slot_shift = slot_shift_of(chunk);
     p.page_vectors = (uint32_t)(hnd ? (int64_t)a.page_size * pool->kv_heads : a.page_size);
@@ -750,7 +752,8 @@ extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_arg
     p.q4_runs = hnd || (pool->kv_heads == 1 && pool->slot_stride == S);
     p.q4_pair = !p.q4_runs && S % 16 != 0;  // (40 bytes are no whole pieces of 16, two heads' are)
     const bool boxes = even && (p.q4_runs ? p.pool.num_pages * pool->kv_heads <= INT32_MAX && (int64_t)a.page_size * S / 8 <= INT32_MAX
-                                          : pool->slot_stride % 16 == 0 && (!p.q4_pair || (pool->kv_heads | p.chunk) % 2 == 0));
+                                          : pool->slot_stride % 16 == 0 && (!p.q4_pair || (pool->kv_heads | p.chunk) % 2 == 0)) &&
+                       attn_q4_maps(p, &k_map, &v_map);  // (a driver that makes none: the other copies do without)
     const bool tokens = !hnd && pool->vec == 16 && p.chunk * S % 16 == 0;
     p.q4_copies = boxes ? kAttnQ4Boxes : tokens ? kAttnQ4Tokens : kAttnQ4Parts;
     if (boxes) {
@@ -770,7 +773,6 @@ extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_arg
     }
   }
   p.unit_cost = q4 ? std::max(kNarrowUnitCost, kQ4UnitCost >> p.slot_shift) : tensor_cores(pool) ? kNarrowUnitCost : 0;
-  p.head_bytes = (int32_t)pool->seg_bytes;
   const uintptr_t q_at = (uintptr_t)a.q | (uintptr_t)p.q_tok | (uintptr_t)p.q_head;
   p.q_even = q_at % 4 == 0;
   p.q_vec = q_at % 16 == 0;
@@ -809,7 +811,7 @@ extern "C" kvx_status kvx_shared_attention(kvx_layout_t pool, const kvx_attn_arg
   if (a.n_q > 0) {
     if (e == cudaSuccess && wide) e = launch_attn_wide(p, pool->dtype, a.q_dtype, hnd, s);
     if (e == cudaSuccess)
-      e = q4                   ? launch_attn_q4(p, a.q_dtype, s)
+      e = q4                   ? launch_attn_q4(p, k_map, v_map, a.q_dtype, s)
           : tensor_cores(pool) ? launch_attn_narrow(p, pool->dtype, a.q_dtype, hnd, s)
                              : launch_attn_general(p, pool->dtype, a.q_dtype, pool->vec == 16 && pool->seg_bytes % 16 == 0, s);
   }

@@ -521,8 +521,6 @@ __device__ __forceinline__ void attn_wait_announced(const AttnParams &p) {
 cudaError_t launch_attn_general(const AttnParams &p, int32_t dtype, int32_t io, bool vec, cudaStream_t s);
 // head_dim 64 or 128, 16-bit or 8-bit pool with 16-byte aligned heads.
 cudaError_t launch_attn_narrow(const AttnParams &p, int32_t dtype, int32_t io, bool hnd, cudaStream_t s);
-// head_dim 64 or 128, 4-bit pool with head vectors on 8- or 16-byte boundaries.
-cudaError_t launch_attn_q4(const AttnParams &p, int32_t io, cudaStream_t s);
 cudaError_t launch_attn_wide(const AttnParams &p, int32_t dtype, int32_t io, bool hnd, cudaStream_t s);
 
 }  // namespace kvx

@@ -721,23 +721,21 @@ __global__ void __launch_bounds__(kThreads, 2) attn_q4_kernel(const __grid_const
 }
 
 template <typename IO, int D>
-cudaError_t launch(const AttnParams &p, cudaStream_t s) {
+cudaError_t launch(const AttnParams &p, const CUtensorMap &k_map, const CUtensorMap &v_map, cudaStream_t s) {
   const void *fn = (const void *)attn_q4_kernel<IO, D>;
   constexpr int kSmem = (int)sizeof(Smem<D>) + 128;
   static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs an SM");
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  CUtensorMap km = {}, vm = {};
-  if (p.q4_copies == kAttnQ4Boxes && !attn_q4_maps(p, &km, &vm)) return cudaErrorInvalidValue;
-  void *args[] = {const_cast<AttnParams *>(&p), &km, &vm};
+  void *args[] = {const_cast<AttnParams *>(&p), const_cast<CUtensorMap *>(&k_map), const_cast<CUtensorMap *>(&v_map)};
   return launch_pdl(fn, dim3(p.groups * p.group_ctas), dim3(kThreads), args, s, kSmem);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_q4(const AttnParams &p, int32_t io, cudaStream_t s) {
-  if (io == KVX_F16) return p.head_dim == 64 ? launch<__half, 64>(p, s) : launch<__half, 128>(p, s);
-  return p.head_dim == 64 ? launch<__nv_bfloat16, 64>(p, s) : launch<__nv_bfloat16, 128>(p, s);
+cudaError_t launch_attn_q4(const AttnParams &p, const CUtensorMap &k_map, const CUtensorMap &v_map, int32_t io, cudaStream_t s) {
+  if (io == KVX_F16) return p.head_dim == 64 ? launch<__half, 64>(p, k_map, v_map, s) : launch<__half, 128>(p, k_map, v_map, s);
+  return p.head_dim == 64 ? launch<__nv_bfloat16, 64>(p, k_map, v_map, s) : launch<__nv_bfloat16, 128>(p, k_map, v_map, s);
 }
 
 }  // namespace kvx

@@ -98,5 +98,7 @@ void attn_make_tma(const AttnParams &p, int keys, bool fp8, bool hnd, AttnTma *t
 // The planes of a 4-bit pool for boxes of 16 tokens and a chunk's heads, in words of 8 bytes.  Token rows: [head, or pair of
 // heads of 64][token][its bytes]; head-major pages: [page and head][the bytes of its tokens].  False: no such map.
 bool attn_q4_maps(const AttnParams &p, CUtensorMap *km, CUtensorMap *vm);
+// head_dim 64 or 128, 4-bit pool with head vectors on 8- or 16-byte boundaries; the maps for kAttnQ4Boxes.
+cudaError_t launch_attn_q4(const AttnParams &p, const CUtensorMap &k_map, const CUtensorMap &v_map, int32_t io, cudaStream_t s);
 
 }  // namespace kvx
