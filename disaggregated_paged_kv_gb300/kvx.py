@@ -767,7 +767,10 @@ def _index_list(x) -> int:
 def _cast_args(pool: Layout, layer: int, k, v, slots, rows, k_scale, v_scale) -> CastArgs:
     # (a decode step makes these calls layer by layer: each attribute of a tensor is asked for once)
     shape, strides = k.shape, k.stride()
-    if v.shape != shape or v.stride() != strides or v.dtype is not k.dtype or not 3 <= len(shape) <= 4:
+    other = v.stride()
+    if other != strides and len(other) == len(strides):  # (an axis of one has no stride that counts)
+        other = tuple(s if n == 1 else o for n, s, o in zip(shape, strides, other))
+    if v.shape != shape or other != strides or v.dtype is not k.dtype or not 3 <= len(shape) <= 4:
         raise ValueError("k and v are [tokens, kv_heads, head_dim] or [layers, tokens, kv_heads, head_dim], "
                          "of one type and shape and of the same strides")
     n_rows, heads, dim = shape[-3:]
@@ -780,7 +783,6 @@ def _cast_args(pool: Layout, layer: int, k, v, slots, rows, k_scale, v_scale) ->
     if n_rows != n if rows is None else _index_list(rows) != n:
         raise ValueError("slots and " + ("k" if rows is None else "rows") + " differ in length")
     layers = shape[0] if len(shape) == 4 else 1
-    # (an axis of one has no stride that counts)
     return CastArgs(layer, layers, _row_dtype(k.dtype), n, k.data_ptr(), v.data_ptr(),
                     strides[0] if layers > 1 else 0, token if n_rows > 1 else 0, head if heads > 1 else 0,
                     slots.data_ptr(), None if rows is None else rows.data_ptr(), n_rows, k_scale, v_scale, 0)
