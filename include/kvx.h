@@ -172,9 +172,9 @@ typedef struct kvx_layout_desc {
   /* Plane addresses: either plane_ptrs (host array of P = kv_planes * L device pointers, read
    * during kvx_layout_create and not kept) or, when plane_ptrs is NULL, plane p at
    * base + p * plane_stride.  Every plane address must be a multiple of the element size.
-   * Rows move in the widest access (16, 8, 4, 2 or 1 bytes) that divides R, every plane
-   * address, the slot stride (KVX_NHD) and the head vector (KVX_HND_PAGED): 16 for the usual
-   * shapes; kvx_stream, kvx_reshard and kvx_stream_reshard need 16. */
+   * Rows move in the widest access (16, 8, 4, 2 or 1 bytes) that divides the head vector, every
+   * plane address and the slot stride (KVX_NHD): 16 for the usual shapes; kvx_stream, kvx_reshard and
+   * kvx_stream_reshard need 16 (KVX_Q4: a head_dim that is a multiple of 128). */
   void *const *plane_ptrs;
   void *base;
   int64_t plane_stride;
