@@ -506,8 +506,8 @@ constexpr int kPlanReqs = 2048;
 constexpr double kWideWork = 4.5e9, kWideBeside = 0.7e9, kWideBytes = 2e8;
 
 // The same of 4-bit pools, whose wide kernel takes some 20 us to begin and whose other one reads short tiles at about 100
-// TFLOP/s.  64 requests of 1000-2000 tokens behind 2048 shared ones (2.1e9): 57 us without the wide kernel, 64 to 78 with
-// it; 100-1000 tokens behind 4096 (4.3e9): 55 and 42.
+// TFLOP/s.  64 requests of 1000-2000 tokens behind 2048 shared ones (2.1e9): 57 us without the wide kernel (then; 61 now), 64
+// to 78 with it; 100-1000 tokens behind 4096 (4.3e9): 55 and 42.
 constexpr double kQ4WideWork = 2.5e9;
 
 // A narrow unit's begin and end take about as long as some tiles of 16 rows.  Counted as 0, 2, 3 and 4 of
@@ -607,7 +607,8 @@ bool shape_ok(const kvx_layout *l, int64_t n_q, int64_t n_reqs, int64_t q_heads,
          n_q * q_heads <= (int64_t)1 << 30;
 }
 
-// Whether a call may have work for the wide kernel: more rows than the narrow kernel has in a unit.
+// Whether a call may have work for the wide kernel: more rows than the narrow kernel has in a unit (and than 4-bit pools' may
+// have, whose units are of 8 to 64 rows).
 bool takes_wide(const kvx_layout *l, int64_t n_q, int64_t q_heads) {
   return tensor_cores(l) && n_q * (q_heads / l->kv_heads) > kAttnNarrowRows;
 }

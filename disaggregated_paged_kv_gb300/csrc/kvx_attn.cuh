@@ -314,7 +314,7 @@ struct AttnShare {
 // of cost, two CTAs on the SM, at least, and of 16 bytes of a tile; of 1 MB at the memory's rate; and what a launch takes
 // before and after its tiles.  Of 4-bit pools: a wide tile; a narrow one, for each place that a CTA has for a head (a warp
 // works through its own keys, whatever the bytes); and what the wide kernel takes before and after its tiles.  (With
-// the 16-bit pools' figures 29 calls of 16 to 200 decode requests or drafts behind 512 to 16384 shared tokens took 60.1
+// the 16-bit pools' figures 29 calls of 8 to 200 decode requests or drafts behind 512 to 16384 shared tokens took 60.1
 // us in the geometric mean, with these 52.3; 96 of 1-900 tokens 55 to 72, and 47.  A narrow tile of 200, 250 and 400:
 // 54.0, 53.6 and 54.9; beginnings of 15000 and 25000: 56.0 and 52.9.)
 constexpr int kAttnSms = 152;

@@ -6,7 +6,9 @@
 //   <q, k>       = sum_g scale_g <q_g, code_g> + low_g sum(q_g)
 //   sum_j p_j v_j = sum_j (p_j scale_gj) code_j + p_j low_gj :
 // the scores' sums of a group are multiplied by its scale in 32 bits; the weights, which are rounded to f16 for
-// the product in any case, are multiplied by the scales of their keys' values, group by group, and rounded once more.
+// the product in any case, are multiplied by the scales of their keys' values, group by group, and rounded once more.  So
+// that such a product is a normal f16 number, the scales are first multiplied by a power of two (see Worker::piece); where that
+// would cost bits, or rows differ in what they see, the products are made in 32 bits (all of a call's: 256 requests 119 -> 136 us).
 // The lows are a product of their own: (scale, low) words as they stand are its operand, against the sums of the
 // queries (as two f16 numbers, so exact to 2^-22) and against the weights.
 //
@@ -20,9 +22,10 @@
 // head a CTA, took 16, 9 of them for the copies alone (each fetches whole sectors of 32 bytes).  A bulk copy takes the
 // copy engine some 45 cycles whatever its size: two a token of eight heads are 11.  By tensor copies it is 7.5 to 8.
 //
-// Bound: the memory for long requests, and begins and ends of units for short ones.  In a graph, plan and join included: one
-// request of 2^20 tokens, 8 x 4 heads of 128, 5.85 TB/s (86 % of a copy's rate); one of 131072 tokens 61 us (its bytes 25); 256
-// requests of 1000 to 2000 tokens 126 us (75); 64 of them behind 2048 shared tokens 57 us (19).
+// Bound: instructions, some 390 a block of 16 keys and head, close before the memory for long requests, and begins and ends of
+// units for short ones.  In a graph, join included: one request of 2^20 tokens, 8 x 4 heads of 128, 267 us (its bytes 197), 328
+// in pages of one token; one of 131072 tokens 63 us (25); 256 requests of 1000 to 2000 tokens 118 us (73); 64 of them behind
+// 2048 shared tokens 61 us (19).
 #include <type_traits>
 
 #include "kvx_attn.cuh"

@@ -13,7 +13,7 @@
 // against one exponential and about five instructions a score on four warps.  Measured: eight prompts
 // behind a shared prefix, 842 GFLOP in all, 682-708 us with the plan and the join (1.19-1.23 PFLOP/s); the tensor
 // cores are busy 61-64 % of this kernel's time and wait for weights in the rest.  Two threads a row, each with
-// half of its keys, took longer (749 against 704 us then).  The same prompts over a 4-bit pool take 1,150 to 1,180 us: its tiles
+// half of its keys, took longer (749 against 704 us then).  The same prompts over a 4-bit pool take 1,160 to 1,185 us: its tiles
 // are made from codes by warps 8-11, keys as two tiles (see there), so that the products are half as many again.
 //
 // A row's sums refer to a maximum that is renewed only when a score passes it by 2^8 (f16: 2^2): the factor

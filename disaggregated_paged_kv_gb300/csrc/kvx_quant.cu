@@ -9,7 +9,7 @@
 //
 // Bound: bytes, 2 + 5/8 of them an element of a 16-bit tensor and a 4-bit pool, and instructions close behind: an element
 // costs about five to encode and four to decode.  2048 tokens of 36 layers of 8 heads of 128, written from bf16 and read
-// back, 152 us (the bytes take 103); 20000 tokens of 28 layers of 4 heads read back 136 us (111), 5.5 TB/s.  Stores alone keep
+// back, 152 us (the bytes take 103); 20000 tokens of 28 layers of 2 heads read back 136 us (111), 5.5 TB/s.  Stores alone keep
 // 69 % of the issue slots busy.  A call of few tokens is 2.3 us on the GPU, less than its host side.
 #include <cuda_bf16.h>
 

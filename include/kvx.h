@@ -702,10 +702,11 @@ typedef struct kvx_attn_args {
  *   out = v_scale * sum_j exp(s_j) V_j / sum_j exp(s_j),   lse = log sum_j exp(s_j).
  * Sums are held in 32 bits; with 16- and 8-bit pools the weights exp(s_j - max) are rounded to the
  * pool's 16-bit type (F16 for an FP8 or KVX_Q4 pool, its queries too) for the product with V.  With a
- * KVX_Q4 pool the weights' products with the scales of V are rounded to F16 too, or, where many rows
- * meet the same keys, V's elements; K's elements are exact (to 2^-24 where a scale is below 2^-13).
- * Elements are expected within +-65504, as kvx_store_kv leaves them.  Results do not depend on
- * scheduling: the same call gives the same bits.
+ * KVX_Q4 pool the weights' products with the scales of V are rounded to F16's 11 bits too (to 2^-37 of the greatest
+ * weight times the greatest scale where they are below 2^-26 of that), or, where many rows meet the same
+ * keys, V's elements (to 2^-25 where they are below 2^-14); K's elements are exact (to 2^-24 where a scale
+ * is below 2^-13).  Elements that a row sees are expected within +-65504, as kvx_store_kv leaves them: beyond,
+ * they may count as infinite.  Results do not depend on scheduling: the same call gives the same bits.
  * A row that sees nothing (a length of 0, or fewer positions than query tokens), or whose every
  * score is -inf, is 0 with lse -inf.  What masked positions and other slots hold, NaN and
  * infinities included, does not reach a result.  Tokens of no request (at or past
