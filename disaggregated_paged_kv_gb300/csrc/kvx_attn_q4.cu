@@ -359,10 +359,11 @@ struct Worker {
     }
     float o[G][2][4] = {}, z[4] = {};  // z: of the unit of (scale, low) words that is r8's
     int odd = 0;
-    // Weights' products with the values' scales are f16 numbers times `factor`, a power of two.  While all scales of the
-    // piece so far, and it is the same for all rows, are 0 or within kLeast .. 1 once multiplied by it, that is exact, and the products of
-    // the greatest weights are far above f16's least numbers; from the first that is not, or
-    // from where on rows differ in what they see, products are of 32 bits, rounded once, and the factor is the block's and row r8's own.
+    // Weights' products with the values' scales are f16 numbers, up_by times what they are.  up_by is a power of two, by which
+    // the greatest scale of the piece so far comes to 1/2 .. 1, the same for all rows.  While no other scale but 0 then is below
+    // kLeast, scales times up_by are exact, and products of weights far below the greatest are normal numbers still.  From
+    // the first that is below, and from where on rows differ in what they see, products are made in 32 bits and rounded once, and up_by
+    // is of row r8, by its greatest product in the block.
     float up_by = 0x1p15f;
     bool apart = false;
     const uint32_t kp = p.q4_key_pitch, mine = (slot >> p.q4_pair) * p.q4_head_pitch + (slot & p.q4_pair) * q4_bytes(D);
@@ -452,9 +453,9 @@ struct Worker {
           if (odd_word(zw[i] & 0xffff0000u)) zw[i] &= 0xffffu, odd = 1;
         }
       }
-      // ---- weights; what they refer to is renewed where a score passes it by far, the scales' factor where one asks for it
+      // ---- weights; what they refer to is renewed where a score passes it by far, up_by where a scale asks for it
       float e[4] = {s[0] - base[0], s[1] - base[1], s[2] - base[0], s[3] - base[1]};
-      uint32_t zs[2];  // the scales times the factor
+      uint32_t zs[2];  // the scales times up_by
       auto scales_fit = [&]() {
         // (units of scales; lows are of no account)
         const __half2 none = as_half2(0), by = __float2half2_rn(up_by), s0 = as_half2(r8 & 1 ? 0 : zw[0]), s1 = as_half2(r8 & 1 ? 0 : zw[1]);
@@ -503,7 +504,7 @@ struct Worker {
         const uint32_t f[4] = {zw[0], 0, zw[1], 0};
         mma16816<__half>(z, f, p0, p1);
       }
-      if (apart) {  // the factor by the row's greatest product in the block
+      if (apart) {
         __half2 h[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
